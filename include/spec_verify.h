@@ -177,6 +177,29 @@ spec_status spec_verify_attn(const void* q, const void* k_new,
                              void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * spec_verify_attn_window -- spec_verify_attn with a sliding window and sinks.
+ *
+ * Page 3 (tree-attention section) and page 2 §3.3 leave the cache's growth to
+ * the engine; a model with a sliding window reads only the last `window`
+ * positions and the first `sinks` ones.  Row i stands at position
+ * ctx + depth(i) (ctx + i in a chain); of the keys that spec_verify_attn shows
+ * it, it sees those at positions below `sinks` or greater than its own less
+ * `window` (itself included; a new key stands at ctx plus its node's depth).
+ *
+ *   window >= 1, sinks >= 0
+ * Other arguments as in spec_verify_attn.  Table entries of pages that hold
+ * neither one of the first `sinks` positions nor a position from
+ * ctx - window + 1 on are not read and may hold anything
+ * (spec_block_tables returns those pages).  A window of the whole context
+ * gives spec_verify_attn's results.
+ */
+spec_status spec_verify_attn_window(const void* q, const void* k_new, const void* v_new,
+                                    void* k_cache, void* v_cache, const int32_t* block_table,
+                                    const int32_t* ctx_lens, const int32_t* parent, int32_t window,
+                                    int32_t sinks, void* out, float* lse, const spec_dims* dims,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/*
  * spec_reject_sample -- accept / reject / resample of the drafts.
  *
  * p = softmax(target/T), q = softmax(draft/T) with the request's temperature
@@ -372,6 +395,128 @@ spec_status spec_reject_sample_noalloc(const void* target_logits,
                                        int32_t* out_tokens, int32_t* path,
                                        int32_t* accepted_len, float* probe,
                                        const spec_dims* dims, void* stream);
+
+/*
+ * spec_block_tables -- block tables, slot map and positions of a step's new
+ * rows, from the requests' lengths.
+ *
+ * Page 2 §4.3 and page 3: the cache is paged and a block table maps a
+ * request's positions to blocks; page 2 §3.3: what lies past the accepted
+ * prefix is dropped.  One call before a step makes each request hold exactly
+ * the pages that the step reads or writes: it takes pages for the new rows
+ * from a ring of free block ids and returns the pages that a rollback
+ * (kv_commit), a window that moved on, or the request's end left over.
+ *
+ *   ctx_lens  [B] int32   cached tokens; -1: the request has ended (or its
+ *                         place is empty) and returns every page
+ *   row_start [B+1] int32 or NULL   rows row_start[b] .. row_start[b+1]-1 are
+ *                         request b's new rows (ascending, within [0, rows]);
+ *                         NULL: M rows each, b*M .. b*M+M-1
+ *   parent    [B, M] int32 or NULL   trees (only without row_start): positions
+ *                         follow the nodes' depths; slots stay ctx + i
+ *   rows                  rows of slots and positions (>= B*M without row_start)
+ *   window, sinks         0, or the window and sinks of
+ *                         spec_verify_attn_window: only pages of the first
+ *                         `sinks` positions and of positions from
+ *                         ctx - window + 1 on are held
+ *   block_table [B, max_blocks] int32 (in/out)   entries of pages not held: -1
+ *   span      [B, 2] int32, 8-byte aligned (in/out)   pages (lo, hi) held: p < hi
+ *                         with p >= lo or among the sinks' pages; 0, 0 at first
+ *   pool      [num_blocks] int32 (in/out)   ring of free ids
+ *   pool_state [2] int32 (in/out)   head, count: entries (head + i) %
+ *                         num_blocks, i < count, are free
+ *   slots     [rows] int64    block * 16 + offset of each row, -1 without one
+ *   positions [rows] int32    position of each row, -1 without one
+ *   ok        [B] int32 or NULL   1: the request may run this step
+ *
+ * Pages are taken from the ring's head and returned to its tail, both in
+ * (request, page) order; returned pages are free from the next call on.  A
+ * request gets its pages if the ring holds those that it and all requests
+ * before it ask for; else it takes none (it still returns what it no longer
+ * needs), its rows get -1, ok is 0 and SPEC_ERR_CAPACITY is raised.  Rows
+ * behind the last request's are left as they are.  A request with bad rows or
+ * topology (SPEC_ERR_INVALID_ARG), one that needs pages again that its
+ * window has returned (SPEC_ERR_INVALID_ARG), one whose rows pass max_blocks
+ * (SPEC_ERR_CAPACITY) or a bad span (SPEC_ERR_DEVICE_BOUNDS) is left
+ * unchanged, with rows of -1 and ok 0.  A bad pool_state leaves every request
+ * unchanged.  Calls that share a page state or a workspace must not overlap.
+ */
+spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
+                              const int32_t* parent, int32_t rows, int32_t window, int32_t sinks,
+                              int32_t* block_table, int32_t* span, int32_t* pool,
+                              int32_t* pool_state, int64_t* slots, int32_t* positions, int32_t* ok,
+                              const spec_dims* dims, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * spec_qk_norm_rope -- RMS norm of every query and key head and the position
+ * rotation in one pass; keys and values to the paged cache by slot.
+ *
+ * The queries and keys that spec_verify_attn takes, with their position
+ * encoding applied.  For a head x at position t:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight       (no norm without a weight)
+ *   (a, b) -> (a cos - b sin, b cos + a sin), angle t * inv_freq[j], for the
+ *   pairs (j, j + rot_dim/2), or (2j, 2j + 1) if interleaved, j < rot_dim/2
+ * in fp32 (angles reduced exactly), rounded once.
+ *
+ *   q [rows, Hq, D], k, v [rows, Hkv, D]  kv_dtype   rows q_stride, k_stride,
+ *                 v_stride elements apart (multiples of 16 bytes), heads dense:
+ *                 views of one projection's output will do
+ *   q_weight, k_weight [D] kv_dtype or NULL
+ *   positions [rows] int32   -1: the row's outputs are zero and the caches
+ *                 stay as they are
+ *   inv_freq [rot_dim/2] double   rot_dim: a multiple of 16 up to D (0: no
+ *                 rotation)
+ *   q_out [rows, Hq, D], k_out [rows, Hkv, D]   dense; q_out may be q itself
+ *                 and k_out k itself where those are dense
+ *   slots [rows] int64 or NULL   with slots, the rotated key and the value of
+ *                 each row also go to k_cache / v_cache ([num_blocks, Hkv, 16,
+ *                 D]) at that slot; slots < 0 write nothing, slots past the
+ *                 cache raise SPEC_ERR_DEVICE_BOUNDS and write nothing.  Slots
+ *                 must differ from one another.  v, k_cache and v_cache are
+ *                 needed with slots (k_out may then be NULL) and not read
+ *                 without
+ */
+spec_status spec_qk_norm_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const void* q_weight,
+                              const void* k_weight, float eps, const int32_t* positions,
+                              const double* inv_freq, int32_t rot_dim, int32_t interleaved,
+                              int32_t rows, void* q_out, void* k_out, const int64_t* slots,
+                              void* k_cache, void* v_cache, const spec_dims* dims, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * spec_sample -- one token per logits row from given uniforms, with
+ * temperature, top-k, top-p and min-p.
+ *
+ * The draft's own draws, and plain decoding (gamma 0, the fallback of
+ * spec_ctrl_update).  The law of a row is softmax(x / T) (page 1 §3.3)
+ * restricted as in spec_reject_sample_filtered (the first top_k tokens by
+ * logit, the smaller index first among equal ones; of those the shortest
+ * prefix whose mass reaches top_p times theirs) and then to the tokens of at
+ * least min_p times the largest probability, renormalised; the token is the
+ * smallest i with C_i > u * Z in vocabulary order.  T = 0 is greedy: the first
+ * largest logit.
+ *
+ *   logits [rows, V] logits_dtype, rows row_stride elements apart (any
+ *                 stride >= V, any alignment of the elements); -inf: never drawn
+ *   temperature [rows] float   as in spec_reject_sample
+ *   top_k [rows] int32 or NULL   >= 0 (0: off)
+ *   top_p [rows] float or NULL   in (0, 1] (1: off)
+ *   min_p [rows] float or NULL   in [0, 1] (0: off)
+ *   uniform [rows] float         in [0, 1)
+ *   out_tokens [rows] int32; out_prob [rows] float or NULL   the token and its
+ *                 probability under the restricted law (1 when greedy)
+ *   ws, ws_bytes  at least 16 bytes (its first word is the status word)
+ * V up to 2^20.  A bad parameter (SPEC_ERR_INVALID_ARG) or a row with NaN,
+ * +inf or only -inf (SPEC_ERR_NONFINITE) gives token -1 and probability 0.
+ * Sums are held to about 2^-40, so the token is the definition's unless u * Z
+ * lies that close to a step.  No state is kept in the workspace.
+ */
+spec_status spec_sample(const void* logits, int64_t row_stride, int32_t rows, int32_t V,
+                        int32_t logits_dtype, const float* temperature, const int32_t* top_k,
+                        const float* top_p, const float* min_p, const float* uniform,
+                        int32_t* out_tokens, float* out_prob, void* ws, size_t ws_bytes,
+                        void* stream);
 
 /*
  * Host-side controller and metrics (no GPU work; plain host memory).

@@ -24,6 +24,9 @@ Modules:
                  token-by-token)
   kv             KV commit: rollback to the accepted prefix, tree-path
                  compaction
+  pages          block tables, slot map and positions from request lengths
+  rope           per-head norm and position rotation
+  sample         sampling with temperature, top-k, top-p and min-p
 
 Parity status: every function here is pinned by tests under tests/ against
 closed forms, exact enumeration, published known-answer vectors or brute
@@ -49,8 +52,12 @@ from .attention import (  # noqa: F401
     oracle_kv_append,
     oracle_verify_attn,
     oracle_verify_attn_tokenwise,
+    oracle_verify_attn_window,
     gather_positions,
     ancestors_or_self,
 )
 from .kv import oracle_kv_commit  # noqa: F401
 from .lm_head import oracle_lm_head  # noqa: F401
+from .pages import oracle_block_tables  # noqa: F401
+from .rope import oracle_norm_rope  # noqa: F401
+from .sample import oracle_sample  # noqa: F401

@@ -67,6 +67,44 @@ def oracle_kv_append(k_cache, v_cache, block_table, ctx_lens, k_new, v_new,
     return k, v
 
 
+def oracle_verify_attn_window(q, k_cache, v_cache, block_table, ctx_lens, k_new, v_new, window,
+                              sinks=0, parent=None, scale=None, block=16):
+    """Verify attention with a sliding window and sinks: node i stands at
+    position ctx + depth(i) and sees, of the cached positions and of its
+    ancestors-or-self (at ctx plus their depths), those below `sinks` or
+    greater than its own position less `window`.  Key by key, like
+    token-by-token decoding; cached positions that no row sees are not read.
+    Returns (out, lse, k_after, v_after)."""
+    q = np.asarray(q, dtype=np.float64)
+    B, M, Hq, D = q.shape
+    group = Hq // k_new.shape[2]
+    if scale is None:
+        scale = 1.0 / np.sqrt(D)
+    out = np.zeros((B, M, Hq, D), dtype=np.float64)
+    lse = np.zeros((B, M, Hq), dtype=np.float64)
+    for b in range(B):
+        ctx = int(ctx_lens[b])
+        par = None if parent is None else np.asarray(parent[b])
+        for i in range(M):
+            path = ancestors_or_self(par, i)
+            here = ctx + len(path) - 1
+            cached = np.array([t for t in range(ctx) if t < sinks or t > here - window],
+                              dtype=np.int64)
+            seen = [n for d, n in enumerate(path) if ctx + d < sinks or ctx + d > here - window]
+            K = np.concatenate([gather_positions(k_cache, block_table[b], cached, block),
+                                k_new[b, seen]]).astype(np.float64)
+            V = np.concatenate([gather_positions(v_cache, block_table[b], cached, block),
+                                v_new[b, seen]]).astype(np.float64)
+            s = np.einsum("phd,hgd->hgp", K, q[b, i].reshape(-1, group, D)) * scale
+            m = s.max(axis=-1, keepdims=True)
+            w = np.exp(s - m)
+            z = w.sum(axis=-1, keepdims=True)
+            out[b, i] = np.einsum("hgp,phd->hgd", w / z, V).reshape(Hq, D)
+            lse[b, i] = (m + np.log(z))[..., 0].reshape(Hq)
+    kc, vc = oracle_kv_append(k_cache, v_cache, block_table, ctx_lens, k_new, v_new, block)
+    return out, lse, kc, vc
+
+
 def oracle_verify_attn(q, k_cache, v_cache, block_table, ctx_lens, k_new,
                        v_new, parent=None, scale=None, block=16):
     """Batched masked verify attention after the append.

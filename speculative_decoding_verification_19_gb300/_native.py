@@ -33,6 +33,7 @@ EXPORTS = (
     "spec_status_string", "spec_last_launch_count", "spec_reject_sample_noalloc",
     "spec_ctrl_default_config", "spec_ctrl_init", "spec_ctrl_update", "spec_ctrl_metrics",
     "spec_step_stats",
+    "spec_verify_attn_window", "spec_block_tables", "spec_qk_norm_rope", "spec_sample",
 )
 
 
@@ -93,6 +94,16 @@ def lib() -> ctypes.CDLL:
     L.spec_reject_sample_noalloc.restype = i32
     L.kv_commit.argtypes = [vp] * 7 + [pd, vp, sz, vp]
     L.kv_commit.restype = i32
+    f32, i64 = ctypes.c_float, ctypes.c_int64
+    L.spec_verify_attn_window.argtypes = [vp] * 8 + [i32, i32, vp, vp, pd, vp, sz, vp]
+    L.spec_verify_attn_window.restype = i32
+    L.spec_block_tables.argtypes = [vp, vp, vp, i32, i32, i32] + [vp] * 7 + [pd, vp, sz, vp]
+    L.spec_block_tables.restype = i32
+    L.spec_qk_norm_rope.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, f32, vp, vp, i32, i32, i32,
+                                    vp, vp, vp, vp, vp, pd, vp, sz, vp]
+    L.spec_qk_norm_rope.restype = i32
+    L.spec_sample.argtypes = [vp, i64, i32, i32, i32] + [vp] * 7 + [vp, sz, vp]
+    L.spec_sample.restype = i32
     L.spec_philox_block.argtypes = [ctypes.POINTER(u64)] * 3
     L.spec_philox_block.restype = None
     L.spec_status_string.argtypes = [i32]
@@ -165,8 +176,69 @@ def device_status(ws: torch.Tensor, clear: bool = True, stream=None) -> int:
     return int(out.value)
 
 
+def _expect(name, t, dtype, shape=None, device=None, optional=False):
+    """A tensor's address after checks of its type, shape and device; dense
+    unless `shape` is None."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is needed")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} is wanted, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} lives on {t.device}, not on {device}")
+    if shape is not None:
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}: shape {shape} is wanted, not {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on(t, name):
+    """The device of a call's first tensor (which must be a GPU)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    return t.device
+
+
+def _launch(fn, device, stream, *args):
+    """Calls the library on the tensors' device and its current stream."""
+    L = lib()
+    with_guard = device.index != torch.cuda.current_device()
+    if with_guard:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            code = getattr(L, fn)(*args, s.cuda_stream)
+    else:
+        s = torch.cuda.current_stream() if stream is None else stream
+        code = getattr(L, fn)(*args, s.cuda_stream)
+    if code != 0:
+        raise SpecError(fn, code)
+    return L.spec_last_launch_count()
+
+
 def spec_verify_attn(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens,
-                     parent, out, lse, dims: SpecDims, ws, stream=None) -> int:
+                     parent, out, lse, dims: SpecDims, ws, stream=None, window=None,
+                     sinks=0) -> int:
+    """spec_verify_attn; with a window (and sinks) spec_verify_attn_window."""
+    if window is not None:
+        dev = _on(q, "q")
+        kv = torch.bfloat16 if dims.kv_dtype == SPEC_BF16 else torch.float32
+        B, M, Hq, Hkv, D = dims.B, dims.M, dims.Hq, dims.Hkv, dims.D
+        cache = (dims.num_blocks, Hkv, dims.block, D)
+        return _launch(
+            "spec_verify_attn_window", dev, stream,
+            _expect("q", q, kv, (B, M, Hq, D), dev),
+            _expect("k_new", k_new, kv, (B, M, Hkv, D), dev),
+            _expect("v_new", v_new, kv, (B, M, Hkv, D), dev),
+            _expect("k_cache", k_cache, kv, cache, dev), _expect("v_cache", v_cache, kv, cache, dev),
+            _expect("block_table", block_table, torch.int32, (B, dims.max_blocks), dev),
+            _expect("ctx_lens", ctx_lens, torch.int32, (B,), dev),
+            _expect("parent", parent, torch.int32, (B, M), dev, True), int(window), int(sinks),
+            _expect("out", out, kv, (B, M, Hq, D), dev),
+            _expect("lse", lse, torch.float32, (B, M, Hq), dev, True),
+            ctypes.byref(dims), _expect("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel())
     code = lib().spec_verify_attn(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
         _ptr(block_table), _ptr(ctx_lens), _ptr(parent), _ptr(out), _ptr(lse),
@@ -197,6 +269,85 @@ def spec_reject_sample(target_logits, draft_logits, tokens, parent, temperature,
             _stream(stream))
         _check("spec_reject_sample_filtered", code)
     return lib().spec_last_launch_count()
+
+
+def spec_block_tables(ctx_lens, row_start, parent, block_table, span, pool, pool_state, slots,
+                      positions, ok, dims: SpecDims, ws, window=0, sinks=0, stream=None) -> int:
+    """Block tables, slot map and positions of a step's new rows from the
+    requests' lengths; pages come from and go back to a ring of free ids
+    (block_table, span, pool and pool_state are updated in place)."""
+    dev, i32 = _on(ctx_lens, "ctx_lens"), torch.int32
+    B, rows = dims.B, slots.numel()
+    return _launch(
+        "spec_block_tables", dev, stream, _expect("ctx_lens", ctx_lens, i32, (B,), dev),
+        _expect("row_start", row_start, i32, (B + 1,), dev, True),
+        _expect("parent", parent, i32, (B, dims.M), dev, True), rows, int(window), int(sinks),
+        _expect("block_table", block_table, i32, (B, dims.max_blocks), dev),
+        _expect("span", span, i32, (B, 2), dev), _expect("pool", pool, i32, (dims.num_blocks,), dev),
+        _expect("pool_state", pool_state, i32, (2,), dev),
+        _expect("slots", slots, torch.int64, (rows,), dev),
+        _expect("positions", positions, i32, (rows,), dev), _expect("ok", ok, i32, (B,), dev, True),
+        ctypes.byref(dims), _expect("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel())
+
+
+def _rows_of(name, t, dtype, rows, heads, D, device):
+    """Address and row stride of a [rows, heads, D] view with dense heads."""
+    p = _expect(name, t, dtype, None, device)
+    if tuple(t.shape) != (rows, heads, D):
+        raise ValueError(f"{name}: shape {(rows, heads, D)} is wanted, not {tuple(t.shape)}")
+    s = t.stride()
+    if (D > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
+        raise ValueError(f"{name}: heads must be dense")
+    return p, (s[0] if rows > 1 else heads * D)
+
+
+def spec_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out,
+                      dims: SpecDims, ws, eps=1e-6, interleaved=False, slots=None, k_cache=None,
+                      v_cache=None, stream=None) -> int:
+    """RMS norm of every query and key head and the position rotation
+    (2 * len(inv_freq) values of each head turn); with slots, the keys and
+    values also go to the paged cache."""
+    dev = _on(q, "q")
+    kv = torch.bfloat16 if dims.kv_dtype == SPEC_BF16 else torch.float32
+    rows, Hq, Hkv, D = positions.numel(), dims.Hq, dims.Hkv, dims.D
+    qp, qs = _rows_of("q", q, kv, rows, Hq, D, dev)
+    kp, ks = _rows_of("k", k, kv, rows, Hkv, D, dev)
+    vp, vs = (None, 0) if slots is None else _rows_of("v", v, kv, rows, Hkv, D, dev)
+    cache = (dims.num_blocks, Hkv, dims.block, D)
+    half = 0 if inv_freq is None else inv_freq.numel()
+    return _launch(
+        "spec_qk_norm_rope", dev, stream, qp, kp, vp, qs, ks, vs,
+        _expect("q_weight", q_weight, kv, (D,), dev, True),
+        _expect("k_weight", k_weight, kv, (D,), dev, True), float(eps),
+        _expect("positions", positions, torch.int32, (rows,), dev),
+        _expect("inv_freq", inv_freq, torch.float64, (half,), dev, True), 2 * half,
+        1 if interleaved else 0, rows, _expect("q_out", q_out, kv, (rows, Hq, D), dev),
+        _expect("k_out", k_out, kv, (rows, Hkv, D), dev, slots is not None),
+        _expect("slots", slots, torch.int64, (rows,), dev, True),
+        _expect("k_cache", k_cache, kv, cache, dev, slots is None),
+        _expect("v_cache", v_cache, kv, cache, dev, slots is None),
+        ctypes.byref(dims), _expect("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel())
+
+
+def spec_sample(logits, temperature, uniform, out_tokens, out_prob, ws, top_k=None, top_p=None,
+                min_p=None, stream=None) -> int:
+    """One token per row of logits [rows, V] (any row stride) from given
+    uniforms, with temperature, top-k, top-p and min-p."""
+    dev, f32 = _on(logits, "logits"), torch.float32
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits: [rows, V] with dense rows is wanted")
+    rows, V = logits.shape
+    return _launch(
+        "spec_sample", dev, stream, _expect("logits", logits, logits.dtype, None, dev),
+        logits.stride(0) if rows > 1 else V, rows, V, dtype_code(logits.dtype),
+        _expect("temperature", temperature, f32, (rows,), dev),
+        _expect("top_k", top_k, torch.int32, (rows,), dev, True),
+        _expect("top_p", top_p, f32, (rows,), dev, True),
+        _expect("min_p", min_p, f32, (rows,), dev, True),
+        _expect("uniform", uniform, f32, (rows,), dev),
+        _expect("out_tokens", out_tokens, torch.int32, (rows,), dev),
+        _expect("out_prob", out_prob, f32, (rows,), dev, True),
+        _expect("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel())
 
 
 def spec_lm_head(hidden, weight, logits, ws, stream=None) -> int:

@@ -5,11 +5,14 @@
 #include <string.h>
 
 #include "attn.cuh"
+#include "block_tables.cuh"
 #include "common.cuh"
 #include "kv_commit.cuh"
 #include "philox.cuh"
 #include "lm_head.cuh"
+#include "qk_norm_rope.cuh"
 #include "reject_sample.cuh"
+#include "sample.cuh"
 
 namespace specv {
 
@@ -46,6 +49,8 @@ WsLayout workspace_layout(const spec_dims& d) {
   L.tc_pair_off = take(sizeof(int32_t) * (size_t)d.B * (size_t)(d.Hkv > 0 ? d.Hkv : 0));
   L.tc_anc_off = take(2 * sizeof(uint64_t) * (size_t)d.B * d.M);
   L.tc_sync_off = take(16);
+  L.win_depth_off = take(sizeof(int32_t) * (size_t)d.B * d.M);
+  L.pg_sync_off = take(16);
   const int group = d.Hkv > 0 ? d.Hq / d.Hkv : 0;
   L.rows = group * d.M;
   L.split_keys = attn_split_keys(d);
@@ -140,10 +145,11 @@ spec_status spec_get_device_status(void* ws, void* stream, int32_t* flags, int32
   return SPEC_OK;
 }
 
-spec_status spec_verify_attn(const void* q, const void* k_new, const void* v_new, void* k_cache,
-                             void* v_cache, const int32_t* block_table, const int32_t* ctx_lens,
-                             const int32_t* parent, void* out, float* lse, const spec_dims* dims,
-                             void* ws, size_t ws_bytes, void* stream) {
+static spec_status attn_common(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                               void* v_cache, const int32_t* block_table, const int32_t* ctx_lens,
+                               const int32_t* parent, int32_t window, int32_t sinks, void* out,
+                               float* lse, const spec_dims* dims, void* ws, size_t ws_bytes,
+                               void* stream) {
   g_launches = 0;
   spec_status s = check_common(dims);
   if (s != SPEC_OK) return s;
@@ -190,12 +196,39 @@ spec_status spec_verify_attn(const void* q, const void* k_new, const void* v_new
   a.lse = lse;
   a.d = *dims;
   a.scale = dims->softmax_scale != 0.f ? dims->softmax_scale : 1.0f / sqrtf((float)dims->D);
+  a.window = window;
+  a.sinks = sinks;
   a.ws = ws;
   int launches = 0;
   const cudaError_t e = use_tc ? attn_launch_tc(a, lay, static_cast<cudaStream_t>(stream), &launches)
                                : attn_launch_simt(a, lay, static_cast<cudaStream_t>(stream), &launches);
   g_launches = launches;
   return from_cuda(e);
+}
+
+spec_status spec_verify_attn(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                             void* v_cache, const int32_t* block_table, const int32_t* ctx_lens,
+                             const int32_t* parent, void* out, float* lse, const spec_dims* dims,
+                             void* ws, size_t ws_bytes, void* stream) {
+  return attn_common(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, 0, 0, out,
+                     lse, dims, ws, ws_bytes, stream);
+}
+
+spec_status spec_verify_attn_window(const void* q, const void* k_new, const void* v_new,
+                                    void* k_cache, void* v_cache, const int32_t* block_table,
+                                    const int32_t* ctx_lens, const int32_t* parent, int32_t window,
+                                    int32_t sinks, void* out, float* lse, const spec_dims* dims,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  if (dims == nullptr || window < 1 || sinks < 0) return SPEC_ERR_INVALID_ARG;
+  // positions stay below 2^31; a window or sinks past the table's last
+  // position mean all of it
+  const int64_t cap = (int64_t)dims->max_blocks * kBlock;
+  if (cap > INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
+  const int32_t most = cap > 0 ? (int32_t)cap : 1;
+  return attn_common(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent,
+                     window < most ? window : most, sinks < most ? sinks : most, out, lse, dims, ws,
+                     ws_bytes, stream);
 }
 
 static spec_status reject_common(const void* target_logits, const void* draft_logits,
@@ -384,6 +417,138 @@ spec_status kv_commit(void* k_cache, void* v_cache, const int32_t* block_table,
   a.ws = ws;
   int launches = 0;
   const cudaError_t e = commit_launch(a, lay, static_cast<cudaStream_t>(stream), &launches);
+  g_launches = launches;
+  return from_cuda(e);
+}
+
+spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
+                              const int32_t* parent, int32_t rows, int32_t window, int32_t sinks,
+                              int32_t* block_table, int32_t* span, int32_t* pool,
+                              int32_t* pool_state, int64_t* slots, int32_t* positions, int32_t* ok,
+                              const spec_dims* dims, void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  spec_status s = check_common(dims);
+  if (s != SPEC_OK) return s;
+  if (dims->B > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (dims->max_blocks < 1 || dims->num_blocks < 1) return SPEC_ERR_INVALID_ARG;
+  if ((int64_t)dims->max_blocks * kBlock > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+  if ((s = check_ws(dims, ws, ws_bytes)) != SPEC_OK) return s;
+  if (!ctx_lens || !block_table || !span || !pool || !pool_state || !slots || !positions)
+    return SPEC_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(span) & 7u) != 0) return SPEC_ERR_INVALID_ARG;
+  if (rows < 0 || window < 0 || sinks < 0) return SPEC_ERR_INVALID_ARG;
+  if (row_start != nullptr ? parent != nullptr : (int64_t)dims->B * dims->M > rows)
+    return SPEC_ERR_INVALID_ARG;
+  const int cap = dims->max_blocks * kBlock;
+  PageArgs a;
+  a.ctx_lens = ctx_lens;
+  a.row_start = row_start;
+  a.parent = parent;
+  a.rows = rows;
+  a.window = window;
+  a.sinks = sinks < cap ? sinks : cap;
+  a.block_table = block_table;
+  a.span = span;
+  a.pool = pool;
+  a.pool_state = pool_state;
+  a.slots = slots;
+  a.positions = positions;
+  a.ok = ok;
+  a.d = *dims;
+  a.ws = ws;
+  int launches = 0;
+  const cudaError_t e = block_tables_launch(a, workspace_layout(*dims),
+                                            static_cast<cudaStream_t>(stream), &launches);
+  g_launches = launches;
+  return from_cuda(e);
+}
+
+spec_status spec_qk_norm_rope(const void* q, const void* k, const void* v, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, const void* q_weight,
+                              const void* k_weight, float eps, const int32_t* positions,
+                              const double* inv_freq, int32_t rot_dim, int32_t interleaved,
+                              int32_t rows, void* q_out, void* k_out, const int64_t* slots,
+                              void* k_cache, void* v_cache, const spec_dims* dims, void* ws,
+                              size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  spec_status s = check_common(dims);
+  if (s != SPEC_OK) return s;
+  if ((s = check_kv(dims)) != SPEC_OK) return s;
+  if ((s = check_ws(dims, ws, ws_bytes)) != SPEC_OK) return s;
+  if (rows < 0 || !(eps >= 0.f) || !(eps < INFINITY)) return SPEC_ERR_INVALID_ARG;
+  if (!q || !k || !positions || !q_out) return SPEC_ERR_INVALID_ARG;
+  if (slots != nullptr ? (!v || !k_cache || !v_cache) : !k_out) return SPEC_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > dims->D || (rot_dim > 0 && !inv_freq)) return SPEC_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return SPEC_ERR_UNSUPPORTED;
+  const int vec = dims->kv_dtype == SPEC_BF16 ? 8 : 4;
+  const int64_t q_row = (int64_t)dims->Hq * dims->D, k_row = (int64_t)dims->Hkv * dims->D;
+  if (q_stride < q_row || k_stride < k_row || (slots != nullptr && v_stride < k_row))
+    return SPEC_ERR_INVALID_ARG;
+  if (q_stride % vec != 0 || k_stride % vec != 0 || (slots != nullptr && v_stride % vec != 0))
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(k_cache) || !aligned16(v_cache))
+    return SPEC_ERR_INVALID_ARG;
+  if (rows == 0) return SPEC_OK;
+  RopeArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved;
+  a.rows = rows;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.slots = slots;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.d = *dims;
+  a.ws = ws;
+  int launches = 0;
+  const cudaError_t e = qk_norm_rope_launch(a, workspace_layout(*dims),
+                                            static_cast<cudaStream_t>(stream), &launches);
+  g_launches = launches;
+  return from_cuda(e);
+}
+
+spec_status spec_sample(const void* logits, int64_t row_stride, int32_t rows, int32_t V,
+                        int32_t logits_dtype, const float* temperature, const int32_t* top_k,
+                        const float* top_p, const float* min_p, const float* uniform,
+                        int32_t* out_tokens, float* out_prob, void* ws, size_t ws_bytes,
+                        void* stream) {
+  g_launches = 0;
+  if (ws == nullptr || ws_bytes < 16 || !aligned16(ws)) return SPEC_ERR_INVALID_ARG;
+  if (logits_dtype != SPEC_BF16 && logits_dtype != SPEC_F32) return SPEC_ERR_INVALID_ARG;
+  if (rows < 0 || V < 1 || row_stride < V) return SPEC_ERR_INVALID_ARG;
+  if (V > kSampleMaxVocab || rows > (1 << 27)) return SPEC_ERR_UNSUPPORTED;
+  if (!logits || !temperature || !uniform || !out_tokens) return SPEC_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) % (logits_dtype == SPEC_BF16 ? 2 : 4) != 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (rows == 0) return SPEC_OK;
+  SampleArgs a;
+  a.logits = logits;
+  a.stride = row_stride;
+  a.rows = rows;
+  a.V = V;
+  a.dtype = logits_dtype;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.uniform = uniform;
+  a.out_tokens = out_tokens;
+  a.out_prob = out_prob;
+  a.status = static_cast<uint32_t*>(ws);
+  int launches = 0;
+  const cudaError_t e = sample_launch(a, static_cast<cudaStream_t>(stream), &launches);
   g_launches = launches;
   return from_cuda(e);
 }

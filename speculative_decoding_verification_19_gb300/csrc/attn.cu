@@ -31,8 +31,8 @@ template <typename T>
 __global__ void __launch_bounds__(256) kv_append_kernel(
     const T* __restrict__ k_new, const T* __restrict__ v_new, T* __restrict__ k_cache,
     T* __restrict__ v_cache, const int32_t* __restrict__ block_table,
-    const int32_t* ctx_lens, const int32_t* __restrict__ parent, spec_dims d,
-    int32_t* __restrict__ req_ok, uint32_t* __restrict__ status) {
+    const int32_t* ctx_lens, const int32_t* __restrict__ parent, spec_dims d, int window,
+    int sinks, int32_t* __restrict__ req_ok, uint32_t* __restrict__ status) {
   pdl_trigger();
   pdl_wait();  // the inputs and the cache may come from the previous kernel
   const int b = blockIdx.x;
@@ -44,13 +44,15 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
 
   // capacity
   const bool cap_ok = ctx >= 0 && L <= cap;
-  // block ids of every page the request reads or writes
+  // block ids of every page the request reads or writes (with a window, not
+  // of the pages between the sinks and it)
   int bad_block = 0;
   if (cap_ok) {
     const int pages = (int)ceil_div64(L, kBlock);
     for (int p = tid; p < pages; p += blockDim.x) {
       const int id = bt[p];
-      bad_block |= (id < 0 || id >= d.num_blocks);
+      bad_block |= (id < 0 || id >= d.num_blocks) &&
+                   (window <= 0 || win_page(p, ctx, window, sinks));
     }
   }
   // topology
@@ -112,21 +114,25 @@ constexpr int kMaxRows = 128;  // new rows per request (tree nodes)
 
 size_t attn_simt_smem_bytes(int R, int D) {
   return sizeof(float) * ((size_t)R * D + kTileKeys * (D + 4) + kTileKeys * D + (size_t)R * kTileKeys) +
-         sizeof(unsigned long long) * 2 * kMaxRows;
+         sizeof(unsigned long long) * 2 * kMaxRows + sizeof(int) * kMaxRows;
 }
 
-template <typename T, int D, int RPW>
+// kWin: a sliding window and sinks; the key axis is then the sinks' tiles and
+// the window's, without the tiles between them.
+template <typename T, int D, int RPW, bool kWin>
 __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
     const T* __restrict__ q, const T* __restrict__ k_cache, const T* __restrict__ v_cache,
     const int32_t* __restrict__ block_table, const int32_t* __restrict__ ctx_lens,
-    const int32_t* __restrict__ parent, const int32_t* __restrict__ req_ok, spec_dims d,
-    float qscale, int split_keys, int max_splits, float* __restrict__ part) {
+    const int32_t* __restrict__ parent, const int32_t* __restrict__ req_ok, spec_dims d, int window,
+    int sinks, float qscale, int split_keys, int max_splits, float* __restrict__ part) {
   constexpr int DPL = D / kWarp;  // d values per lane in the PV step
   static_assert(DPL == 2 || DPL == 4, "D must be 64 or 128");
   const int s = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   if (!req_ok[b]) return;
   const int ctx = ctx_lens[b];
-  const int L = ctx + d.M;
+  const int skip = kWin ? win_skip(ctx, window, sinks, kTileKeys) * kTileKeys : 0;
+  const int skip_at = kWin ? ceil_div(sinks, kTileKeys) * kTileKeys : 0;
+  const int L = ctx + d.M - skip;  // keys of the axis
   const int k0 = s * split_keys;
   if (k0 >= L) return;
   const int k1 = min(k0 + split_keys, L);
@@ -141,6 +147,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
   float* ps = vs + kTileKeys * D;
   // [row][2]: bits 0..63 and 64..127 of each row's mask
   unsigned long long* anc = reinterpret_cast<unsigned long long*>(ps + R * kTileKeys);
+  int* depth = reinterpret_cast<int*>(anc + 2 * kMaxRows);  // of each new row (kWin)
 
   // queries of the rows that read KV head h: row r = i*group + g
   for (int e = tid; e < R * D; e += kSimtThreads) {
@@ -151,7 +158,22 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
   // ancestor-or-self masks of the new rows
   for (int i = tid; i < d.M; i += kSimtThreads) {
     unsigned long long lo = 0, hi = 0;
-    if (parent == nullptr) {
+    if (kWin) {
+      // ancestors-or-self fewer than `window` positions above, or sinks (the
+      // append kernel has checked the topology)
+      const int32_t* par = parent != nullptr ? parent + (int64_t)b * d.M : nullptr;
+      int di = i;
+      if (par != nullptr) {
+        di = 0;
+        for (int n = i; n > 0 && di < kMaxRows; n = par[n]) ++di;
+      }
+      depth[i] = di;
+      for (int n = i, dn = di; n >= 0 && dn >= 0; n = par != nullptr ? par[n] : n - 1, --dn) {
+        if (di - dn >= window && ctx + dn >= sinks) continue;
+        if (n < 64) lo |= 1ull << n;
+        else hi |= 1ull << (n - 64);
+      }
+    } else if (parent == nullptr) {
       lo = i >= 63 ? ~0ull : ((1ull << (i + 1)) - 1);
       hi = i >= 127 ? ~0ull : (i >= 64 ? ((1ull << (i - 63)) - 1) : 0ull);
     } else {
@@ -185,9 +207,10 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
     __syncthreads();  // previous tile fully consumed
     for (int e = tid; e < kTileKeys * kVecPerKey; e += kSimtThreads) {
       const int kk = e / kVecPerKey, vi = e % kVecPerKey;
-      const int t = t0 + kk;
+      const int t = t0 + kk + (kWin && t0 >= skip_at ? skip : 0);
       float kf[kVec], vf[kVec];
-      if (t < k1) {
+      // a window's first tile may begin with pages that are not held
+      if (t0 + kk < k1 && (!kWin || win_page(t / kBlock, ctx, window, sinks))) {
         const int64_t base = (((int64_t)bt[t / kBlock] * d.Hkv + h) * kBlock + t % kBlock) * D;
         const uint4 kr = reinterpret_cast<const uint4*>(k_cache + base)[vi];
         const uint4 vr = reinterpret_cast<const uint4*>(v_cache + base)[vi];
@@ -206,7 +229,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
     __syncthreads();
 
     // scores: lane = key of the tile, rows warp + kSimtWarps*j
-    const int t = t0 + lane;
+    const int t = t0 + lane + (kWin && t0 >= skip_at ? skip : 0);
     float sc[RPW];
 #pragma unroll
     for (int j = 0; j < RPW; ++j) sc[j] = 0.f;
@@ -228,7 +251,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
       const int r = warp + kSimtWarps * j;
       if (r >= R) break;  // warp-uniform
       const int i = r / group;
-      bool vis = t < k1;
+      bool vis = t0 + lane < k1;
+      if (kWin && vis && t < ctx) vis = t < sinks || t > ctx + depth[i] - window;
       if (vis && t >= ctx) {
         const int k = t - ctx;  // new position, < M
         vis = (anc[2 * i + (k >> 6)] >> (k & 63)) & 1ull;
@@ -297,14 +321,15 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
 template <typename T>
 __global__ void __launch_bounds__(256) attn_combine_kernel(
     const float* __restrict__ part, const int32_t* __restrict__ ctx_lens,
-    const int32_t* __restrict__ req_ok, spec_dims d, int split_keys, int max_splits,
-    T* __restrict__ out, float* __restrict__ lse) {
+    const int32_t* __restrict__ req_ok, spec_dims d, int window, int sinks, int split_keys,
+    int max_splits, T* __restrict__ out, float* __restrict__ lse) {
   const int h = blockIdx.x, b = blockIdx.y;
   const int group = d.Hq / d.Hkv;
   const int R = group * d.M;
   const int D = d.D;
   const bool ok = req_ok[b] != 0;
-  const int L = ok ? ctx_lens[b] + d.M : 0;
+  int L = ok ? ctx_lens[b] + d.M : 0;  // keys of the split axis
+  if (ok && window > 0) L -= win_skip(ctx_lens[b], window, sinks, kTileKeys) * kTileKeys;
   const int nsp = ok ? ceil_div(L, split_keys) : 0;
   const float* pbase = part + ((int64_t)b * d.Hkv + h) * max_splits * (int64_t)R * (D + 1);
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
@@ -349,12 +374,12 @@ cudaError_t kv_append_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_
     e = cudaLaunchKernelEx(&L.cfg, kv_append_kernel<T>, static_cast<const T*>(a.k_new),
                            static_cast<const T*>(a.v_new), static_cast<T*>(a.k_cache),
                            static_cast<T*>(a.v_cache), a.block_table, a.ctx_lens, a.parent, d,
-                           req_ok, status);
+                           a.window, a.sinks, req_ok, status);
   } else {
     e = cudaLaunchKernelEx(&L.cfg, kv_append_kernel<float>, static_cast<const float*>(a.k_new),
                            static_cast<const float*>(a.v_new), static_cast<float*>(a.k_cache),
                            static_cast<float*>(a.v_cache), a.block_table, a.ctx_lens, a.parent,
-                           d, req_ok, status);
+                           d, a.window, a.sinks, req_ok, status);
   }
   ++*launches;
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -375,14 +400,15 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
   cudaError_t e = cudaSuccess;
 #define SPECV_SIMT(DD, RPW)                                                                   \
   do {                                                                                        \
-    auto k = attn_split_kernel<T, DD, RPW>;                                                   \
+    auto k = a.window > 0 ? attn_split_kernel<T, DD, RPW, true>                               \
+                          : attn_split_kernel<T, DD, RPW, false>;                                                   \
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);      \
     if (e != cudaSuccess) return e;                                                           \
     k<<<grid, kSimtThreads, smem, st>>>(static_cast<const T*>(a.q),                           \
                                         static_cast<const T*>(a.k_cache),                     \
                                         static_cast<const T*>(a.v_cache), a.block_table,      \
-                                        a.ctx_lens, a.parent, req_ok, d, qscale,              \
-                                        lay.split_keys, lay.max_splits, part);                \
+                                        a.ctx_lens, a.parent, req_ok, d, a.window, a.sinks,   \
+                                        qscale, lay.split_keys, lay.max_splits, part);                \
   } while (0)
   const int rpw = ceil_div(R, kSimtWarps);
   if (d.D == 128) {
@@ -402,7 +428,7 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
   ++*launches;
 
   attn_combine_kernel<T><<<dim3(d.Hkv, d.B), 256, 0, st>>>(
-      part, a.ctx_lens, req_ok, d, lay.split_keys, lay.max_splits, static_cast<T*>(a.out), a.lse);
+      part, a.ctx_lens, req_ok, d, a.window, a.sinks, lay.split_keys, lay.max_splits, static_cast<T*>(a.out), a.lse);
   ++*launches;
   return cudaGetLastError();
 }

@@ -18,8 +18,26 @@ struct AttnArgs {
   float* lse;
   spec_dims d;
   float scale;
+  int window, sinks;  // window 0: every cached position is visible
   void* ws;
 };
+
+// What a sliding window and sinks leave of a request with ctx cached tokens:
+// the first position of the window of its first new row (the others' windows
+// start later), the first page of the window, the pages of the sinks.
+__host__ __device__ __forceinline__ int win_first(int ctx, int window) {
+  return ctx - window + 1 > 0 ? ctx - window + 1 : 0;
+}
+__host__ __device__ __forceinline__ bool win_page(int page, int ctx, int window, int sinks) {
+  return page < ceil_div(sinks, kBlock) || page >= win_first(ctx, window) / kBlock;
+}
+// Key tiles of `keys` positions: the sinks' tiles come first, then the
+// window's; tiles between them are skipped.  Tile j of the kept ones is tile
+// j, or j + skip from the sinks' tiles on.
+__host__ __device__ __forceinline__ int win_skip(int ctx, int window, int sinks, int keys) {
+  const int s = win_first(ctx, window) / keys - ceil_div(sinks, keys);
+  return s > 0 ? s : 0;
+}
 
 // CTAs of the persistent tensor-core kernel never exceed this (partials are
 // sized for it).

@@ -127,11 +127,21 @@ size_t smem_bytes() { return kSmemBytes; }
 // pair, with the request's record (ctx, tiles per head, next request with
 // tiles) and the next request's record loaded one request ahead, so that no
 // role waits for a global load when it crosses into a new request.
+// With a window (kWin) tiles are counted over the kept ones (sinks, then
+// window), and real() is a tile's place in the request.
+template <bool kWin>
 struct Cursor {
   int b, h, tile, nt, ctx, next_b;
   int4 nrec;
+  int ns, skip;  // sink tiles, tiles left out after them (kWin)
+  __device__ int real() const { return kWin && tile >= ns ? tile + skip : tile; }
+  __device__ int real_of(int j) const { return kWin && j >= ns ? j + skip : j; }
+  // the same for the next request
+  __device__ int next_real_of(int j) const { return kWin && j >= ns ? j + nrec.w : j; }
   // st0 = (first tile, b, h, tile), st1 = (ctx, tiles, next request, end tile)
-  __device__ void start(int4 st0, int4 st1, const int4* rq, int B) {
+  __device__ void start(int4 st0, int4 st1, const int4* rq, int B, int sinks) {
+    ns = kWin ? ceil_div(sinks, kTileKeys) : 0;
+    skip = kWin ? __ldcg(&rq[st0.y].w) : 0;
     b = st0.y;
     h = st0.z;
     tile = st0.w;
@@ -150,6 +160,7 @@ struct Cursor {
     ctx = nrec.x;
     nt = nrec.y;
     next_b = nrec.z;
+    if (kWin) skip = nrec.w;
     if (next_b < B) nrec = __ldcg(rq + next_b);
   }
 };
@@ -198,6 +209,23 @@ __device__ __forceinline__ unsigned long long tile_visibility_wide(int kpos0, in
   return v & (pre | mask_window(anc_lo, anc_hi, -c0));
 }
 
+// Bits 0..n-1 of a word (none for n <= 0, all for n >= 64).
+__device__ __forceinline__ unsigned long long low_bits(int n) {
+  return n >= 64 ? ~0ull : (n <= 0 ? 0ull : ((1ull << n) - 1));
+}
+
+// The same with a window: cached positions are visible below `sinks` and from
+// wlo on; anc holds only the ancestors that the window leaves.
+__device__ __forceinline__ unsigned long long tile_visibility_win(
+    int kpos0, int nkeys, int ctx, int L, int sinks, int wlo, unsigned long long anc_lo,
+    unsigned long long anc_hi, bool real) {
+  if (!real) return 0ull;
+  const int c0 = ctx - kpos0;  // tile columns in the cached prefix
+  const unsigned long long pre =
+      low_bits(c0) & (low_bits(sinks - kpos0) | ~low_bits(wlo - kpos0));
+  return low_bits(min(L - kpos0, nkeys)) & (pre | mask_window(anc_lo, anc_hi, -c0));
+}
+
 // Ancestor-or-self mask of row i of a chain: bits 0..i.
 __device__ __forceinline__ void chain_mask(int i, unsigned long long* lo, unsigned long long* hi) {
   *lo = i >= 63 ? ~0ull : ((1ull << (i + 1)) - 1);
@@ -226,13 +254,15 @@ __device__ __forceinline__ void store32_bf16(__nv_bfloat16* dst, const uint32_t 
 // kWide: more than 64 new rows per request (128-bit ancestor masks); the
 // narrow kernel keeps one 64-bit word per row.  kShort: the wait limit is
 // short (ptx::mbar_wait_t).
-template <bool kWide, bool kShort>
+// kWin: a sliding window and sinks (masks and depths of the new rows come from
+// the prep kernel for chains too).
+template <bool kWide, bool kShort, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __nv_bfloat16* __restrict__ k_new,
     const __nv_bfloat16* __restrict__ v_new, __nv_bfloat16* __restrict__ k_cache,
     __nv_bfloat16* __restrict__ v_cache, const int32_t* __restrict__ block_table,
-    const int4* rq, const int4* starts, const ulonglong2* anc_ws, int* pairs, spec_dims d,
-    float qscale2, float* part, __nv_bfloat16* __restrict__ out,
+    const int4* rq, const int4* starts, const ulonglong2* anc_ws, const int* depth_ws, int window,
+    int sinks, int* pairs, spec_dims d, float qscale2, float* part, __nv_bfloat16* __restrict__ out,
     float* __restrict__ lse, uint32_t* __restrict__ status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -367,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     const int c16 = ct & 15;                                 // 16-byte chunk of a 256-byte row
     const int r0 = ct >> 4;                                  // rows r0, r0 + 4, r0 + 8, r0 + 12
     const uint32_t swz_half = (uint32_t)(c16 >> 3) * kHalfBytes;
-    Cursor cu;
-    cu.start(st0, st1, rq, B);
+    Cursor<kWin> cu;
+    cu.start(st0, st1, rq, B, sinks);
     int seg = -1, L = 0;
     int wb = -1, ww = -1, nb = -1, nw = -1;  // window held in ids and window loaded into nids
     int ids[kPages] = {0, 0, 0, 0}, nids[kPages] = {0, 0, 0, 0};
@@ -404,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
 #pragma unroll
           for (int p = 0; p < kPages; ++p) ids[p] = nids[p];
         } else {
-          const int page0 = ((w << 5) + lane) * kPages;
+          const int page0 = cu.real_of((w << 5) + lane) * kPages;
           const int32_t* bt = block_table + (int64_t)cu.b * d.max_blocks;
 #pragma unroll
           for (int p = 0; p < kPages; ++p) ids[p] = (page0 + p < d.max_blocks) ? bt[page0 + p] : 0;
@@ -425,13 +455,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
 #pragma unroll
           for (int p = 0; p < kPages; ++p) nids[p] = ids[p];
         } else if (nb < B) {
-          const int page0 = ((nw << 5) + lane) * kPages;
+          const int nj = (nw << 5) + lane;
+          const int page0 = (nb == cu.b ? cu.real_of(nj) : cu.next_real_of(nj)) * kPages;
           const int32_t* bt = block_table + (int64_t)nb * d.max_blocks;
 #pragma unroll
           for (int p = 0; p < kPages; ++p) nids[p] = (page0 + p < d.max_blocks) ? bt[page0 + p] : 0;
         }
       }
-      const int np = tile_pages(L, cu.tile);
+      const int rt = cu.real();
+      const int np = tile_pages(L, rt);
       const int src = cu.tile & 31;
       int blk[kPages];
 #pragma unroll
@@ -444,8 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
         break;
       }
       const uint32_t sb = ptx::smem_u32(stages + stage * kStageBytes);
-      const int kpos0 = cu.tile * kTileKeys;
-      if (kpos0 + kTileKeys <= cu.ctx) {  // all keys in the cached prefix
+      const int kpos0 = rt * kTileKeys;
+      // with a window, pages that no row sees are not held: they read as zero
+      const bool held = !kWin || rt * kPages >= win_first(cu.ctx, window) / kBlock ||
+                        rt * kPages + kPages <= ceil_div(sinks, kBlock);
+      if (kpos0 + kTileKeys <= cu.ctx && held) {  // all keys in the cached prefix
 #pragma unroll
         for (int p = 0; p < kPages; ++p) {
           const int64_t page = ((int64_t)blk[p] * Hkv + cu.h) * kBlock;  // row of slot 0
@@ -472,7 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
               const int pos = kpos0 + p * kBlock + r;
               const uint32_t so = swz_half + (uint32_t)p * kBoxBytes + (uint32_t)r * 128u +
                                   ((uint32_t)((c16 & 7) ^ (r & 7)) << 4);
-              if (pos < cu.ctx) {
+              if (kWin && !win_page(rt * kPages + p, cu.ctx, window, sinks)) {
+                ptx::cp_async16_fill(sb + so, k_new, 0u);
+                ptx::cp_async16_fill(sb + 2 * kHalfBytes + so, v_new, 0u);
+              } else if (pos < cu.ctx) {
                 const int64_t e = (page + r) * 128 + c16 * 8;
                 ptx::cp_async16(sb + so, k_cache + e);
                 ptx::cp_async16(sb + 2 * kHalfBytes + so, v_cache + e);
@@ -511,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     // ------------------------------------------------------------- MMA: Q K^T
     if (lane == 0) {
       const uint32_t id_qk_full = ptx::idesc_bf16_f32(128, kTileKeys, false, false);
-      Cursor cu;
-      cu.start(st0, st1, rq, B);
+      Cursor<kWin> cu;
+      cu.start(st0, st1, rq, B, sinks);
       int seg = -1, L = 0;
       int64_t t = 0;
       // Shared-memory descriptors built once; an operand at byte offset o
@@ -542,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
                                            wait))
           break;
         ptx::tc_fence_after();
-        const int np = tile_pages(L, cu.tile);
+        const int np = tile_pages(L, cu.real());
         const uint32_t idqk = np == kPages ? id_qk_full : ptx::idesc_bf16_f32(128, np * 16, false, false);
         const uint64_t dq = dq0 + (uint64_t)((qb * kQBytes) >> 4);
         const uint64_t dk = dk0 + (uint64_t)((stage * kStageBytes) >> 4);
@@ -570,14 +608,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     if (lane == 0) {
       const uint32_t id_pv = ptx::idesc_bf16_f32(128, 128, false, true);
       const uint64_t dv0 = ptx::sdesc_sw128(ptx::smem_u32(stages + 2 * kHalfBytes), kHalfBytes, 1024);
-      Cursor cu;
-      cu.start(st0, st1, rq, B);
+      Cursor<kWin> cu;
+      cu.start(st0, st1, rq, B, sinks);
       int L = 0;
       int64_t u = 0;
       for (int64_t g = g0; g < g1; ++g, ++u) {
         const bool first = (g == g0) || cu.tile == 0;
         if (first) L = cu.ctx + M;
-        const int np = tile_pages(L, cu.tile);
+        const int np = tile_pages(L, cu.real());
         const int sbuf = (int)(u % kSBufs);
         const int stage = (int)(u % kStages);
         if (!ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->p_full[sbuf]), (uint32_t)((u / kSBufs) & 1), abort,
@@ -607,14 +645,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     if (sp < n_sm_warps) {
       const uint32_t lane_base = tmem + ((uint32_t)(sp * 32) << 16);
       const int S = tc_part_stride(d.D);
-      Cursor cu;
-      cu.start(st0, st1, rq, B);
+      Cursor<kWin> cu;
+      cu.start(st0, st1, rq, B, sinks);
       int64_t t = 0;
       float m_used = -INFINITY, l = 0.f;
       unsigned long long anc = 0, anc_n = 0;        // mask bits 0..63
       unsigned long long anc_hi = 0, anc_hi_n = 0;  // bits 64..127 (kWide)
       int anc_b = -1, anc_nb = -1;  // requests whose masks anc and anc_n hold
       int ctx = 0, L = 0, tile0 = 0;
+      int depth = 0, depth_n = 0;  // this row's depth (kWin), the next request's
       int n_whole = 0;  // pair ends with output so far (barrier phase)
       const bool real = row < R;
       const int i = real ? row / group : 0;
@@ -627,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
           tile0 = cu.tile;
           m_used = -INFINITY;
           l = 0.f;
-          if (anc_ws == nullptr) {
+          if (!kWin && anc_ws == nullptr) {
             if (kWide) chain_mask(i, &anc, &anc_hi);
             else anc = (i >= 63) ? ~0ull : ((1ull << (i + 1)) - 1);
           } else if (real && cu.b != anc_b) {
@@ -637,14 +676,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
             if (cu.b == anc_nb) {
               anc = anc_n;
               if (kWide) anc_hi = anc_hi_n;
+              if (kWin) depth = depth_n;
             } else {
               anc = __ldcg(aw + 2 * ((int64_t)cu.b * M + i));
               if (kWide) anc_hi = __ldcg(aw + 2 * ((int64_t)cu.b * M + i) + 1);
+              if (kWin) depth = __ldcg(depth_ws + (int64_t)cu.b * M + i);
             }
             anc_b = cu.b;
             if (cu.next_b < B) {
               anc_n = __ldcg(aw + 2 * ((int64_t)cu.next_b * M + i));
               if (kWide) anc_hi_n = __ldcg(aw + 2 * ((int64_t)cu.next_b * M + i) + 1);
+              if (kWin) depth_n = __ldcg(depth_ws + (int64_t)cu.next_b * M + i);
               anc_nb = cu.next_b;
             }
           }
@@ -654,10 +696,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
                                                      (uint32_t)((t / kSBufs) & 1), abort, wait)))
           break;
         ptx::tc_fence_after();
-        const int kpos0 = cu.tile * kTileKeys;
-        const int nkeys = tile_pages(L, cu.tile) * kBlock;
-        // tiles wholly inside the cached prefix need no mask
-        const bool plain = kpos0 + kTileKeys <= ctx && nkeys == kTileKeys;
+        const int rt = cu.real();
+        const int kpos0 = rt * kTileKeys;
+        const int nkeys = tile_pages(L, rt) * kBlock;
+        // tiles wholly inside the cached prefix need no mask; with a window,
+        // those inside every row's window (a row's depth is at most M - 1) or
+        // inside the sinks
+        const bool plain = kpos0 + kTileKeys <= ctx && nkeys == kTileKeys &&
+                           (!kWin || kpos0 >= L - window || kpos0 + kTileKeys <= sinks);
         const int jbase = half * 32;
         uint32_t vh = 0xffffffffu;  // visible keys of this half (non-plain tiles)
         uint32_t sv[32], so[32];
@@ -690,8 +736,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
           // visibility of the tile's keys as a bitmask, then the same maximum
           // as the plain path over the visible ones
           const unsigned long long vis =
-              kWide ? tile_visibility_wide(kpos0, nkeys, ctx, L, anc, anc_hi, real)
-                    : tile_visibility(kpos0, nkeys, ctx, L, anc, real);
+              kWin    ? tile_visibility_win(kpos0, nkeys, ctx, L, sinks, ctx + depth + 1 - window,
+                                            anc, anc_hi, real)
+              : kWide ? tile_visibility_wide(kpos0, nkeys, ctx, L, anc, anc_hi, real)
+                      : tile_visibility(kpos0, nkeys, ctx, L, anc, real);
           vh = (uint32_t)(vis >> jbase);
           const uint32_t vo = (uint32_t)(vis >> (jbase ^ 32));
           float a0 = -INFINITY, a1 = -INFINITY;
@@ -959,10 +1007,14 @@ __device__ __forceinline__ void block_scan(int64_t& a, int64_t& c, int& m, int64
 // page it reads or writes, the tree topology) and records it for the plan.
 // A request that fails gets out = 0, lse = -inf and no tiles (the attention
 // kernel then neither reads nor appends it).  The CTA that arrives last
-// plans the split of the tiles.
+// plans the split of the tiles.  With a window (kWin) only the pages of the
+// sinks and of the window are checked, only their tiles are counted, and
+// every new row gets its depth and the mask of the ancestors it sees.
+template <bool kWin>
 __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     const int32_t* block_table, const int32_t* ctx_lens,
-    const int32_t* __restrict__ parent, spec_dims d, int G, int32_t* __restrict__ ntiles,
+    const int32_t* __restrict__ parent, spec_dims d, int window, int sinks, int G,
+    int32_t* __restrict__ depth_ws, int32_t* __restrict__ ntiles,
     int64_t* __restrict__ pre, int4* __restrict__ rq, int4* __restrict__ starts,
     int* __restrict__ pairs, ulonglong2* __restrict__ anc_ws,
     uint32_t* __restrict__ arrivals, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
@@ -988,7 +1040,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
 #pragma unroll
   for (int k = 0; k < kPrepPages; ++k) {
     const int p = tid + k * kPrepThreads;
-    ids[k] = p < d.max_blocks ? __ldcg(bt + p) : 0;
+    ids[k] = !kWin && p < d.max_blocks ? __ldcg(bt + p) : 0;
   }
   const int ctx = __ldcg(ctx_lens + b);
   const int64_t L = (int64_t)ctx + M;
@@ -998,11 +1050,21 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
   int bad_block = 0;
   if (cap_ok) {
     const int pages = (int)ceil_div64(L, kBlock);
+    if (kWin) {
+      const int sp = min(ceil_div(sinks, kBlock), pages);
+      const int lo = max(sp, win_first(ctx, window) / kBlock);
+      const int n = sp + pages - lo;  // pages of the sinks, then of the window
+#pragma unroll 4
+      for (int j = tid; j < n; j += kPrepThreads) {
+        const int id = __ldcg(bt + (j < sp ? j : j - sp + lo));
+        bad_block |= (id < 0 || id >= d.num_blocks);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kPrepPages; ++k)
-      if (tid + k * kPrepThreads < pages) bad_block |= (ids[k] < 0 || ids[k] >= d.num_blocks);
+      if (!kWin && tid + k * kPrepThreads < pages) bad_block |= (ids[k] < 0 || ids[k] >= d.num_blocks);
 #pragma unroll 4
-    for (int p = tid + kPrepPages * kPrepThreads; p < pages; p += kPrepThreads) {
+    for (int p = tid + kPrepPages * kPrepThreads; !kWin && p < pages; p += kPrepThreads) {
       const int id = __ldcg(bt + p);
       bad_block |= (id < 0 || id >= d.num_blocks);
     }
@@ -1020,7 +1082,26 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
   const bool ok = cap_ok && !bad_block && !bad_topo;
   // tile counts of the request's (request, head) pairs start at zero
   for (int h = tid; h < Hkv; h += blockDim.x) pairs[(int64_t)b * Hkv + h] = 0;
-  if (ok && parent != nullptr) {
+  if (kWin && ok) {
+    // depth of each new row, and the mask of the ancestors-or-self that are
+    // fewer than `window` positions above it or among the sinks
+    const int32_t* par = parent != nullptr ? parent + (int64_t)b * M : nullptr;
+    for (int n = tid; n < M; n += blockDim.x) {
+      int depth = n;
+      if (par != nullptr) {
+        depth = 0;
+        for (int k = n; k > 0; k = par[k]) ++depth;
+      }
+      unsigned long long lo = 0, hi = 0;
+      for (int k = n, dk = depth; k >= 0; k = par != nullptr ? par[k] : k - 1, --dk) {
+        if (depth - dk >= window && ctx + dk >= sinks) continue;
+        if (k < 64) lo |= 1ull << k;
+        else hi |= 1ull << (k - 64);
+      }
+      anc_ws[(int64_t)b * M + n] = make_ulonglong2(lo, hi);
+      depth_ws[(int64_t)b * M + n] = depth;
+    }
+  } else if (ok && parent != nullptr) {
     // ancestor-or-self mask of each tree row (the topology is valid here,
     // so every walk ends at the root within M steps)
     const int32_t* par = parent + (int64_t)b * M;
@@ -1037,7 +1118,9 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     if (!cap_ok) raise_status(status, SPEC_ERR_CAPACITY);
     if (bad_block) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
     if (bad_topo) raise_status(status, SPEC_ERR_INVALID_ARG);
-    ntiles[b] = ok ? (int)ceil_div64(L, kTileKeys) : 0;
+    ntiles[b] = ok ? (int)ceil_div64(L, kTileKeys) -
+                         (kWin ? win_skip(ctx, window, sinks, kTileKeys) : 0)
+                   : 0;
     __threadfence();
     s_last = atomicAdd(arrivals, 1u) == (uint32_t)(B - 1);
   }
@@ -1080,7 +1163,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     if (r < B) {
       tpre[r] = carry_t + vt;
       cpre[r] = carry_c + vc;
-      rq[r] = make_int4(cx, nt, B, 0);
+      rq[r] = make_int4(cx, nt, B, kWin ? win_skip(cx, window, sinks, kTileKeys) : 0);
       if (small) {
         s_nt[r] = nt;
         s_ctx[r] = cx;
@@ -1189,6 +1272,7 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
   int4* starts = reinterpret_cast<int4*>(ws + lay.tc_start_off);
   int* pairs = reinterpret_cast<int*>(ws + lay.tc_pair_off);
   ulonglong2* anc = reinterpret_cast<ulonglong2*>(ws + lay.tc_anc_off);
+  int32_t* depth = reinterpret_cast<int32_t*>(ws + lay.win_depth_off);
   uint32_t* arrivals = reinterpret_cast<uint32_t*>(ws + lay.tc_sync_off);
   float* part = reinterpret_cast<float*>(ws + lay.attn_off);
   uint32_t* status = reinterpret_cast<uint32_t*>(ws + lay.status_off);
@@ -1210,15 +1294,19 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
 
   {
     PdlLaunch L(dim3(d.B), dim3(kPrepThreads), 0, st);
-    e = cudaLaunchKernelEx(&L.cfg, attn_prep_kernel, a.block_table, a.ctx_lens,
-                           a.parent, d, G, ntiles, pre, rq, starts, pairs, anc, arrivals,
+    e = cudaLaunchKernelEx(&L.cfg, a.window > 0 ? attn_prep_kernel<true> : attn_prep_kernel<false>,
+                           a.block_table, a.ctx_lens, a.parent, d, a.window, a.sinks, G, depth, ntiles, pre, rq, starts, pairs, anc, arrivals,
                            static_cast<__nv_bfloat16*>(a.out), a.lse, status);
     if (e != cudaSuccess) return e;
   }
   ++*launches;
   const bool wide = d.M > 64, short_wait = wait_limit_cycles(d) < ptx::kShortWait;
-  auto kern = wide ? (short_wait ? attn_tc_kernel<true, true> : attn_tc_kernel<true, false>)
-                   : (short_wait ? attn_tc_kernel<false, true> : attn_tc_kernel<false, false>);
+  auto kern = wide ? (short_wait ? attn_tc_kernel<true, true, false> : attn_tc_kernel<true, false, false>)
+                   : (short_wait ? attn_tc_kernel<false, true, false>
+                                 : attn_tc_kernel<false, false, false>);
+  if (a.window > 0)
+    kern = wide ? (short_wait ? attn_tc_kernel<true, true, true> : attn_tc_kernel<true, false, true>)
+                : (short_wait ? attn_tc_kernel<false, true, true> : attn_tc_kernel<false, false, true>);
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   const float qscale2 = a.scale * 1.4426950408889634f;
@@ -1230,8 +1318,8 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
                            static_cast<__nv_bfloat16*>(a.k_cache),
                            static_cast<__nv_bfloat16*>(a.v_cache), a.block_table,
                            (const int4*)rq, (const int4*)starts,
-                           a.parent != nullptr ? (const ulonglong2*)anc : nullptr, pairs, d,
-                           qscale2, part, static_cast<__nv_bfloat16*>(a.out), a.lse, status);
+                           a.parent != nullptr || a.window > 0 ? (const ulonglong2*)anc : nullptr,
+                           (const int*)depth, a.window, a.sinks, pairs, d, qscale2, part, static_cast<__nv_bfloat16*>(a.out), a.lse, status);
     if (e != cudaSuccess) return e;
   }
   ++*launches;

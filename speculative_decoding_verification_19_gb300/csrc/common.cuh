@@ -147,6 +147,8 @@ struct WsLayout {
   size_t tc_pair_off;     // [B*Hkv] int32 per (request, KV head): tiles run by the later CTAs
   size_t tc_anc_off;      // [B*M] 128-bit ancestor-or-self mask of every tree row (2 u64)
   size_t tc_sync_off;     // uint32 arrival count of the request-check kernel
+  size_t win_depth_off;   // [B*M] int32 depth of every new row (windowed attention)
+  size_t pg_sync_off;     // uint32 arrival count of the block-table kernel
   size_t attn_off;        // split-KV partials of either attention path (f32)
   size_t attn_bytes;
   int split_keys;         // keys per split (multiple of 16)
