@@ -25,20 +25,27 @@
 // compare are 42-bit fixed-point integers: their sums do not depend on the
 // order of the atomics that form them.
 //
-// One cluster of up to 16 CTAs per row, each with a slice of the row in shared
-// memory: the row is read from HBM once, whatever the filters ask for, and
-// what the CTAs tell one another (maxima, histograms, masses) goes through
-// distributed shared memory.  Rows whose slices do not fit are read again
-// through L2 instead.  Steps:
-//   1  slice to shared memory, maximum, rows without a distribution
-//   2  with top-k or top-p: a radix select over the order keys, 8 bits a
-//      level, on counts or on masses.  Only tokens that can matter take part:
-//      for top-k those at or above a lower bound of the k-th value taken from
-//      the threads' maxima (n threads' maxima >= v make n tokens >= v), for
-//      top-p those above every thread's maximum's minimum, if they hold the
-//      mass that is asked for (checked; else all)
-//   3  the kept mass of every warp's run of tokens, exchanged; the warp that
-//      holds u Z walks its run in order
+// Two kernels read the logits.  Without filters sample_plain_kernel streams a
+// row through registers once (its comment has the arithmetic).  With any
+// filter sample_kernel takes a row with one cluster of up to 8 CTAs, each with
+// a slice of the row in shared memory: the row is read from HBM once, whatever
+// the filters ask for, and what the CTAs tell one another (maxima, candidates,
+// histograms, masses) goes through distributed shared memory.  Slices that do
+// not fit are read again through L2.  Its steps:
+//   1   slice to shared memory, maximum, rows without a distribution
+//   2a  with top-k or top-p: the tokens at or above a bound go to the first
+//       CTA, which finishes the row alone.  The bound comes from the threads'
+//       maxima: if n of them reach v, at least n tokens do; for top-k that
+//       makes it safe, for top-p the candidates' mass is checked
+//   2   else (a large k, a top-p that reaches far down) a radix select over
+//       the slices' order keys, on counts or on masses, gives the threshold
+//   3   the kept mass of every warp's run of tokens, exchanged; the warp that
+//       holds u Z walks its run in order
+// Measured (queued calls, us): 640 rows of 152064 bf16 logits, temperature
+// alone, 75 (195 MB: 29 at the copy rate; the stream 54, the marked rows 21);
+// 33 rows of 32001 fp32 logits with mixed filters 33 (57 before step 2a); one
+// row of 32000: 9 without filters, 16 with top-k 50, 20 with top-p 0.9.  A
+// filtered row is bound by its chain of barriers, not by bytes.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -53,10 +60,11 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 256;
+constexpr int kBinBits = 9;
+constexpr int kBins = 1 << kBinBits;  // one per thread
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // order key of -inf
 constexpr int kUnroll = 4;
-constexpr size_t kMaxSliceBytes = 200 * 1024;
+constexpr size_t kMaxSliceBytes = 160 * 1024;
 
 // 2^(j/32) as hi + lo
 __device__ const float2 kPow2[32] = {
@@ -77,23 +85,32 @@ __device__ const float2 kPow2[32] = {
     {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f},
     {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.f50766p+0f, -0x1.246ebp-26f}};
 
-struct Shared {
+// What the exact draw exchanges.
+struct DrawShared {
   float2 pow2[32];
-  uint32_t hist[2][4][kBins];  // counts, then the masses' three 14-bit limbs
   float2 mass[kMaxCluster * kWarps];
   int ties[kMaxCluster * kWarps];
+  int pick, pick_ties;
+  float2 pick_base, pick_z;
+};
+
+struct Shared {
+  DrawShared draw;
+  uint32_t hist[2][4][kBins];  // counts, then the masses' three 14-bit limbs
   float ex_max[kMaxCluster];
-  uint32_t ex_bad[kMaxCluster], ex_theta[kMaxCluster];
+  uint32_t ex_bad[kMaxCluster], ex_theta[kMaxCluster], ex_low[kMaxCluster];
   float2 ex_z[kMaxCluster];
+  long long ex_mass[kMaxCluster];
+  int ex_n[kMaxCluster];
   int ex_first[kMaxCluster];
+  int n_list;
   float red[kWarps];
-  uint32_t scan_cnt[kBins / kWarp];
-  long long scan_mass[kBins / kWarp];
+  uint32_t red_low[kWarps];
+  uint32_t scan_cnt[kWarps];
+  long long scan_mass[kWarps];
   int sel_bin;
   uint32_t sel_above, sel_count;
   long long sel_mass;
-  int pick, pick_ties;
-  float2 pick_base, pick_z;
 };
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -119,6 +136,11 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 struct Law {
   float m, c_hi, c_lo;  // maximum; log2(e) / T as a double-float
   const float2* pow2;
+  // log2(e) / T: log2(e) as a double-float, the quotient's remainder exact
+  __device__ __forceinline__ Law(float max, float T, const float2* table)
+      : m(max), c_hi(1.44269502f / T), pow2(table) {
+    c_lo = (fmaf(-c_hi, T, 1.44269502f) + 1.92596303e-8f) / T;
+  }
   // exp((x - m) / T) as a double-float; 0 below 2^-120
   __device__ __forceinline__ dfloat weight(float x) const {
     const dfloat d = df_two_sum(x, -m);
@@ -203,21 +225,29 @@ struct Selected {
   long long mass;  // of the tokens above tau (when masses were summed)
 };
 
-// Radix select over the tokens with order key >= low: the value of rank
-// `rank` (1 = largest), or, with by_mass, the first at which the running mass
-// reaches `mass`.  Not found when all of them together fall short.
+// Radix select over the tokens with order key >= low (the largest key being
+// `high`): the value of rank `rank` (1 = largest), or, with by_mass, the first
+// at which the running mass reaches `mass`.  Not found when all of them
+// together fall short.  A level cuts the range of keys that is left into 512
+// bins; keys are counted from `low`, so that the bins fill evenly and a range
+// of a few octaves takes one level for bf16 and three for fp32 (digits of the
+// key itself put every candidate into two or three bins: their atomics then
+// run one after another).
 template <typename T, bool kSmem>
 __device__ Selected radix_select(Shared& sh, const Slice<T, kSmem>& sl, int nv, const Law& law,
-                                 uint32_t low, bool by_mass, bool with_mass, long long rank,
-                                 long long mass, int C, int& buf) {
+                                 uint32_t low, uint32_t high, bool by_mass, bool with_mass,
+                                 long long rank, long long mass, int C, int& buf) {
   constexpr int kVec = Slice<T, kSmem>::kVec;
+  constexpr int kShift = sizeof(T) == 2 ? 16 : 0;  // bits that a key of this type does not use
   const int tid = threadIdx.x, lane = tid % kWarp;
   cg::cluster_group cluster = cg::this_cluster();
   Selected r{true, 0, 0, 0, 0};
-  uint32_t prefix = 0, mask = 0;
-  constexpr int kLast = sizeof(T) == 2 ? 16 : 0;
   if (low <= kKeyNegInf) low = kKeyNegInf + 1;
-  for (int shift = 24; shift >= kLast; shift -= 8) {
+  uint32_t base = low >> kShift;
+  int bits = 32 - __clz((high >> kShift) - base);  // keys base .. base + 2^bits - 1
+  do {
+    const int sh_bits = max(0, bits - kBinBits);
+    const uint32_t span = bits < 32 ? (1u << bits) - 1 : ~0u;
     // the other CTAs read this buffer two levels ago, before they arrived at
     // the last level's barrier
     for (int i = tid; i < 4 * kBins; i += kThreads) (&sh.hist[buf][0][0])[i] = 0;
@@ -230,8 +260,9 @@ __device__ Selected radix_select(Shared& sh, const Slice<T, kSmem>& sl, int nv, 
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         const uint32_t key = order_key(x[i]);
-        if (key >= low && (key & mask) == prefix) {
-          const int bin = (key >> shift) & (kBins - 1);
+        const uint32_t at = (key >> kShift) - base;
+        if (key >= low && at <= span) {
+          const uint32_t bin = at >> sh_bits;
           atomicAdd(&sh.hist[buf][0][bin], 1u);
           if (with_mass) {
             uint32_t l[3];
@@ -244,251 +275,75 @@ __device__ Selected radix_select(Shared& sh, const Slice<T, kSmem>& sl, int nv, 
       }
     }
     cluster_sync();
-    // thread i: bin 255 - i, summed over the cluster, then the running sums
-    uint32_t cnt = 0, ci = 0;
-    long long ms = 0, mi = 0;
-    if (tid < kBins) {
-      const int bin = kBins - 1 - tid;
-      for (int q = 0; q < C; ++q) {
-        const uint32_t* h = cluster.map_shared_rank(&sh.hist[buf][0][0], q);
-        cnt += h[bin];
-        if (with_mass)
-          ms += limbs_value(h[kBins + bin], h[2 * kBins + bin], h[3 * kBins + bin]);
-      }
-      ci = cnt;
-      mi = ms;
+    // thread i: bin 511 - i, summed over the cluster, then the running sums
+    const int bin = kBins - 1 - tid;
+    uint32_t cnt = 0;
+    long long ms = 0;
+    for (int q = 0; q < C; ++q) {
+      const uint32_t* h = cluster.map_shared_rank(&sh.hist[buf][0][0], q);
+      cnt += h[bin];
+      if (with_mass) ms += limbs_value(h[kBins + bin], h[2 * kBins + bin], h[3 * kBins + bin]);
+    }
+    uint32_t ci = cnt;
+    long long mi = ms;
 #pragma unroll
-      for (int o = 1; o < kWarp; o <<= 1) {
-        const uint32_t yc = __shfl_up_sync(0xffffffffu, ci, o);
-        const long long ym = __shfl_up_sync(0xffffffffu, mi, o);
-        if (lane >= o) {
-          ci += yc;
-          mi += ym;
-        }
-      }
-      if (lane == kWarp - 1) {
-        sh.scan_cnt[tid / kWarp] = ci;
-        sh.scan_mass[tid / kWarp] = mi;
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const uint32_t yc = __shfl_up_sync(0xffffffffu, ci, o);
+      const long long ym = __shfl_up_sync(0xffffffffu, mi, o);
+      if (lane >= o) {
+        ci += yc;
+        mi += ym;
       }
     }
+    if (lane == kWarp - 1) {
+      sh.scan_cnt[tid / kWarp] = ci;
+      sh.scan_mass[tid / kWarp] = mi;
+    }
     __syncthreads();
-    if (tid < kBins) {
-      for (int w = 0; w < tid / kWarp; ++w) {
-        ci += sh.scan_cnt[w];
-        mi += sh.scan_mass[w];
-      }
-      const long long before = by_mass ? r.mass + mi - ms : (long long)r.above + ci - cnt;
-      const long long upto = by_mass ? r.mass + mi : (long long)r.above + ci;
-      const long long want = by_mass ? mass : rank;
-      if (before < want && want <= upto) {
-        sh.sel_bin = kBins - 1 - tid;
-        sh.sel_above = ci - cnt;
-        sh.sel_mass = mi - ms;
-        sh.sel_count = cnt;
-      }
+    for (int w = 0; w < tid / kWarp; ++w) {
+      ci += sh.scan_cnt[w];
+      mi += sh.scan_mass[w];
+    }
+    const long long before = by_mass ? r.mass + mi - ms : (long long)r.above + ci - cnt;
+    const long long upto = by_mass ? r.mass + mi : (long long)r.above + ci;
+    const long long want = by_mass ? mass : rank;
+    if (before < want && want <= upto) {
+      sh.sel_bin = bin;
+      sh.sel_above = ci - cnt;
+      sh.sel_mass = mi - ms;
+      sh.sel_count = cnt;
     }
     __syncthreads();
     buf ^= 1;
-    const int bin = sh.sel_bin;
-    if (bin < 0) {
+    if (sh.sel_bin < 0) {
       r.found = false;
       return r;
     }
     r.above += sh.sel_above;
     r.mass += sh.sel_mass;
     r.ties = sh.sel_count;
-    prefix |= (uint32_t)bin << shift;
-    mask |= (uint32_t)(kBins - 1) << shift;
+    base += (uint32_t)sh.sel_bin << sh_bits;
+    bits = sh_bits;
     __syncthreads();  // sel_* are read
-  }
+  } while (bits > 0);
   // the bits below a bf16 key: zeros, or ones for a negative value
-  r.tau = sizeof(T) == 2 && !(prefix & 0x80000000u) ? prefix | 0xffffu : prefix;
+  const uint32_t key = base << kShift;
+  r.tau = sizeof(T) == 2 && !(key & 0x80000000u) ? key | 0xffffu : key;
   return r;
 }
 
-template <typename T, bool kSmem>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int C, int slice,
-                                                          int warp_vecs) {
-  constexpr int kVec = 16 / sizeof(T);
-  __shared__ Shared sh;
-  extern __shared__ uint4 data[];
+// The draw, exactly: the kept mass of every warp's run of tokens (warp_vecs
+// vectors of the CTA's slice, which begins at token `first`), exchanged over
+// the cluster; the warp whose run holds u Z walks it in vocabulary order.
+// Kept are the tokens above tau, the first keep_ties of those equal to it
+// (everything for tau = kKeyNegInf), and of these the ones of weight >= mp.
+template <int kW, typename T, bool kSmem>
+__device__ void exact_draw(DrawShared& sh, const Slice<T, kSmem>& sl, const Law& law, uint32_t tau,
+                           int keep_ties, float mp, float u, int warp_vecs, int C, int rank,
+                           int first, const SampleArgs& a, int64_t row) {
+  constexpr int kVec = Slice<T, kSmem>::kVec;
   const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = blockIdx.x % C;
-  const int64_t row = blockIdx.x / C;
-  pdl_trigger();
-  cluster_arrive();  // every CTA of the cluster runs before its shared memory is written
-  if (tid < 32) sh.pow2[tid] = kPow2[tid];
-  pdl_wait();  // the logits may come from the previous kernel
-
-  const float T_ = a.temperature[row], u = a.uniform[row];
-  const int k = a.top_k != nullptr ? a.top_k[row] : 0;
-  const float tp = a.top_p != nullptr ? a.top_p[row] : 1.f;
-  const float mp = a.min_p != nullptr ? a.min_p[row] : 0.f;
-  const bool valid = temperature_valid(T_) && u >= 0.f && u < 1.f && k >= 0 && tp > 0.f &&
-                     tp <= 1.f && mp >= 0.f && mp <= 1.f;
-  const bool greedy = T_ == 0.f;
-  const bool has_k = !greedy && k > 0 && k < a.V, has_p = !greedy && tp < 1.f;
-
-  Slice<T, kSmem> sl;
-  sl.src = static_cast<const T*>(a.logits) + row * a.stride + (int64_t)rank * slice;
-  sl.off = (int)((reinterpret_cast<uintptr_t>(sl.src) & 15u) / sizeof(T));
-  sl.n = max(0, min(slice, a.V - rank * slice));
-  sl.sm = data;
-  const int nv = kWarps * warp_vecs;
-
-  // ---- 1: the slice, its maximum, elements that make the row fail
-  float tmax = -INFINITY;
-  int bad = 0;
-  for (int v0 = tid; v0 < nv; v0 += kUnroll * kThreads) {
-    uint4 raw[kUnroll];
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
-      if (v0 + j * kThreads < nv) raw[j] = sl.load(v0 + j * kThreads);
-#pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      if (v0 + j * kThreads >= nv) break;
-      if (kSmem) data[v0 + j * kThreads] = raw[j];
-      float x[kVec];
-      unpack16(raw[j], x);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        bad |= !(x[i] < INFINITY);  // NaN or +inf
-        tmax = fmaxf(tmax, x[i]);
-      }
-    }
-  }
-  const float wm = warp_max(tmax);
-  if (lane == 0) sh.red[warp] = wm;
-  bad = __syncthreads_or(bad);
-  float m = sh.red[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.red[w]);
-  // lower bound of the tokens that can matter: the largest 16-bit key that at
-  // least `need` of the threads' maxima reach
-  uint32_t theta = 0;
-  if (valid && (has_k || has_p)) {
-    const int need = has_k ? ceil_div(k, C) : kThreads;
-    if (need <= kThreads) {
-      const uint32_t key = order_key(tmax) >> 16;
-      for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1)
-        if (__syncthreads_count(key >= (theta | bit)) >= need) theta |= bit;
-    }
-  }
-  cluster_wait();
-  if (tid < C) {
-    *cluster.map_shared_rank(&sh.ex_max[rank], tid) = m;
-    *cluster.map_shared_rank(&sh.ex_bad[rank], tid) = (uint32_t)bad;
-    *cluster.map_shared_rank(&sh.ex_theta[rank], tid) = theta << 16;
-  }
-  cluster_sync();
-  for (int q = 0; q < C; ++q) {
-    m = fmaxf(m, sh.ex_max[q]);
-    bad |= (int)sh.ex_bad[q];
-    theta = q == 0 ? sh.ex_theta[0] : min(theta, sh.ex_theta[q]);
-  }
-  if (!valid || bad || m == -INFINITY) {
-    if (rank == 0 && tid == 0) {
-      raise_status(a.status, valid ? SPEC_ERR_NONFINITE : SPEC_ERR_INVALID_ARG);
-      a.out_tokens[row] = -1;
-      if (a.out_prob != nullptr) a.out_prob[row] = 0.f;
-    }
-    return;
-  }
-  if (greedy) {
-    int first = 0x7fffffff;
-    for (int v = tid; v < nv; v += kThreads) {
-      const uint4 raw = sl.get(v);
-      float x[kVec];
-      unpack16(raw, x);
-#pragma unroll
-      for (int i = kVec - 1; i >= 0; --i)
-        if (x[i] == m) first = min(first, rank * slice + v * kVec - sl.off + i);
-    }
-    first = __reduce_min_sync(0xffffffffu, first);
-    if (lane == 0) sh.ties[warp] = first;
-    __syncthreads();
-    if (tid == 0) {
-      for (int w = 0; w < kWarps; ++w) first = min(first, sh.ties[w]);
-      *cluster.map_shared_rank(&sh.ex_first[rank], 0) = first;
-    }
-    cluster_sync();
-    if (rank == 0 && tid == 0) {
-      for (int q = 0; q < C; ++q) first = min(first, sh.ex_first[q]);
-      a.out_tokens[row] = first;
-      if (a.out_prob != nullptr) a.out_prob[row] = 1.f;
-    }
-    return;
-  }
-
-  Law law;
-  law.m = m;
-  law.pow2 = sh.pow2;
-  // log2(e) / T: log2(e) as a double-float, the quotient's remainder exact
-  law.c_hi = 1.44269502f / T_;
-  law.c_lo = (fmaf(-law.c_hi, T_, 1.44269502f) + 1.92596303e-8f) / T_;
-
-  // ---- 2: the filters' threshold tau and how many tokens equal to it are kept
-  uint32_t tau = kKeyNegInf;
-  int keep_ties = 0;
-  int buf = 0;
-  if (has_k) {
-    Selected s = radix_select<T, kSmem>(sh, sl, nv, law, theta, false, has_p, k, 0, C, buf);
-    if (s.found) {
-      tau = s.tau;
-      keep_ties = k - (int)s.above;
-      if (has_p) {
-        const long long each = fixed_value(law.weight(key_value(tau)));
-        const long long want = mass_target(tp, s.mass + each * keep_ties);
-        if (s.mass >= want) {
-          const Selected p =
-              radix_select<T, kSmem>(sh, sl, nv, law, tau + 1, true, true, 0, want, C, buf);
-          tau = p.tau;
-          keep_ties = ties_for(want - p.mass, fixed_value(law.weight(key_value(tau))), (int)p.ties);
-        } else {
-          keep_ties = ties_for(want - s.mass, each, keep_ties);
-        }
-      }
-    }
-  }
-  if (has_p && tau == kKeyNegInf) {  // no top-k, or fewer tokens than k
-    dfloat z = df_make(0.f);
-    for (int v = tid; v < nv; v += kThreads) {
-      const uint4 raw = sl.get(v);
-      float x[kVec];
-      unpack16(raw, x);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const dfloat w = law.weight(x[i]);
-        const dfloat s = df_two_sum(z.hi, w.hi);
-        z.hi = s.hi;
-        z.lo += s.lo + w.lo;
-      }
-    }
-    z = df_warp_sum(df_norm(z.hi, z.lo));
-    if (lane == 0) sh.mass[warp] = make_float2(z.hi, z.lo);
-    __syncthreads();
-    if (tid < C) {
-      z = df_make(0.f);
-      for (int w = 0; w < kWarps; ++w) z = df_add(z, dfloat{sh.mass[w].x, sh.mass[w].y});
-      *cluster.map_shared_rank(&sh.ex_z[rank], tid) = make_float2(z.hi, z.lo);
-    }
-    cluster_sync();
-    z = df_make(0.f);
-    for (int q = 0; q < C; ++q) z = df_add(z, dfloat{sh.ex_z[q].x, sh.ex_z[q].y});
-    const long long zi = __float2ll_rn(z.hi * 0x1p42f) + __float2ll_rn(z.lo * 0x1p42f);
-    const long long want = mass_target(tp, zi);
-    Selected p = radix_select<T, kSmem>(sh, sl, nv, law, has_k ? 0u : theta, true, true, 0, want,
-                                        C, buf);
-    if (!p.found && !has_k)
-      p = radix_select<T, kSmem>(sh, sl, nv, law, 0u, true, true, 0, want, C, buf);
-    if (p.found) {
-      tau = p.tau;
-      keep_ties = ties_for(want - p.mass, fixed_value(law.weight(key_value(tau))), (int)p.ties);
-    }
-  }
-
-  // ---- 3: kept masses of the warps' runs, in vocabulary order
   const bool filtered = tau != kKeyNegInf || mp > 0.f;
   dfloat w_tau = df_make(0.f);
   if (tau != kKeyNegInf) {
@@ -497,7 +352,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int C, i
   }
   const int v_lo = warp * warp_vecs, v_hi = v_lo + warp_vecs;
   {
-    dfloat z = df_make(0.f);
+    // four sums, so that one's chain of additions does not wait for another's
+    dfloat acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = df_make(0.f);
     int ties = 0;
     for (int v = v_lo + lane; v < v_hi; v += kWarp) {
       const uint4 raw = sl.get(v);
@@ -512,22 +370,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int C, i
         }
         dfloat w = law.weight(x[i]);
         if ((w.hi - mp) + w.lo < 0.f) w = df_make(0.f);
-        const dfloat s = df_two_sum(z.hi, w.hi);
-        z.hi = s.hi;
-        z.lo += s.lo + w.lo;
+        const dfloat s = df_two_sum(acc[i & 3].hi, w.hi);
+        acc[i & 3].hi = s.hi;
+        acc[i & 3].lo += s.lo + w.lo;
       }
     }
-    z = df_warp_sum(df_norm(z.hi, z.lo));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = df_norm(acc[i].hi, acc[i].lo);
+    const dfloat z = df_warp_sum(df_add(df_add(acc[0], acc[1]), df_add(acc[2], acc[3])));
     ties = (int)__reduce_add_sync(0xffffffffu, (unsigned)ties);
     if (lane < C) {
-      *cluster.map_shared_rank(&sh.mass[rank * kWarps + warp], lane) = make_float2(z.hi, z.lo);
-      *cluster.map_shared_rank(&sh.ties[rank * kWarps + warp], lane) = ties;
+      *cluster.map_shared_rank(&sh.mass[rank * kW + warp], lane) = make_float2(z.hi, z.lo);
+      *cluster.map_shared_rank(&sh.ties[rank * kW + warp], lane) = ties;
     }
   }
   cluster_sync();  // from here on each CTA touches only its own shared memory
   if (warp == 0) {
-    const int per = kMaxCluster * kWarps / kWarp;  // runs of a lane
-    const int runs = C * kWarps;
+    const int per = kMaxCluster * kW / kWarp;  // runs of a lane
+    const int runs = C * kW;
     int t[per], ts = 0;
 #pragma unroll
     for (int i = 0; i < per; ++i) {
@@ -582,7 +442,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int C, i
   }
   __syncthreads();
   const int pick = sh.pick;
-  if (pick / kWarps != rank || pick % kWarps != warp) return;
+  if (pick / kW != rank || pick % kW != warp) return;
   const dfloat Z{sh.pick_z.x, sh.pick_z.y};
   const dfloat thr = df_mul_f(Z, u);
   dfloat cum{sh.pick_base.x, sh.pick_base.y};
@@ -604,10 +464,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int C, i
       for (int i = 0; i < kVec; ++i) nt += order_key(x[i]) == tau;
     }
     int it = nt;
+    if (tau != kKeyNegInf) {
 #pragma unroll
-    for (int o = 1; o < kWarp; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, it, o);
-      if (lane >= o) it += y;
+      for (int o = 1; o < kWarp; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, it, o);
+        if (lane >= o) it += y;
+      }
     }
     int tr = tie_base + it - nt;
     dfloat w[kVec], sum = df_make(0.f);
@@ -643,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int C, i
             wt = w[i].hi;
           }
         }
-        a.out_tokens[row] = rank * slice + at - sl.off;
+        a.out_tokens[row] = first + at - sl.off;
         if (a.out_prob != nullptr) a.out_prob[row] = wt / df_to_f(Z);
       }
       return;
@@ -653,16 +515,1032 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int C, i
   // u Z at the run's very end, within the sums' rounding: its last kept token
   const int top = __reduce_max_sync(0xffffffffu, last);
   if (last == top && top >= 0) {
-    a.out_tokens[row] = rank * slice + top - sl.off;
+    a.out_tokens[row] = first + top - sl.off;
     if (a.out_prob != nullptr) a.out_prob[row] = last_w / df_to_f(Z);
   }
 }
 
+// Sum and maximum of one number a thread over the CTA.
+__device__ __forceinline__ long long block_sum(Shared& sh, long long v) {
+#pragma unroll
+  for (int o = kWarp / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (threadIdx.x % kWarp == 0) sh.scan_mass[threadIdx.x / kWarp] = v;
+  __syncthreads();
+  v = 0;
+  for (int w = 0; w < kWarps; ++w) v += sh.scan_mass[w];
+  __syncthreads();
+  return v;
+}
+__device__ __forceinline__ long long block_max(Shared& sh, long long v) {
+#pragma unroll
+  for (int o = kWarp / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if (threadIdx.x % kWarp == 0) sh.scan_mass[threadIdx.x / kWarp] = v;
+  __syncthreads();
+  v = sh.scan_mass[0];
+  for (int w = 1; w < kWarps; ++w) v = max(v, sh.scan_mass[w]);
+  __syncthreads();
+  return v;
+}
+
+// ---------------------------------------------------------------------------
+// the candidates of a filtered row in one CTA
+// ---------------------------------------------------------------------------
+// When few tokens can matter they are sent to the cluster's first CTA (at
+// most kListCap from each), and the filters and the draw run there on
+// registers: a level of the select is then a few block barriers, where one
+// over the cluster's slices costs a cluster barrier and 32 remote loads a
+// thread.  Masses are 40-bit fractions in two limbs of 20 bits (the limbs of
+// 4096 weights add up in 32 bits).
+constexpr int kListCap = 512;
+// Of a CTA's 512 threads' maxima, how many reach the lower bound of the
+// candidates: 256 leave about 355 candidates (512 ln 2, the more tokens a
+// thread has), 300 about 450 of the 512 that fit.
+constexpr int kListNeedK = 256, kListNeedP = 300;
+
+struct Picked {
+  bool found;
+  uint32_t key;  // the key at the place asked for
+  uint32_t above, ties;
+  long long mass;  // of the keys above it
+};
+
+__device__ __forceinline__ void fixed_pair(dfloat w, uint32_t& hi, uint32_t& lo) {
+  float a = floorf(w.hi * 0x1p20f);
+  if (fmaf(a, -0x1p-20f, w.hi) + w.lo < 0.f) a -= 1.f;
+  const float r = fmaf(a, -0x1p-20f, w.hi) + w.lo;
+  hi = (uint32_t)a;
+  lo = (uint32_t)__float2int_rn(r * 0x1p40f);
+}
+__device__ __forceinline__ long long pair_value(uint32_t hi, uint32_t lo) {
+  return ((long long)hi << 20) + lo;
+}
+
+// Among the CTA's keys (those of bit i in `active`, all in [base, base +
+// 2^bits)), in descending order: the key of rank `want`, or at which the
+// running mass reaches `want`.
+__device__ Picked list_select(Shared& sh, const uint32_t (&key)[kMaxCluster],
+                              const uint32_t (&mh)[kMaxCluster], const uint32_t (&ml)[kMaxCluster],
+                              uint32_t active, uint32_t base, int bits, bool by_mass,
+                              long long want) {
+  const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
+  uint32_t(&hist)[4][kBins] = sh.hist[0];
+  Picked r{true, 0, 0, 0, 0};
+  do {
+    const int sh_bits = max(0, bits - kBinBits);
+    const uint32_t span = bits < 32 ? (1u << bits) - 1 : ~0u;
+    hist[0][tid] = 0;
+    hist[1][tid] = 0;
+    hist[2][tid] = 0;
+    __syncthreads();
+    if (tid == 0) sh.sel_bin = -1;  // the last level's sel_* are read
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) {
+      const uint32_t at = key[i] - base;
+      if (((active >> i) & 1u) && at <= span) {
+        const uint32_t bin = at >> sh_bits;
+        atomicAdd(&hist[0][bin], 1u);
+        if (mh[i] != 0) atomicAdd(&hist[1][bin], mh[i]);
+        if (ml[i] != 0) atomicAdd(&hist[2][bin], ml[i]);
+      }
+    }
+    __syncthreads();
+    const int bin = kBins - 1 - tid;
+    const uint32_t cnt = hist[0][bin];
+    const long long ms = pair_value(hist[1][bin], hist[2][bin]);
+    uint32_t ci = cnt;
+    long long mi = ms;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const uint32_t yc = __shfl_up_sync(0xffffffffu, ci, o);
+      const long long ym = __shfl_up_sync(0xffffffffu, mi, o);
+      if (lane >= o) {
+        ci += yc;
+        mi += ym;
+      }
+    }
+    if (lane == kWarp - 1) {
+      sh.scan_cnt[warp] = ci;
+      sh.scan_mass[warp] = mi;
+    }
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) {
+      ci += sh.scan_cnt[w];
+      mi += sh.scan_mass[w];
+    }
+    const long long before = by_mass ? r.mass + mi - ms : (long long)r.above + ci - cnt;
+    const long long upto = by_mass ? r.mass + mi : (long long)r.above + ci;
+    if (before < want && want <= upto) {
+      sh.sel_bin = bin;
+      sh.sel_above = ci - cnt;
+      sh.sel_mass = mi - ms;
+      sh.sel_count = cnt;
+    }
+    __syncthreads();
+    if (sh.sel_bin < 0) {
+      r.found = false;
+      return r;
+    }
+    r.above += sh.sel_above;
+    r.mass += sh.sel_mass;
+    r.ties = sh.sel_count;
+    base += (uint32_t)sh.sel_bin << sh_bits;
+    bits = sh_bits;
+  } while (bits > 0);
+  r.key = base;
+  return r;
+}
+
+// The filters and the draw over the list (the first CTA; n[q] tokens (value,
+// index) of CTA q at list[q * kListCap]).
 template <typename T>
-static cudaError_t launch_t(const SampleArgs& a, cudaStream_t st) {
+__device__ void list_draw(Shared& sh, const uint2* list, const Law& law, int C, int k, bool has_k,
+                          long long want_p, float tp, float mp, float u, uint32_t low,
+                          const SampleArgs& a, int64_t row) {
+  constexpr int kShift = sizeof(T) == 2 ? 16 : 0;
+  const int tid = threadIdx.x;
+  uint32_t key[kMaxCluster], idx[kMaxCluster], mh[kMaxCluster], ml[kMaxCluster];
+  float x[kMaxCluster];
+  uint32_t active = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxCluster; ++q) {
+    key[q] = idx[q] = mh[q] = ml[q] = 0;
+    x[q] = 0.f;
+    if (q < C && tid < sh.ex_n[q]) {
+      const uint2 e = list[q * kListCap + tid];
+      x[q] = __uint_as_float(e.x);
+      idx[q] = e.y;
+      key[q] = order_key(x[q]) >> kShift;
+      fixed_pair(law.weight(x[q]), mh[q], ml[q]);
+      active |= 1u << q;
+    }
+  }
+  const uint32_t base = max(low, kKeyNegInf + 1) >> kShift;
+  const int bits = 32 - __clz((order_key(law.m) >> kShift) - base);
+  uint32_t tau = 0;
+  int keep_ties = 0, ties = 0;  // kept of the tokens at tau, all of them (tau 0: every token)
+  long long each = 0;
+  if (has_k) {
+    const Picked s = list_select(sh, key, mh, ml, active, base, bits, false, k);
+    if (s.found) {
+      tau = s.key;
+      ties = (int)s.ties;
+      keep_ties = k - (int)s.above;
+      if (tp < 1.f) {
+#pragma unroll
+        for (int q = 0; q < kMaxCluster; ++q)
+          if (((active >> q) & 1u) && key[q] == tau) each = pair_value(mh[q], ml[q]);
+        each = block_max(sh, each);
+        want_p = mass_target(tp, s.mass + each * keep_ties);
+        if (s.mass < want_p) {
+          keep_ties = ties_for(want_p - s.mass, each, keep_ties);
+          want_p = 0;
+        }
+      }
+    } else if (tp < 1.f) {  // fewer tokens than k: all of them
+      long long z = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) z += pair_value(mh[q], ml[q]);
+      want_p = mass_target(tp, block_sum(sh, z));
+    }
+  }
+  if (want_p > 0) {
+    const Picked s = list_select(sh, key, mh, ml, active, base, bits, true, want_p);
+    if (s.found) {
+      tau = s.key;
+      ties = (int)s.ties;
+      each = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q)
+        if (((active >> q) & 1u) && key[q] == tau) each = pair_value(mh[q], ml[q]);
+      each = block_max(sh, each);
+      keep_ties = ties_for(want_p - s.mass, each, ties);
+    }
+  }
+  // kept: above tau, and at tau the first keep_ties by index
+  uint32_t cut = ~0u;
+  constexpr uint32_t kTop = kSampleMaxVocab - 1;  // descending keys of ascending indices
+  uint32_t back[kMaxCluster];
+#pragma unroll
+  for (int q = 0; q < kMaxCluster; ++q) back[q] = kTop - idx[q];
+  if (keep_ties < ties) {
+    uint32_t at_tau = 0;
+#pragma unroll
+    for (int q = 0; q < kMaxCluster; ++q)
+      if (((active >> q) & 1u) && key[q] == tau) at_tau |= 1u << q;
+    cut = kTop - list_select(sh, back, mh, ml, at_tau, 0, 20, false, keep_ties).key;
+  }
+  long long z = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxCluster; ++q) {
+    const dfloat w = law.weight(x[q]);
+    const bool keep = ((active >> q) & 1u) && (key[q] > tau || (key[q] == tau && idx[q] <= cut)) &&
+                      (w.hi - mp) + w.lo >= 0.f;
+    if (!keep) active &= ~(1u << q);
+    else z += pair_value(mh[q], ml[q]);
+  }
+  z = block_sum(sh, z);
+  const long long past = __double2ll_rd((double)u * (double)z) + 1;  // C_i > u Z
+  const Picked s = list_select(sh, back, mh, ml, active, 0, 20, true, past);
+#pragma unroll
+  for (int q = 0; q < kMaxCluster; ++q) {
+    if (((active >> q) & 1u) && back[q] == s.key) {
+      a.out_tokens[row] = (int)idx[q];
+      if (a.out_prob != nullptr)
+        a.out_prob[row] = law.weight(x[q]).hi / ((float)z * 0x1p-40f);
+    }
+  }
+}
+
+template <typename T, bool kSmem>
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C, int slice,
+                                                          int warp_vecs) {
   constexpr int kVec = 16 / sizeof(T);
-  // CTAs per row: slices of at most 24 KB, so that several clusters share an SM
+  __shared__ Shared sh;
+  extern __shared__ uint4 data[];
+  const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = blockIdx.x % C;
+  const int64_t row = blockIdx.x / C;
+  pdl_trigger();
+  cluster_arrive();  // every CTA of the cluster runs before its shared memory is written
+  if (tid < 32) sh.draw.pow2[tid] = kPow2[tid];
+  pdl_wait();  // the logits may come from the previous kernel
+
+  const float T_ = a.temperature[row], u = a.uniform[row];
+  const int k = a.top_k != nullptr ? a.top_k[row] : 0;
+  const float tp = a.top_p != nullptr ? a.top_p[row] : 1.f;
+  const float mp = a.min_p != nullptr ? a.min_p[row] : 0.f;
+  const bool valid = temperature_valid(T_) && u >= 0.f && u < 1.f && k >= 0 && tp > 0.f &&
+                     tp <= 1.f && mp >= 0.f && mp <= 1.f;
+  const bool greedy = T_ == 0.f;
+  const bool has_k = !greedy && k > 0 && k < a.V, has_p = !greedy && tp < 1.f;
+
+  Slice<T, kSmem> sl;
+  sl.src = static_cast<const T*>(a.logits) + row * a.stride + (int64_t)rank * slice;
+  sl.off = (int)((reinterpret_cast<uintptr_t>(sl.src) & 15u) / sizeof(T));
+  sl.n = max(0, min(slice, a.V - rank * slice));
+  sl.sm = data;
+  const int nv = kWarps * warp_vecs;
+
+  // ---- 1: the slice, its maximum, elements that make the row fail
+  float tmax = -INFINITY;
+  int bad = 0;
+  for (int v0 = tid; v0 < nv; v0 += kUnroll * kThreads) {
+    uint4 raw[kUnroll];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j)
+      if (v0 + j * kThreads < nv) raw[j] = sl.load(v0 + j * kThreads);
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      if (v0 + j * kThreads >= nv) break;
+      if (kSmem) data[v0 + j * kThreads] = raw[j];
+      float x[kVec];
+      unpack16(raw[j], x);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        bad |= !(x[i] < INFINITY);  // NaN or +inf
+        tmax = fmaxf(tmax, x[i]);
+      }
+    }
+  }
+  const float wm = warp_max(tmax);
+  const uint32_t wl = __reduce_min_sync(0xffffffffu, order_key(tmax));
+  if (lane == 0) {
+    sh.red[warp] = wm;
+    sh.red_low[warp] = wl;
+  }
+  bad = __syncthreads_or(bad);
+  float m = sh.red[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.red[w]);
+  // lower bound of the tokens that can matter: the largest 16-bit key that at
+  // least `need` of the threads' maxima reach
+  uint32_t theta = 0;
+  const int need = has_k ? ceil_div(k, C) : kListNeedP;
+  if (valid && (has_k || has_p)) {
+    if (need <= kThreads) {
+      const uint32_t key = order_key(tmax) >> 16;
+      for (uint32_t bit = 0x8000u; bit != 0; bit >>= 1)
+        if (__syncthreads_count(key >= (theta | bit)) >= need) theta |= bit;
+    }
+  }
+  cluster_wait();
+  if (tid < C) {
+    *cluster.map_shared_rank(&sh.ex_max[rank], tid) = m;
+    *cluster.map_shared_rank(&sh.ex_bad[rank], tid) = (uint32_t)bad;
+    *cluster.map_shared_rank(&sh.ex_theta[rank], tid) = theta << 16;
+    uint32_t low = sh.red_low[0];
+    for (int w = 1; w < kWarps; ++w) low = min(low, sh.red_low[w]);
+    *cluster.map_shared_rank(&sh.ex_low[rank], tid) = low;
+  }
+  cluster_sync();
+  for (int q = 0; q < C; ++q) {
+    m = fmaxf(m, sh.ex_max[q]);
+    bad |= (int)sh.ex_bad[q];
+    // for top-k every CTA's share has to lie above it; for top-p no CTA may
+    // send more than its place
+    theta = q == 0 ? sh.ex_theta[0]
+            : has_k ? min(theta, sh.ex_theta[q]) : max(theta, sh.ex_theta[q]);
+  }
+  if (!valid || bad || m == -INFINITY) {
+    if (rank == 0 && tid == 0) {
+      raise_status(a.status, valid ? SPEC_ERR_NONFINITE : SPEC_ERR_INVALID_ARG);
+      a.out_tokens[row] = -1;
+      if (a.out_prob != nullptr) a.out_prob[row] = 0.f;
+    }
+    return;
+  }
+  if (greedy) {
+    int first = 0x7fffffff;
+    for (int v = tid; v < nv; v += kThreads) {
+      const uint4 raw = sl.get(v);
+      float x[kVec];
+      unpack16(raw, x);
+#pragma unroll
+      for (int i = kVec - 1; i >= 0; --i)
+        if (x[i] == m) first = min(first, rank * slice + v * kVec - sl.off + i);
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) sh.draw.ties[warp] = first;
+    __syncthreads();
+    if (tid == 0) {
+      for (int w = 0; w < kWarps; ++w) first = min(first, sh.draw.ties[w]);
+      *cluster.map_shared_rank(&sh.ex_first[rank], 0) = first;
+    }
+    cluster_sync();
+    if (rank == 0 && tid == 0) {
+      for (int q = 0; q < C; ++q) first = min(first, sh.ex_first[q]);
+      a.out_tokens[row] = first;
+      if (a.out_prob != nullptr) a.out_prob[row] = 1.f;
+    }
+    return;
+  }
+
+  const Law law(m, T_, sh.draw.pow2);
+
+  // ---- 2a: few candidates go to the first CTA, which finishes the row
+  const bool want_list = has_k ? need <= kListNeedK : has_p;
+  if (want_list) {
+    if (tid == 0) sh.n_list = 0;
+    __syncthreads();
+    uint2* list = reinterpret_cast<uint2*>(data + (kSmem ? nv : 0));
+    uint2* to = cluster.map_shared_rank(list, 0) + rank * kListCap;
+    const uint32_t low = max(theta, kKeyNegInf + 1);
+    dfloat z = df_make(0.f);
+    long long mass = 0;
+    for (int v0 = 0; v0 < nv; v0 += kThreads) {
+      const int v = v0 + tid;
+      float x[kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[i] = -INFINITY;
+      if (v < nv) unpack16(sl.get(v), x);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const bool in = order_key(x[i]) >= low;
+        n += in;
+        if (!has_k) {
+          const dfloat w = law.weight(x[i]);
+          const dfloat s = df_two_sum(z.hi, w.hi);
+          z.hi = s.hi;
+          z.lo += s.lo + w.lo;
+          if (in) {
+            uint32_t hi, lo;
+            fixed_pair(w, hi, lo);
+            mass += pair_value(hi, lo);
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, n > 0)) {
+        int at = n;
+#pragma unroll
+        for (int o = 1; o < kWarp; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += y;
+        }
+        int first = 0;
+        if (lane == kWarp - 1) first = atomicAdd(&sh.n_list, at);
+        at += __shfl_sync(0xffffffffu, first, kWarp - 1) - n;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          if (order_key(x[i]) >= low) {
+            if (at < kListCap)
+              to[at] = make_uint2(__float_as_uint(x[i]), rank * slice + v * kVec - sl.off + i);
+            ++at;
+          }
+      }
+    }
+    if (!has_k) {
+      z = df_warp_sum(df_norm(z.hi, z.lo));
+      if (lane == 0) sh.draw.mass[warp] = make_float2(z.hi, z.lo);
+      mass = block_sum(sh, mass);
+      z = df_make(0.f);
+      for (int w = 0; w < kWarps; ++w) z = df_add(z, dfloat{sh.draw.mass[w].x, sh.draw.mass[w].y});
+    } else {
+      __syncthreads();
+    }
+    if (tid < C) {
+      *cluster.map_shared_rank(&sh.ex_z[rank], tid) = make_float2(z.hi, z.lo);
+      *cluster.map_shared_rank(&sh.ex_mass[rank], tid) = mass;
+      *cluster.map_shared_rank(&sh.ex_n[rank], tid) = sh.n_list;
+    }
+    cluster_sync();
+    bool fits = true;
+    z = df_make(0.f);
+    mass = 0;
+    for (int q = 0; q < C; ++q) {
+      fits &= sh.ex_n[q] <= kListCap;
+      z = df_add(z, dfloat{sh.ex_z[q].x, sh.ex_z[q].y});
+      mass += sh.ex_mass[q];
+    }
+    const long long want =
+        has_k ? 0 : mass_target(tp, __float2ll_rn(z.hi * 0x1p40f) + __float2ll_rn(z.lo * 0x1p40f));
+    if (fits && mass >= want) {  // the same in every CTA
+      if (rank == 0)
+        list_draw<T>(sh, list, law, C, k, has_k, want, tp, mp, u, low, a, row);
+      return;
+    }
+  }
+
+  // ---- 2: the filters' threshold tau and how many tokens equal to it are kept
+  uint32_t tau = kKeyNegInf;
+  int keep_ties = 0;
+  int buf = 0;
+  const uint32_t high = order_key(m);
+  if (has_k) {
+    Selected s = radix_select<T, kSmem>(sh, sl, nv, law, theta, high, false, has_p, k, 0, C, buf);
+    if (s.found) {
+      tau = s.tau;
+      keep_ties = k - (int)s.above;
+      if (has_p) {
+        const long long each = fixed_value(law.weight(key_value(tau)));
+        const long long want = mass_target(tp, s.mass + each * keep_ties);
+        if (s.mass >= want) {
+          const Selected p =
+              radix_select<T, kSmem>(sh, sl, nv, law, tau + 1, high, true, true, 0, want, C,
+                                            buf);
+          tau = p.tau;
+          keep_ties = ties_for(want - p.mass, fixed_value(law.weight(key_value(tau))), (int)p.ties);
+        } else {
+          keep_ties = ties_for(want - s.mass, each, keep_ties);
+        }
+      }
+    }
+  }
+  if (has_p && tau == kKeyNegInf) {  // no top-k, or fewer tokens than k
+    dfloat z = df_make(0.f);
+    for (int v = tid; v < nv; v += kThreads) {
+      const uint4 raw = sl.get(v);
+      float x[kVec];
+      unpack16(raw, x);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const dfloat w = law.weight(x[i]);
+        const dfloat s = df_two_sum(z.hi, w.hi);
+        z.hi = s.hi;
+        z.lo += s.lo + w.lo;
+      }
+    }
+    z = df_warp_sum(df_norm(z.hi, z.lo));
+    if (lane == 0) sh.draw.mass[warp] = make_float2(z.hi, z.lo);
+    __syncthreads();
+    if (tid < C) {
+      z = df_make(0.f);
+      for (int w = 0; w < kWarps; ++w) z = df_add(z, dfloat{sh.draw.mass[w].x, sh.draw.mass[w].y});
+      *cluster.map_shared_rank(&sh.ex_z[rank], tid) = make_float2(z.hi, z.lo);
+    }
+    cluster_sync();
+    z = df_make(0.f);
+    for (int q = 0; q < C; ++q) z = df_add(z, dfloat{sh.ex_z[q].x, sh.ex_z[q].y});
+    const long long zi = __float2ll_rn(z.hi * 0x1p42f) + __float2ll_rn(z.lo * 0x1p42f);
+    const long long want = mass_target(tp, zi);
+    // first the tokens that no thread's maximum is below, if they hold enough
+    uint32_t low = has_k ? 0u : sh.ex_low[0];
+    for (int q = 1; q < C; ++q) low = min(low, sh.ex_low[q]);
+    Selected p = radix_select<T, kSmem>(sh, sl, nv, law, low, high, true, true, 0, want, C, buf);
+    if (!p.found && low > kKeyNegInf + 1)
+      p = radix_select<T, kSmem>(sh, sl, nv, law, 0u, high, true, true, 0, want, C, buf);
+    if (p.found) {
+      tau = p.tau;
+      keep_ties = ties_for(want - p.mass, fixed_value(law.weight(key_value(tau))), (int)p.ties);
+    }
+  }
+
+  // ---- 3
+  exact_draw<kWarps>(sh.draw, sl, law, tau, keep_ties, mp, u, warp_vecs, C, rank, rank * slice, a, row);
+}
+
+// ---------------------------------------------------------------------------
+// rows without filters
+// ---------------------------------------------------------------------------
+// The row streams through registers once: a warp takes a chunk of 256
+// vectors, its maximum, and its mass relative to that maximum with the
+// hardware's exp2 -- five instructions an element against 45 for an exact
+// weight.  The chunk that holds u Z is then walked with exact weights, and
+// the token stands if u Z is further from both its steps than the masses can
+// be off: per weight 1.47e-7 (ex2.approx: 2^-22.73 is the largest error over
+// all arguments in [-126, 0], measured) and 2 * 2^-24 ln2 |y| for the two
+// roundings of its exponent y, 2 * 2^-24 for the sum of a vector's four pairs
+// (vectors and lanes add up as double-floats); sum w |y| is formed with the
+// mass.  The
+// rounding of log2(e)/T itself is taken out to first order by the same sum.
+// Else (a few rows in a hundred at 150k tokens) the row is drawn exactly.
+constexpr uint32_t kMarkMask = 0xfffff;
+constexpr int kPlainThreads = 256;
+constexpr int kPlainWarps = kPlainThreads / kWarp;
+constexpr int kChunkVecs = 256;  // 8 vectors a lane
+constexpr int kMarkedClusters = 38;  // clusters of 8 CTAs that share the marked rows
+
+struct PlainShared {
+  DrawShared draw;
+  // maximum, mass (hi, lo) and error of each chunk, relative to its maximum;
+  // then mass (hi, lo) and error relative to the row's, and the maximum
+  float4 stat[(kSampleMaxVocab / 4 + 8) / kChunkVecs + 1];
+  float2 warp_mass[kPlainWarps];
+  float pick_err;
+  int sure;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// Two fp32 numbers in one register pair and the packed operations on them.
+struct pair2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ pair2 pk(float a, float b) {
+  pair2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpk(pair2 p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ pair2 add2(pair2 a, pair2 b) {
+  pair2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ pair2 sub2(pair2 a, pair2 b) {
+  pair2 r;
+  asm("{.reg .b64 m; mov.b64 m, 0xbf800000bf800000; fma.rn.f32x2 %0, %2, m, %1;}"
+      : "=l"(r.v)
+      : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ pair2 mul2(pair2 a, pair2 b) {
+  pair2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ pair2 fma2(pair2 a, pair2 b, pair2 c) {
+  pair2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+__device__ __forceinline__ float vec_max(const uint4& r, __nv_bfloat16) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+  return max_nan(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float vec_max(const uint4& r, float) {
+  return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)),
+                 max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
+}
+
+// Elements of a vector, none below `low` (whose weight is 0), in pairs.
+__device__ __forceinline__ void vec_pairs(const uint4& r, __nv_bfloat16 low, pair2 (&p)[4]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  const __nv_bfloat162 l2 = __halves2bfloat162(low, low);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), l2);
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+    p[i] = pk(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+}
+__device__ __forceinline__ void vec_pairs(const uint4& r, float low, pair2 (&p)[2]) {
+  p[0] = pk(fmaxf(__uint_as_float(r.x), low), fmaxf(__uint_as_float(r.y), low));
+  p[1] = pk(fmaxf(__uint_as_float(r.z), low), fmaxf(__uint_as_float(r.w), low));
+}
+// A value of the type at or below m - gap, and below m.
+__device__ __forceinline__ __nv_bfloat16 below(float m, float gap, __nv_bfloat16) {
+  const uint32_t b = __float_as_uint(m) >> 16;  // m is a bf16
+  const uint32_t next = m > 0.f ? b - 1 : (m < 0.f ? b + 1 : 0x8001u);
+  return __float2bfloat16_rd(fminf(m - gap, __uint_as_float(next << 16)));
+}
+__device__ __forceinline__ float below(float m, float gap, float) {
+  return fminf(m - gap, nextafterf(m, -INFINITY));
+}
+
+// This lane's vectors of a chunk of the row.
+template <typename T>
+__device__ __forceinline__ void load_chunk(const Slice<T, false>& row, int ch,
+                                           uint4 (&raw)[kChunkVecs / kWarp]) {
+  constexpr int kVec = 16 / sizeof(T);
+  const int lane = threadIdx.x % kWarp;
+  const int p = ch * kChunkVecs * kVec - row.off;
+  if (p >= 0 && p + kChunkVecs * kVec <= row.n) {  // wholly inside
+    const uint4* q = reinterpret_cast<const uint4*>(row.src + p) + lane;
+#pragma unroll
+    for (int j = 0; j < kChunkVecs / kWarp; ++j) raw[j] = __ldcs(q + j * kWarp);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kChunkVecs / kWarp; ++j)
+      raw[j] = row.load(ch * kChunkVecs + j * kWarp + lane);
+  }
+}
+
+// kDefer: rows that need the exact draw are marked for sample_marked_kernel.
+template <typename T, bool kDefer>
+__global__ void __launch_bounds__(kPlainThreads, 5)
+    sample_plain_kernel(SampleArgs a, int C, int chunks, int slice, int warp_vecs) {
+  constexpr int kVec = 16 / sizeof(T), kPairs = kVec / 2;
+  constexpr int kLaneVecs = kChunkVecs / kWarp;
+  constexpr int kSets = kLaneVecs / kPlainWarps;
+  __shared__ PlainShared sh;
+  const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = blockIdx.x % C;
+  const int64_t row = blockIdx.x / C;
+  pdl_trigger();
+  cluster_arrive();  // every CTA of the cluster runs before its shared memory is written
+  if (tid < 32) sh.draw.pow2[tid] = kPow2[tid];
+  if (tid == 0) sh.sure = 0;
+  pdl_wait();  // the logits may come from the previous kernel
+
+  const float T_ = a.temperature[row], u = a.uniform[row];
+  const bool valid = temperature_valid(T_) && u >= 0.f && u < 1.f;
+  const bool greedy = T_ == 0.f;
+  Slice<T, false> whole;  // the row
+  whole.src = static_cast<const T*>(a.logits) + row * a.stride;
+  whole.off = (int)((reinterpret_cast<uintptr_t>(whole.src) & 15u) / sizeof(T));
+  whole.n = a.V;
+  whole.sm = nullptr;
+  const Law scale(0.f, valid && !greedy ? T_ : 1.f, sh.draw.pow2);
+  const float c = scale.c_hi;
+  cluster_wait();
+
+  for (int ch = rank * kPlainWarps + warp; ch < chunks; ch += C * kPlainWarps) {
+    uint4 raw[kLaneVecs];
+    load_chunk(whole, ch, raw);
+    float m = vec_max(raw[0], T());
+#pragma unroll
+    for (int j = 1; j < kLaneVecs; ++j) m = max_nan(m, vec_max(raw[j], T()));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float4 st = make_float4(m, 0.f, 0.f, 0.f);
+    if (m < INFINITY && m > -INFINITY && !greedy) {
+      const pair2 neg = pk(-m, -m), c2 = pk(c, c);
+      const T low = below(m, 300.f / c, T());  // weights below 2^-300 are 0
+      pair2 sum = pk(0.f, 0.f), lost = sum, moment = sum;
+#pragma unroll
+      for (int j = 0; j < kLaneVecs; ++j) {
+        pair2 p[kPairs];
+        vec_pairs(raw[j], low, p);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const pair2 d = add2(p[i], neg);
+          float y0, y1;
+          unpk(mul2(d, c2), y0, y1);
+          const pair2 e = pk(fast_exp2(y0), fast_exp2(y1));
+          moment = fma2(e, d, moment);
+          p[i] = e;
+        }
+#pragma unroll
+        for (int w = 1; w < kPairs; w *= 2)
+#pragma unroll
+          for (int i = 0; i + w < kPairs; i += 2 * w) p[i] = add2(p[i], p[i + w]);
+        // the vector's sum joins the lane's, with what the addition rounds off
+        const pair2 s = add2(sum, p[0]), b = sub2(s, sum);
+        lost = add2(lost, add2(sub2(sum, sub2(s, b)), sub2(p[0], b)));
+        sum = s;
+      }
+      float s0, s1, l0, l1, a0, a1;
+      unpk(sum, s0, s1);
+      unpk(lost, l0, l1);
+      unpk(moment, a0, a1);
+      const dfloat s = df_warp_sum(df_add(df_two_sum(s0, s1), df_make(l0 + l1)));
+      const float mom = warp_sum(a0 + a1);  // sum w (x - m), negative
+      const dfloat fixed = df_add(s, df_make(mom * 0.693147181f * scale.c_lo));
+      st.y = fixed.hi;
+      st.z = fixed.lo;
+      st.w = s.hi * (1.47e-7f + 2 * 0x1p-24f) - mom * c * (2 * 0.6931472f * 0x1p-24f);
+    }
+    if (lane < C) *cluster.map_shared_rank(&sh.stat[ch], lane) = st;
+  }
+  cluster_sync();  // every CTA has every chunk's statistics
+  float m = -INFINITY;
+  for (int ch = lane; ch < chunks; ch += kWarp) m = max_nan(m, sh.stat[ch].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!valid || !(m < INFINITY) || m == -INFINITY) {
+    if (rank == 0 && tid == 0) {
+      raise_status(a.status, valid ? SPEC_ERR_NONFINITE : SPEC_ERR_INVALID_ARG);
+      a.out_tokens[row] = -1;
+      if (a.out_prob != nullptr) a.out_prob[row] = 0.f;
+    }
+    return;
+  }
+  if (greedy) {
+    if (rank != 0 || warp != 0) return;
+    int ch = 0x7fffffff;  // the first chunk that holds the maximum
+    for (int i = chunks - 1 - lane; i >= 0; i -= kWarp)
+      if (sh.stat[i].x == m) ch = i;
+    ch = __reduce_min_sync(0xffffffffu, ch);
+    int first = 0x7fffffff;
+    for (int j = 0; j < kLaneVecs; ++j) {
+      const int v = ch * kChunkVecs + j * kWarp + lane;
+      const uint4 raw = whole.load(v);
+      float x[kVec];
+      unpack16(raw, x);
+#pragma unroll
+      for (int i = kVec - 1; i >= 0; --i)
+        if (x[i] == m) first = min(first, v * kVec + i - whole.off);
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) {
+      a.out_tokens[row] = first;
+      if (a.out_prob != nullptr) a.out_prob[row] = 1.f;
+    }
+    return;
+  }
+  const Law law(m, T_, sh.draw.pow2);
+  __syncthreads();  // the maxima are read
+  for (int ch = tid; ch < chunks; ch += kPlainThreads) {
+    const float4 st = sh.stat[ch];
+    const dfloat f = law.weight(st.x);
+    const dfloat mass = df_add(df_mul_f(f, st.y), df_make(f.hi * st.z));
+    sh.stat[ch] = make_float4(mass.hi, mass.lo, f.hi * st.w, st.x);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int per = ceil_div(chunks, kWarp), c0 = lane * per, c1 = min(chunks, c0 + per);
+    dfloat sum = df_make(0.f);
+    float err = 0.f;
+    for (int ch = c0; ch < c1; ++ch) {
+      const float4 st = sh.stat[ch];
+      sum = df_add(sum, dfloat{st.x, st.y});
+      err += st.z;
+    }
+    const dfloat incl = df_warp_scan(sum);
+    float err_to = err;  // errors of the chunks up to this lane's last
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const float y = __shfl_up_sync(0xffffffffu, err_to, o);
+      if (lane >= o) err_to += y;
+    }
+    const float err_all = __shfl_sync(0xffffffffu, err_to, kWarp - 1);
+    const dfloat Z = df_shfl(incl, kWarp - 1), thr = df_mul_f(Z, u);
+    const unsigned past = __ballot_sync(0xffffffffu, sum.hi > 0.f && df_gt(incl, thr));
+    const int owner = past != 0 ? __ffs(past) - 1 : -1;
+    if (lane == owner) {
+      dfloat cum = df_sub(incl, sum);
+      int ch = c0;
+      float before = fmaxf(0.f, err_to - err);
+      for (; ch + 1 < c1; ++ch) {
+        const float4 st = sh.stat[ch];
+        const dfloat next = df_add(cum, dfloat{st.x, st.y});
+        if (df_gt(next, thr)) break;
+        cum = next;
+        before += st.z;
+      }
+      sh.draw.pick = ch;
+      sh.draw.pick_base = make_float2(cum.hi, cum.lo);
+      sh.draw.pick_z = make_float2(Z.hi, Z.lo);
+      // C_i - u Z is off by at most (1 - u) times the error of the masses up to
+      // i and u times that of the others (the chunk's own counted in both;
+      // 1.0001 for the roundings of these sums)
+      sh.pick_err = 1.0001f * ((1.f - u) * (before + sh.stat[ch].z) + u * (err_all - before));
+    }
+    if (owner < 0 && lane == 0) sh.draw.pick = -1;
+  }
+  __syncthreads();
+  // one CTA walks the chunk and tells the others whether the token stands
+  const int pick = sh.draw.pick;
+  if (pick >= 0 && pick % C == rank) {
+    // warp w holds the vectors [w, w + 1) * 256 / warps of the chunk, 32 at a time
+    dfloat w[kSets][kVec], incl[kSets], sum[kSets], total = df_make(0.f);
+    const int v0 = pick * kChunkVecs + warp * kSets * kWarp + lane;
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      const uint4 raw = whole.load(v0 + j * kWarp);
+      float x[kVec];
+      unpack16(raw, x);
+      sum[j] = df_make(0.f);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        w[j][i] = law.weight(x[i]);
+        sum[j] = df_add(sum[j], w[j][i]);
+      }
+      incl[j] = df_add(total, df_warp_scan(sum[j]));
+      total = df_shfl(incl[j], kWarp - 1);
+    }
+    if (lane == 0) sh.warp_mass[warp] = make_float2(total.hi, total.lo);
+    __syncthreads();
+    dfloat base{sh.draw.pick_base.x, sh.draw.pick_base.y};
+    for (int i = 0; i < warp; ++i)
+      base = df_add(base, dfloat{sh.warp_mass[i].x, sh.warp_mass[i].y});
+    const dfloat Z{sh.draw.pick_z.x, sh.draw.pick_z.y}, thr = df_mul_f(Z, u);
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      const dfloat upto = df_add(base, incl[j]);
+      dfloat cum = df_sub(upto, sum[j]);
+      if (sum[j].hi > 0.f && df_gt(upto, thr) && !df_gt(cum, thr)) {  // one thread at most
+        int at = -1;
+        float wt = 0.f;
+        dfloat before = cum;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          if ((at < 0 || !df_gt(cum, thr)) && w[j][i].hi > 0.f) {
+            before = cum;
+            cum = df_add(cum, w[j][i]);
+            at = i;
+            wt = w[j][i].hi;
+          }
+        }
+        const float gap = fminf(df_to_f(df_sub(thr, before)), df_to_f(df_sub(cum, thr)));
+        if (gap > sh.pick_err) {
+          for (int q = 0; q < C; ++q) *cluster.map_shared_rank(&sh.sure, q) = 1;
+          a.out_tokens[row] = (v0 + j * kWarp) * kVec + at - whole.off;
+          if (a.out_prob != nullptr) a.out_prob[row] = wt / df_to_f(Z);
+        }
+      }
+    }
+  }
+  cluster_sync();
+  if (sh.sure) return;
+  if (kDefer) {
+    if (rank == 0 && tid == 0)
+      a.out_tokens[row] = -2 - (int)(atomicAdd(a.status + 1, 1u) & kMarkMask);
+    return;
+  }
+  Slice<T, false> sl;
+  sl.src = whole.src + (int64_t)rank * slice;
+  sl.off = (int)((reinterpret_cast<uintptr_t>(sl.src) & 15u) / sizeof(T));
+  sl.n = max(0, min(slice, a.V - rank * slice));
+  sl.sm = nullptr;
+  exact_draw<kPlainWarps>(sh.draw, sl, law, kKeyNegInf, 0, 0.f, u, warp_vecs, C, rank, rank * slice,
+                          a, row);
+}
+
+// The exact draw of the rows that sample_plain_kernel<T, true> marked with a
+// token of -2 - i (i counts the marks): cluster i % G of the G takes them.  A
+// few rows in a hundred come here, so the whole GPU shares them, where a CTA
+// that drew its own row exactly kept the others waiting at the end (640 rows
+// of 152064 bf16 logits: 105 us, against 75 us with this kernel).
+constexpr int kMarkedRows = 4;  // rows a thread looks at in one round
+
+struct MarkedShared {
+  DrawShared draw;
+  float ex_max[kMaxCluster];
+  float red[kWarps];
+  int warp_n[kWarps];
+  int list[kMarkedRows * kThreads];
+};
+
+template <typename T, bool kSmem>
+__global__ void __launch_bounds__(kThreads) sample_marked_kernel(SampleArgs a, int C, int slice,
+                                                                 int warp_vecs) {
+  constexpr int kVec = 16 / sizeof(T);
+  __shared__ MarkedShared sh;
+  extern __shared__ uint4 data[];
+  const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = blockIdx.x % C, G = gridDim.x / C, mine = blockIdx.x / C;
+  pdl_trigger();
+  cluster_arrive();
+  if (tid < 32) sh.draw.pow2[tid] = kPow2[tid];
+  pdl_wait();
+  cluster_wait();
+  for (int base = 0; base < a.rows; base += kMarkedRows * kThreads) {
+    // marked rows of this block of rows that are this cluster's, in order
+    // (other clusters may be writing tokens over their own marks)
+    int mark[kMarkedRows], n = 0;
+#pragma unroll
+    for (int j = 0; j < kMarkedRows; ++j) {
+      const int r = base + tid * kMarkedRows + j;
+      mark[j] = r < a.rows ? -2 - a.out_tokens[r] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kMarkedRows; ++j) n += mark[j] >= 0 && mark[j] % G == mine;
+    int at = n;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
+    }
+    if (lane == kWarp - 1) sh.warp_n[warp] = at;
+    __syncthreads();
+    at -= n;
+    n = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += sh.warp_n[w];
+      n += sh.warp_n[w];
+    }
+#pragma unroll
+    for (int j = 0; j < kMarkedRows; ++j)
+      if (mark[j] >= 0 && mark[j] % G == mine) sh.list[at++] = base + tid * kMarkedRows + j;
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+      const int64_t row = sh.list[i];
+      Slice<T, kSmem> sl;
+      sl.src = static_cast<const T*>(a.logits) + row * a.stride + (int64_t)rank * slice;
+      sl.off = (int)((reinterpret_cast<uintptr_t>(sl.src) & 15u) / sizeof(T));
+      sl.n = max(0, min(slice, a.V - rank * slice));
+      sl.sm = data;
+      float m = -INFINITY;
+      for (int v = tid; v < kWarps * warp_vecs; v += kThreads) {
+        const uint4 raw = sl.load(v);
+        if (kSmem) data[v] = raw;
+        float x[kVec];
+        unpack16(raw, x);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) m = fmaxf(m, x[j]);
+      }
+      m = warp_max(m);
+      if (lane == 0) sh.red[warp] = m;
+      __syncthreads();
+      if (tid < C) {
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sh.red[w]);
+        *cluster.map_shared_rank(&sh.ex_max[rank], tid) = m;
+      }
+      cluster_sync();
+      for (int q = 0; q < C; ++q) m = fmaxf(m, sh.ex_max[q]);
+      const Law law(m, a.temperature[row], sh.draw.pow2);
+      exact_draw<kWarps>(sh.draw, sl, law, kKeyNegInf, 0, 0.f, a.uniform[row], warp_vecs, C, rank,
+                         rank * slice, a, row);
+      cluster_sync();  // the exchange is read
+    }
+    __syncthreads();  // the list is read
+  }
+}
+
+struct ClusterLaunch {  // use in place: cfg points at attr
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg;
+  ClusterLaunch(int64_t rows, int C, int threads, size_t smem, cudaStream_t st) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg = cudaLaunchConfig_t{};
+    cfg.gridDim = dim3((unsigned)(rows * C));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+  ClusterLaunch(const ClusterLaunch&) = delete;
+  ClusterLaunch& operator=(const ClusterLaunch&) = delete;
+};
+
+template <typename T>
+static cudaError_t launch_t(const SampleArgs& a, cudaStream_t st, int* launches) {
+  constexpr int kVec = 16 / sizeof(T);
+  const bool plain = a.top_k == nullptr && a.top_p == nullptr && a.min_p == nullptr;
   int C = 1;
+  if (plain) {
+    const int chunks = ceil_div(ceil_div(a.V, kVec) + 1, kChunkVecs);
+    auto slice_of = [&](int c) { return ceil_div(ceil_div(a.V, c), kVec) * kVec; };
+    auto vecs_of = [&](int c, int warps) { return ceil_div(slice_of(c) / kVec + 1, warps); };
+    // enough CTAs to fill the GPU twice over, as long as each has a chunk a warp
+    while (C < kMaxCluster && C * kPlainWarps < chunks && (int64_t)a.rows * C < 608) C *= 2;
+    const bool defer = C <= 2 && chunks > 8;
+    {
+      ClusterLaunch L(a.rows, C, kPlainThreads, 0, st);
+      const cudaError_t e = cudaLaunchKernelEx(
+          &L.cfg, defer ? sample_plain_kernel<T, true> : sample_plain_kernel<T, false>, a, C, chunks,
+          slice_of(C), vecs_of(C, kPlainWarps));
+      ++*launches;
+      if (e != cudaSuccess || !defer) return e;
+    }
+    C = kMaxCluster;
+    const int vecs = vecs_of(C, kWarps);
+    const size_t bytes = (size_t)kWarps * vecs * 16;
+    const bool fits = bytes <= kMaxSliceBytes;
+    auto kern = fits ? sample_marked_kernel<T, true> : sample_marked_kernel<T, false>;
+    const size_t smem = fits ? bytes : 0;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    ClusterLaunch L(min(kMarkedClusters, a.rows), C, kThreads, smem, st);
+    ++*launches;
+    return cudaLaunchKernelEx(&L.cfg, kern, a, C, slice_of(C), vecs);
+  }
+  // CTAs per row: slices of at least 8 KB.  Fewer CTAs for many rows were no
+  // faster (256 rows of 128256 bf16 logits: top-k 50 in 117 us with 8 CTAs a
+  // row, 124 us with 4)
   while (C < kMaxCluster && ceil_div64(a.V, C) * (int)sizeof(T) > 8192) C *= 2;
   const int slice = ceil_div(ceil_div(a.V, C), kVec) * kVec;
   // a row may start anywhere in a 16-byte vector: up to one more vector
@@ -670,33 +1548,20 @@ static cudaError_t launch_t(const SampleArgs& a, cudaStream_t st) {
   const size_t bytes = (size_t)kWarps * warp_vecs * 16;
   const bool fits = bytes <= kMaxSliceBytes;
   auto kern = fits ? sample_kernel<T, true> : sample_kernel<T, false>;
-  const size_t smem = fits ? bytes : 0;
-  cudaError_t e =
+  const size_t smem = (fits ? bytes : 0) + sizeof(uint2) * kMaxCluster * kListCap;
+  const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((int64_t)a.rows * C));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, a, C, slice, warp_vecs);
+  ClusterLaunch L(a.rows, C, kThreads, smem, st);
+  ++*launches;
+  return cudaLaunchKernelEx(&L.cfg, kern, a, C, slice, warp_vecs);
 }
 
 }  // namespace smp
 
 cudaError_t sample_launch(const SampleArgs& a, cudaStream_t st, int* launches) {
-  const cudaError_t e =
-      a.dtype == SPEC_BF16 ? smp::launch_t<__nv_bfloat16>(a, st) : smp::launch_t<float>(a, st);
-  ++*launches;
+  const cudaError_t e = a.dtype == SPEC_BF16 ? smp::launch_t<__nv_bfloat16>(a, st, launches)
+                                             : smp::launch_t<float>(a, st, launches);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
