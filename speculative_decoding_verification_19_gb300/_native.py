@@ -176,19 +176,19 @@ def device_status(ws: torch.Tensor, clear: bool = True, stream=None) -> int:
     return int(out.value)
 
 
-def _expect(name, t, dtype, shape=None, device=None, optional=False):
-    """A tensor's address after checks of its type, shape and device; dense
-    unless `shape` is None."""
+def _expect(name, t, dtype, shape, device, optional=False):
+    """A tensor's address after checks of its type, shape and GPU (by index);
+    dense unless `shape` is None."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is needed")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} is wanted, not {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} lives on {t.device}, not on {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} lives on {t.device}, not on cuda:{device}")
     if shape is not None:
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"{name}: shape {shape} is wanted, not {tuple(t.shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -196,23 +196,21 @@ def _expect(name, t, dtype, shape=None, device=None, optional=False):
 
 
 def _on(t, name):
-    """The device of a call's first tensor (which must be a GPU)."""
+    """The GPU (its index) of a call's first tensor."""
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
-    return t.device
+    return t.get_device()
 
 
 def _launch(fn, device, stream, *args):
-    """Calls the library on the tensors' device and its current stream."""
-    L = lib()
-    with_guard = device.index != torch.cuda.current_device()
-    if with_guard:
-        with torch.cuda.device(device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            code = getattr(L, fn)(*args, s.cuda_stream)
+    """Calls the library on the tensors' GPU, on its current stream or `stream`."""
+    L = _lib or lib()
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        code = getattr(L, fn)(*args, s)
     else:
-        s = torch.cuda.current_stream() if stream is None else stream
-        code = getattr(L, fn)(*args, s.cuda_stream)
+        with torch.cuda.device(device):
+            code = getattr(L, fn)(*args, s)
     if code != 0:
         raise SpecError(fn, code)
     return L.spec_last_launch_count()

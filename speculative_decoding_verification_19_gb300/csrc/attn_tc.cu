@@ -99,6 +99,7 @@ constexpr int kPCol = kOCol + 128;  // P of S buffer k (bf16 pairs) at kPCol + 3
 // Split cost of one (request, head) segment, in tiles: the Q load, the
 // masks and the drain of the pipeline at a pair's end cost about this much.
 constexpr int kSegCost = 3;
+constexpr int kWinMinCost = 8;
 constexpr int kPrepThreads = 256;
 constexpr int kPlanReqs = 1024;  // requests whose plan arrays fit the prep kernel's shared memory
 
@@ -496,29 +497,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
         }
       } else {
         // the tile reaches the new rows: those come from k_new / v_new (the
-        // append into the cache runs concurrently), rows past L are zero
+        // append into the cache runs concurrently), rows past L are zero, and
+        // with a window so are pages that are not held.  Pages wholly in the
+        // cached prefix are copied as above; in the others each row picks its
+        // source without a branch.
+        const int64_t row_stride = (int64_t)Hkv * 128;
+        const int64_t new0 = (((int64_t)cu.b * M - cu.ctx) * Hkv + cu.h) * 128 + c16 * 8;
 #pragma unroll
         for (int p = 0; p < kPages; ++p) {
           if (p < np) {
-            const int64_t page = ((int64_t)blk[p] * Hkv + cu.h) * kBlock;
+            const int64_t page = ((int64_t)blk[p] * Hkv + cu.h) * kBlock * 128 + c16 * 8;
+            const int pos0 = kpos0 + p * kBlock;
+            const uint32_t so0 = swz_half + (uint32_t)p * kBoxBytes;
+            const bool have = !kWin || win_page(rt * kPages + p, cu.ctx, window, sinks);
+            if (have && pos0 + kBlock <= cu.ctx) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int r = r0 + 4 * k;
-              const int pos = kpos0 + p * kBlock + r;
-              const uint32_t so = swz_half + (uint32_t)p * kBoxBytes + (uint32_t)r * 128u +
-                                  ((uint32_t)((c16 & 7) ^ (r & 7)) << 4);
-              if (kWin && !win_page(rt * kPages + p, cu.ctx, window, sinks)) {
-                ptx::cp_async16_fill(sb + so, k_new, 0u);
-                ptx::cp_async16_fill(sb + 2 * kHalfBytes + so, v_new, 0u);
-              } else if (pos < cu.ctx) {
-                const int64_t e = (page + r) * 128 + c16 * 8;
-                ptx::cp_async16(sb + so, k_cache + e);
-                ptx::cp_async16(sb + 2 * kHalfBytes + so, v_cache + e);
-              } else {
-                const bool in = pos < L;
-                const int64_t e = in ? (((int64_t)cu.b * M + (pos - cu.ctx)) * Hkv + cu.h) * 128 + c16 * 8 : 0;
-                ptx::cp_async16_fill(sb + so, k_new + e, in ? 16u : 0u);
-                ptx::cp_async16_fill(sb + 2 * kHalfBytes + so, v_new + e, in ? 16u : 0u);
+              for (int k = 0; k < 4; ++k) {
+                const int r = r0 + 4 * k;
+                const uint32_t so = so0 + (uint32_t)r * 128u + ((uint32_t)((c16 & 7) ^ (r & 7)) << 4);
+                ptx::cp_async16(sb + so, k_cache + page + r * 128);
+                ptx::cp_async16(sb + 2 * kHalfBytes + so, v_cache + page + r * 128);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = r0 + 4 * k, pos = pos0 + r;
+                const uint32_t so = so0 + (uint32_t)r * 128u + ((uint32_t)((c16 & 7) ^ (r & 7)) << 4);
+                const bool cached = pos < cu.ctx, in = have && pos < L;
+                const __nv_bfloat16* ks = cached ? k_cache + page + r * 128 : k_new + new0 + pos * row_stride;
+                const __nv_bfloat16* vs = cached ? v_cache + page + r * 128 : v_new + new0 + pos * row_stride;
+                ptx::cp_async16_fill(sb + so, in ? ks : k_new, in ? 16u : 0u);
+                ptx::cp_async16_fill(sb + 2 * kHalfBytes + so, in ? vs : v_new, in ? 16u : 0u);
               }
             }
           }
@@ -1181,6 +1190,10 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     __syncthreads();
   }
   const int64_t T = carry_t, Ctot = carry_c;
+  // With a window a small batch has few tiles: each CTA then takes at least
+  // kWinMinCost of the cost, because every further CTA of a pair is a partial
+  // that the pair's first CTA reads in turn.
+  const int Ge = kWin ? (int)max((int64_t)1, min((int64_t)G, Ctot / kWinMinCost)) : G;
   if (tid == 0) {
     tpre[B] = T;
     cpre[B] = Ctot;
@@ -1197,29 +1210,43 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     }
     return;
   }
-  for (int r = tid; r < B; r += blockDim.x) {
-    const int64_t c0 = cpre[r], c1 = cpre[r + 1];
-    if (c1 == c0) continue;
+  // CTA k: the request r with cpre[r] <= floor(k * Ctot / Ge) < cpre[r + 1] by
+  // bisection, one thread per CTA (a thread per request walking its CTAs took
+  // 30 us for a single request)
+  for (int k = tid; k < G; k += blockDim.x) {
+    if (k >= Ge) {  // no tiles
+      starts[2 * k] = make_int4((int)T, B, 0, 0);
+      s_g0[k] = (int)T;
+      s_req[k] = -1;
+      continue;
+    }
+    const int64_t at = (int64_t)k * Ctot / Ge;
+    int r = 0;
+    for (int hi = B; hi - r > 1;) {
+      const int mid = (r + hi) >> 1;
+      if (cpre[mid] <= at) r = mid;
+      else hi = mid;
+    }
     const int nt = small ? s_nt[r] : __ldcg(ntiles + r);
     const int64_t per = nt + kSegCost;
-    // CTAs k with c0 <= floor(k * Ctot / G) < c1
-    const int k0 = (int)((c0 * G + Ctot - 1) / Ctot), k1 = (int)((c1 * G + Ctot - 1) / Ctot);
-    for (int k = k0; k < k1; ++k) {
-      int64_t rem = (int64_t)k * Ctot / G - c0;
-      const int h = (int)(rem / per);
-      rem -= h * per;
-      const int j = (int)max((int64_t)0, rem - kSegCost);  // rem < nt + kSegCost: j < nt
-      const int g0 = (int)(tpre[r] + (int64_t)h * nt + j);
-      starts[2 * k] = make_int4(g0, r, h, j);
-      s_g0[k] = g0;
-      s_req[k] = r;
-    }
+    int64_t rem = at - cpre[r];
+    const int h = (int)(rem / per);
+    rem -= h * per;
+    const int j = (int)max((int64_t)0, rem - kSegCost);  // rem < nt + kSegCost: j < nt
+    const int g0 = (int)(tpre[r] + (int64_t)h * nt + j);
+    starts[2 * k] = make_int4(g0, r, h, j);
+    s_g0[k] = g0;
+    s_req[k] = r;
   }
   __syncthreads();
   // second half of each start record: the first request's record and the
   // CTA's end tile (a CTA with tiles starts inside a request)
   for (int k = tid; k < G; k += blockDim.x) {
     const int r = s_req[k];
+    if (r < 0) {
+      starts[2 * k + 1] = make_int4(0, 0, B, (int)T);
+      continue;
+    }
     const int4 rec = small ? make_int4(s_ctx[r], s_nt[r], s_next[r], 0) : rq[r];
     starts[2 * k + 1] = make_int4(rec.x, rec.y, rec.z, s_g0[k + 1]);
   }
