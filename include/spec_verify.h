@@ -191,7 +191,7 @@ spec_status spec_verify_attn(const void* q, const void* k_new,
  * neither one of the first `sinks` positions nor a position from
  * ctx - window + 1 on are not read and may hold anything
  * (spec_block_tables returns those pages).  A window of the whole context
- * gives spec_verify_attn's results.
+ * gives spec_verify_attn's results, up to the order of the sums.
  */
 spec_status spec_verify_attn_window(const void* q, const void* k_new, const void* v_new,
                                     void* k_cache, void* v_cache, const int32_t* block_table,

@@ -9,9 +9,10 @@
 //
 // Kernels in this file (CUDA cores; the tensor-core path lives in
 // attn_tc.cu):
-//   kv_append_kernel   one CTA per request: checks the request (capacity,
-//                      block ids, topology), records the verdict, writes the
-//                      new K/V and clears the rest of the last block.
+//   kv_append_kernel   up to eight CTAs per request: each checks the request
+//                      (capacity, block ids, topology) and writes its share of
+//                      the new K/V and the cleared rest of the last block; the
+//                      first records the verdict.
 //   attn_split_kernel  split-KV attention: one CTA per (request, KV head,
 //                      key range); all group*M query rows that read the KV
 //                      head are handled together, so every K/V byte is read
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
   bad_block = __syncthreads_or(bad_block);
   bad_topo = __syncthreads_or(bad_topo);
   const bool ok = cap_ok && !bad_block && !bad_topo;
-  if (tid == 0) {
+  if (tid == 0 && blockIdx.y == 0) {
     req_ok[b] = ok ? 1 : 0;
     if (!cap_ok) raise_status(status, SPEC_ERR_CAPACITY);
     if (bad_block) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
   const int64_t end = ceil_div64(L, kBlock) * kBlock;
   const int npos = (int)(end - ctx);
   const int work = npos * d.Hkv * lanes;
-  for (int w = tid; w < work; w += blockDim.x) {
+  for (int w = blockIdx.y * blockDim.x + tid; w < work; w += gridDim.y * blockDim.x) {
     const int lane = w % lanes;
     const int h = (w / lanes) % d.Hkv;
     const int i = w / (lanes * d.Hkv);
@@ -111,6 +112,7 @@ constexpr int kTileKeys = 32;
 constexpr int kSimtThreads = 128;
 constexpr int kSimtWarps = kSimtThreads / kWarp;
 constexpr int kMaxRows = 128;  // new rows per request (tree nodes)
+constexpr int kMinWinSplit = 64;  // fewest keys of a range with a window
 
 size_t attn_simt_smem_bytes(int R, int D) {
   return sizeof(float) * ((size_t)R * D + kTileKeys * (D + 4) + kTileKeys * D + (size_t)R * kTileKeys) +
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(
     const float* __restrict__ part, const int32_t* __restrict__ ctx_lens,
     const int32_t* __restrict__ req_ok, spec_dims d, int window, int sinks, int split_keys,
     int max_splits, T* __restrict__ out, float* __restrict__ lse) {
-  const int h = blockIdx.x, b = blockIdx.y;
+  const int h = blockIdx.x, b = blockIdx.z;
   const int group = d.Hq / d.Hkv;
   const int R = group * d.M;
   const int D = d.D;
@@ -333,8 +335,8 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(
   const int nsp = ok ? ceil_div(L, split_keys) : 0;
   const float* pbase = part + ((int64_t)b * d.Hkv + h) * max_splits * (int64_t)R * (D + 1);
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
-  const int nwarps = blockDim.x / kWarp;
-  for (int r = warp; r < R; r += nwarps) {
+  const int nwarps = gridDim.y * (blockDim.x / kWarp);
+  for (int r = blockIdx.y * (blockDim.x / kWarp) + warp; r < R; r += nwarps) {
     const int i = r / group, hq = h * group + r % group;
     float m = -INFINITY;
     for (int s = 0; s < nsp; ++s) m = fmaxf(m, pbase[((int64_t)s * R + r) * (D + 1) + D]);
@@ -367,7 +369,11 @@ cudaError_t kv_append_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_
   const spec_dims& d = a.d;
   int32_t* req_ok = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + lay.attn_ok_off);
   uint32_t* status = reinterpret_cast<uint32_t*>(static_cast<char*>(a.ws) + lay.status_off);
-  PdlLaunch L(dim3(d.B), dim3(256), 0, st);
+  // one CTA per 1024 vectors of 16 bytes (8 requests of 64 rows x 8 heads x 64
+  // fp32 values: 19 us with one CTA each)
+  const int64_t work = (int64_t)d.M * d.Hkv * d.D * (d.kv_dtype == SPEC_BF16 ? 2 : 4) / 16;
+  const int split = work <= 1024 ? 1 : work >= 8 * 1024 ? 8 : (int)(work / 1024);
+  PdlLaunch L(dim3(d.B, split), dim3(256), 0, st);
   cudaError_t e;
   if (d.kv_dtype == SPEC_BF16) {
     using T = __nv_bfloat16;
@@ -395,7 +401,19 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
   kv_append_launch(a, lay, st, launches);
 
   const size_t smem = attn_simt_smem_bytes(R, d.D);
-  const dim3 grid(lay.max_splits, d.Hkv, d.B);
+  // Key ranges: the layout's, or, with a window, of the fewer keys that a
+  // request then has at most, again for about eight CTAs per SM, in whole
+  // tiles, no more ranges than the partials' workspace holds.
+  int split_keys = lay.split_keys, splits = lay.max_splits;
+  if (a.window > 0) {
+    const int64_t most = min((int64_t)d.max_blocks * kBlock,
+                             (int64_t)ceil_div(a.sinks, kTileKeys) * kTileKeys + a.window + d.M +
+                                 kTileKeys);
+    const int64_t want = max((int64_t)kMinWinSplit, (int64_t)d.B * d.Hkv * most / 1216);
+    split_keys = (int)(ceil_div64(max(want, ceil_div64(most, lay.max_splits)), kTileKeys) * kTileKeys);
+    splits = (int)ceil_div64(most, split_keys);
+  }
+  const dim3 grid(splits, d.Hkv, d.B);
   const float qscale = a.scale * 1.4426950408889634f;
   cudaError_t e = cudaSuccess;
 #define SPECV_SIMT(DD, RPW)                                                                   \
@@ -408,7 +426,7 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
                                         static_cast<const T*>(a.k_cache),                     \
                                         static_cast<const T*>(a.v_cache), a.block_table,      \
                                         a.ctx_lens, a.parent, req_ok, d, a.window, a.sinks,   \
-                                        qscale, lay.split_keys, lay.max_splits, part);                \
+                                        qscale, split_keys, splits, part);                \
   } while (0)
   const int rpw = ceil_div(R, kSimtWarps);
   if (d.D == 128) {
@@ -427,8 +445,8 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
 #undef SPECV_SIMT
   ++*launches;
 
-  attn_combine_kernel<T><<<dim3(d.Hkv, d.B), 256, 0, st>>>(
-      part, a.ctx_lens, req_ok, d, a.window, a.sinks, lay.split_keys, lay.max_splits, static_cast<T*>(a.out), a.lse);
+  attn_combine_kernel<T><<<dim3(d.Hkv, ceil_div(R, 8), d.B), 256, 0, st>>>(
+      part, a.ctx_lens, req_ok, d, a.window, a.sinks, split_keys, splits, static_cast<T*>(a.out), a.lse);
   ++*launches;
   return cudaGetLastError();
 }
