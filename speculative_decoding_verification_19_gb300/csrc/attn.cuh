@@ -47,6 +47,26 @@ constexpr int kMaxAttnCtas = 512;
 // at index D, padded so every row starts on a 16-byte boundary.
 __host__ __device__ constexpr int tc_part_stride(int D) { return D + 4; }
 
+// Depth of new row n of a request, and the mask of its ancestors-or-self that
+// are fewer than `window` positions above it or among the sinks (par: the
+// request's checked topology, or NULL for a chain).
+__device__ __forceinline__ void win_row_mask(const int32_t* par, int n, int ctx, int window,
+                                             int sinks, ulonglong2* mask, int32_t* depth) {
+  int at = n;
+  if (par != nullptr) {
+    at = 0;
+    for (int k = n; k > 0 && at < kMaxNodes; k = par[k]) ++at;
+  }
+  unsigned long long lo = 0, hi = 0;
+  for (int k = n, dk = at; k >= 0 && dk >= 0; k = par != nullptr ? par[k] : k - 1, --dk) {
+    if (at - dk >= window && ctx + dk >= sinks) continue;
+    if (k < 64) lo |= 1ull << k;
+    else hi |= 1ull << (k - 64);
+  }
+  *mask = make_ulonglong2(lo, hi);
+  *depth = at;
+}
+
 size_t attn_simt_smem_bytes(int R, int D);
 size_t attn_tc_part_floats(const spec_dims& d);
 cudaError_t kv_append_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, int* launches);

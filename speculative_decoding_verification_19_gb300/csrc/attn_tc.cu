@@ -1095,21 +1095,9 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     // depth of each new row, and the mask of the ancestors-or-self that are
     // fewer than `window` positions above it or among the sinks
     const int32_t* par = parent != nullptr ? parent + (int64_t)b * M : nullptr;
-    for (int n = tid; n < M; n += blockDim.x) {
-      int depth = n;
-      if (par != nullptr) {
-        depth = 0;
-        for (int k = n; k > 0; k = par[k]) ++depth;
-      }
-      unsigned long long lo = 0, hi = 0;
-      for (int k = n, dk = depth; k >= 0; k = par != nullptr ? par[k] : k - 1, --dk) {
-        if (depth - dk >= window && ctx + dk >= sinks) continue;
-        if (k < 64) lo |= 1ull << k;
-        else hi |= 1ull << (k - 64);
-      }
-      anc_ws[(int64_t)b * M + n] = make_ulonglong2(lo, hi);
-      depth_ws[(int64_t)b * M + n] = depth;
-    }
+    for (int n = tid; n < M; n += blockDim.x)
+      win_row_mask(par, n, ctx, window, sinks, anc_ws + (int64_t)b * M + n,
+                   depth_ws + (int64_t)b * M + n);
   } else if (ok && parent != nullptr) {
     // ancestor-or-self mask of each tree row (the topology is valid here,
     // so every walk ends at the root within M steps)
