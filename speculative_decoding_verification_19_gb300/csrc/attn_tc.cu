@@ -99,6 +99,7 @@ constexpr int kPCol = kOCol + 128;  // P of S buffer k (bf16 pairs) at kPCol + 3
 // Split cost of one (request, head) segment, in tiles: the Q load, the
 // masks and the drain of the pipeline at a pair's end cost about this much.
 constexpr int kSegCost = 3;
+constexpr int kWinSegCost = 3;
 constexpr int kWinMinCost = 8;
 constexpr int kPrepThreads = 256;
 constexpr int kPlanReqs = 1024;  // requests whose plan arrays fit the prep kernel's shared memory
@@ -128,17 +129,18 @@ size_t smem_bytes() { return kSmemBytes; }
 // pair, with the request's record (ctx, tiles per head, next request with
 // tiles) and the next request's record loaded one request ahead, so that no
 // role waits for a global load when it crosses into a new request.
-// With a window (kWin) tiles are counted over the kept ones (sinks, then
-// window), and real() is a tile's place in the request.
+// With a window (kWin) tiles are counted over the kept pages (the sinks', then
+// the window's from its first page on), and page() is the place of a tile's
+// first page in the request.
 template <bool kWin>
 struct Cursor {
   int b, h, tile, nt, ctx, next_b;
   int4 nrec;
-  int ns, skip;  // sink tiles, tiles left out after them (kWin)
-  __device__ int real() const { return kWin && tile >= ns ? tile + skip : tile; }
-  __device__ int real_of(int j) const { return kWin && j >= ns ? j + skip : j; }
+  int ns, skip;  // sink tiles, pages left out after them (kWin)
+  __device__ int page() const { return page_of(tile); }
+  __device__ int page_of(int j) const { return j * kPages + (kWin && j >= ns ? skip : 0); }
   // the same for the next request
-  __device__ int next_real_of(int j) const { return kWin && j >= ns ? j + nrec.w : j; }
+  __device__ int next_page_of(int j) const { return j * kPages + (kWin && j >= ns ? nrec.w : 0); }
   // st0 = (first tile, b, h, tile), st1 = (ctx, tiles, next request, end tile)
   __device__ void start(int4 st0, int4 st1, const int4* rq, int B, int sinks) {
     ns = kWin ? ceil_div(sinks, kTileKeys) : 0;
@@ -233,9 +235,21 @@ __device__ __forceinline__ void chain_mask(int i, unsigned long long* lo, unsign
   *hi = i >= 127 ? ~0ull : (i >= 64 ? ((1ull << (i - 63)) - 1) : 0ull);
 }
 
-__device__ __forceinline__ int tile_pages(int L, int tile) {
-  const int keys = L - tile * kTileKeys;
+__device__ __forceinline__ int tile_pages(int L, int page) {
+  const int keys = L - page * kBlock;
   return keys >= kTileKeys ? kPages : ceil_div(keys, kBlock);
+}
+// With a window, a tile of the sinks that the window does not reach ends with
+// the sinks' last page.
+template <bool kWin>
+__device__ __forceinline__ int tile_pages_of(int L, int page, int ctx, int window, int sinks) {
+  const int np = tile_pages(L, page);
+  if (!kWin || page + kPages > win_first(ctx, window) / kBlock) return np;
+  return min(np, ceil_div(sinks, kBlock) - page);
+}
+// Pages left out between the sinks' tiles and the window's first page.
+__device__ __forceinline__ int win_skip_pages(int ctx, int window, int sinks) {
+  return max(0, win_first(ctx, window) / kBlock - ceil_div(sinks, kTileKeys) * kPages);
 }
 
 // 32 fp32 values (as bits) scaled and stored as bf16: a quarter row of out.
@@ -435,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
 #pragma unroll
           for (int p = 0; p < kPages; ++p) ids[p] = nids[p];
         } else {
-          const int page0 = cu.real_of((w << 5) + lane) * kPages;
+          const int page0 = cu.page_of((w << 5) + lane);
           const int32_t* bt = block_table + (int64_t)cu.b * d.max_blocks;
 #pragma unroll
           for (int p = 0; p < kPages; ++p) ids[p] = (page0 + p < d.max_blocks) ? bt[page0 + p] : 0;
@@ -457,14 +471,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
           for (int p = 0; p < kPages; ++p) nids[p] = ids[p];
         } else if (nb < B) {
           const int nj = (nw << 5) + lane;
-          const int page0 = (nb == cu.b ? cu.real_of(nj) : cu.next_real_of(nj)) * kPages;
+          const int page0 = nb == cu.b ? cu.page_of(nj) : cu.next_page_of(nj);
           const int32_t* bt = block_table + (int64_t)nb * d.max_blocks;
 #pragma unroll
           for (int p = 0; p < kPages; ++p) nids[p] = (page0 + p < d.max_blocks) ? bt[page0 + p] : 0;
         }
       }
-      const int rt = cu.real();
-      const int np = tile_pages(L, rt);
+      const int pg = cu.page();
+      const int np = tile_pages_of<kWin>(L, pg, cu.ctx, window, sinks);
       const int src = cu.tile & 31;
       int blk[kPages];
 #pragma unroll
@@ -477,10 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
         break;
       }
       const uint32_t sb = ptx::smem_u32(stages + stage * kStageBytes);
-      const int kpos0 = rt * kTileKeys;
+      const int kpos0 = pg * kBlock;
       // with a window, pages that no row sees are not held: they read as zero
-      const bool held = !kWin || rt * kPages >= win_first(cu.ctx, window) / kBlock ||
-                        rt * kPages + kPages <= ceil_div(sinks, kBlock);
+      const bool held = !kWin || pg >= win_first(cu.ctx, window) / kBlock ||
+                        pg + kPages <= ceil_div(sinks, kBlock);
       if (kpos0 + kTileKeys <= cu.ctx && held) {  // all keys in the cached prefix
 #pragma unroll
         for (int p = 0; p < kPages; ++p) {
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
             const int64_t page = ((int64_t)blk[p] * Hkv + cu.h) * kBlock * 128 + c16 * 8;
             const int pos0 = kpos0 + p * kBlock;
             const uint32_t so0 = swz_half + (uint32_t)p * kBoxBytes;
-            const bool have = !kWin || win_page(rt * kPages + p, cu.ctx, window, sinks);
+            const bool have = !kWin || win_page(pg + p, cu.ctx, window, sinks);
             if (have && pos0 + kBlock <= cu.ctx) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -589,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
                                            wait))
           break;
         ptx::tc_fence_after();
-        const int np = tile_pages(L, cu.real());
+        const int np = tile_pages_of<kWin>(L, cu.page(), cu.ctx, window, sinks);
         const uint32_t idqk = np == kPages ? id_qk_full : ptx::idesc_bf16_f32(128, np * 16, false, false);
         const uint64_t dq = dq0 + (uint64_t)((qb * kQBytes) >> 4);
         const uint64_t dk = dk0 + (uint64_t)((stage * kStageBytes) >> 4);
@@ -624,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
       for (int64_t g = g0; g < g1; ++g, ++u) {
         const bool first = (g == g0) || cu.tile == 0;
         if (first) L = cu.ctx + M;
-        const int np = tile_pages(L, cu.real());
+        const int np = tile_pages_of<kWin>(L, cu.page(), cu.ctx, window, sinks);
         const int sbuf = (int)(u % kSBufs);
         const int stage = (int)(u % kStages);
         if (!ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->p_full[sbuf]), (uint32_t)((u / kSBufs) & 1), abort,
@@ -705,9 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
                                                      (uint32_t)((t / kSBufs) & 1), abort, wait)))
           break;
         ptx::tc_fence_after();
-        const int rt = cu.real();
-        const int kpos0 = rt * kTileKeys;
-        const int nkeys = tile_pages(L, rt) * kBlock;
+        const int pg = cu.page();
+        const int kpos0 = pg * kBlock;
+        const int nkeys = tile_pages_of<kWin>(L, pg, cu.ctx, window, sinks) * kBlock;
         // tiles wholly inside the cached prefix need no mask; with a window,
         // those inside every row's window (a row's depth is at most M - 1) or
         // inside the sinks
@@ -715,6 +729,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
                            (!kWin || kpos0 >= L - window || kpos0 + kTileKeys <= sinks);
         const int jbase = half * 32;
         uint32_t vh = 0xffffffffu;  // visible keys of this half (non-plain tiles)
+        // groups of 8 columns of the tile that some row of the warp sees, and
+        // that every row sees (non-plain tiles): only the others are masked
+        // key by key
+        uint32_t some = 0, every = 0;
         uint32_t sv[32], so[32];
         ptx::tmem_ld32(lane_base + sbuf * kTileKeys + jbase, sv);
         ptx::tmem_ld32(lane_base + sbuf * kTileKeys + (jbase ^ 32), so);
@@ -751,17 +769,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
                       : tile_visibility(kpos0, nkeys, ctx, L, anc, real);
           vh = (uint32_t)(vis >> jbase);
           const uint32_t vo = (uint32_t)(vis >> (jbase ^ 32));
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t bh = (vh >> (8 * g)) & 0xffu, bo = (vo >> (8 * g)) & 0xffu;
+            some |= (__any_sync(0xffffffffu, bh != 0) ? 1u : 0u) << g;
+            some |= (__any_sync(0xffffffffu, bo != 0) ? 16u : 0u) << g;
+            every |= (__all_sync(0xffffffffu, bh == 0xffu || !real) ? 1u : 0u) << g;
+            every |= (__all_sync(0xffffffffu, bo == 0xffu || !real) ? 16u : 0u) << g;
+          }
           float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            a0 = fmaxf(a0, (vh >> j) & 1u ? __uint_as_float(sv[j]) : -INFINITY);
-            a1 = fmaxf(a1, (vh >> (j + 1)) & 1u ? __uint_as_float(sv[j + 1]) : -INFINITY);
-          }
+          for (int g = 0; g < 8; ++g) {
+            const uint32_t(&sc)[32] = g < 4 ? sv : so;
+            const uint32_t vb = g < 4 ? vh : vo;
+            const int j0 = (g & 3) * 8;
+            if ((every >> g) & 1u) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            a0 = fmaxf(a0, (vo >> j) & 1u ? __uint_as_float(so[j]) : -INFINITY);
-            a1 = fmaxf(a1, (vo >> (j + 1)) & 1u ? __uint_as_float(so[j + 1]) : -INFINITY);
+              for (int j = j0; j < j0 + 8; j += 2) {
+                a0 = fmaxf(a0, __uint_as_float(sc[j]));
+                a1 = fmaxf(a1, __uint_as_float(sc[j + 1]));
+              }
+            } else if ((some >> g) & 1u) {
+#pragma unroll
+              for (int j = j0; j < j0 + 8; j += 2) {
+                a0 = fmaxf(a0, (vb >> j) & 1u ? __uint_as_float(sc[j]) : -INFINITY);
+                a1 = fmaxf(a1, (vb >> (j + 1)) & 1u ? __uint_as_float(sc[j + 1]) : -INFINITY);
+              }
+            }
           }
+          if (!real) a0 = a1 = -INFINITY;
           mt = fmaxf(a0, a1) * qscale2;
         }
         bool need = false;
@@ -809,18 +845,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
             pk[j] = ptx::pack_bf16x2(pa, pb);
           }
         } else {
-          const float nm = -m_used;  // finite whenever a key of the row is visible
+          // finite whenever a key of the row is visible
+          const float nm = real ? -m_used : -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float pa = (vh >> (2 * j)) & 1u
-                                 ? fast_exp2(fmaf(__uint_as_float(sv[2 * j]), qscale2, nm))
-                                 : 0.f;
-            const float pb = (vh >> (2 * j + 1)) & 1u
-                                 ? fast_exp2(fmaf(__uint_as_float(sv[2 * j + 1]), qscale2, nm))
-                                 : 0.f;
-            l0 += pa;
-            l1 += pb;
-            pk[j] = ptx::pack_bf16x2(pa, pb);
+          for (int g = 0; g < 4; ++g) {
+            const int j0 = g * 4;  // pairs of columns
+            if ((every >> g) & 1u) {
+#pragma unroll
+              for (int j = j0; j < j0 + 4; ++j) {
+                const float pa = fast_exp2(fmaf(__uint_as_float(sv[2 * j]), qscale2, nm));
+                const float pb = fast_exp2(fmaf(__uint_as_float(sv[2 * j + 1]), qscale2, nm));
+                l0 += pa;
+                l1 += pb;
+                pk[j] = ptx::pack_bf16x2(pa, pb);
+              }
+            } else if ((some >> g) & 1u) {
+#pragma unroll
+              for (int j = j0; j < j0 + 4; ++j) {
+                const float pa = (vh >> (2 * j)) & 1u
+                                     ? fast_exp2(fmaf(__uint_as_float(sv[2 * j]), qscale2, nm))
+                                     : 0.f;
+                const float pb = (vh >> (2 * j + 1)) & 1u
+                                     ? fast_exp2(fmaf(__uint_as_float(sv[2 * j + 1]), qscale2, nm))
+                                     : 0.f;
+                l0 += pa;
+                l1 += pb;
+                pk[j] = ptx::pack_bf16x2(pa, pb);
+              }
+            } else {
+#pragma unroll
+              for (int j = j0; j < j0 + 4; ++j) pk[j] = 0u;
+            }
           }
         }
         l += l0 + l1;
@@ -1115,8 +1170,9 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     if (!cap_ok) raise_status(status, SPEC_ERR_CAPACITY);
     if (bad_block) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
     if (bad_topo) raise_status(status, SPEC_ERR_INVALID_ARG);
-    ntiles[b] = ok ? (int)ceil_div64(L, kTileKeys) -
-                         (kWin ? win_skip(ctx, window, sinks, kTileKeys) : 0)
+    ntiles[b] = ok ? (int)ceil_div64(ceil_div64(L, kBlock) -
+                                         (kWin ? win_skip_pages(ctx, window, sinks) : 0),
+                                     kPages)
                    : 0;
     __threadfence();
     s_last = atomicAdd(arrivals, 1u) == (uint32_t)(B - 1);
@@ -1142,6 +1198,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
   // Up to kPlanReqs requests the plan's per-request arrays live in shared
   // memory (no global round trips after the first load), beyond that in the
   // workspace.
+  const int seg = kWin ? kWinSegCost : kSegCost;
   const bool small = B <= kPlanReqs;
   int64_t* tpre = small ? s_tpre : pre;          // [B+1] tiles before request r
   int64_t* cpre = small ? s_cpre : pre + B + 1;  // [B+1] split cost before request r
@@ -1151,7 +1208,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     const int r = base + tid;
     const int nt = r < B ? __ldcg(ntiles + r) : 0;
     const int cx = r < B ? ctx_lens[r] : 0;
-    int64_t vt = (int64_t)nt * Hkv, vc = nt > 0 ? (int64_t)Hkv * (nt + kSegCost) : 0;
+    int64_t vt = (int64_t)nt * Hkv, vc = nt > 0 ? (int64_t)Hkv * (nt + seg) : 0;
     int vm = nt > 0 ? r : -1;
     int64_t tt, tcst;
     int tm;
@@ -1160,7 +1217,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     if (r < B) {
       tpre[r] = carry_t + vt;
       cpre[r] = carry_c + vc;
-      rq[r] = make_int4(cx, nt, B, kWin ? win_skip(cx, window, sinks, kTileKeys) : 0);
+      rq[r] = make_int4(cx, nt, B, kWin ? win_skip_pages(cx, window, sinks) : 0);
       if (small) {
         s_nt[r] = nt;
         s_ctx[r] = cx;
@@ -1216,11 +1273,11 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
       else hi = mid;
     }
     const int nt = small ? s_nt[r] : __ldcg(ntiles + r);
-    const int64_t per = nt + kSegCost;
+    const int64_t per = nt + seg;
     int64_t rem = at - cpre[r];
     const int h = (int)(rem / per);
     rem -= h * per;
-    const int j = (int)max((int64_t)0, rem - kSegCost);  // rem < nt + kSegCost: j < nt
+    const int j = (int)max((int64_t)0, rem - seg);  // rem < nt + seg: j < nt
     const int g0 = (int)(tpre[r] + (int64_t)h * nt + j);
     starts[2 * k] = make_int4(g0, r, h, j);
     s_g0[k] = g0;
