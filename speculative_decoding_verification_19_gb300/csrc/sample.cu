@@ -43,9 +43,10 @@
 //       holds u Z walks its run in order
 // Measured (queued calls, us): 640 rows of 152064 bf16 logits, temperature
 // alone, 75 (195 MB: 29 at the copy rate; the stream 54, the marked rows 21);
-// 33 rows of 32001 fp32 logits with mixed filters 33 (57 before step 2a); one
-// row of 32000: 9 without filters, 16 with top-k 50, 20 with top-p 0.9.  A
-// filtered row is bound by its chain of barriers, not by bytes.
+// 33 rows of 32001 fp32 logits with mixed filters 28 (44 by the selects over
+// the cluster alone); one row of 32000: 9 without filters, 13 with top-k 50,
+// 18 with top-p 0.9.  A filtered row is bound by its chain of barriers, not by
+// bytes; the slowest are rows whose top-p reaches past the candidates.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -64,7 +65,7 @@ constexpr int kBinBits = 9;
 constexpr int kBins = 1 << kBinBits;  // one per thread
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // order key of -inf
 constexpr int kUnroll = 4;
-constexpr size_t kMaxSliceBytes = 160 * 1024;
+constexpr size_t kMaxSharedBytes = 224 * 1024;  // static and dynamic, of an SM's CTAs
 
 // 2^(j/32) as hi + lo
 __device__ const float2 kPow2[32] = {
@@ -96,7 +97,7 @@ struct DrawShared {
 
 struct Shared {
   DrawShared draw;
-  uint32_t hist[2][4][kBins];  // counts, then the masses' three 14-bit limbs
+  alignas(16) uint32_t hist[2][4][kBins];  // counts, then the masses' three 14-bit limbs
   float ex_max[kMaxCluster];
   uint32_t ex_bad[kMaxCluster], ex_theta[kMaxCluster], ex_low[kMaxCluster];
   float2 ex_z[kMaxCluster];
@@ -218,6 +219,35 @@ struct Slice {
   __device__ __forceinline__ uint4 get(int v) const { return kSmem ? sm[v] : load(v); }
 };
 
+// Inclusive running sums of a count and a mass over the CTA's threads.
+__device__ __forceinline__ void block_running(Shared& sh, uint32_t& c, long long& m, bool with_mass) {
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+#pragma unroll
+  for (int o = 1; o < kWarp; o <<= 1) {
+    const uint32_t yc = __shfl_up_sync(0xffffffffu, c, o);
+    if (lane >= o) c += yc;
+    if (with_mass) {
+      const long long ym = __shfl_up_sync(0xffffffffu, m, o);
+      if (lane >= o) m += ym;
+    }
+  }
+  if (lane == kWarp - 1) {
+    sh.scan_cnt[warp] = c;
+    sh.scan_mass[warp] = m;
+  }
+  __syncthreads();
+  // the sums of the warps before, lane w holding warp w's
+  uint32_t wc = lane < warp ? sh.scan_cnt[lane] : 0;
+  wc = __reduce_add_sync(0xffffffffu, wc);
+  c += wc;
+  if (with_mass) {
+    long long wm = lane < warp ? sh.scan_mass[lane] : 0;
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) wm += __shfl_xor_sync(0xffffffffu, wm, o);
+    m += __shfl_sync(0xffffffffu, wm, 0);
+  }
+}
+
 struct Selected {
   bool found;
   uint32_t tau;   // order key of the threshold
@@ -239,7 +269,7 @@ __device__ Selected radix_select(Shared& sh, const Slice<T, kSmem>& sl, int nv, 
                                  long long rank, long long mass, int C, int& buf) {
   constexpr int kVec = Slice<T, kSmem>::kVec;
   constexpr int kShift = sizeof(T) == 2 ? 16 : 0;  // bits that a key of this type does not use
-  const int tid = threadIdx.x, lane = tid % kWarp;
+  const int tid = threadIdx.x;
   cg::cluster_group cluster = cg::this_cluster();
   Selected r{true, 0, 0, 0, 0};
   if (low <= kKeyNegInf) low = kKeyNegInf + 1;
@@ -286,24 +316,7 @@ __device__ Selected radix_select(Shared& sh, const Slice<T, kSmem>& sl, int nv, 
     }
     uint32_t ci = cnt;
     long long mi = ms;
-#pragma unroll
-    for (int o = 1; o < kWarp; o <<= 1) {
-      const uint32_t yc = __shfl_up_sync(0xffffffffu, ci, o);
-      const long long ym = __shfl_up_sync(0xffffffffu, mi, o);
-      if (lane >= o) {
-        ci += yc;
-        mi += ym;
-      }
-    }
-    if (lane == kWarp - 1) {
-      sh.scan_cnt[tid / kWarp] = ci;
-      sh.scan_mass[tid / kWarp] = mi;
-    }
-    __syncthreads();
-    for (int w = 0; w < tid / kWarp; ++w) {
-      ci += sh.scan_cnt[w];
-      mi += sh.scan_mass[w];
-    }
+    block_running(sh, ci, mi, with_mass);
     const long long before = by_mass ? r.mass + mi - ms : (long long)r.above + ci - cnt;
     const long long upto = by_mass ? r.mass + mi : (long long)r.above + ci;
     const long long want = by_mass ? mass : rank;
@@ -548,16 +561,25 @@ __device__ __forceinline__ long long block_max(Shared& sh, long long v) {
 // the candidates of a filtered row in one CTA
 // ---------------------------------------------------------------------------
 // When few tokens can matter they are sent to the cluster's first CTA (at
-// most kListCap from each), and the filters and the draw run there on
+// most kListCap / C from each), and the filters and the draw run there on
 // registers: a level of the select is then a few block barriers, where one
 // over the cluster's slices costs a cluster barrier and 32 remote loads a
 // thread.  Masses are 40-bit fractions in two limbs of 20 bits (the limbs of
-// 4096 weights add up in 32 bits).
-constexpr int kListCap = 512;
-// Of a CTA's 512 threads' maxima, how many reach the lower bound of the
-// candidates: 256 leave about 355 candidates (512 ln 2, the more tokens a
-// thread has), 300 about 450 of the 512 that fit.
-constexpr int kListNeedK = 256, kListNeedP = 300;
+// up to 4096 weights add up in 32 bits).
+// candidates of a row; a CTA has its share of the places (28 KB: two CTAs with
+// a quarter of 128k bf16 logits each fit an SM)
+constexpr int kListCap = 7 * kThreads;
+constexpr int kListEach = kListCap / kThreads;  // of a thread of the first CTA
+// Of a CTA's 512 threads' maxima, how many have to reach the candidates' lower
+// bound: n of them leave about 512 ln(512 / (512 - n)) candidates, the more
+// tokens a thread has.  For top-p as many as fill seven eighths of the CTA's
+// places; for top-k the count asked for, up to the one that fills two thirds.
+__device__ __forceinline__ int list_need_p(int C) {
+  return C == 8 ? 274 : C == 4 ? 401 : C == 2 ? 488 : 511;
+}
+__device__ __forceinline__ int list_most_k(int C) {
+  return C == 8 ? 226 : C == 4 ? 352 : C == 2 ? 462 : 507;
+}
 
 struct Picked {
   bool found;
@@ -579,24 +601,19 @@ __device__ __forceinline__ long long pair_value(uint32_t hi, uint32_t lo) {
 
 // Among the CTA's keys (those of bit i in `active`, all in [base, base +
 // 2^bits)), in descending order: the key of rank `want`, or at which the
-// running mass reaches `want`.
-__device__ Picked list_select(Shared& sh, const uint32_t (&key)[kMaxCluster],
-                              const uint32_t (&mh)[kMaxCluster], const uint32_t (&ml)[kMaxCluster],
+// running mass reaches `want`.  sh.hist[buf] is zero on entry, and on return.
+__device__ Picked list_select(Shared& sh, const uint32_t (&key)[kListEach],
+                              const uint32_t (&mh)[kListEach], const uint32_t (&ml)[kListEach],
                               uint32_t active, uint32_t base, int bits, bool by_mass,
-                              long long want) {
-  const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
-  uint32_t(&hist)[4][kBins] = sh.hist[0];
+                              long long want, int& buf) {
+  const int tid = threadIdx.x;
   Picked r{true, 0, 0, 0, 0};
   do {
+    uint32_t(&hist)[4][kBins] = sh.hist[buf];
     const int sh_bits = max(0, bits - kBinBits);
     const uint32_t span = bits < 32 ? (1u << bits) - 1 : ~0u;
-    hist[0][tid] = 0;
-    hist[1][tid] = 0;
-    hist[2][tid] = 0;
-    __syncthreads();
-    if (tid == 0) sh.sel_bin = -1;  // the last level's sel_* are read
 #pragma unroll
-    for (int i = 0; i < kMaxCluster; ++i) {
+    for (int i = 0; i < kListEach; ++i) {
       const uint32_t at = key[i] - base;
       if (((active >> i) & 1u) && at <= span) {
         const uint32_t bin = at >> sh_bits;
@@ -605,30 +622,17 @@ __device__ Picked list_select(Shared& sh, const uint32_t (&key)[kMaxCluster],
         if (ml[i] != 0) atomicAdd(&hist[2][bin], ml[i]);
       }
     }
+    if (tid == 0) sh.sel_bin = -1;  // the last level's sel_* are read: its last barrier but one
     __syncthreads();
     const int bin = kBins - 1 - tid;
     const uint32_t cnt = hist[0][bin];
     const long long ms = pair_value(hist[1][bin], hist[2][bin]);
+    hist[0][bin] = 0;
+    hist[1][bin] = 0;
+    hist[2][bin] = 0;
     uint32_t ci = cnt;
     long long mi = ms;
-#pragma unroll
-    for (int o = 1; o < kWarp; o <<= 1) {
-      const uint32_t yc = __shfl_up_sync(0xffffffffu, ci, o);
-      const long long ym = __shfl_up_sync(0xffffffffu, mi, o);
-      if (lane >= o) {
-        ci += yc;
-        mi += ym;
-      }
-    }
-    if (lane == kWarp - 1) {
-      sh.scan_cnt[warp] = ci;
-      sh.scan_mass[warp] = mi;
-    }
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-      ci += sh.scan_cnt[w];
-      mi += sh.scan_mass[w];
-    }
+    block_running(sh, ci, mi, true);
     const long long before = by_mass ? r.mass + mi - ms : (long long)r.above + ci - cnt;
     const long long upto = by_mass ? r.mass + mi : (long long)r.above + ci;
     if (before < want && want <= upto) {
@@ -638,37 +642,125 @@ __device__ Picked list_select(Shared& sh, const uint32_t (&key)[kMaxCluster],
       sh.sel_count = cnt;
     }
     __syncthreads();
-    if (sh.sel_bin < 0) {
+    const int got = sh.sel_bin;
+    const uint32_t above = sh.sel_above, count = sh.sel_count;
+    const long long mass = sh.sel_mass;
+    buf ^= 1;
+    __syncthreads();  // sel_* are read
+    if (got < 0) {
       r.found = false;
       return r;
     }
-    r.above += sh.sel_above;
-    r.mass += sh.sel_mass;
-    r.ties = sh.sel_count;
-    base += (uint32_t)sh.sel_bin << sh_bits;
+    r.above += above;
+    r.mass += mass;
+    r.ties = count;
+    base += (uint32_t)got << sh_bits;
     bits = sh_bits;
   } while (bits > 0);
   r.key = base;
   return r;
 }
 
+// The filters and the draw over a short list, n <= kShortList tokens: every
+// token is compared with every other, two threads a token, so that its rank
+// and the mass of the tokens before it (by value, then by index) come without
+// a select.  Two passes and a few barriers: n = 80 takes 3 us where the
+// selects below take 16.
+constexpr int kShortList = 256;
+
+__device__ void short_draw(Shared& sh, const uint2* list, const Law& law, int C, int n, int k,
+                           long long want_p, float tp, float mp, float u, const SampleArgs& a,
+                           int64_t row) {
+  static_assert(kThreads == 2 * kShortList, "two threads a token");
+  // token j: order key, index, mass; the list's places are dealt out in turn
+  uint4* tok = reinterpret_cast<uint4*>(&sh.hist[0][0][0]);
+  const int tid = threadIdx.x, e = tid >> 1, part = tid & 1;
+  uint32_t key = 0, idx = 0;
+  float x = 0.f;
+  dfloat w = df_make(0.f);
+  long long mass = 0;
+  if (e < n) {
+    int q = 0, at = e;
+    while (at >= sh.ex_n[q]) at -= sh.ex_n[q++];  // e < n: q stays below C
+    const uint2 t = list[q * (kListCap / C) + at];
+    x = __uint_as_float(t.x);
+    key = order_key(x);
+    idx = t.y;
+    w = law.weight(x);
+    uint32_t hi, lo;
+    fixed_pair(w, hi, lo);
+    mass = pair_value(hi, lo);
+    if (part == 0) tok[e] = make_uint4(key, idx, (uint32_t)mass, (uint32_t)(mass >> 32));
+  }
+  __syncthreads();
+  const int j0 = part * (kShortList / 2), j1 = min(n, j0 + kShortList / 2);
+  int rank = 0;
+  long long before = 0, all = 0;
+  for (int j = j0; j < j1; ++j) {
+    const uint4 o = tok[j];
+    const long long m = (long long)o.z | ((long long)o.w << 32);
+    const bool first = o.x > key || (o.x == key && o.y < idx);
+    rank += first;
+    if (first) before += m;
+    all += m;
+  }
+  rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+  before += __shfl_xor_sync(0xffffffffu, before, 1);
+  all += __shfl_xor_sync(0xffffffffu, all, 1);
+  if (tp < 1.f && want_p == 0) {  // the mass of the first k, from the token of rank k - 1
+    if (e < n && part == 0 && rank == k - 1) sh.sel_mass = before + mass;
+    __syncthreads();
+    want_p = mass_target(tp, n >= k ? sh.sel_mass : all);
+  }
+  const bool keep = e < n && (k == 0 || rank < k) && (tp >= 1.f || before < want_p) &&
+                    (w.hi - mp) + w.lo >= 0.f;
+  const long long kept = keep ? mass : 0;
+  __syncthreads();  // tok is read
+  if (e < n && part == 0) tok[e] = make_uint4(0, idx, (uint32_t)kept, (uint32_t)(kept >> 32));
+  __syncthreads();
+  long long z = 0;
+  before = 0;
+  for (int j = j0; j < j1; ++j) {
+    const uint4 o = tok[j];
+    const long long m = (long long)o.z | ((long long)o.w << 32);
+    if (o.y < idx) before += m;
+    z += m;
+  }
+  before += __shfl_xor_sync(0xffffffffu, before, 1);
+  z += __shfl_xor_sync(0xffffffffu, z, 1);
+  const long long past = __double2ll_rd((double)u * (double)z);
+  if (part == 0 && kept > 0 && before <= past && past < before + kept) {
+    a.out_tokens[row] = (int)idx;
+    if (a.out_prob != nullptr) a.out_prob[row] = w.hi / ((float)z * 0x1p-40f);
+  }
+}
+
 // The filters and the draw over the list (the first CTA; n[q] tokens (value,
-// index) of CTA q at list[q * kListCap]).
+// index) of CTA q at list[q * (kListCap / C)]).
 template <typename T>
 __device__ void list_draw(Shared& sh, const uint2* list, const Law& law, int C, int k, bool has_k,
                           long long want_p, float tp, float mp, float u, uint32_t low,
                           const SampleArgs& a, int64_t row) {
   constexpr int kShift = sizeof(T) == 2 ? 16 : 0;
   const int tid = threadIdx.x;
-  uint32_t key[kMaxCluster], idx[kMaxCluster], mh[kMaxCluster], ml[kMaxCluster];
-  float x[kMaxCluster];
+  int n = 0, buf = 0;
+  for (int q = 0; q < C; ++q) n += sh.ex_n[q];
+  if (n <= kShortList) {
+    short_draw(sh, list, law, C, n, has_k ? k : 0, want_p, tp, mp, u, a, row);
+    return;
+  }
+  for (int i = tid; i < 2 * 4 * kBins; i += kThreads) (&sh.hist[0][0][0])[i] = 0;
+  __syncthreads();
+  uint32_t key[kListEach], idx[kListEach], mh[kListEach], ml[kListEach];
+  float x[kListEach];
   uint32_t active = 0;
 #pragma unroll
-  for (int q = 0; q < kMaxCluster; ++q) {
+  for (int q = 0; q < kListEach; ++q) {
     key[q] = idx[q] = mh[q] = ml[q] = 0;
     x[q] = 0.f;
-    if (q < C && tid < sh.ex_n[q]) {
-      const uint2 e = list[q * kListCap + tid];
+    const int at = q * kThreads + tid, cta = at / (kListCap / C);
+    if (at % (kListCap / C) < sh.ex_n[cta]) {
+      const uint2 e = list[at];
       x[q] = __uint_as_float(e.x);
       idx[q] = e.y;
       key[q] = order_key(x[q]) >> kShift;
@@ -682,14 +774,14 @@ __device__ void list_draw(Shared& sh, const uint2* list, const Law& law, int C, 
   int keep_ties = 0, ties = 0;  // kept of the tokens at tau, all of them (tau 0: every token)
   long long each = 0;
   if (has_k) {
-    const Picked s = list_select(sh, key, mh, ml, active, base, bits, false, k);
+    const Picked s = list_select(sh, key, mh, ml, active, base, bits, false, k, buf);
     if (s.found) {
       tau = s.key;
       ties = (int)s.ties;
       keep_ties = k - (int)s.above;
       if (tp < 1.f) {
 #pragma unroll
-        for (int q = 0; q < kMaxCluster; ++q)
+        for (int q = 0; q < kListEach; ++q)
           if (((active >> q) & 1u) && key[q] == tau) each = pair_value(mh[q], ml[q]);
         each = block_max(sh, each);
         want_p = mass_target(tp, s.mass + each * keep_ties);
@@ -701,18 +793,18 @@ __device__ void list_draw(Shared& sh, const uint2* list, const Law& law, int C, 
     } else if (tp < 1.f) {  // fewer tokens than k: all of them
       long long z = 0;
 #pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) z += pair_value(mh[q], ml[q]);
+      for (int q = 0; q < kListEach; ++q) z += pair_value(mh[q], ml[q]);
       want_p = mass_target(tp, block_sum(sh, z));
     }
   }
   if (want_p > 0) {
-    const Picked s = list_select(sh, key, mh, ml, active, base, bits, true, want_p);
+    const Picked s = list_select(sh, key, mh, ml, active, base, bits, true, want_p, buf);
     if (s.found) {
       tau = s.key;
       ties = (int)s.ties;
       each = 0;
 #pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q)
+      for (int q = 0; q < kListEach; ++q)
         if (((active >> q) & 1u) && key[q] == tau) each = pair_value(mh[q], ml[q]);
       each = block_max(sh, each);
       keep_ties = ties_for(want_p - s.mass, each, ties);
@@ -720,20 +812,21 @@ __device__ void list_draw(Shared& sh, const uint2* list, const Law& law, int C, 
   }
   // kept: above tau, and at tau the first keep_ties by index
   uint32_t cut = ~0u;
-  constexpr uint32_t kTop = kSampleMaxVocab - 1;  // descending keys of ascending indices
-  uint32_t back[kMaxCluster];
+  const uint32_t kTop = a.V - 1;  // descending keys of ascending indices
+  const int idx_bits = 32 - __clz(kTop);
+  uint32_t back[kListEach];
 #pragma unroll
-  for (int q = 0; q < kMaxCluster; ++q) back[q] = kTop - idx[q];
+  for (int q = 0; q < kListEach; ++q) back[q] = kTop - idx[q];
   if (keep_ties < ties) {
     uint32_t at_tau = 0;
 #pragma unroll
-    for (int q = 0; q < kMaxCluster; ++q)
+    for (int q = 0; q < kListEach; ++q)
       if (((active >> q) & 1u) && key[q] == tau) at_tau |= 1u << q;
-    cut = kTop - list_select(sh, back, mh, ml, at_tau, 0, 20, false, keep_ties).key;
+    cut = kTop - list_select(sh, back, mh, ml, at_tau, 0, idx_bits, false, keep_ties, buf).key;
   }
   long long z = 0;
 #pragma unroll
-  for (int q = 0; q < kMaxCluster; ++q) {
+  for (int q = 0; q < kListEach; ++q) {
     const dfloat w = law.weight(x[q]);
     const bool keep = ((active >> q) & 1u) && (key[q] > tau || (key[q] == tau && idx[q] <= cut)) &&
                       (w.hi - mp) + w.lo >= 0.f;
@@ -742,9 +835,9 @@ __device__ void list_draw(Shared& sh, const uint2* list, const Law& law, int C, 
   }
   z = block_sum(sh, z);
   const long long past = __double2ll_rd((double)u * (double)z) + 1;  // C_i > u Z
-  const Picked s = list_select(sh, back, mh, ml, active, 0, 20, true, past);
+  const Picked s = list_select(sh, back, mh, ml, active, 0, idx_bits, true, past, buf);
 #pragma unroll
-  for (int q = 0; q < kMaxCluster; ++q) {
+  for (int q = 0; q < kListEach; ++q) {
     if (((active >> q) & 1u) && back[q] == s.key) {
       a.out_tokens[row] = (int)idx[q];
       if (a.out_prob != nullptr)
@@ -818,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
   // lower bound of the tokens that can matter: the largest 16-bit key that at
   // least `need` of the threads' maxima reach
   uint32_t theta = 0;
-  const int need = has_k ? ceil_div(k, C) : kListNeedP;
+  const int need = has_k ? ceil_div(k, C) : list_need_p(C);
   if (valid && (has_k || has_p)) {
     if (need <= kThreads) {
       const uint32_t key = order_key(tmax) >> 16;
@@ -881,12 +974,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
   const Law law(m, T_, sh.draw.pow2);
 
   // ---- 2a: few candidates go to the first CTA, which finishes the row
-  const bool want_list = has_k ? need <= kListNeedK : has_p;
+  dfloat total = df_make(0.f);  // mass of every token (top-p without top-k)
+  const bool want_list = has_k ? need <= list_most_k(C) : has_p;
+  const int places = kListCap / C;
   if (want_list) {
     if (tid == 0) sh.n_list = 0;
     __syncthreads();
     uint2* list = reinterpret_cast<uint2*>(data + (kSmem ? nv : 0));
-    uint2* to = cluster.map_shared_rank(list, 0) + rank * kListCap;
+    uint2* to = cluster.map_shared_rank(list, 0) + rank * places;
     const uint32_t low = max(theta, kKeyNegInf + 1);
     dfloat z = df_make(0.f);
     long long mass = 0;
@@ -926,7 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
           if (order_key(x[i]) >= low) {
-            if (at < kListCap)
+            if (at < places)
               to[at] = make_uint2(__float_as_uint(x[i]), rank * slice + v * kVec - sl.off + i);
             ++at;
           }
@@ -951,10 +1046,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
     z = df_make(0.f);
     mass = 0;
     for (int q = 0; q < C; ++q) {
-      fits &= sh.ex_n[q] <= kListCap;
+      fits &= sh.ex_n[q] <= places;
       z = df_add(z, dfloat{sh.ex_z[q].x, sh.ex_z[q].y});
       mass += sh.ex_mass[q];
     }
+    total = z;
     const long long want =
         has_k ? 0 : mass_target(tp, __float2ll_rn(z.hi * 0x1p40f) + __float2ll_rn(z.lo * 0x1p40f));
     if (fits && mass >= want) {  // the same in every CTA
@@ -990,30 +1086,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
     }
   }
   if (has_p && tau == kKeyNegInf) {  // no top-k, or fewer tokens than k
-    dfloat z = df_make(0.f);
-    for (int v = tid; v < nv; v += kThreads) {
-      const uint4 raw = sl.get(v);
-      float x[kVec];
-      unpack16(raw, x);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const dfloat w = law.weight(x[i]);
-        const dfloat s = df_two_sum(z.hi, w.hi);
-        z.hi = s.hi;
-        z.lo += s.lo + w.lo;
-      }
-    }
-    z = df_warp_sum(df_norm(z.hi, z.lo));
-    if (lane == 0) sh.draw.mass[warp] = make_float2(z.hi, z.lo);
-    __syncthreads();
-    if (tid < C) {
+    // the mass of every token: known from 2a, or formed here
+    dfloat z = total;
+    if (has_k) {
       z = df_make(0.f);
-      for (int w = 0; w < kWarps; ++w) z = df_add(z, dfloat{sh.draw.mass[w].x, sh.draw.mass[w].y});
-      *cluster.map_shared_rank(&sh.ex_z[rank], tid) = make_float2(z.hi, z.lo);
+      for (int v = tid; v < nv; v += kThreads) {
+        const uint4 raw = sl.get(v);
+        float x[kVec];
+        unpack16(raw, x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          const dfloat w = law.weight(x[i]);
+          const dfloat s = df_two_sum(z.hi, w.hi);
+          z.hi = s.hi;
+          z.lo += s.lo + w.lo;
+        }
+      }
+      z = df_warp_sum(df_norm(z.hi, z.lo));
+      if (lane == 0) sh.draw.mass[warp] = make_float2(z.hi, z.lo);
+      __syncthreads();
+      if (tid < C) {
+        z = df_make(0.f);
+        for (int w = 0; w < kWarps; ++w) z = df_add(z, dfloat{sh.draw.mass[w].x, sh.draw.mass[w].y});
+        *cluster.map_shared_rank(&sh.ex_z[rank], tid) = make_float2(z.hi, z.lo);
+      }
+      cluster_sync();
+      z = df_make(0.f);
+      for (int q = 0; q < C; ++q) z = df_add(z, dfloat{sh.ex_z[q].x, sh.ex_z[q].y});
     }
-    cluster_sync();
-    z = df_make(0.f);
-    for (int q = 0; q < C; ++q) z = df_add(z, dfloat{sh.ex_z[q].x, sh.ex_z[q].y});
     const long long zi = __float2ll_rn(z.hi * 0x1p42f) + __float2ll_rn(z.lo * 0x1p42f);
     const long long want = mass_target(tp, zi);
     // first the tokens that no thread's maximum is below, if they hold enough
@@ -1528,7 +1628,7 @@ static cudaError_t launch_t(const SampleArgs& a, cudaStream_t st, int* launches)
     C = kMaxCluster;
     const int vecs = vecs_of(C, kWarps);
     const size_t bytes = (size_t)kWarps * vecs * 16;
-    const bool fits = bytes <= kMaxSliceBytes;
+    const bool fits = bytes + sizeof(MarkedShared) <= kMaxSharedBytes;
     auto kern = fits ? sample_marked_kernel<T, true> : sample_marked_kernel<T, false>;
     const size_t smem = fits ? bytes : 0;
     const cudaError_t e =
@@ -1538,23 +1638,42 @@ static cudaError_t launch_t(const SampleArgs& a, cudaStream_t st, int* launches)
     ++*launches;
     return cudaLaunchKernelEx(&L.cfg, kern, a, C, slice_of(C), vecs);
   }
-  // CTAs per row: slices of at least 8 KB.  Fewer CTAs for many rows were no
-  // faster (256 rows of 128256 bf16 logits: top-k 50 in 117 us with 8 CTAs a
-  // row, 124 us with 4)
-  while (C < kMaxCluster && ceil_div64(a.V, C) * (int)sizeof(T) > 8192) C *= 2;
-  const int slice = ceil_div(ceil_div(a.V, C), kVec) * kVec;
+  // CTAs per row: those of the least estimated time.  A row takes about 12 us
+  // for its chain of barriers, and for each KB of a slice 0.05 us with top-k
+  // alone and about 0.2 where every token is weighted (top-p, min-p).  An SM
+  // holds two CTAs, or one when their shared memory is over half of it, and a
+  // cluster stays inside one of eight parts of 19 SMs.  (33 rows of 32001 fp32
+  // logits, top-k 50: 24 us with 8 CTAs a row, which makes two waves, 18 with
+  // 4; 33 rows of 128256 bf16, top-p 0.9: 45 us with 8, 61 with 2; 256 of them,
+  // top-k 50: 122 us with 8, 78 with 2.)
+  auto slice_of = [&](int c) { return ceil_div(ceil_div(a.V, c), kVec) * kVec; };
   // a row may start anywhere in a 16-byte vector: up to one more vector
-  const int warp_vecs = ceil_div(slice / kVec + 1, kWarps);
-  const size_t bytes = (size_t)kWarps * warp_vecs * 16;
-  const bool fits = bytes <= kMaxSliceBytes;
+  auto vecs_of = [&](int c) { return ceil_div(slice_of(c) / kVec + 1, kWarps); };
+  const size_t list = sizeof(uint2) * kListCap;
+  const int64_t per_kb = a.top_p == nullptr && a.min_p == nullptr ? 50 : 200;
+  C = kMaxCluster;
+  int64_t best = INT64_MAX;
+  for (int c = kMaxCluster; c >= 1; c /= 2) {
+    const size_t bytes = (size_t)kWarps * vecs_of(c) * 16, all = bytes + list + sizeof(Shared);
+    if (all > kMaxSharedBytes) break;
+    const int per_sm = 2 * (all + 1024) <= 228 * 1024 ? 2 : 1;
+    const int64_t waves = ceil_div64(a.rows, 8 * (19 * per_sm / c));
+    const int64_t ns = waves * (12000 + per_kb * (int64_t)(bytes / 1024));
+    if (ns < best) {
+      best = ns;
+      C = c;
+    }
+  }
+  const bool fits = best != INT64_MAX;
+  const int warp_vecs = vecs_of(C);
   auto kern = fits ? sample_kernel<T, true> : sample_kernel<T, false>;
-  const size_t smem = (fits ? bytes : 0) + sizeof(uint2) * kMaxCluster * kListCap;
+  const size_t smem = (fits ? (size_t)kWarps * warp_vecs * 16 : 0) + list;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   ClusterLaunch L(a.rows, C, kThreads, smem, st);
   ++*launches;
-  return cudaLaunchKernelEx(&L.cfg, kern, a, C, slice, warp_vecs);
+  return cudaLaunchKernelEx(&L.cfg, kern, a, C, slice_of(C), warp_vecs);
 }
 
 }  // namespace smp
