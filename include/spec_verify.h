@@ -3,7 +3,7 @@
  *
  * The verify step of speculative decoding (draft model proposes gamma tokens
  * or a tree of them; the target model checks them all in one forward) has
- * three data-parallel parts, and this library does exactly those:
+ * three data-parallel parts:
  *
  *   spec_verify_attn    append the new rows' K/V to a paged cache and run the
  *                       masked attention of the gamma+1 (or tree) queries;
@@ -11,7 +11,16 @@
  *                       accept/reject of each draft token, and the
  *                       replacement or bonus draw;
  *   kv_commit           roll the cache back to the accepted prefix, or
- *                       compact the accepted tree path.
+ *                       compact the accepted tree path;
+ *
+ * and beside them what a serving step needs around the verify:
+ *
+ *   spec_block_tables   block tables, slot map and positions of the new rows
+ *                       from the requests' lengths;
+ *   spec_qk_norm_rope   per-head norm and position rotation of the queries and
+ *                       keys that spec_verify_attn takes;
+ *   spec_verify_attn_window  verify attention with a sliding window and sinks;
+ *   spec_sample         the draft's own draws, and plain decoding.
  *
  * Conventions shared by every call
  *   - Every tensor pointer is caller-owned DEVICE memory, dense and
@@ -187,10 +196,11 @@ spec_status spec_verify_attn(const void* q, const void* k_new,
  * `window` (itself included; a new key stands at ctx plus its node's depth).
  *
  *   window >= 1, sinks >= 0
- * Other arguments as in spec_verify_attn.  Table entries of pages that hold
- * neither one of the first `sinks` positions nor a position from
- * ctx - window + 1 on are not read and may hold anything
- * (spec_block_tables returns those pages).  A window of the whole context
+ * Other arguments as in spec_verify_attn.  Keys and values at positions that
+ * are neither among the first `sinks` nor from ctx - window + 1 on are not
+ * read and may be anything, and so may the table entries of pages that hold
+ * only such positions (spec_block_tables returns those pages).  Keys and
+ * values that some row of a request sees have to be finite.  A window of the whole context
  * gives spec_verify_attn's results, up to the order of the sums.
  */
 spec_status spec_verify_attn_window(const void* q, const void* k_new, const void* v_new,
@@ -416,9 +426,9 @@ spec_status spec_reject_sample_noalloc(const void* target_logits,
  *                         follow the nodes' depths; slots stay ctx + i
  *   rows                  rows of slots and positions (>= B*M without row_start)
  *   window, sinks         0, or the window and sinks of
- *                         spec_verify_attn_window: only pages of the first
- *                         `sinks` positions and of positions from
- *                         ctx - window + 1 on are held
+ *                         spec_verify_attn_window, the same in every call:
+ *                         only pages of the first `sinks` positions and of
+ *                         positions from ctx - window + 1 on are held
  *   block_table [B, max_blocks] int32 (in/out)   entries of pages not held: -1
  *   span      [B, 2] int32, 8-byte aligned (in/out)   pages (lo, hi) held: p < hi
  *                         with p >= lo or among the sinks' pages; 0, 0 at first
@@ -426,6 +436,7 @@ spec_status spec_reject_sample_noalloc(const void* target_logits,
  *   pool_state [2] int32 (in/out)   head, count: entries (head + i) %
  *                         num_blocks, i < count, are free
  *   slots     [rows] int64    block * 16 + offset of each row, -1 without one
+ *                         (NULL, like positions, if rows is 0)
  *   positions [rows] int32    position of each row, -1 without one
  *   ok        [B] int32 or NULL   1: the request may run this step
  *
@@ -456,7 +467,7 @@ spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
  *   y = x * rsqrt(mean(x^2) + eps) * weight       (no norm without a weight)
  *   (a, b) -> (a cos - b sin, b cos + a sin), angle t * inv_freq[j], for the
  *   pairs (j, j + rot_dim/2), or (2j, 2j + 1) if interleaved, j < rot_dim/2
- * in fp32 (angles reduced exactly), rounded once.
+ * in fp32 (angles reduced exactly), rounded once.  rows = 0 does nothing.
  *
  *   q [rows, Hq, D], k, v [rows, Hkv, D]  kv_dtype   rows q_stride, k_stride,
  *                 v_stride elements apart (multiples of 16 bytes), heads dense:
@@ -510,7 +521,9 @@ spec_status spec_qk_norm_rope(const void* q, const void* k, const void* v, int64
  * V up to 2^20.  A bad parameter (SPEC_ERR_INVALID_ARG) or a row with NaN,
  * +inf or only -inf (SPEC_ERR_NONFINITE) gives token -1 and probability 0.
  * Sums are held to about 2^-40, so the token is the definition's unless u * Z
- * lies that close to a step.  No state is kept in the workspace.
+ * lies that close to a step.  rows = 0 does nothing.  Of the workspace the
+ * second word counts rows that needed a second look, modulo 2^32; its value
+ * does not matter, and calls that overlap may share it.
  */
 spec_status spec_sample(const void* logits, int64_t row_stride, int32_t rows, int32_t V,
                         int32_t logits_dtype, const float* temperature, const int32_t* top_k,

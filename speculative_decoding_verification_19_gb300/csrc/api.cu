@@ -433,8 +433,8 @@ spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
   if (dims->max_blocks < 1 || dims->num_blocks < 1) return SPEC_ERR_INVALID_ARG;
   if ((int64_t)dims->max_blocks * kBlock > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
   if ((s = check_ws(dims, ws, ws_bytes)) != SPEC_OK) return s;
-  if (!ctx_lens || !block_table || !span || !pool || !pool_state || !slots || !positions)
-    return SPEC_ERR_INVALID_ARG;
+  if (!ctx_lens || !block_table || !span || !pool || !pool_state) return SPEC_ERR_INVALID_ARG;
+  if (rows > 0 && (!slots || !positions)) return SPEC_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(span) & 7u) != 0) return SPEC_ERR_INVALID_ARG;
   if (rows < 0 || window < 0 || sinks < 0) return SPEC_ERR_INVALID_ARG;
   if (row_start != nullptr ? parent != nullptr : (int64_t)dims->B * dims->M > rows)
@@ -476,6 +476,7 @@ spec_status spec_qk_norm_rope(const void* q, const void* k, const void* v, int64
   if ((s = check_kv(dims)) != SPEC_OK) return s;
   if ((s = check_ws(dims, ws, ws_bytes)) != SPEC_OK) return s;
   if (rows < 0 || !(eps >= 0.f) || !(eps < INFINITY)) return SPEC_ERR_INVALID_ARG;
+  if (rows == 0) return SPEC_OK;
   if (!q || !k || !positions || !q_out) return SPEC_ERR_INVALID_ARG;
   if (slots != nullptr ? (!v || !k_cache || !v_cache) : !k_out) return SPEC_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > dims->D || (rot_dim > 0 && !inv_freq)) return SPEC_ERR_INVALID_ARG;
@@ -489,7 +490,6 @@ spec_status spec_qk_norm_rope(const void* q, const void* k, const void* v, int64
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
       !aligned16(k_cache) || !aligned16(v_cache))
     return SPEC_ERR_INVALID_ARG;
-  if (rows == 0) return SPEC_OK;
   RopeArgs a;
   a.q = q;
   a.k = k;
@@ -529,10 +529,10 @@ spec_status spec_sample(const void* logits, int64_t row_stride, int32_t rows, in
   if (logits_dtype != SPEC_BF16 && logits_dtype != SPEC_F32) return SPEC_ERR_INVALID_ARG;
   if (rows < 0 || V < 1 || row_stride < V) return SPEC_ERR_INVALID_ARG;
   if (V > kSampleMaxVocab || rows > (1 << 27)) return SPEC_ERR_UNSUPPORTED;
+  if (rows == 0) return SPEC_OK;
   if (!logits || !temperature || !uniform || !out_tokens) return SPEC_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(logits) % (logits_dtype == SPEC_BF16 ? 2 : 4) != 0)
     return SPEC_ERR_INVALID_ARG;
-  if (rows == 0) return SPEC_OK;
   SampleArgs a;
   a.logits = logits;
   a.stride = row_stride;

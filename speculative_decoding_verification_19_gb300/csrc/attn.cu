@@ -369,15 +369,16 @@ __global__ void __launch_bounds__(kWinThreads, RPW <= 8 ? 3 : (D == 64 ? 2 : 1))
   static_assert(kItems >= 1, "a tile has at least one vector per thread");
   const int32_t* bt = block_table + (int64_t)b * d.max_blocks;
   uint4 kr[kItems], vr[kItems];
-  // vectors of the tile at t0; keys past the range and pages that no row sees
-  // (and that are not held) are zero
+  // vectors of the tile at t0; keys past the range and keys that no row sees
+  // (their pages may not be held, their values may be anything) are zero
+  const int wf = win_first(ctx, window);
   auto fetch = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
       const int e = tid + i * kWinThreads, kk = e / kVecPerKey, vi = e % kVecPerKey;
       const int t = t0 + kk + (t0 >= skip_at ? skip : 0);
       kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-      if (t0 + kk < k1 && win_page(t / kBlock, ctx, window, sinks)) {
+      if (t0 + kk < k1 && (t >= wf || t < sinks)) {
         const int64_t base = (((int64_t)bt[t / kBlock] * d.Hkv + h) * kBlock + t % kBlock) * D;
         kr[i] = reinterpret_cast<const uint4*>(k_cache + base)[vi];
         vr[i] = reinterpret_cast<const uint4*>(v_cache + base)[vi];

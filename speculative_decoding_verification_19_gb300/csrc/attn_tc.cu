@@ -492,9 +492,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
       }
       const uint32_t sb = ptx::smem_u32(stages + stage * kStageBytes);
       const int kpos0 = pg * kBlock;
-      // with a window, pages that no row sees are not held: they read as zero
-      const bool held = !kWin || pg >= win_first(cu.ctx, window) / kBlock ||
-                        pg + kPages <= ceil_div(sinks, kBlock);
+      // with a window, positions that no row sees read as zero: their pages may
+      // not be held, their values may be anything
+      const int wf = kWin ? win_first(cu.ctx, window) : 0;
+      const bool held = !kWin || kpos0 >= wf || kpos0 + kTileKeys <= sinks;
       if (kpos0 + kTileKeys <= cu.ctx && held) {  // all keys in the cached prefix
 #pragma unroll
         for (int p = 0; p < kPages; ++p) {
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
       } else {
         // the tile reaches the new rows: those come from k_new / v_new (the
         // append into the cache runs concurrently), rows past L are zero, and
-        // with a window so are pages that are not held.  Pages wholly in the
+        // with a window so are those that no row sees.  Pages wholly in the
         // cached prefix are copied as above; in the others each row picks its
         // source without a branch.
         const int64_t row_stride = (int64_t)Hkv * 128;
@@ -523,8 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
             const int64_t page = ((int64_t)blk[p] * Hkv + cu.h) * kBlock * 128 + c16 * 8;
             const int pos0 = kpos0 + p * kBlock;
             const uint32_t so0 = swz_half + (uint32_t)p * kBoxBytes;
-            const bool have = !kWin || win_page(pg + p, cu.ctx, window, sinks);
-            if (have && pos0 + kBlock <= cu.ctx) {
+            if (pos0 + kBlock <= cu.ctx && (!kWin || pos0 >= wf || pos0 + kBlock <= sinks)) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const int r = r0 + 4 * k;
@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
               for (int k = 0; k < 4; ++k) {
                 const int r = r0 + 4 * k, pos = pos0 + r;
                 const uint32_t so = so0 + (uint32_t)r * 128u + ((uint32_t)((c16 & 7) ^ (r & 7)) << 4);
-                const bool cached = pos < cu.ctx, in = have && pos < L;
+                const bool cached = pos < cu.ctx;
+                const bool in = pos < L && (!kWin || pos >= wf || pos < sinks);
                 const __nv_bfloat16* ks = cached ? k_cache + page + r * 128 : k_new + new0 + pos * row_stride;
                 const __nv_bfloat16* vs = cached ? v_cache + page + r * 128 : v_new + new0 + pos * row_stride;
                 ptx::cp_async16_fill(sb + so, in ? ks : k_new, in ? 16u : 0u);

@@ -1,0 +1,282 @@
+"""Edges of the step operators on the GPU: large batches (the sampler's
+second look, the attention plan past shared memory), nothing to do, values
+that no row sees, side streams, captured calls that share a workspace, and
+waits that run out.
+
+Tolerances as in test_gpu_step.py.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+import speculative_decoding_verification_19_gb300 as sv  # noqa: E402
+from harness import to_dev  # noqa: E402
+from oracle import oracle_verify_attn_window  # noqa: E402
+from synth import kv_inputs_host, workload  # noqa: E402
+from test_gpu_step import (BF, F32, I32, Pages, sample_check, sample_gpu,  # noqa: E402
+                           window_case)
+
+
+# -------------------------------------------------------------------- sampling
+
+def sample_ref(x, T, u):
+    """Token, probability and distance to the nearest step, in fp64 on the GPU
+    (temperature alone)."""
+    out = []
+    for r in range(x.shape[0]):
+        w = torch.exp((x[r].double() - x[r].double().max()) / float(T[r]))
+        c = w.cumsum(0)
+        t = float(u[r]) * float(c[-1])
+        i = int((c <= t).sum())
+        near = min(float(c[i]) - t, t - (float(c[i - 1]) if i else -math.inf)) / float(c[-1])
+        out.append((i, float(w[i] / c[-1]), near))
+    return [np.array(v) for v in zip(*out)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("scale", [0.05, 3.0])
+def test_sample_many_rows_without_filters(dt, scale):
+    """Rows enough for the streaming kernel to leave doubtful draws to the
+    second one: nearly flat rows make most of them doubtful."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n, V = 700, 30011
+    x = (torch.randn(n, V, device="cuda", generator=g) * scale).to(dt)
+    rng = np.random.default_rng(4)
+    T = rng.choice([0.3, 1.0, 4.0], n).astype(np.float32)
+    u = (rng.integers(0, 1 << 24, n) / (1 << 24)).astype(np.float32)
+    u[:3] = (0.0, 1 - 2.0 ** -24, 0.5)
+    T[5:40], x[7, 100], x[8, :] = 0.0, float("nan"), -math.inf
+    x[45, 30010], T[50], u[51] = math.inf, -1.0, 1.0
+    x[60, 5:] = -math.inf               # five tokens left
+    x[61] = float(torch.finfo(dt).min)  # flat at the lowest value
+    bad = [7, 8, 45, 50, 51]
+    tok, prob, status = sample_gpu(x, T, u)
+    assert np.all(tok[bad] == -1) and np.all(prob[bad] == 0) and status == (1 << 5 | 1 << 1)
+    greedy = [r for r in range(n) if T[r] == 0 and r not in bad]
+    top = x[greedy].float().max(1, keepdim=True)[0]
+    first = torch.where(x[greedy].float() == top, torch.arange(V, device="cuda"), V).amin(1)
+    assert np.array_equal(tok[greedy], first.cpu().numpy()) and np.all(prob[greedy] == 1)
+    rest = [r for r in range(n) if r not in bad and r not in greedy]
+    i, p, near = sample_ref(x[rest], T[rest], u[rest])
+    sure = near > 1e-9
+    assert sure.mean() > 0.95
+    assert np.array_equal(tok[rest][sure], i[sure])
+    assert np.all(np.abs(prob[rest][sure] - p[sure]) <= 2.0 ** -21 * p[sure])
+    # the same rows a few at a time, which draw exactly in one kernel
+    few = rest[:20]
+    again = sample_gpu(x[few], T[few], u[few])
+    assert np.array_equal(again[0][sure[:20]], tok[few][sure[:20]])
+
+
+def test_sample_many_rows_of_the_largest_vocabulary():
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n, V = 304, 1 << 20
+    x = torch.randn(n, V, device="cuda", generator=g, dtype=BF)
+    T = np.full(n, 1.0, np.float32)
+    u = (np.random.default_rng(6).integers(0, 1 << 24, n) / (1 << 24)).astype(np.float32)
+    tok, prob, status = sample_gpu(x, T, u)
+    i, p, near = sample_ref(x, T, u)
+    sure = near > 1e-9
+    assert status == 0 and np.array_equal(tok[sure], i[sure])
+    assert np.all(np.abs(prob[sure] - p[sure]) <= 2.0 ** -21 * p[sure])
+
+
+def test_sample_filters_over_batch_sizes():
+    """The number of CTAs a row takes goes by the batch; the law does not."""
+    rng = np.random.default_rng(7)
+    for n, V in ((40, 64000), (130, 64000), (300, 9000)):
+        x = (rng.standard_normal((n, V)) * 3).astype(np.float32)
+        k = rng.choice([0, 1, 60, 300, 900, 2500], n)
+        p = rng.choice([1.0, 0.5, 0.9, 0.999], n)
+        mp = rng.choice([0.0, 0.01], n)
+        T, u = rng.choice([0.5, 1.0], n), (rng.integers(0, 1 << 20, n) + 0.5) / (1 << 20)
+        for dt in (BF, F32):
+            sample_check(x, T, u, k, p, mp, dt)
+            sample_check(x, T, u, k=k, dt=dt)
+
+
+def test_sample_two_captured_calls_share_a_workspace():
+    """Two graphs on two streams over one workspace: large batches, so both
+    count their doubtful rows in it."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    n, V = 640, 20000
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    runs = []
+    for s in range(2):
+        x = torch.randn(n, V, device="cuda", generator=g, dtype=F32) * 0.1
+        T = torch.ones(n, device="cuda")
+        u = torch.rand(n, device="cuda", generator=g)
+        want = torch.empty(n, dtype=I32, device="cuda")
+        sv.spec_sample(x, T, u, want, None, ws)
+        tok = torch.empty(n, dtype=I32, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            sv.spec_sample(x, T, u, tok, None, ws)
+        runs.append((graph, tok, want, (x, T, u)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(5):
+        for (graph, tok, _, _), st in zip(runs, streams):
+            with torch.cuda.stream(st):
+                tok.fill_(-7)
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, tok, want, _ in runs:
+        assert torch.equal(tok, want)
+    assert sv.device_status(ws) == 0
+
+
+# ------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("impl", [sv.ATTN_TENSOR_CORES, sv.ATTN_CUDA_CORES])
+@pytest.mark.parametrize("window,sinks", [(40, 3), (50, 0), (7, 20)])
+def test_window_values_that_no_row_sees(impl, window, sinks):
+    """NaN at every cached position outside the window and the sinks, also in
+    pages that are held."""
+    wl = workload("chain_gqa_128k").scaled(gamma=4, Hq=4, Hkv=2)
+    ctx = np.array([300, 45, 129])
+    kv = kv_inputs_host(wl, seed=11, B=3, ctx=ctx)
+    dims = sv.make_dims(B=3, M=5, Hq=4, Hkv=2, D=128, max_blocks=kv["max_blocks"],
+                        num_blocks=kv["num_blocks"], attn_impl=impl)
+    ws = sv.workspace(dims)
+    kc, vc = to_dev(kv["k_cache"], BF), to_dev(kv["v_cache"], BF)
+    for b in range(3):
+        for t in range(ctx[b]):
+            if t >= sinks and t <= ctx[b] - window:
+                blk = kv["block_table"][b, t // 16]
+                kc[blk, :, t % 16] = float("nan")
+                vc[blk, :, t % 16] = float("inf")
+    q = to_dev(kv["q"], BF)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    sv.spec_verify_attn(q, to_dev(kv["k_new"], BF), to_dev(kv["v_new"], BF), kc, vc,
+                        to_dev(kv["block_table"], I32), to_dev(ctx, I32), None, out, lse, dims, ws,
+                        window=window, sinks=sinks)
+    o, l, _, _ = oracle_verify_attn_window(kv["q"], kv["k_cache"], kv["v_cache"], kv["block_table"],
+                                           ctx, kv["k_new"], kv["v_new"], window, sinks)
+    assert np.all(np.abs(out.double().cpu().numpy() - o) <= 2.0 ** -7 * 4.5)
+    assert np.max(np.abs(lse.cpu().numpy() - l)) <= 1e-4
+
+
+def test_window_of_many_requests():
+    """More requests than the split plan keeps in shared memory."""
+    wl = workload("chain_gqa_128k").scaled(gamma=1, Hq=2, Hkv=1)
+    ctx = np.random.default_rng(12).integers(0, 90, 1100).tolist()
+    window_case(wl, ctx, 30, 5, False, seed=12, impl=sv.ATTN_TENSOR_CORES)
+
+
+def test_window_wait_gives_up_then_recovers():
+    """A limit of a thousand clocks runs out in the copy pipeline or in the
+    merge of a split pair; an ordinary call afterwards is right again."""
+    wl = workload("chain_gqa_128k").scaled(gamma=3)
+    kv = kv_inputs_host(wl, seed=13, B=1, ctx=np.array([40000]))
+    buf = torch.empty(96 << 20, device="cuda")
+    for limit in (1, 0):
+        dims = sv.make_dims(B=1, M=4, Hq=wl.Hq, Hkv=wl.Hkv, D=128, max_blocks=kv["max_blocks"],
+                            num_blocks=kv["num_blocks"], wait_limit_kcycles=limit)
+        ws = sv.workspace(dims)
+        args = [to_dev(kv[k], BF) for k in ("q", "k_new", "v_new", "k_cache", "v_cache")]
+        out, lse = torch.empty_like(args[0]), torch.empty(1, 4, wl.Hq, device="cuda")
+        buf.fill_(1.0)  # the cache out of L2
+        sv.spec_verify_attn(*args, to_dev(kv["block_table"], I32), to_dev(kv["ctx_lens"], I32), None,
+                            out, lse, dims, ws, window=20000, sinks=4)
+        status = sv.device_status(ws)
+        assert (status & (1 << 7)) if limit else status == 0
+    o, l, _, _ = oracle_verify_attn_window(kv["q"], kv["k_cache"], kv["v_cache"], kv["block_table"],
+                                           kv["ctx_lens"], kv["k_new"], kv["v_new"], 20000, 4)
+    assert np.all(np.abs(out.double().cpu().numpy() - o) <= 2e-2 + 1e-2 * np.abs(o))
+
+
+# ----------------------------------------------------------- lengths and streams
+
+def test_nothing_to_do():
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    e = lambda *s, dt=F32: torch.empty(*s, dtype=dt, device="cuda")  # noqa: E731
+    sv.spec_sample(e(0, 50), e(0), e(0), e(0, dt=I32), e(0), ws)
+    dims = sv.make_dims(B=1, M=1, Hq=2, Hkv=1, D=64, kv_dtype=F32)
+    w = sv.workspace(dims)
+    f = torch.ones(32, dtype=torch.float64, device="cuda")
+    sv.spec_qk_norm_rope(e(0, 2, 64), e(0, 1, 64), None, None, None, e(0, dt=I32), f, e(0, 2, 64),
+                         e(0, 1, 64), dims, w)
+    # requests without new rows: lengths change, pages come and go
+    st = Pages(3, 5, 9)
+    st.call(np.array([40, 0, -1]), np.zeros(4, np.int64), 0)
+    st.call(np.array([12, 17, -1]), np.zeros(4, np.int64), 0)
+    st.call(np.array([-1, -1, -1]), np.zeros(4, np.int64), 0)
+    assert st.h["pool_state"][1] == 9
+
+
+def test_step_operators_on_a_side_stream_and_in_a_graph():
+    """Tables, norm and rotation with the cache written, attention, captured
+    as one graph on a stream of its own, against the same calls one by one."""
+    B, M, Hq, Hkv, mb, nb = 2, 3, 4, 2, 8, 24
+    dims = sv.make_dims(B=B, M=M, Hq=Hq, Hkv=Hkv, D=128, max_blocks=mb, num_blocks=nb)
+    g = torch.Generator(device="cuda").manual_seed(14)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g).to(BF)  # noqa: E731
+    qkv, w = rand(B * M, Hq + 2 * Hkv, 128), rand(128)
+    inv = to_dev(10000.0 ** (-np.arange(64) / 64), torch.float64)
+    kc0, vc0 = rand(nb, Hkv, 16, 128), rand(nb, Hkv, 16, 128)
+    ctx = to_dev(np.array([50, 7]), I32)
+
+    def state():
+        return dict(table=torch.full((B, mb), -1, dtype=I32, device="cuda"),
+                    span=torch.zeros(B, 2, dtype=I32, device="cuda"),
+                    pool=torch.arange(nb, dtype=I32, device="cuda"),
+                    ring=to_dev(np.array([5, nb]), I32), kc=kc0.clone(), vc=vc0.clone(),
+                    slots=torch.empty(B * M, dtype=torch.int64, device="cuda"),
+                    pos=torch.empty(B * M, dtype=I32, device="cuda"),
+                    q=torch.empty(B * M, Hq, 128, dtype=BF, device="cuda"),
+                    k=torch.empty(B * M, Hkv, 128, dtype=BF, device="cuda"),
+                    out=torch.empty(B, M, Hq, 128, dtype=BF, device="cuda"),
+                    lse=torch.empty(B, M, Hq, device="cuda"), ws=sv.workspace(dims))
+
+    def step(s, stream=None):
+        sv.spec_block_tables(ctx, None, None, s["table"], s["span"], s["pool"], s["ring"], s["slots"],
+                             s["pos"], None, dims, s["ws"], window=20, sinks=2, stream=stream)
+        sv.spec_qk_norm_rope(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], w, w, s["pos"], inv,
+                             s["q"], s["k"], dims, s["ws"], slots=s["slots"], k_cache=s["kc"],
+                             v_cache=s["vc"], stream=stream)
+        v = qkv[:, Hq + Hkv:].contiguous().view(B, M, Hkv, 128) if stream is None else s["v"]
+        sv.spec_verify_attn(s["q"].view(B, M, Hq, 128), s["k"].view(B, M, Hkv, 128), v, s["kc"],
+                            s["vc"], s["table"], ctx, None, s["out"], s["lse"], dims, s["ws"],
+                            window=20, sinks=2, stream=stream)
+
+    a, b, c = state(), state(), state()
+    step(a)
+    b["v"] = qkv[:, Hq + Hkv:].contiguous().view(B, M, Hkv, 128)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    step(b, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    c["v"] = b["v"]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(c, stream=torch.cuda.current_stream())
+    graph.replay()
+    torch.cuda.synchronize()
+    for o in (b, c):
+        for k in ("table", "span", "pool", "ring", "slots", "pos", "q", "k", "out", "lse", "kc", "vc"):
+            assert torch.equal(a[k], o[k]), k
+        assert sv.device_status(o["ws"]) == 0
+    assert torch.isfinite(a["out"]).all()
+
+
+def test_binding_refusals():
+    x = torch.zeros(2, 64, device="cuda")
+    one = torch.ones(2, device="cuda")
+    tok = torch.zeros(2, dtype=I32, device="cuda")
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    for bad in (dict(temperature=one[:1]), dict(uniform=one.double()), dict(out_tokens=tok.long()),
+                dict(uniform=one.cpu()), dict(logits=x.t()), dict(logits=x.half()),
+                dict(uniform=torch.ones(4, device="cuda")[::2])):
+        kw = dict(logits=x, temperature=one, uniform=one, out_tokens=tok, out_prob=None, ws=ws) | bad
+        with pytest.raises(ValueError):
+            sv.spec_sample(**kw)
+    with pytest.raises(sv.SpecError):
+        sv.spec_sample(x[:, :40].expand(2, 40).as_strided((2, 40), (8, 1)), one, one, tok, None, ws)
+    sv.spec_sample(x, one, one * 0.5, tok, None, ws)
+    assert sv.device_status(ws) == 0
