@@ -1,4 +1,5 @@
-"""ctypes binding of libspecverify.so (argument marshalling only).
+"""Binding of libspecverify.so (argument marshalling only): ctypes, and for the
+step operators the native checks of csrc/binding.cpp.
 
 Every function here takes torch tensors that already live on the GPU,
 passes their device pointers, sizes and the current CUDA stream to the C ABI
@@ -56,6 +57,7 @@ class SpecDims(ctypes.Structure):
 
 
 _lib = None
+_binding = None
 
 
 def lib() -> ctypes.CDLL:
@@ -176,44 +178,21 @@ def device_status(ws: torch.Tensor, clear: bool = True, stream=None) -> int:
     return int(out.value)
 
 
-def _expect(name, t, dtype, shape, device, optional=False):
-    """A tensor's address after checks of its type, shape and GPU (by index);
-    dense unless `shape` is None."""
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is needed")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: {dtype} is wanted, not {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} lives on {t.device}, not on cuda:{device}")
-    if shape is not None:
-        if t.shape != shape:
-            raise ValueError(f"{name}: shape {shape} is wanted, not {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+def _bind():
+    """The native argument checks of the step operators (raises if they have
+    not been built)."""
+    global _binding
+    if _binding is None:
+        lib()
+        from . import _specbind
+        _binding = _specbind
+    return _binding
 
 
-def _on(t, name):
-    """The GPU (its index) of a call's first tensor."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on the GPU")
-    return t.get_device()
-
-
-def _launch(fn, device, stream, *args):
-    """Calls the library on the tensors' GPU, on its current stream or `stream`."""
-    L = _lib or lib()
-    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-    if device == torch._C._cuda_getDevice():
-        code = getattr(L, fn)(*args, s)
-    else:
-        with torch.cuda.device(device):
-            code = getattr(L, fn)(*args, s)
-    if code != 0:
-        raise SpecError(fn, code)
-    return L.spec_last_launch_count()
+def _done(fn: str, result: int) -> int:
+    if result < 0:
+        raise SpecError(fn, -result)
+    return result
 
 
 def spec_verify_attn(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens,
@@ -221,22 +200,9 @@ def spec_verify_attn(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens,
                      sinks=0) -> int:
     """spec_verify_attn; with a window (and sinks) spec_verify_attn_window."""
     if window is not None:
-        dev = _on(q, "q")
-        kv = torch.bfloat16 if dims.kv_dtype == SPEC_BF16 else torch.float32
-        B, M, Hq, Hkv, D = dims.B, dims.M, dims.Hq, dims.Hkv, dims.D
-        cache = (dims.num_blocks, Hkv, dims.block, D)
-        return _launch(
-            "spec_verify_attn_window", dev, stream,
-            _expect("q", q, kv, (B, M, Hq, D), dev),
-            _expect("k_new", k_new, kv, (B, M, Hkv, D), dev),
-            _expect("v_new", v_new, kv, (B, M, Hkv, D), dev),
-            _expect("k_cache", k_cache, kv, cache, dev), _expect("v_cache", v_cache, kv, cache, dev),
-            _expect("block_table", block_table, torch.int32, (B, dims.max_blocks), dev),
-            _expect("ctx_lens", ctx_lens, torch.int32, (B,), dev),
-            _expect("parent", parent, torch.int32, (B, M), dev, True), int(window), int(sinks),
-            _expect("out", out, kv, (B, M, Hq, D), dev),
-            _expect("lse", lse, torch.float32, (B, M, Hq), dev, True),
-            ctypes.byref(dims), _expect("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel())
+        return _done("spec_verify_attn_window", _bind().verify_attn_window(
+            q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, out, lse, dims, ws,
+            window, sinks, None if stream is None else stream.cuda_stream))
     code = lib().spec_verify_attn(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
         _ptr(block_table), _ptr(ctx_lens), _ptr(parent), _ptr(out), _ptr(lse),
@@ -274,29 +240,9 @@ def spec_block_tables(ctx_lens, row_start, parent, block_table, span, pool, pool
     """Block tables, slot map and positions of a step's new rows from the
     requests' lengths; pages come from and go back to a ring of free ids
     (block_table, span, pool and pool_state are updated in place)."""
-    dev, i32 = _on(ctx_lens, "ctx_lens"), torch.int32
-    B, rows = dims.B, slots.numel()
-    return _launch(
-        "spec_block_tables", dev, stream, _expect("ctx_lens", ctx_lens, i32, (B,), dev),
-        _expect("row_start", row_start, i32, (B + 1,), dev, True),
-        _expect("parent", parent, i32, (B, dims.M), dev, True), rows, int(window), int(sinks),
-        _expect("block_table", block_table, i32, (B, dims.max_blocks), dev),
-        _expect("span", span, i32, (B, 2), dev), _expect("pool", pool, i32, (dims.num_blocks,), dev),
-        _expect("pool_state", pool_state, i32, (2,), dev),
-        _expect("slots", slots, torch.int64, (rows,), dev),
-        _expect("positions", positions, i32, (rows,), dev), _expect("ok", ok, i32, (B,), dev, True),
-        ctypes.byref(dims), _expect("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel())
-
-
-def _rows_of(name, t, dtype, rows, heads, D, device):
-    """Address and row stride of a [rows, heads, D] view with dense heads."""
-    p = _expect(name, t, dtype, None, device)
-    if tuple(t.shape) != (rows, heads, D):
-        raise ValueError(f"{name}: shape {(rows, heads, D)} is wanted, not {tuple(t.shape)}")
-    s = t.stride()
-    if (D > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
-        raise ValueError(f"{name}: heads must be dense")
-    return p, (s[0] if rows > 1 else heads * D)
+    return _done("spec_block_tables", _bind().block_tables(
+        ctx_lens, row_start, parent, block_table, span, pool, pool_state, slots, positions, ok, dims,
+        ws, window, sinks, None if stream is None else stream.cuda_stream))
 
 
 def spec_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out,
@@ -305,47 +251,18 @@ def spec_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k
     """RMS norm of every query and key head and the position rotation
     (2 * len(inv_freq) values of each head turn); with slots, the keys and
     values also go to the paged cache."""
-    dev = _on(q, "q")
-    kv = torch.bfloat16 if dims.kv_dtype == SPEC_BF16 else torch.float32
-    rows, Hq, Hkv, D = positions.numel(), dims.Hq, dims.Hkv, dims.D
-    qp, qs = _rows_of("q", q, kv, rows, Hq, D, dev)
-    kp, ks = _rows_of("k", k, kv, rows, Hkv, D, dev)
-    vp, vs = (None, 0) if slots is None else _rows_of("v", v, kv, rows, Hkv, D, dev)
-    cache = (dims.num_blocks, Hkv, dims.block, D)
-    half = 0 if inv_freq is None else inv_freq.numel()
-    return _launch(
-        "spec_qk_norm_rope", dev, stream, qp, kp, vp, qs, ks, vs,
-        _expect("q_weight", q_weight, kv, (D,), dev, True),
-        _expect("k_weight", k_weight, kv, (D,), dev, True), float(eps),
-        _expect("positions", positions, torch.int32, (rows,), dev),
-        _expect("inv_freq", inv_freq, torch.float64, (half,), dev, True), 2 * half,
-        1 if interleaved else 0, rows, _expect("q_out", q_out, kv, (rows, Hq, D), dev),
-        _expect("k_out", k_out, kv, (rows, Hkv, D), dev, slots is not None),
-        _expect("slots", slots, torch.int64, (rows,), dev, True),
-        _expect("k_cache", k_cache, kv, cache, dev, slots is None),
-        _expect("v_cache", v_cache, kv, cache, dev, slots is None),
-        ctypes.byref(dims), _expect("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel())
+    return _done("spec_qk_norm_rope", _bind().qk_norm_rope(
+        q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out, dims, ws, eps, interleaved,
+        slots, k_cache, v_cache, None if stream is None else stream.cuda_stream))
 
 
 def spec_sample(logits, temperature, uniform, out_tokens, out_prob, ws, top_k=None, top_p=None,
                 min_p=None, stream=None) -> int:
     """One token per row of logits [rows, V] (any row stride) from given
     uniforms, with temperature, top-k, top-p and min-p."""
-    dev, f32 = _on(logits, "logits"), torch.float32
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits: [rows, V] with dense rows is wanted")
-    rows, V = logits.shape
-    return _launch(
-        "spec_sample", dev, stream, _expect("logits", logits, logits.dtype, None, dev),
-        logits.stride(0) if rows > 1 else V, rows, V, dtype_code(logits.dtype),
-        _expect("temperature", temperature, f32, (rows,), dev),
-        _expect("top_k", top_k, torch.int32, (rows,), dev, True),
-        _expect("top_p", top_p, f32, (rows,), dev, True),
-        _expect("min_p", min_p, f32, (rows,), dev, True),
-        _expect("uniform", uniform, f32, (rows,), dev),
-        _expect("out_tokens", out_tokens, torch.int32, (rows,), dev),
-        _expect("out_prob", out_prob, f32, (rows,), dev, True),
-        _expect("ws", ws, torch.uint8, (ws.numel(),), dev), ws.numel())
+    return _done("spec_sample", _bind().sample(
+        logits, temperature, uniform, out_tokens, out_prob, ws, top_k, top_p, min_p,
+        None if stream is None else stream.cuda_stream))
 
 
 def spec_lm_head(hidden, weight, logits, ws, stream=None) -> int:

@@ -1,8 +1,10 @@
 """Build libspecverify.so (sm_103a) in-tree with nvcc.
 
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
-speculative_decoding_verification_19_gb300/libspecverify.so.  Objects are
-rebuilt when any source or header changed (content hash stamp).
+speculative_decoding_verification_19_gb300/libspecverify.so, and
+csrc/binding.cpp (the step operators' argument checks) into _specbind.so
+beside it.  Everything is rebuilt when any source or header changed (content
+hash stamp).
 """
 from __future__ import annotations
 
@@ -13,6 +15,9 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libspecverify.so")
+BIND = os.path.join(PKG, "_specbind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -45,7 +51,7 @@ def _digest() -> str:
         h.update(os.path.basename(f).encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
-    h.update(" ".join(ARCH + FLAGS).encode())
+    h.update(" ".join(ARCH + FLAGS + [torch.__version__, sys.version]).encode())
     return h.hexdigest()
 
 
@@ -54,7 +60,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     stamp = os.path.join(BUILD, "stamp")
     dig = _digest()
-    if not force and os.path.exists(LIB) and os.path.exists(stamp):
+    if not force and os.path.exists(LIB) and os.path.exists(BIND) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == dig:
                 return LIB
@@ -74,14 +80,40 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    def compile_binding():
+        troot = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(cc))
+        inc = [INCLUDE, troot + "/include", troot + "/include/torch/csrc/api/include",
+               sysconfig.get_paths()["include"], cuda + "/include"]
+        obj = os.path.join(BUILD, "binding.o")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *["-I" + i for i in inc], "-c",
+               os.path.join(CSRC, "binding.cpp"), "-o", obj]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj
+
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        bind = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        bind_obj = bind.result()
     tmp = LIB + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # the binding finds the library beside it and torch's libraries loaded
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, bind_obj, "-L" + PKG, "-l:" + os.path.basename(LIB),
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
     with open(stamp, "w") as f:
         f.write(dig)
     return LIB
