@@ -37,8 +37,9 @@ constexpr int kThreads = 512;  // also the requests of one round
 constexpr int kWarps = kThreads / kWarp;
 constexpr int kMaxCtas = 152;
 // Items of one CTA when the call has more than that (host rule): below it the
-// launch is one CTA, which needs no arrival count.
-constexpr int kItemsPerCta = 2048;
+// launch is one CTA, which needs no arrival count.  One item a thread: 65541
+// rows of 512 requests take 7.6 us so, 11.2 us with four (2048 items a CTA).
+constexpr int kItemsPerCta = kThreads;
 
 struct Shared {
   // exclusive prefixes over the round's requests, relative to its first
@@ -128,11 +129,16 @@ __device__ void plan_round(Shared& sh, const PageArgs& a, int base, int sp, bool
   }
   if (lane == kWarp - 1) sh.warp_need[warp] = incl;
   __syncthreads();
-  int64_t total_need = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) incl += sh.warp_need[w];
-    total_need += sh.warp_need[w];
+  // lane w holds warp w's sum: those of the warps before, and all of them
+  const int64_t wn = lane < kWarps ? sh.warp_need[lane] : 0;
+  int64_t before_need = lane < warp ? wn : 0, total_need = wn;
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) {
+    before_need += __shfl_xor_sync(0xffffffffu, before_need, o);
+    total_need += __shfl_xor_sync(0xffffffffu, total_need, o);
   }
+  incl += __shfl_sync(0xffffffffu, before_need, 0);
+  total_need = __shfl_sync(0xffffffffu, total_need, 0);
   if (good == 2 && need > 0 && carry.need + incl > count) {
     if (report) raise_status(status, SPEC_ERR_CAPACITY);
     good = 1;            // gives back what it no longer needs, takes nothing
@@ -161,15 +167,10 @@ __device__ void plan_round(Shared& sh, const PageArgs& a, int base, int sp, bool
     sh.warp_give[warp] = ig;
   }
   __syncthreads();
-  int tt = 0, tg = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) {
-      it += sh.warp_take[w];
-      ig += sh.warp_give[w];
-    }
-    tt += sh.warp_take[w];
-    tg += sh.warp_give[w];
-  }
+  const int wt = lane < kWarps ? sh.warp_take[lane] : 0, wg = lane < kWarps ? sh.warp_give[lane] : 0;
+  it += __reduce_add_sync(0xffffffffu, lane < warp ? wt : 0);
+  ig += __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0);
+  const int tt = __reduce_add_sync(0xffffffffu, wt), tg = __reduce_add_sync(0xffffffffu, wg);
   sh.take_pre[tid] = it - take;
   sh.give_pre[tid] = ig - give;
   const int n = min(kThreads, B - base);
