@@ -58,11 +58,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
     }
   }
   // topology
+  __shared__ int32_t s_par[kMaxNodes];  // for the walks to the root below
   int bad_topo = 0;
   if (parent != nullptr) {
     const int32_t* par = parent + (int64_t)b * d.M;
     for (int n = tid; n < d.M; n += blockDim.x) {
       const int pn = par[n];
+      s_par[n] = pn;
       bad_topo |= (n == 0) ? (pn != -1) : (pn < 0 || pn >= n);
     }
   }
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
   if (!ok) return;
   if (window > 0 && blockIdx.y == 0)
     for (int n = tid; n < d.M; n += blockDim.x)
-      win_row_mask(parent != nullptr ? parent + (int64_t)b * d.M : nullptr, n, ctx, window, sinks,
+      win_row_mask(parent != nullptr ? s_par : nullptr, n, ctx, window, sinks,
                    anc_ws + (int64_t)b * d.M + n, depth_ws + (int64_t)b * d.M + n);
 
   // append: positions ctx .. end-1 where end = ceil(L/16)*16; rows past
@@ -334,14 +336,15 @@ __device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, uns
 
 template <typename T, int D, int RPW>
 __global__ void __launch_bounds__(kWinThreads, RPW <= 8 ? 3 : (D == 64 ? 2 : 1)) attn_win_split_kernel(
-    const T* __restrict__ q, const T* __restrict__ k_cache, const T* __restrict__ v_cache,
-    const int32_t* __restrict__ block_table, const int32_t* __restrict__ ctx_lens,
-    const ulonglong2* __restrict__ anc_ws, const int32_t* __restrict__ depth_ws,
-    const int32_t* __restrict__ req_ok, spec_dims d, int window, int sinks, float qscale,
+    const T* q, const T* k_cache, const T* v_cache, const int32_t* block_table,
+    const int32_t* ctx_lens, const ulonglong2* anc_ws, const int32_t* depth_ws,
+    const int32_t* req_ok, spec_dims d, int window, int sinks, float qscale,
     int split_keys, int max_splits, float* __restrict__ part) {
   constexpr int DPL = D / kWarp;  // d values per lane in the PV step
   static_assert(DPL == 2 || DPL == 4, "D must be 64 or 128");
   const int s = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  pdl_trigger();
+  pdl_wait();  // the cache, the masks and the verdict come from the append kernel
   if (!req_ok[b]) return;
   const int ctx = ctx_lens[b];
   const int skip = win_skip(ctx, window, sinks, kTileKeys) * kTileKeys;
@@ -532,9 +535,10 @@ __global__ void __launch_bounds__(kWinThreads, RPW <= 8 ? 3 : (D == 64 ? 2 : 1))
 // ---------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256) attn_combine_kernel(
-    const float* __restrict__ part, const int32_t* __restrict__ ctx_lens,
-    const int32_t* __restrict__ req_ok, spec_dims d, int window, int sinks, int split_keys,
-    int max_splits, T* __restrict__ out, float* __restrict__ lse) {
+    const float* part, const int32_t* ctx_lens, const int32_t* req_ok, spec_dims d, int window,
+    int sinks, int split_keys, int max_splits, T* __restrict__ out, float* __restrict__ lse) {
+  pdl_trigger();
+  pdl_wait();  // the partials come from the previous kernel
   const int h = blockIdx.x, b = blockIdx.z;
   const int group = d.Hq / d.Hkv;
   const int R = group * d.M;
@@ -654,11 +658,12 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
     auto k = attn_win_split_kernel<T, DD, RPW>;                                               \
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)win_smem);  \
     if (e != cudaSuccess) return e;                                                           \
-    k<<<grid, kWinThreads, win_smem, st>>>(static_cast<const T*>(a.q),                        \
-                                           static_cast<const T*>(a.k_cache),                  \
-                                           static_cast<const T*>(a.v_cache), a.block_table,   \
-                                           a.ctx_lens, anc, depth, req_ok, d, a.window,       \
-                                           a.sinks, qscale, split_keys, splits, part);        \
+    PdlLaunch L(grid, dim3(kWinThreads), win_smem, st);                                       \
+    e = cudaLaunchKernelEx(&L.cfg, k, static_cast<const T*>(a.q),                             \
+                           static_cast<const T*>(a.k_cache), static_cast<const T*>(a.v_cache),\
+                           a.block_table, a.ctx_lens, anc, depth, (const int32_t*)req_ok, d,  \
+                           a.window, a.sinks, qscale, split_keys, splits, part);              \
+    if (e != cudaSuccess) return e;                                                           \
   } while (0)
   const int rpw = ceil_div(R, a.window > 0 ? kWinWarps : kSimtWarps);
   if (a.window > 0) {
@@ -694,8 +699,13 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
 #undef SPECV_SIMT
   ++*launches;
 
-  attn_combine_kernel<T><<<dim3(d.Hkv, ceil_div(R, 8), d.B), 256, 0, st>>>(
-      part, a.ctx_lens, req_ok, d, a.window, a.sinks, split_keys, splits, static_cast<T*>(a.out), a.lse);
+  {
+    PdlLaunch L(dim3(d.Hkv, ceil_div(R, 8), d.B), dim3(256), 0, st);
+    e = cudaLaunchKernelEx(&L.cfg, attn_combine_kernel<T>, (const float*)part, a.ctx_lens,
+                           (const int32_t*)req_ok, d, a.window, a.sinks, split_keys, splits,
+                           static_cast<T*>(a.out), a.lse);
+    if (e != cudaSuccess) return e;
+  }
   ++*launches;
   return cudaGetLastError();
 }

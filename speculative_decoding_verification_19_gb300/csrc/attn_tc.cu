@@ -1134,11 +1134,13 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
       bad_block |= (id < 0 || id >= d.num_blocks);
     }
   }
+  __shared__ int32_t s_par[kMaxNodes];  // for the walks to the root below
   int bad_topo = 0;
   if (parent != nullptr) {
     const int32_t* par = parent + (int64_t)b * M;
     for (int n = tid; n < M; n += blockDim.x) {
       const int pn = par[n];
+      s_par[n] = pn;
       bad_topo |= (n == 0) ? (pn != -1) : (pn < 0 || pn >= n);
     }
   }
@@ -1150,17 +1152,16 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
   if (kWin && ok) {
     // depth of each new row, and the mask of the ancestors-or-self that are
     // fewer than `window` positions above it or among the sinks
-    const int32_t* par = parent != nullptr ? parent + (int64_t)b * M : nullptr;
+    const int32_t* par = parent != nullptr ? s_par : nullptr;
     for (int n = tid; n < M; n += blockDim.x)
       win_row_mask(par, n, ctx, window, sinks, anc_ws + (int64_t)b * M + n,
                    depth_ws + (int64_t)b * M + n);
   } else if (ok && parent != nullptr) {
     // ancestor-or-self mask of each tree row (the topology is valid here,
     // so every walk ends at the root within M steps)
-    const int32_t* par = parent + (int64_t)b * M;
     for (int n = tid; n < M; n += blockDim.x) {
       unsigned long long lo = 0, hi = 0;  // bits 0..63, 64..127
-      for (int k = n; k >= 0; k = par[k]) {
+      for (int k = n; k >= 0; k = s_par[k]) {
         if (k < 64) lo |= 1ull << k;
         else hi |= 1ull << (k - 64);
       }
