@@ -1142,9 +1142,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
 // the token stands if u Z is further from both its steps than the masses can
 // be off: per weight 1.47e-7 (ex2.approx: 2^-22.73 is the largest error over
 // all arguments in [-126, 0], measured) and 2 * 2^-24 ln2 |y| for the two
-// roundings of its exponent y, 2 * 2^-24 for the sum of a vector's four pairs
-// (vectors and lanes add up as double-floats); sum w |y| is formed with the
-// mass.  The
+// roundings of its exponent y, 3 * 2^-24 for the sum of two vectors' eight
+// pairs (these sums and the lanes' add up as double-floats); sum w |y| is
+// formed with the mass.  The
 // rounding of log2(e)/T itself is taken out to first order by the same sum.
 // Else (a few rows in a hundred at 150k tokens) the row is drawn exactly.
 constexpr uint32_t kMarkMask = 0xfffff;
@@ -1203,16 +1203,26 @@ __device__ __forceinline__ pair2 fma2(pair2 a, pair2 b, pair2 c) {
   return r;
 }
 
-__device__ __forceinline__ float vec_max(const uint4& r, __nv_bfloat16) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&w[0]);
+// Maximum of a lane's vectors, NaN if any element is.
+template <int N>
+__device__ __forceinline__ float lane_max(const uint4 (&r)[N], __nv_bfloat16) {
+  __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(&r[0].x);
 #pragma unroll
-  for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+  for (int j = 0; j < N; ++j) {
+    const uint32_t w[4] = {r[j].x, r[j].y, r[j].z, r[j].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __hmax2_nan(m, *reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+  }
   return max_nan(__low2float(m), __high2float(m));
 }
-__device__ __forceinline__ float vec_max(const uint4& r, float) {
-  return max_nan(max_nan(__uint_as_float(r.x), __uint_as_float(r.y)),
-                 max_nan(__uint_as_float(r.z), __uint_as_float(r.w)));
+template <int N>
+__device__ __forceinline__ float lane_max(const uint4 (&r)[N], float) {
+  float m = __uint_as_float(r[0].x);
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    m = max_nan(max_nan(max_nan(m, __uint_as_float(r[j].x)), __uint_as_float(r[j].y)),
+                max_nan(__uint_as_float(r[j].z), __uint_as_float(r[j].w)));
+  return m;
 }
 
 // Elements of a vector, none below `low` (whose weight is 0), in pairs.
@@ -1291,9 +1301,7 @@ __global__ void __launch_bounds__(kPlainThreads, 5)
   for (int ch = rank * kPlainWarps + warp; ch < chunks; ch += C * kPlainWarps) {
     uint4 raw[kLaneVecs];
     load_chunk(whole, ch, raw);
-    float m = vec_max(raw[0], T());
-#pragma unroll
-    for (int j = 1; j < kLaneVecs; ++j) m = max_nan(m, vec_max(raw[j], T()));
+    float m = lane_max(raw, T());
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     float4 st = make_float4(m, 0.f, 0.f, 0.f);
@@ -1302,23 +1310,28 @@ __global__ void __launch_bounds__(kPlainThreads, 5)
       const T low = below(m, 300.f / c, T());  // weights below 2^-300 are 0
       pair2 sum = pk(0.f, 0.f), lost = sum, moment = sum;
 #pragma unroll
-      for (int j = 0; j < kLaneVecs; ++j) {
-        pair2 p[kPairs];
-        vec_pairs(raw[j], low, p);
+      for (int j = 0; j < kLaneVecs; j += 2) {
+        pair2 p[2 * kPairs];
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          const pair2 d = add2(p[i], neg);
-          float y0, y1;
-          unpk(mul2(d, c2), y0, y1);
-          const pair2 e = pk(fast_exp2(y0), fast_exp2(y1));
-          moment = fma2(e, d, moment);
-          p[i] = e;
+        for (int v = 0; v < 2; ++v) {
+          pair2 x[kPairs];
+          vec_pairs(raw[j + v], low, x);
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            const pair2 d = add2(x[i], neg);
+            float y0, y1;
+            unpk(mul2(d, c2), y0, y1);
+            const pair2 e = pk(fast_exp2(y0), fast_exp2(y1));
+            moment = fma2(e, d, moment);
+            p[v * kPairs + i] = e;
+          }
         }
 #pragma unroll
-        for (int w = 1; w < kPairs; w *= 2)
+        for (int w = 1; w < 2 * kPairs; w *= 2)
 #pragma unroll
-          for (int i = 0; i + w < kPairs; i += 2 * w) p[i] = add2(p[i], p[i + w]);
-        // the vector's sum joins the lane's, with what the addition rounds off
+          for (int i = 0; i + w < 2 * kPairs; i += 2 * w) p[i] = add2(p[i], p[i + w]);
+        // the two vectors' sum joins the lane's, with what the addition
+        // rounds off
         const pair2 s = add2(sum, p[0]), b = sub2(s, sum);
         lost = add2(lost, add2(sub2(sum, sub2(s, b)), sub2(p[0], b)));
         sum = s;
@@ -1332,7 +1345,7 @@ __global__ void __launch_bounds__(kPlainThreads, 5)
       const dfloat fixed = df_add(s, df_make(mom * 0.693147181f * scale.c_lo));
       st.y = fixed.hi;
       st.z = fixed.lo;
-      st.w = s.hi * (1.47e-7f + 2 * 0x1p-24f) - mom * c * (2 * 0.6931472f * 0x1p-24f);
+      st.w = s.hi * (1.47e-7f + 3 * 0x1p-24f) - mom * c * (2 * 0.6931472f * 0x1p-24f);
     }
     if (lane < C) *cluster.map_shared_rank(&sh.stat[ch], lane) = st;
   }
