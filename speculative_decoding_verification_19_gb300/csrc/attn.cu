@@ -17,7 +17,9 @@
 //                      key range); all group*M query rows that read the KV
 //                      head are handled together, so every K/V byte is read
 //                      once per range.  Online softmax in base 2.
-//   attn_combine_kernel  merges the per-range partials by log-sum-exp.
+//   attn_win_split_kernel  the same over a sliding window and sinks.
+//   attn_combine_kernel  merges the per-range partials by log-sum-exp, a warp
+//                      per row.
 #include <math.h>
 
 #include "attn.cuh"
@@ -313,9 +315,11 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
 // next tile's keys and values are loaded while a tile is used, masks and
 // depths come from the append kernel, tiles that every row sees whole skip
 // the mask, and a score's sum runs over two values of D at once (packed fp32
-// FMA).  8 trees of 64 rows x 8 heads of 64 fp32 values, window 500: 53 us for
-// the call, 38 of them here, where the kernel above with a window took 100 of
-// 147; it waits for shared memory (46% of the issue slots used).
+// FMA).  8 trees of 64 rows x 8 heads of 64 fp32 values, window 500: 49 us for
+// the call, 35 of them here, where the kernel above with a window took 100 of
+// 147; it waits for shared memory (46% of the issue slots used).  Tiles of 64
+// keys, two a lane, need a third fewer loads of the queries and leave registers
+// for two CTAs an SM instead of three: 52 us.
 constexpr int kWinWarps = 8;
 constexpr int kWinThreads = kWinWarps * kWarp;
 

@@ -50,6 +50,22 @@
 //               when the running maximum grows by more than 2^8; at a pair's
 //               end, its output or partial
 //
+// With a sliding window and sinks (page 3 leaves the cache's growth to the
+// engine) a row at position P sees the keys at t < sinks or t > P - window.
+// The kernels' kWin instances then run over the sinks' pages and the window's,
+// the latter in tiles that begin at the window's first page, so a tile is never
+// more than a page emptier than it has to be; the pages between are neither
+// checked nor read.  Rows of a tile that no query row sees are copied as zeros
+// (their pages may not be held), and depth and windowed ancestor mask of every
+// new row come from the prep kernel, for chains too.  Masked tiles -- the
+// sinks' and the window's edges, the new rows -- are tested key by key only in
+// groups of eight keys that some rows see and others do not.  128 requests of
+// 5 rows, 64/8 heads, window 4096 + 4 sinks (2.18 GB): 389 us, 0.83 of the copy
+// rate, where the same keys without a window take 357 us; what is left is the
+// drain at a pair's end (every 67 tiles) and the edges' masks.  32 requests of
+// 9 rows, window 2048: 71 us for 0.24 GB; with one or two pairs a CTA the
+// start, the plan (6 us) and the merge of split pairs are half of it.
+//
 // TMEM: S0..S3 cols [0,64) .. [192,256), O [256,384), P0..P3 (bf16 pairs of
 // S0..S3) [384,416) .. [480,512).  Four S buffers let Q K^T of tile t wait
 // only for P V of tile t-4: the hand-off chain QK -> softmax -> PV -> QK of a
@@ -99,7 +115,10 @@ constexpr int kPCol = kOCol + 128;  // P of S buffer k (bf16 pairs) at kPCol + 3
 // Split cost of one (request, head) segment, in tiles: the Q load, the
 // masks and the drain of the pipeline at a pair's end cost about this much.
 constexpr int kSegCost = 3;
-constexpr int kWinSegCost = 3;
+// With a window, the least cost (tiles plus kSegCost a segment) of a CTA.  One
+// request of 8 KV heads, window 1024: 67 us with its 18 tiles a head over all
+// 152 CTAs (17 partials to merge a pair), 22 with 4, 21 with 8, 23 with 12, 29
+// with 24 (no pair split); window 4096: 40, 30, 28 and 33 with 4, 8, 12, 24.
 constexpr int kWinMinCost = 8;
 constexpr int kPrepThreads = 256;
 constexpr int kPlanReqs = 1024;  // requests whose plan arrays fit the prep kernel's shared memory
@@ -1200,7 +1219,6 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
   // Up to kPlanReqs requests the plan's per-request arrays live in shared
   // memory (no global round trips after the first load), beyond that in the
   // workspace.
-  const int seg = kWin ? kWinSegCost : kSegCost;
   const bool small = B <= kPlanReqs;
   int64_t* tpre = small ? s_tpre : pre;          // [B+1] tiles before request r
   int64_t* cpre = small ? s_cpre : pre + B + 1;  // [B+1] split cost before request r
@@ -1210,7 +1228,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     const int r = base + tid;
     const int nt = r < B ? __ldcg(ntiles + r) : 0;
     const int cx = r < B ? ctx_lens[r] : 0;
-    int64_t vt = (int64_t)nt * Hkv, vc = nt > 0 ? (int64_t)Hkv * (nt + seg) : 0;
+    int64_t vt = (int64_t)nt * Hkv, vc = nt > 0 ? (int64_t)Hkv * (nt + kSegCost) : 0;
     int vm = nt > 0 ? r : -1;
     int64_t tt, tcst;
     int tm;
@@ -1275,11 +1293,11 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
       else hi = mid;
     }
     const int nt = small ? s_nt[r] : __ldcg(ntiles + r);
-    const int64_t per = nt + seg;
+    const int64_t per = nt + kSegCost;
     int64_t rem = at - cpre[r];
     const int h = (int)(rem / per);
     rem -= h * per;
-    const int j = (int)max((int64_t)0, rem - seg);  // rem < nt + seg: j < nt
+    const int j = (int)max((int64_t)0, rem - kSegCost);  // rem < nt + kSegCost: j < nt
     const int g0 = (int)(tpre[r] + (int64_t)h * nt + j);
     starts[2 * k] = make_int4(g0, r, h, j);
     s_g0[k] = g0;
