@@ -42,7 +42,7 @@
 //   3   the kept mass of every warp's run of tokens, exchanged; the warp that
 //       holds u Z walks its run in order
 // Measured (queued calls, us): 640 rows of 152064 bf16 logits, temperature
-// alone, 75 (195 MB: 29 at the copy rate; the stream 54, the marked rows 21);
+// alone, 71 (195 MB: 29 at the copy rate; the stream 53, the marked rows 18);
 // 33 rows of 32001 fp32 logits with mixed filters 28 (44 by the selects over
 // the cluster alone); one row of 32000: 9 without filters, 13 with top-k 50,
 // 18 with top-p 0.9.  A filtered row is bound by its chain of barriers, not by
@@ -1508,7 +1508,7 @@ __global__ void __launch_bounds__(kPlainThreads, 5)
 // token of -2 - i (i counts the marks): cluster i % G of the G takes them.  A
 // few rows in a hundred come here, so the whole GPU shares them, where a CTA
 // that drew its own row exactly kept the others waiting at the end (640 rows
-// of 152064 bf16 logits: 105 us, against 75 us with this kernel).
+// of 152064 bf16 logits: 105 us, against 75 us with this kernel at the time).
 constexpr int kMarkedRows = 4;  // rows a thread looks at in one round
 
 struct MarkedShared {
