@@ -567,12 +567,17 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(
     if (m != -INFINITY) {
 #pragma unroll 4
       for (int s = 0; s < nsp; ++s) {
+        // a partial without a visible key counts for nothing, whatever values of
+        // keys it did not see went into its (unread) sums
         const float* prow = pbase + ((int64_t)s * R + r) * (D + 1);
-        const float w = exp2f(prow[D] - m);  // 0 for a partial without a visible key
+        const float ls = prow[D], w = exp2f(ls - m);
         wsum += w;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < D / kWarp) acc[c] += w * prow[lane + c * kWarp];
+        for (int c = 0; c < 4; ++c) {
+          if (c >= D / kWarp) continue;
+          const float o = prow[lane + c * kWarp];
+          acc[c] += w * (ls == -INFINITY ? 0.f : o);
+        }
       }
     }
     T* orow = out + (((int64_t)b * d.M + i) * d.Hq + hq) * D;

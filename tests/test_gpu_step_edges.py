@@ -191,6 +191,29 @@ def test_window_wait_gives_up_then_recovers():
     assert np.all(np.abs(out.double().cpu().numpy() - o) <= 2e-2 + 1e-2 * np.abs(o))
 
 
+def test_new_values_that_a_row_does_not_see():
+    """Without a window, CUDA cores: the last new rows stand in a key range of
+    their own (the ranges are 256 keys here); what they hold does not reach the
+    rows that see none of them."""
+    M, ctx = 8, 254
+    g = torch.Generator(device="cuda").manual_seed(15)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+    dims = sv.make_dims(B=1, M=M, Hq=4, Hkv=2, D=64, max_blocks=20, num_blocks=20, kv_dtype=F32)
+    ws = sv.workspace(dims)
+    q, kn, vn = r(1, M, 4, 64), r(1, M, 2, 64), r(1, M, 2, 64)
+    kc, vc = r(20, 2, 16, 64), r(20, 2, 16, 64)
+    bt = torch.arange(20, dtype=I32, device="cuda")[None]
+    outs = []
+    for value in (0.5, float("nan"), float("inf")):
+        vn[0, 5] = value
+        out, lse = torch.empty_like(q), torch.empty(1, M, 4, device="cuda")
+        sv.spec_verify_attn(q, kn, vn, kc.clone(), vc.clone(), bt,
+                            torch.tensor([ctx], dtype=I32, device="cuda"), None, out, lse, dims, ws)
+        outs.append(out[0, :2])
+    assert torch.isfinite(outs[0]).all()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
 # ----------------------------------------------------------- lengths and streams
 
 def test_nothing_to_do():
