@@ -445,12 +445,15 @@ spec_status spec_reject_sample_noalloc(const void* target_logits,
  * request gets its pages if the ring holds those that it and all requests
  * before it ask for; else it takes none (it still returns what it no longer
  * needs), its rows get -1, ok is 0 and SPEC_ERR_CAPACITY is raised.  Rows
- * behind the last request's are left as they are.  A request with bad rows or
- * topology (SPEC_ERR_INVALID_ARG), one that needs pages again that its
+ * behind the last request's are left as they are.  A request with a bad length
+ * or topology (SPEC_ERR_INVALID_ARG), one that needs pages again that its
  * window has returned (SPEC_ERR_INVALID_ARG), one whose rows pass max_blocks
  * (SPEC_ERR_CAPACITY) or a bad span (SPEC_ERR_DEVICE_BOUNDS) is left
- * unchanged, with rows of -1 and ok 0.  A bad pool_state leaves every request
- * unchanged.  Calls that share a page state or a workspace must not overlap.
+ * unchanged, with rows of -1 and ok 0.  A bad pool_state (SPEC_ERR_DEVICE_BOUNDS)
+ * leaves every request unchanged, and so does a row_start that does not ascend
+ * within [0, rows] (SPEC_ERR_INVALID_ARG; all of slots and positions are -1
+ * then).  rows and B * max_blocks are at most 2^30.  Calls that share a page
+ * state or a workspace must not overlap.
  */
 spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
                               const int32_t* parent, int32_t rows, int32_t window, int32_t sinks,
@@ -467,7 +470,8 @@ spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
  *   y = x * rsqrt(mean(x^2) + eps) * weight       (no norm without a weight)
  *   (a, b) -> (a cos - b sin, b cos + a sin), angle t * inv_freq[j], for the
  *   pairs (j, j + rot_dim/2), or (2j, 2j + 1) if interleaved, j < rot_dim/2
- * in fp32 (angles reduced exactly), rounded once.  rows = 0 does nothing.
+ * in fp32 (angles reduced exactly), rounded once; values of q and k have to be
+ * finite.  rows = 0 does nothing.
  *
  *   q [rows, Hq, D], k, v [rows, Hkv, D]  kv_dtype   rows q_stride, k_stride,
  *                 v_stride elements apart (multiples of 16 bytes), heads dense:

@@ -37,6 +37,10 @@ def oracle_block_tables(ctx_lens, row_start, parent, rows, block_table, span, po
     if not pool_ok:
         status |= 1 << BOUNDS
     sink_pages = -(-sinks // block) if window else 0
+    rows_ok = row_start is None or bool(
+        np.all(np.diff(row_start) >= 0) and row_start[0] >= 0 and row_start[B] <= rows)
+    if not rows_ok:  # every row is none's
+        slots[:rows], positions[:rows] = -1, -1
 
     def pages(lo, hi):
         return {p for p in range(hi) if p < sink_pages or p >= lo}
@@ -53,7 +57,7 @@ def oracle_block_tables(ctx_lens, row_start, parent, rows, block_table, span, po
         code = None
         if not pool_ok or not 0 <= lo <= hi <= max_blocks:
             code = BOUNDS
-        elif ctx < -1 or not 0 <= r0 <= r1 <= rows:
+        elif ctx < -1 or not rows_ok:
             code = INVALID
         elif parent is not None and ctx >= 0 and (
                 parent[b, 0] != -1 or any(not 0 <= parent[b, n] < n for n in range(1, M))):
@@ -89,7 +93,7 @@ def oracle_block_tables(ctx_lens, row_start, parent, rows, block_table, span, po
                 table[b, p] = -1
             new_state.append((b, lo2, hi2))
         ok[b] = served
-        for r in range(max(0, r0), min(r1, rows)):
+        for r in range(r0, r1) if rows_ok else ():
             slots[r], positions[r] = -1, -1
             if served:
                 i = r - r0

@@ -432,6 +432,9 @@ spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
   if (dims->B > 65535) return SPEC_ERR_UNSUPPORTED;
   if (dims->max_blocks < 1 || dims->num_blocks < 1) return SPEC_ERR_INVALID_ARG;
   if ((int64_t)dims->max_blocks * kBlock > INT32_MAX) return SPEC_ERR_UNSUPPORTED;
+  // counts of rows and pages, and a grid's stride past them, stay 32-bit
+  if (rows > kPagesMaxItems || (int64_t)dims->B * dims->max_blocks > kPagesMaxItems)
+    return SPEC_ERR_UNSUPPORTED;
   if ((s = check_ws(dims, ws, ws_bytes)) != SPEC_OK) return s;
   if (!ctx_lens || !block_table || !span || !pool || !pool_state) return SPEC_ERR_INVALID_ARG;
   if (rows > 0 && (!slots || !positions)) return SPEC_ERR_INVALID_ARG;

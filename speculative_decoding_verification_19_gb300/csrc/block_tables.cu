@@ -67,9 +67,15 @@ __device__ __forceinline__ int pos_part(int x) { return x > 0 ? x : 0; }
 __device__ __forceinline__ int take_low(int hi, int hi2, int sp) { return pos_part(min(sp, hi2) - hi); }
 __device__ __forceinline__ int take_from(int hi, int lo2, int sp) { return max(hi, max(lo2, sp)); }
 
-// One round: the records and prefixes of requests base .. base + 511.
+// Rows [r0, r1) that cannot be a request's.
+__device__ __forceinline__ bool bad_rows(int r0, int r1, int rows) {
+  return r0 < 0 || r1 < r0 || r1 > rows;
+}
+
+// One round: the records and prefixes of requests base .. base + 511.  rows_ok:
+// row_start ascends within the rows (found here when the round is the only one).
 __device__ void plan_round(Shared& sh, const PageArgs& a, int base, int sp, bool pool_ok, int count,
-                           Carry& carry, uint32_t* status, bool report) {
+                           bool& rows_ok, Carry& carry, uint32_t* status, bool report) {
   const int tid = threadIdx.x, lane = tid % kWarp, warp = tid / kWarp;
   const int B = a.d.B, M = a.d.M, mb = a.d.max_blocks;
   const int b = base + tid;
@@ -87,9 +93,13 @@ __device__ void plan_round(Shared& sh, const PageArgs& a, int base, int sp, bool
       r0 = b * M;
       r1 = r0 + M;
     }
+  }
+  if (a.row_start != nullptr && B <= kThreads)
+    rows_ok = !__syncthreads_or(b < B && bad_rows(r0, r1, a.rows));
+  if (b < B) {
     int code = 0;
     if (!pool_ok || lo < 0 || lo > hi || hi > mb) code = SPEC_ERR_DEVICE_BOUNDS;
-    else if (ctx < -1 || r0 < 0 || r1 < r0 || r1 > a.rows) code = SPEC_ERR_INVALID_ARG;
+    else if (ctx < -1 || !rows_ok) code = SPEC_ERR_INVALID_ARG;
     if (a.parent != nullptr && ctx >= 0) {
       const int32_t* par = a.parent + (int64_t)b * M;
       bool bad = par[0] != -1;
@@ -213,9 +223,15 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
   const bool pool_ok = head >= 0 && head < nb && count >= 0 && count <= nb;
   if (!pool_ok && blockIdx.x == 0 && tid == 0) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
   const int gt = blockIdx.x * kThreads + tid, gn = gridDim.x * kThreads;
+  bool rows_ok = true;  // one entry out of order leaves no row certain
+  if (a.row_start != nullptr && B > kThreads) {
+    int bad = 0;
+    for (int b = tid; b < B; b += kThreads) bad |= bad_rows(a.row_start[b], a.row_start[b + 1], a.rows);
+    rows_ok = !__syncthreads_or(bad);
+  }
   Carry carry{0, 0, 0};
   for (int base = 0; base < B; base += kThreads) {
-    plan_round(sh, a, base, sp, pool_ok, count, carry, status, blockIdx.x == 0);
+    plan_round(sh, a, base, sp, pool_ok, count, rows_ok, carry, status, blockIdx.x == 0);
     const int n = min(kThreads, B - base);
     const int n_take = sh.take_pre[kThreads], n_give = sh.give_pre[kThreads];
     // pages given back: to the ring's tail, their table entries cleared
@@ -246,10 +262,11 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
     }
     // rows: slot and position; an entry of a page taken by this call is read
     // from the ring, not from the table that another CTA may be writing
-    const int row_lo = max(0, sh.row0[0]), row_hi = min(a.rows, sh.row0[n]);
+    // (row_start out of order: every row is none's)
+    const int row_lo = rows_ok ? sh.row0[0] : 0;
+    const int row_hi = rows_ok ? sh.row0[n] : (base == 0 ? a.rows : 0);
     for (int row = row_lo + gt; row < row_hi; row += gn) {
-      const int r = a.row_start != nullptr ? find(sh.row0, n, row) : row / M - base;
-      if (row < sh.row0[r] || row >= sh.row0[r + 1]) continue;
+      const int r = !rows_ok ? 0 : a.row_start != nullptr ? find(sh.row0, n, row) : row / M - base;
       int64_t slot = -1;
       int pos = -1;
       if (sh.good[r] == 2) {
@@ -293,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
   }
   Carry again{0, 0, 0};
   for (int base = 0; base < B; base += kThreads) {
-    if (B > kThreads) plan_round(sh, a, base, sp, pool_ok, count, again, status, false);
+    if (B > kThreads) plan_round(sh, a, base, sp, pool_ok, count, rows_ok, again, status, false);
     const int b = base + tid;
     if (b < B) {
       if (a.ok != nullptr) a.ok[b] = sh.good[tid] == 2;

@@ -5,6 +5,9 @@
 
 namespace specv {
 
+// Most rows, and most block-table entries, of one call.
+constexpr int kPagesMaxItems = 1 << 30;
+
 struct PageArgs {
   const int32_t* ctx_lens;
   const int32_t* row_start;

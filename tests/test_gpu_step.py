@@ -114,8 +114,11 @@ def test_pages_refused_requests_stay_as_they_are():
     # past the table; bad length; window pages needed again; rows out of range
     out = st.call(np.array([63, -2, 30, 40]), None, 8)
     assert out["ok"].tolist() == [0, 0, 1, 1] and out["status"] == (1 << 2 | 1 << 1)
-    out = st.call(np.array([10, 20, 30, 40]), np.array([0, 2, 1, 3, 99]), 8)
-    assert out["ok"].tolist() == [1, 0, 1, 0]
+    # one row out of order or out of range leaves no request's rows certain
+    for start in ([0, 2, 1, 3, 4], [0, 2, 4, 6, 99], [-1, 2, 4, 6, 8], [0, 500, 4, 6, 8]):
+        out = st.call(np.array([10, 20, 30, 40]), np.array(start), 8)
+        assert out["ok"].sum() == 0 and out["status"] == 1 << 1
+        assert np.all(out["slots"] == -1) and np.all(out["positions"] == -1)
     st.call(np.array([60, 20, 30, 40]), None, 8, window=17)
     out = st.call(np.array([3, 20, 30, 40]), None, 8, window=17)
     assert out["ok"].tolist()[0] == 0
@@ -131,6 +134,18 @@ def test_pages_refused_requests_stay_as_they_are():
     st.d["pool_state"][1] = 13
     out = st.call(np.array([60, 20, 30, 43]), None, 8, window=17)
     assert out["ok"].sum() == 0 and out["status"] == 1 << 6
+
+
+def test_pages_rows_out_of_order_among_many_requests():
+    st = Pages(1200, 4, 3000)
+    start = np.arange(1201)
+    st.call(np.full(1200, 5), start, 1203)
+    for at, value in ((1100, 3), (600, 1300), (0, -1)):
+        bad = start.copy()
+        bad[at] = value
+        out = st.call(np.full(1200, 20), bad, 1203)
+        assert out["ok"].sum() == 0 and np.all(out["slots"] == -1)
+    assert st.call(np.full(1200, 20), start, 1203)["ok"].all()
 
 
 def test_pages_captured_and_replayed():

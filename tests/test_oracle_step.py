@@ -227,6 +227,9 @@ def test_block_table_refusals(lib):
         assert call(**kw) == 1, kw
     assert call(_dims(max_blocks=0)) == 1 and call(_dims(num_blocks=0)) == 1
     assert call(_dims(max_blocks=1 << 27)) == 3
+    # more rows or table entries than 32-bit counts hold
+    assert call(rows=(1 << 30) + 1) == 3 and call(rows=(1 << 30) + 1, row_start=P) == 3
+    assert call(_dims(B=17, max_blocks=1 << 26), rows=51) == 3
 
 
 def test_norm_rope_refusals(lib):
