@@ -214,6 +214,89 @@ def test_new_values_that_a_row_does_not_see():
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
+# --------------------------------------------- offsets that pass 32 bits
+
+@pytest.mark.parametrize("dt,D,impl", [(BF, 128, sv.ATTN_TENSOR_CORES), (BF, 128, sv.ATTN_CUDA_CORES),
+                                       (F32, 64, sv.ATTN_CUDA_CORES)])
+def test_a_cache_of_more_than_2_31_values(dt, D, impl):
+    """Norm and rotation with the cache written, and windowed attention, on the
+    last blocks of a cache of 2.3e9 values, against the same blocks in a cache
+    of their own: the same bits."""
+    B, M, Hq, Hkv, mb, need = 2, 3, 4, 2, 7, 14
+    nb = int(2.3e9) // (Hkv * 16 * D)
+    g = torch.Generator(device="cuda").manual_seed(16)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g).to(dt)  # noqa: E731
+    q, k, v = rand(B * M, Hq, D), rand(B * M, Hkv, D), rand(B * M, Hkv, D)
+    kc0, vc0 = rand(need, Hkv, 16, D), rand(need, Hkv, 16, D)
+    inv = to_dev(10000.0 ** (-np.arange(D // 2) / (D // 2)), torch.float64)
+    ctx = np.array([100, 47])
+    table = torch.arange(need, device="cuda", dtype=I32).flip(0).view(B, mb).contiguous()
+    runs = []
+    for blocks, first in ((need, 0), (nb, nb - need)):
+        kc = torch.zeros(blocks, Hkv, 16, D, dtype=dt, device="cuda")
+        vc = torch.zeros(blocks, Hkv, 16, D, dtype=dt, device="cuda")
+        kc[first:], vc[first:] = kc0, vc0
+        dims = sv.make_dims(B=B, M=M, Hq=Hq, Hkv=Hkv, D=D, max_blocks=mb, num_blocks=blocks,
+                            kv_dtype=dt, attn_impl=impl)
+        ws = sv.workspace(dims)
+        t = np.concatenate([np.arange(c, c + M) for c in ctx])
+        page = (table.cpu().numpy()[np.arange(B * M) // M, t // 16] + first).astype(np.int64)
+        qo, ko = torch.empty_like(q), torch.empty_like(k)
+        sv.spec_qk_norm_rope(q, k, v, None, None, to_dev(t, I32), inv, qo, ko, dims, ws,
+                             slots=to_dev(page * 16 + t % 16, torch.int64), k_cache=kc, v_cache=vc)
+        written = kc[first:].clone(), vc[first:].clone()
+        out, lse = torch.empty_like(qo).view(B, M, Hq, D), torch.empty(B, M, Hq, device="cuda")
+        sv.spec_verify_attn(qo.view(B, M, Hq, D), ko.view(B, M, Hkv, D), v.view(B, M, Hkv, D), kc, vc,
+                            table + first, to_dev(ctx, I32), None, out, lse, dims, ws, window=60,
+                            sinks=2)
+        assert sv.device_status(ws) == 0
+        assert not kc[:first].any() and not vc[:first].any()
+        runs.append((qo, ko, *written, out, lse, kc[first:].clone(), vc[first:].clone()))
+        del kc, vc
+    for x, y in zip(*runs):
+        assert torch.equal(x, y)
+    assert torch.isfinite(runs[0][4]).all() and not torch.equal(runs[0][2], kc0)
+    torch.cuda.empty_cache()
+
+
+def test_rows_of_more_than_2_31_values():
+    """Many rows of queries (in place), and logits whose rows stand far apart."""
+    rows, Hq = 265000, 64
+    q = torch.zeros(rows, Hq, 128, dtype=BF, device="cuda")
+    k = torch.zeros(rows, 1, 128, dtype=BF, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(17)
+    some = torch.randn(6, Hq, 128, device="cuda", generator=g).to(BF)
+    q[-6:], k[-6:] = some, some[:, :1]
+    w = torch.full((128,), 1.5, dtype=BF, device="cuda")
+    inv = to_dev(10000.0 ** (-np.arange(64) / 64), torch.float64)
+    pos = torch.arange(rows, device="cuda", dtype=I32)
+    dims = sv.make_dims(B=1, M=1, Hq=Hq, Hkv=1, D=128)
+    ws = sv.workspace(dims)
+    few_q, few_k = torch.empty_like(some), torch.empty_like(k[-6:])
+    sv.spec_qk_norm_rope(some, k[-6:].clone(), None, w, w, pos[-6:], inv, few_q, few_k, dims, ws)
+    sv.spec_qk_norm_rope(q, k, None, w, w, pos, inv, q, k, dims, ws)
+    assert torch.equal(q[-6:], few_q) and torch.equal(k[-6:], few_k)
+    assert not q[:-6].any() and not k[:-6].any()
+    del q, k
+
+    V, stride = 50021, 1 << 30
+    far = torch.empty(2 * stride + V, dtype=BF, device="cuda")
+    x = far.as_strided((3, V), (stride, 1))
+    x.copy_(torch.randn(3, V, device="cuda", generator=g).to(BF))
+    one, u = torch.ones(3, device="cuda"), torch.full((3,), 0.625, device="cuda")
+    for kw in ({}, dict(top_k=torch.full((3,), 50, dtype=I32, device="cuda")),
+               dict(top_p=one * 0.99), dict(min_p=one * 0.01)):
+        got = []
+        for logits in (x, x.contiguous()):
+            tok = torch.empty(3, dtype=I32, device="cuda")
+            sv.spec_sample(logits, one, u, tok, None, ws, **kw)
+            got.append(tok)
+        assert torch.equal(*got) and (got[0] >= 0).all()
+    assert sv.device_status(ws) == 0
+    del far, x
+    torch.cuda.empty_cache()
+
+
 # ----------------------------------------------------------- lengths and streams
 
 def test_nothing_to_do():
