@@ -1240,7 +1240,11 @@ __device__ __forceinline__ void vec_pairs(const uint4& r, float low, pair2 (&p)[
   p[0] = pk(fmaxf(__uint_as_float(r.x), low), fmaxf(__uint_as_float(r.y), low));
   p[1] = pk(fmaxf(__uint_as_float(r.z), low), fmaxf(__uint_as_float(r.w), low));
 }
-// A value of the type at or below m - gap, and below m.
+// The type's lowest finite value.
+__device__ __forceinline__ float lowest(__nv_bfloat16) { return __uint_as_float(0xff7f0000u); }
+__device__ __forceinline__ float lowest(float) { return __uint_as_float(0xff7fffffu); }
+// A value of the type at or below m - gap, and below m (a finite one if m is
+// not the lowest).
 __device__ __forceinline__ __nv_bfloat16 below(float m, float gap, __nv_bfloat16) {
   const uint32_t b = __float_as_uint(m) >> 16;  // m is a bf16
   const uint32_t next = m > 0.f ? b - 1 : (m < 0.f ? b + 1 : 0x8001u);
@@ -1305,7 +1309,19 @@ __global__ void __launch_bounds__(kPlainThreads, 5)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     float4 st = make_float4(m, 0.f, 0.f, 0.f);
-    if (m < INFINITY && m > -INFINITY && !greedy) {
+    if (m == lowest(T())) {
+      // a wholly masked chunk: its tokens at the lowest value weigh 1 each (no
+      // value is below it but -inf, whose exponent would spoil the moment)
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < kLaneVecs; ++j) {
+        float x[kVec];
+        unpack16(raw[j], x);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) n += x[i] == m;
+      }
+      st.y = (float)__reduce_add_sync(0xffffffffu, n);
+    } else if (m < INFINITY && m > -INFINITY && !greedy) {
       const pair2 neg = pk(-m, -m), c2 = pk(c, c);
       const T low = below(m, 300.f / c, T());  // weights below 2^-300 are 0
       pair2 sum = pk(0.f, 0.f), lost = sum, moment = sum;

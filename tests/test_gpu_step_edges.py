@@ -73,6 +73,35 @@ def test_sample_many_rows_without_filters(dt, scale):
     assert np.array_equal(again[0][sure[:20]], tok[few][sure[:20]])
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("mask", ["lowest", "inf"])
+def test_sample_masked_vocabulary(dt, mask):
+    """Tokens masked by the type's lowest value or by -inf, to the row's end and
+    in whole chunks between: the draws stay right, and no more rows than
+    without a mask need the second look."""
+    g = torch.Generator(device="cuda").manual_seed(18)
+    n, V = 700, 30011
+    x = (torch.randn(n, V, device="cuda", generator=g) * 2).to(dt)
+    low = float(torch.finfo(dt).min) if mask == "lowest" else -math.inf
+    x[:, 200:9000] = low
+    x[:, 9300:] = low
+    x[3, 1:] = low   # one token left
+    x[4, :-1], x[4, -1] = low, 0.5  # the last one
+    rng = np.random.default_rng(19)
+    T = rng.choice([0.5, 1.0, 2.0], n).astype(np.float32)
+    u = (rng.integers(0, 1 << 24, n) / (1 << 24)).astype(np.float32)
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    tok, prob = torch.empty(n, dtype=I32, device="cuda"), torch.empty(n, device="cuda")
+    sv.spec_sample(x, to_dev(T, F32), to_dev(u, F32), tok, prob, ws)
+    assert sv.device_status(ws) == 0
+    assert int(ws.view(I32)[1]) < n // 10
+    i, p, near = sample_ref(x, T, u)
+    sure = near > 1e-9
+    assert sure.mean() > 0.95
+    assert np.array_equal(tok.cpu().numpy()[sure], i[sure])
+    assert np.all(np.abs(prob.cpu().numpy()[sure] - p[sure]) <= 2.0 ** -21 * p[sure])
+
+
 def test_sample_many_rows_of_the_largest_vocabulary():
     g = torch.Generator(device="cuda").manual_seed(5)
     n, V = 304, 1 << 20
