@@ -982,7 +982,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
     __syncthreads();
     uint2* list = reinterpret_cast<uint2*>(data + (kSmem ? nv : 0));
     uint2* to = cluster.map_shared_rank(list, 0) + rank * places;
-    const uint32_t low = max(theta, kKeyNegInf + 1);
+    // tokens of no weight (2^-120 of the largest: those masked by a low value,
+    // for instance) need no place, whatever the filters keep of them
+    const uint32_t low =
+        max(max(theta, kKeyNegInf + 1), order_key(m - 120.5f / law.c_hi));
     dfloat z = df_make(0.f);
     long long mass = 0;
     for (int v0 = 0; v0 < nv; v0 += kThreads) {

@@ -102,6 +102,29 @@ def test_sample_masked_vocabulary(dt, mask):
     assert np.all(np.abs(prob.cpu().numpy()[sure] - p[sure]) <= 2.0 ** -21 * p[sure])
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("V,live", [(30011, 40), (30011, 700), (128256, 6000)])
+def test_sample_masked_vocabulary_with_filters(dt, V, live):
+    """A mask of the type's lowest value draws as one of -inf does: the masked
+    tokens have no mass, and they are the last that top-k takes."""
+    g = torch.Generator(device="cuda").manual_seed(20)
+    n = 40
+    x = torch.randn(n, V, device="cuda", generator=g).to(dt)
+    masked = torch.rand(V, device="cuda", generator=g).argsort() >= live
+    rng = np.random.default_rng(21)
+    T = rng.choice([0.5, 1.0, 2.0], n).astype(np.float32)
+    u = (rng.integers(0, 1 << 24, n) / (1 << 24)).astype(np.float32)
+    k = rng.choice([0, 1, 30, 50, 1000, V - 1], n)
+    p = rng.choice([1.0, 0.1, 0.9, 0.999], n).astype(np.float32)
+    mp = rng.choice([0.0, 0.01, 0.3], n).astype(np.float32)
+    for kw in (dict(k=k), dict(p=p), dict(mp=mp), dict(k=k, p=p), dict(k=k, p=p, mp=mp)):
+        got = [sample_gpu(x.masked_fill(masked, low), T, u, **kw)
+               for low in (float(torch.finfo(dt).min), -math.inf)]
+        assert np.array_equal(got[0][0], got[1][0]) and got[0][2] == got[1][2] == 0
+        assert np.all(np.abs(got[0][1] - got[1][1]) <= 2.0 ** -21 * got[1][1])
+        assert not masked.cpu().numpy()[got[0][0]].any()
+
+
 def test_sample_many_rows_of_the_largest_vocabulary():
     g = torch.Generator(device="cuda").manual_seed(5)
     n, V = 304, 1 << 20
