@@ -125,6 +125,23 @@ def test_sample_masked_vocabulary_with_filters(dt, V, live):
         assert not masked.cpu().numpy()[got[0][0]].any()
 
 
+@pytest.mark.parametrize("V,dt", [(152064, F32), (1 << 20, BF)])
+def test_sample_cut_inside_many_equal_tokens(V, dt):
+    """Few distinct values, so that a filter's cut falls inside a value's
+    tokens, and runs long enough to be shared out among a CTA's warps."""
+    rng = np.random.default_rng(22)
+    n = 10
+    x = np.round(rng.normal(size=(n, V)) * 2) / 2
+    u = rng.integers(0, 1 << 24, n) / (1 << 24)
+    k = rng.choice([0, 5000, V // 3, V - 7], n)
+    k[:2] = (5000, V // 3)
+    p = rng.choice([1.0, 0.7, 0.98], n)
+    mp = rng.choice([0.0, 0.02], n)
+    sample_check(x, np.ones(n), u, k=k, dt=dt)
+    sample_check(x, np.ones(n), u, p=p, dt=dt)
+    sample_check(x, np.full(n, 0.8), u, k=k, p=p, mp=mp, dt=dt)
+
+
 def test_sample_many_rows_of_the_largest_vocabulary():
     g = torch.Generator(device="cuda").manual_seed(5)
     n, V = 304, 1 << 20
