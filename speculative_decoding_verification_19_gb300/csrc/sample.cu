@@ -37,15 +37,17 @@
 //       CTA, which finishes the row alone.  The bound comes from the threads'
 //       maxima: if n of them reach v, at least n tokens do; for top-k that
 //       makes it safe, for top-p the candidates' mass is checked
-//   2   else (a large k, a top-p that reaches far down) a radix select over
-//       the slices' order keys, on counts or on masses, gives the threshold
+//   2   else (a large k, a top-p that reaches far down) a select over the
+//       slices' order keys, on counts or on masses, gives the threshold: for
+//       bf16 over the values themselves, else level by level
 //   3   the kept mass of every warp's run of tokens, exchanged; the warp that
 //       holds u Z walks its run in order
 // Measured (queued calls, us): 640 rows of 152064 bf16 logits, temperature
-// alone, 71 (195 MB: 29 at the copy rate; the stream 53, the marked rows 18);
-// 33 rows of 32001 fp32 logits with mixed filters 28 (44 by the selects over
+// alone, 72 (195 MB: 29 at the copy rate; the stream 50, the marked rows 21);
+// 33 rows of 32001 fp32 logits with mixed filters 27 (44 by the selects over
 // the cluster alone); one row of 32000: 9 without filters, 13 with top-k 50,
-// 18 with top-p 0.9.  A filtered row is bound by its chain of barriers, not by
+// 18 with top-p 0.9; 33 rows of 128256 bf16 logits with a top-p that keeps
+// 30000 tokens 80.  A filtered row is bound by its chain of barriers, not by
 // bytes; the slowest are rows whose top-p reaches past the candidates.
 #include <cooperative_groups.h>
 #include <math.h>
@@ -115,6 +117,7 @@ struct Shared {
   int sel_bin;
   uint32_t sel_above, sel_count;
   long long sel_mass;
+  uint32_t mid[3];  // value_select: mass of the values about zero, in limbs
 };
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -258,6 +261,148 @@ struct Selected {
   long long mass;  // of the tokens above tau (when masses were summed)
 };
 
+// Select for bf16 logits, arguments as in radix_select below: a 16-bit value
+// has few neighbours, so a bin holds one value, tokens are only counted and a
+// bin's mass is its count times one weight -- one level, one atomic a token,
+// no weight a token.  The bins run down from the largest value: kDirectBins
+// values, those within 2^-10 of zero (36000 of the 65536) together in one bin
+// whose mass is summed.  Not resolved (false) if the place lies in that bin or
+// past the last one.  Each CTA sums its share of the bins over the cluster and
+// the place is found by running sums over the shares.  (33 rows of 128256
+// logits, top-p 0.9 of a normal law of deviation 2: 81 us, against 157 with
+// the levels below; top-k 5000 and that: 56 against 122; 32001 logits: 37
+// against 43 and 34 against 46.)  `buf` is -1 before any select, 2 after this
+// one.
+constexpr int kDirectBins = 8 * kBins;
+// The order key of a bf16 value from its upper half: the bits below are zeros,
+// or ones for a negative value.
+__device__ __forceinline__ uint32_t full_key(uint32_t key) {
+  return key & 0x8000u ? key << 16 : (key << 16) | 0xffffu;
+}
+constexpr uint32_t kMidHigh = 0xba80u, kMidLow = 0x457fu;  // keys of 2^-10 and -2^-10
+
+template <typename T, bool kSmem>
+__device__ bool value_select(Shared& sh, const Slice<T, kSmem>& sl, int nv, const Law& law,
+                             uint32_t low, uint32_t high, bool by_mass, bool with_mass,
+                             long long rank, long long mass, int C, int& buf, Selected& r) {
+  constexpr int kVec = Slice<T, kSmem>::kVec, kPer = kDirectBins / kThreads;
+  static_assert(kPer == 8 && sizeof(sh.hist) == kDirectBins * 4, "both buffers, 8 bins a thread");
+  const int tid = threadIdx.x, rank_of = blockIdx.x % C;
+  cg::cluster_group cluster = cg::this_cluster();
+  const uint32_t top = high >> 16;
+  const int mid = top >= kMidHigh ? (int)(top - kMidHigh) + 1 : top > kMidLow ? 0 : -1;
+  if (buf == 2) __syncthreads();  // the last select's sel_* are read
+  else if (buf >= 0) cluster_sync();  // and its bins, by the other CTAs
+  buf = 2;
+  uint32_t* hist = &sh.hist[0][0][0];
+  for (int i = tid; i < kDirectBins; i += kThreads) hist[i] = 0;
+  if (tid < 3) sh.mid[tid] = 0;
+  if (tid == 0) sh.sel_bin = -1;
+  __syncthreads();
+  for (int v = tid; v < nv; v += kThreads) {
+    const uint4 raw = sl.get(v);
+    float x[kVec];
+    unpack16(raw, x);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const uint32_t full = order_key(x[i]), key = full >> 16;
+      if (full < low || full <= kKeyNegInf) continue;
+      const uint32_t at = mid < 0 || key >= kMidHigh ? top - key
+                          : key > kMidLow            ? (uint32_t)mid
+                                                     : mid + 1 + (kMidLow - key);
+      if (at >= (uint32_t)kDirectBins) continue;
+      atomicAdd(hist + at, 1u);
+      if (with_mass && (int)at == mid) {
+        uint32_t l[3];
+        fixed_limbs(law.weight(x[i]), l);
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (l[j] != 0) atomicAdd(&sh.mid[j], l[j]);
+      }
+    }
+  }
+  cluster_sync();
+  // each CTA sums its share of the bins over the cluster, 8 / C of them a thread
+  const int per = kPer / C, b0 = (rank_of * kThreads + tid) * per;
+  uint32_t cnt[kPer], c = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) cnt[i] = 0;
+#pragma unroll
+  for (int q = 0; q < kMaxCluster; ++q) {
+    if (q >= C) break;
+    const uint32_t* h = cluster.map_shared_rank(hist, q) + b0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < per) cnt[i] += h[i];
+  }
+  long long mid_mass = 0;
+  if (with_mass && mid >= b0 && mid < b0 + per)
+    for (int q = 0; q < C; ++q) {
+      const uint32_t* l = cluster.map_shared_rank(&sh.mid[0], q);
+      mid_mass += limbs_value(l[0], l[1], l[2]);
+    }
+  // mass of a bin's tokens
+  auto bin_mass = [&](int i) -> long long {
+    const int at = b0 + i;
+    if (at == mid) return mid_mass;
+    const uint32_t key = mid < 0 || at < mid ? top - at : kMidLow - (at - mid - 1);
+    return cnt[i] == 0 ? 0 : cnt[i] * fixed_value(law.weight(key_value(full_key(key))));
+  };
+  long long m = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    c += cnt[i];
+    if (with_mass) m += bin_mass(i);
+  }
+  uint32_t ci = c;
+  long long mi = m;
+  block_running(sh, ci, mi, with_mass);
+  if (tid == kThreads - 1)
+    for (int q = 0; q < C; ++q) {
+      *cluster.map_shared_rank(&sh.ex_n[rank_of], q) = (int)ci;
+      *cluster.map_shared_rank(&sh.ex_mass[rank_of], q) = mi;
+    }
+  cluster_sync();
+  for (int q = 0; q < rank_of; ++q) {
+    ci += sh.ex_n[q];
+    mi += sh.ex_mass[q];
+  }
+  const long long want = by_mass ? mass : rank;
+  if ((by_mass ? mi - m : (long long)(ci - c)) < want && want <= (by_mass ? mi : (long long)ci)) {
+    uint32_t above = ci - c, count = 0;
+    long long over = mi - m;
+    int bin = -1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (i >= per || bin >= 0) continue;
+      const long long bm = with_mass ? bin_mass(i) : 0;
+      if (want <= (by_mass ? over + bm : (long long)(above + cnt[i]))) {
+        bin = b0 + i;
+        count = cnt[i];
+      } else {
+        above += cnt[i];
+        over += bm;
+      }
+    }
+    for (int q = 0; q < C; ++q) {
+      *cluster.map_shared_rank(&sh.sel_bin, q) = bin;
+      *cluster.map_shared_rank(&sh.sel_above, q) = above;
+      *cluster.map_shared_rank(&sh.sel_mass, q) = over;
+      *cluster.map_shared_rank(&sh.sel_count, q) = count;
+    }
+  }
+  cluster_sync();
+  const int at = sh.sel_bin;
+  if (at < 0 || at == mid) return false;
+  const uint32_t key = mid < 0 || at < mid ? top - at : kMidLow - (at - mid - 1);
+  r.found = true;
+  r.tau = full_key(key);
+  r.above = sh.sel_above;
+  r.ties = sh.sel_count;
+  r.mass = sh.sel_mass;
+  return true;
+}
+
 // Radix select over the tokens with order key >= low (the largest key being
 // `high`): the value of rank `rank` (1 = largest), or, with by_mass, the first
 // at which the running mass reaches `mass`.  Not found when all of them
@@ -275,6 +420,17 @@ __device__ Selected radix_select(Shared& sh, const Slice<T, kSmem>& sl, int nv, 
   const int tid = threadIdx.x;
   cg::cluster_group cluster = cg::this_cluster();
   Selected r{true, 0, 0, 0, 0};
+  // counts alone are as quick in the levels below while a slice is short (one
+  // row, top-k 5000: 32001 logits 14 us, 18 by value_select, 128256 24 and 27;
+  // 33 of those rows, slices of 32064: 52 and 42)
+  constexpr int kShortSlice = 20000;
+  if constexpr (sizeof(T) == 2) {
+    if ((with_mass || nv * kVec > kShortSlice) &&
+        value_select<T, kSmem>(sh, sl, nv, law, low, high, by_mass, with_mass, rank, mass, C, buf, r))
+      return r;
+  }
+  if (buf == 2) __syncthreads();  // value_select's sel_* are read
+  if (buf != 1) buf = 0;
   if (low <= kKeyNegInf) low = kKeyNegInf + 1;
   uint32_t base = low >> kShift;
   int bits = 32 - __clz((high >> kShift) - base);  // keys base .. base + 2^bits - 1
@@ -342,9 +498,7 @@ __device__ Selected radix_select(Shared& sh, const Slice<T, kSmem>& sl, int nv, 
     bits = sh_bits;
     __syncthreads();  // sel_* are read
   } while (bits > 0);
-  // the bits below a bf16 key: zeros, or ones for a negative value
-  const uint32_t key = base << kShift;
-  r.tau = sizeof(T) == 2 && !(key & 0x80000000u) ? key | 0xffffu : key;
+  r.tau = sizeof(T) == 2 ? full_key(base) : base;
   return r;
 }
 
@@ -1020,6 +1174,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
   }
 
   const Law law(m, T_, sh.draw.pow2);
+  // below it tokens weigh nothing (2^-120 of the largest: those masked by a low
+  // value, for instance) and need no place, whatever the filters keep of them
+  const uint32_t weightless = max(kKeyNegInf + 1, order_key(m - 120.5f / law.c_hi));
 
   // ---- 2a: few candidates go to the first CTA, which finishes the row
   dfloat total = df_make(0.f);  // mass of every token (top-p without top-k)
@@ -1030,10 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
     __syncthreads();
     uint2* list = reinterpret_cast<uint2*>(data + (kSmem ? nv : 0));
     uint2* to = cluster.map_shared_rank(list, 0) + rank * places;
-    // tokens of no weight (2^-120 of the largest: those masked by a low value,
-    // for instance) need no place, whatever the filters keep of them
-    const uint32_t low =
-        max(max(theta, kKeyNegInf + 1), order_key(m - 120.5f / law.c_hi));
+    const uint32_t low = max(theta, weightless);
     dfloat z = df_make(0.f);
     long long mass = 0;
     for (int v0 = 0; v0 < nv; v0 += kThreads) {
@@ -1114,7 +1268,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
   // ---- 2: the filters' threshold tau and how many tokens equal to it are kept
   uint32_t tau = kKeyNegInf;
   int keep_ties = 0;
-  int buf = 0;
+  int buf = -1;
   const uint32_t high = order_key(m);
   if (has_k) {
     Selected s = radix_select<T, kSmem>(sh, sl, nv, law, theta, high, false, has_p, k, 0, C, buf);
@@ -1167,12 +1321,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int C
     }
     const long long zi = __float2ll_rn(z.hi * 0x1p42f) + __float2ll_rn(z.lo * 0x1p42f);
     const long long want = mass_target(tp, zi);
-    // first the tokens that no thread's maximum is below, if they hold enough
-    uint32_t low = has_k ? 0u : sh.ex_low[0];
-    for (int q = 1; q < C; ++q) low = min(low, sh.ex_low[q]);
+    // fp32: first the tokens that no thread's maximum is below, if they hold
+    // enough
+    uint32_t low = has_k || sizeof(T) == 2 ? weightless : sh.ex_low[0];
+    if (!has_k && sizeof(T) == 4) {
+      for (int q = 1; q < C; ++q) low = min(low, sh.ex_low[q]);
+      low = max(low, weightless);
+    }
     Selected p = radix_select<T, kSmem>(sh, sl, nv, law, low, high, true, true, 0, want, C, buf);
-    if (!p.found && low > kKeyNegInf + 1)
-      p = radix_select<T, kSmem>(sh, sl, nv, law, 0u, high, true, true, 0, want, C, buf);
+    if (!p.found && low > weightless)
+      p = radix_select<T, kSmem>(sh, sl, nv, law, weightless, high, true, true, 0, want, C, buf);
     if (p.found) {
       tau = p.tau;
       keep_ties = ties_for(want - p.mass, fixed_value(law.weight(key_value(tau))), (int)p.ties);

@@ -142,6 +142,24 @@ def test_sample_cut_inside_many_equal_tokens(V, dt):
     sample_check(x, np.full(n, 0.8), u, k=k, p=p, mp=mp, dt=dt)
 
 
+@pytest.mark.parametrize("shift,scale", [(0, 1.0), (-40, 2.0), (0, 1e-3), (3e4, 100.0), (0, 1e-5),
+                                         (0, 1e30)])
+def test_sample_deep_top_p_over_signs_and_scales(shift, scale):
+    """Thresholds above, below and about zero, and past the values that the
+    bf16 select holds."""
+    rng = np.random.default_rng(23)
+    n, V = 12, 40000
+    x = rng.normal(size=(n, V)) * scale + shift
+    T = rng.choice([1.0, 0.7], n) * max(1.0, scale / 2)
+    u = rng.integers(0, 1 << 24, n) / (1 << 24)
+    p = rng.choice([0.5, 0.9, 0.999], n)
+    k = rng.choice([6000, 20000, 39000], n)
+    for kw in (dict(p=p), dict(k=k, p=p), dict(k=k)):
+        sample_check(x, T, u, dt=BF, **kw)
+    x[:, ::2] = np.round(x[:, ::2] / scale * 2) / 2 * scale  # and many equal ones
+    sample_check(x, T, u, k=k, p=p, dt=BF)
+
+
 def test_sample_many_rows_of_the_largest_vocabulary():
     g = torch.Generator(device="cuda").manual_seed(5)
     n, V = 304, 1 << 20
