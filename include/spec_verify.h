@@ -430,7 +430,7 @@ spec_status spec_reject_sample_noalloc(const void* target_logits,
  *                         only pages of the first `sinks` positions and of
  *                         positions from ctx - window + 1 on are held
  *   block_table [B, max_blocks] int32 (in/out)   entries of pages not held: -1
- *   span      [B, 2] int32, 8-byte aligned (in/out)   pages (lo, hi) held: p < hi
+ *   span      [B, 2] int32 (in/out)   pages (lo, hi) held: p < hi
  *                         with p >= lo or among the sinks' pages; 0, 0 at first
  *   pool      [num_blocks] int32 (in/out)   ring of free ids
  *   pool_state [2] int32 (in/out)   head, count: entries (head + i) %

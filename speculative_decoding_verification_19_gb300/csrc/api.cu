@@ -438,7 +438,6 @@ spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
   if ((s = check_ws(dims, ws, ws_bytes)) != SPEC_OK) return s;
   if (!ctx_lens || !block_table || !span || !pool || !pool_state) return SPEC_ERR_INVALID_ARG;
   if (rows > 0 && (!slots || !positions)) return SPEC_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(span) & 7u) != 0) return SPEC_ERR_INVALID_ARG;
   if (rows < 0 || window < 0 || sinks < 0) return SPEC_ERR_INVALID_ARG;
   if (row_start != nullptr ? parent != nullptr : (int64_t)dims->B * dims->M > rows)
     return SPEC_ERR_INVALID_ARG;

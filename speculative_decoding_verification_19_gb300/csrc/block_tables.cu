@@ -83,9 +83,8 @@ __device__ void plan_round(Shared& sh, const PageArgs& a, int base, int sp, bool
   int64_t need = 0;
   if (b < B) {
     ctx = a.ctx_lens[b];
-    const int2 sv = *reinterpret_cast<const int2*>(a.span + 2 * (int64_t)b);
-    lo = sv.x;
-    hi = sv.y;
+    lo = a.span[2 * (int64_t)b];
+    hi = a.span[2 * (int64_t)b + 1];
     if (a.row_start != nullptr) {
       r0 = a.row_start[b];
       r1 = a.row_start[b + 1];
@@ -314,7 +313,8 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
     const int b = base + tid;
     if (b < B) {
       if (a.ok != nullptr) a.ok[b] = sh.good[tid] == 2;
-      *reinterpret_cast<int2*>(a.span + 2 * (int64_t)b) = make_int2(sh.lo2[tid], sh.hi2[tid]);
+      a.span[2 * (int64_t)b] = sh.lo2[tid];
+      a.span[2 * (int64_t)b + 1] = sh.hi2[tid];
     }
     __syncthreads();
   }

@@ -136,6 +136,19 @@ def test_pages_refused_requests_stay_as_they_are():
     assert out["ok"].sum() == 0 and out["status"] == 1 << 6
 
 
+def test_pages_state_in_one_buffer():
+    """Tables, spans, ring and ring state as views of one buffer, at odd
+    offsets."""
+    st = Pages(3, 5, 13)
+    buf, at = torch.empty(3 * 5 + 6 + 13 + 2, dtype=I32, device="cuda"), 0
+    for k in ("block_table", "span", "pool", "pool_state"):
+        view = buf[at:at + st.d[k].numel()].view(st.d[k].shape)
+        view.copy_(st.d[k])
+        st.d[k], at = view, at + view.numel()
+    for ctx in ([0, 10, 31], [3, 20, 33], [40, -1, 35]):
+        assert st.call(np.array(ctx), np.array([0, 3, 8, 10]), 11)["ok"].sum() >= 2
+
+
 def test_pages_rows_out_of_order_among_many_requests():
     st = Pages(1200, 4, 3000)
     start = np.arange(1201)

@@ -220,7 +220,7 @@ def test_block_table_refusals(lib):
                                      a["slots"], a["positions"], None, ctypes.byref(d), a["ws"],
                                      a["n"], None)
 
-    for kw in (dict(ctx=None), dict(table=None), dict(span=None), dict(span=P + 4), dict(pool=None),
+    for kw in (dict(ctx=None), dict(table=None), dict(span=None), dict(pool=None),
                dict(state=None), dict(slots=None), dict(positions=None), dict(ws=None), dict(n=4),
                dict(rows=5), dict(rows=-1, row_start=P), dict(window=-1), dict(sinks=-1),
                dict(row_start=P, parent=P)):
