@@ -48,7 +48,7 @@ BAR_WORKLOADS = ("stress_gqa_152k", "chain_gqa_128k")
 # the 128 requests of the default workload and scaled to 128 by the
 # algorithmic bytes (traffic grows with the KV bytes read).  Valid only for
 # the attention kernel sources whose digest is recorded with it.
-TRAFFIC = {"digest": "a8c38fd5bac9f370", "bytes_per_call": 10104412377}
+TRAFFIC = {"digest": "a6ff1df2e45b2ca0", "bytes_per_call": 10104412377}
 TRAFFIC_ALG_BYTES = 10051956736  # algorithmic bytes per call of that workload (seed 0)
 
 

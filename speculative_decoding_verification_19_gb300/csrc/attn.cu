@@ -300,7 +300,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
     const float inv = lrow[j] > 0.f ? 1.f / lrow[j] : 0.f;
     float* prow = pbase + (int64_t)r * (D + 1);
 #pragma unroll
-    for (int c = 0; c < DPL; ++c) prow[lane * DPL + c] = o[j][c] * inv;
+    for (int c = 0; c < DPL; ++c)  // zero without a visible key, whatever the others held
+      prow[lane * DPL + c] = lrow[j] > 0.f ? o[j][c] * inv : 0.f;
     if (lane == 0) prow[D] = lrow[j] > 0.f ? mrow[j] + log2f(lrow[j]) : -INFINITY;
   }
 }
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kWinThreads, RPW <= 8 ? 3 : (D == 64 ? 2 : 1))
     const float inv = l > 0.f ? 1.f / l : 0.f;
     float* prow = pbase + (int64_t)r * (D + 1);
 #pragma unroll
-    for (int c = 0; c < DPL; ++c) prow[lane * DPL + c] = o[j][c] * inv;
+    for (int c = 0; c < DPL; ++c) prow[lane * DPL + c] = l > 0.f ? o[j][c] * inv : 0.f;
     if (lane == 0) prow[D] = l > 0.f ? mrow[j] + log2f(l) : -INFINITY;
   }
 }
@@ -567,17 +568,12 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(
     if (m != -INFINITY) {
 #pragma unroll 4
       for (int s = 0; s < nsp; ++s) {
-        // a partial without a visible key counts for nothing, whatever values of
-        // keys it did not see went into its (unread) sums
         const float* prow = pbase + ((int64_t)s * R + r) * (D + 1);
-        const float ls = prow[D], w = exp2f(ls - m);
+        const float w = exp2f(prow[D] - m);  // 0 for a partial without a visible key
         wsum += w;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= D / kWarp) continue;
-          const float o = prow[lane + c * kWarp];
-          acc[c] += w * (ls == -INFINITY ? 0.f : o);
-        }
+        for (int c = 0; c < 4; ++c)
+          if (c < D / kWarp) acc[c] += w * prow[lane + c * kWarp];
       }
     }
     T* orow = out + (((int64_t)b * d.M + i) * d.Hq + hq) * D;
