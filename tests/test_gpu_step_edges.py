@@ -458,6 +458,64 @@ def test_step_operators_on_a_side_stream_and_in_a_graph():
     assert torch.isfinite(a["out"]).all()
 
 
+def test_calls_on_two_streams_at_once():
+    """Sampling calls that share a workspace, and windowed attention with a
+    workspace each, queued on two streams: the results of the calls alone."""
+    g = torch.Generator(device="cuda").manual_seed(24)
+    x = torch.randn(400, 40007, device="cuda", generator=g).to(BF)
+    one, u = torch.ones(400, device="cuda"), torch.rand(400, device="cuda", generator=g)
+    k = torch.randint(0, 9000, (400,), dtype=I32, device="cuda", generator=g)
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    kinds = [({}, 400), (dict(top_k=k, top_p=one * 0.95), 400), (dict(min_p=one[:90] * 0.01), 90),
+             ({}, 30)]
+
+    def sample(i, tok, prob, stream=None):
+        kw, n = kinds[i]
+        sv.spec_sample(x[:n], one[:n], u[:n], tok[:n], prob[:n], ws, stream=stream, **kw)
+
+    B, M, Hq, Hkv, mb = 6, 5, 16, 4, 130
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g).to(BF)  # noqa: E731
+    q, kn, vn = rand(B, M, Hq, 128), rand(B, M, Hkv, 128), rand(B, M, Hkv, 128)
+    table = torch.randperm(B * mb, device="cuda", generator=g).to(I32).view(B, mb)
+    ctx = to_dev(np.array([0, 100, 600, 1000, 1500, 2000]), I32)
+    dims = sv.make_dims(B=B, M=M, Hq=Hq, Hkv=Hkv, D=128, max_blocks=mb, num_blocks=B * mb)
+    states = [dict(kc=rand(B * mb, Hkv, 16, 128), vc=rand(B * mb, Hkv, 16, 128),
+                   out=torch.empty_like(q), lse=torch.empty(B, M, Hq, device="cuda"),
+                   ws=sv.workspace(dims), tok=torch.zeros(400, dtype=I32, device="cuda"),
+                   prob=torch.zeros(400, device="cuda")) for _ in range(2)]
+
+    def attn(s, stream=None):
+        sv.spec_verify_attn(q, kn, vn, s["kc"], s["vc"], table, ctx, None, s["out"], s["lse"], dims,
+                            s["ws"], stream=stream, window=700, sinks=5)
+
+    alone = []
+    for i, s in enumerate(states):
+        for j in range(4):
+            sample(j, s["tok"], s["prob"])
+            alone.append((s["tok"].clone(), s["prob"].clone()))
+        attn(s)
+        alone.append((s["out"].clone(), s["lse"].clone()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [[], []]
+        for j in range(4):
+            for i, (s, st) in enumerate(zip(states, streams)):
+                with torch.cuda.stream(st):
+                    sample(j, s["tok"], s["prob"])
+                    got[i].append((s["tok"].clone(), s["prob"].clone()))
+                    attn(s)
+        torch.cuda.synchronize()
+        for i, s in enumerate(states):
+            for j in range(4):
+                for a, b in zip(got[i][j], alone[5 * i + j]):
+                    assert torch.equal(a, b), (i, j)
+            assert torch.equal(s["out"], alone[5 * i + 4][0])
+            assert torch.equal(s["lse"], alone[5 * i + 4][1])
+            assert sv.device_status(s["ws"]) == 0
+    assert sv.device_status(ws) == 0
+
+
 def test_binding_refusals():
     x = torch.zeros(2, 64, device="cuda")
     one = torch.ones(2, device="cuda")
