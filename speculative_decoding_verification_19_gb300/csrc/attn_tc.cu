@@ -292,12 +292,12 @@ __device__ __forceinline__ void store32_bf16(__nv_bfloat16* dst, const uint32_t 
 // the prep kernel for chains too).
 template <bool kWide, bool kShort, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
-    const __grid_constant__ CUtensorMap tm_q, const __nv_bfloat16* __restrict__ k_new,
-    const __nv_bfloat16* __restrict__ v_new, __nv_bfloat16* __restrict__ k_cache,
-    __nv_bfloat16* __restrict__ v_cache, const int32_t* __restrict__ block_table,
-    const int4* rq, const int4* starts, const ulonglong2* anc_ws, const int* depth_ws, int window,
-    int sinks, int* pairs, spec_dims d, float qscale2, float* part, __nv_bfloat16* __restrict__ out,
-    float* __restrict__ lse, uint32_t* __restrict__ status) {
+    const __grid_constant__ CUtensorMap tm_q, const __nv_bfloat16* k_new,
+    const __nv_bfloat16* v_new, __nv_bfloat16* k_cache, __nv_bfloat16* v_cache,
+    const int32_t* block_table, const int4* rq, const int4* starts, const ulonglong2* anc_ws,
+    const int* depth_ws, int window, int sinks, int* pairs, spec_dims d, float qscale2,
+    float* part, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
+    uint32_t* __restrict__ status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -1097,7 +1097,7 @@ __device__ __forceinline__ void block_scan(int64_t& a, int64_t& c, int& m, int64
 template <bool kWin>
 __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     const int32_t* block_table, const int32_t* ctx_lens,
-    const int32_t* __restrict__ parent, spec_dims d, int window, int sinks, int G,
+    const int32_t* parent, spec_dims d, int window, int sinks, int G,
     int32_t* __restrict__ depth_ws, int32_t* __restrict__ ntiles,
     int64_t* __restrict__ pre, int4* __restrict__ rq, int4* __restrict__ starts,
     int* __restrict__ pairs, ulonglong2* __restrict__ anc_ws,

@@ -15,7 +15,7 @@ namespace specv {
 
 template <typename T>
 __global__ void __launch_bounds__(256) kv_commit_kernel(
-    T* k_cache, T* v_cache, const int32_t* __restrict__ block_table, const int32_t* ctx_lens,
+    T* k_cache, T* v_cache, const int32_t* block_table, const int32_t* ctx_lens,
     int32_t* new_ctx_lens, const int32_t* path, const int32_t* accepted_len, spec_dims d,
     uint32_t* __restrict__ status) {
   pdl_trigger();

@@ -101,8 +101,8 @@ __device__ __forceinline__ int64_t next_needed(int64_t t, int64_t nw, int64_t nt
 // reducing the current ones, so 2 x 4 KB per warp stay in flight.
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kRsThreads) rs_rowstats_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ parent,
-    const float* __restrict__ temperature, spec_dims d, int n_chunks, RowStat* __restrict__ stats) {
+    const T* target, const T* draft, const int32_t* parent,
+    const float* temperature, spec_dims d, int n_chunks, RowStat* __restrict__ stats) {
   constexpr int EPV = 16 / sizeof(T);
   constexpr int kChunk = kWarp * kStatVecs * EPV;
   const int lane = threadIdx.x % kWarp;
@@ -262,8 +262,8 @@ struct StatCursor {
 
 template <typename T>
 __global__ void __launch_bounds__(kBulkWarps * kWarp, 1) rs_rowstats_bulk_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ parent,
-    const float* __restrict__ temperature, spec_dims d, int n_chunks, RowStat* __restrict__ stats,
+    const T* target, const T* draft, const int32_t* parent,
+    const float* temperature, spec_dims d, int n_chunks, RowStat* __restrict__ stats,
     uint32_t* __restrict__ status) {
   constexpr int EPV = 16 / sizeof(T);
   constexpr int kChunk = kWarp * kStatVecs * EPV;
@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(kBulkWarps * kWarp, 1) rs_rowstats_bulk_kernel
 // their balanced static range first, so that the stream ends together.
 template <typename T>
 __global__ void __launch_bounds__(kBulkWarps * kWarp, 1) rs_rowstats_pool_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ parent,
-    const float* __restrict__ temperature, spec_dims d, int n_chunks, RowStat* __restrict__ stats,
+    const T* target, const T* draft, const int32_t* parent,
+    const float* temperature, spec_dims d, int n_chunks, RowStat* __restrict__ stats,
     uint32_t* __restrict__ status, uint32_t* pool) {
   constexpr int EPV = 16 / sizeof(T);
   constexpr int kChunk = kWarp * kStatVecs * EPV;
@@ -731,9 +731,9 @@ __device__ void filter_nth(const T* row, int V, uint32_t gkey, uint32_t gshift, 
 
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kFiltThreads) rs_filter_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ parent,
-    const float* __restrict__ temperature, const int32_t* __restrict__ top_k,
-    const float* __restrict__ top_p, spec_dims d, int n_chunks, const RowStat* stats,
+    const T* target, const T* draft, const int32_t* parent,
+    const float* temperature, const int32_t* top_k,
+    const float* top_p, spec_dims d, int n_chunks, const RowStat* stats,
     FilterInfo* __restrict__ finfo) {
   __shared__ FilterSmem sh;
   const int M = d.M, V = d.V;
@@ -1261,8 +1261,8 @@ struct DecideSmem {
 // so the request is failed without being decided.
 template <typename T, bool kAligned>
 __device__ void decide_request(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
-    const int32_t* __restrict__ parent, const float* __restrict__ temperature, uint64_t seed,
+    const T* target, const T* draft, const int32_t* tokens,
+    const int32_t* parent, const float* temperature, uint64_t seed,
     uint64_t offset, uint64_t b_base, int32_t* __restrict__ out_tokens, int32_t* __restrict__ path,
     int32_t* __restrict__ accepted_len, float* __restrict__ probe, const spec_dims& d, int n_chunks,
     int chunk, const RowStat* stats, DrawState* draws, uint32_t* status, int b, bool stats_lost,
@@ -1727,8 +1727,8 @@ __device__ void decide_request(
 
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kDecThreads) rs_decide_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
-    const int32_t* __restrict__ parent, const float* __restrict__ temperature, uint64_t seed,
+    const T* target, const T* draft, const int32_t* tokens,
+    const int32_t* parent, const float* temperature, uint64_t seed,
     uint64_t offset, uint64_t b_base, int32_t* __restrict__ out_tokens, int32_t* __restrict__ path,
     int32_t* __restrict__ accepted_len, float* __restrict__ probe, spec_dims d, int n_chunks,
     int chunk, const RowStat* stats, DrawState* __restrict__ draws, uint32_t* status,
@@ -1760,7 +1760,7 @@ __host__ __device__ __forceinline__ int rs_res_spans(int n_chunks) {
 
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kResThreads) rs_residual_sums_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, spec_dims d, int n_chunks,
+    const T* target, const T* draft, spec_dims d, int n_chunks,
     int chunk, const DrawState* draws, double* __restrict__ zsum) {
   constexpr int EPV = 16 / sizeof(T);
   const int n_spans = rs_res_spans(n_chunks);
@@ -1809,7 +1809,7 @@ __global__ void __launch_bounds__(kResThreads) rs_residual_sums_kernel(
 // the masses and searches it element by element (one warp for aligned rows).
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kResThreads) rs_residual_draw_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, spec_dims d, int n_chunks,
+    const T* target, const T* draft, spec_dims d, int n_chunks,
     int chunk, const RowStat* stats, const DrawState* draws, const double* zsum,
     int32_t* __restrict__ out_tokens, float* __restrict__ probe) {
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -2037,8 +2037,8 @@ __device__ __forceinline__ void tail_row_norm(const RowStat* st, int n_chunks, i
 
 template <typename T>
 __global__ void __launch_bounds__(kTailThreads, 2) rs_chain_tail_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
-    const float* __restrict__ temperature, uint64_t seed, uint64_t offset, uint64_t b_base,
+    const T* target, const T* draft, const int32_t* tokens,
+    const float* temperature, uint64_t seed, uint64_t offset, uint64_t b_base,
     int32_t* __restrict__ out_tokens, int32_t* __restrict__ path,
     int32_t* __restrict__ accepted_len, float* __restrict__ probe, spec_dims d, int n_chunks,
     int chunk, const RowStat* stats, double* zsum, uint32_t* done_cnt, uint32_t* status, int S,
@@ -2574,8 +2574,8 @@ __device__ __forceinline__ void fused_finish(uint32_t* ctl) {
 // (bonus from p here; a residual is posted as units).
 template <typename T>
 __device__ __noinline__ void fused_decide(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
-    const float* __restrict__ temperature, uint64_t seed, uint64_t offset, uint64_t b_base,
+    const T* target, const T* draft, const int32_t* tokens,
+    const float* temperature, uint64_t seed, uint64_t offset, uint64_t b_base,
     int32_t* __restrict__ out_tokens, int32_t* __restrict__ path, int32_t* __restrict__ accepted_len,
     float* __restrict__ probe, const spec_dims& d, int n_chunks, int chunk, const FusedWs& w,
     int b) {
@@ -2761,8 +2761,8 @@ __device__ __noinline__ void fused_decide(
 // [kFUnit g, kFUnit g + kFUnit)), by one warp: each chunk's residual mass;
 // the unit that completes its request draws the token.
 template <typename T>
-__device__ __noinline__ bool fused_residual_unit(const T* __restrict__ target,
-                                                 const T* __restrict__ draft,
+__device__ __noinline__ bool fused_residual_unit(const T* target,
+                                                 const T* draft,
                                                  int32_t* __restrict__ out_tokens,
                                                  float* __restrict__ probe, const spec_dims& d,
                                                  int n_chunks, int chunk, const FusedWs& w,
@@ -2863,8 +2863,8 @@ __device__ __noinline__ bool fused_residual_unit(const T* __restrict__ target,
 
 template <typename T>
 __global__ void __launch_bounds__(kFWarps * kWarp, 1) rs_fused_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
-    const float* __restrict__ temperature, uint64_t seed, uint64_t offset, uint64_t b_base,
+    const T* target, const T* draft, const int32_t* tokens,
+    const float* temperature, uint64_t seed, uint64_t offset, uint64_t b_base,
     int32_t* __restrict__ out_tokens, int32_t* __restrict__ path,
     int32_t* __restrict__ accepted_len, float* __restrict__ probe, spec_dims d, int n_chunks,
     int chunk, FusedWs w) {

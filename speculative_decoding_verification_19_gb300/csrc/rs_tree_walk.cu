@@ -411,8 +411,8 @@ __device__ void tw_slice_draw(const T* trow, const T* drow, int64_t v0, int64_t 
 
 template <typename T>
 __global__ void __launch_bounds__(kTwThreads) rs_tree_walk_kernel(
-    const T* __restrict__ target, const T* __restrict__ draft, const int32_t* __restrict__ tokens,
-    const int32_t* __restrict__ parent, const float* __restrict__ temperature, uint64_t seed,
+    const T* target, const T* draft, const int32_t* tokens,
+    const int32_t* parent, const float* temperature, uint64_t seed,
     uint64_t offset, uint64_t b_base, int32_t* __restrict__ out_tokens, int32_t* __restrict__ path,
     int32_t* __restrict__ accepted_len, float* __restrict__ probe, spec_dims d, int n_chunks,
     const RowStat* stats, uint32_t* status, int inputs_ready) {
