@@ -136,7 +136,15 @@ size_t spec_workspace_size(const spec_dims* dims);
 
 /* Zero the workspace (status word included).  Call once after allocating it;
  * afterwards every call leaves it ready for the next.  An async memset on
- * `stream`. */
+ * `stream`.
+ *
+ * Calls of different dims may take turns on one workspace (of the largest
+ * one's size) if they are spec_verify_attn, spec_verify_attn_window,
+ * spec_block_tables, spec_qk_norm_rope, spec_sample, spec_lm_head and
+ * kv_commit.  spec_reject_sample, its filtered form and
+ * spec_reject_sample_lm_head keep counters at places that depend on dims: a
+ * workspace that they use serves one spec_dims, or is zeroed again before a
+ * call of theirs that follows one of other dims. */
 spec_status spec_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream` and read the device status word: bit (1 << code) is

@@ -40,7 +40,11 @@ WsLayout workspace_layout(const spec_dims& d) {
     off = align_up(off + bytes, 256);
     return o;
   };
-  L.status_off = take(16);
+  // the status word, and the counters that have to be zero between calls of
+  // any dims: their places do not depend on dims
+  L.status_off = take(256);
+  L.tc_sync_off = L.status_off + 64;
+  L.pg_sync_off = L.status_off + 128;
   L.attn_ok_off = take(sizeof(int32_t) * (size_t)d.B);
   L.tc_ntiles_off = take(sizeof(int32_t) * (size_t)d.B);
   L.tc_pre_off = take(sizeof(int64_t) * 2 * ((size_t)d.B + 1));
@@ -48,9 +52,7 @@ WsLayout workspace_layout(const spec_dims& d) {
   L.tc_start_off = take(32 * ((size_t)kMaxAttnCtas + 1));
   L.tc_pair_off = take(sizeof(int32_t) * (size_t)d.B * (size_t)(d.Hkv > 0 ? d.Hkv : 0));
   L.tc_anc_off = take(2 * sizeof(uint64_t) * (size_t)d.B * d.M);
-  L.tc_sync_off = take(16);
   L.win_depth_off = take(sizeof(int32_t) * (size_t)d.B * d.M);
-  L.pg_sync_off = take(16);
   const int group = d.Hkv > 0 ? d.Hq / d.Hkv : 0;
   L.rows = group * d.M;
   L.split_keys = attn_split_keys(d);
