@@ -649,7 +649,9 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
 #define SPECV_SIMT(DD, RPW)                                                                   \
   do {                                                                                        \
     auto k = attn_split_kernel<T, DD, RPW>;                                                   \
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);      \
+    /* the most of any call: another thread's may come between this and the launch */       \
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,                  \
+                             (int)attn_simt_smem_bytes(RPW * kSimtWarps, DD));                \
     if (e != cudaSuccess) return e;                                                           \
     k<<<grid, kSimtThreads, smem, st>>>(static_cast<const T*>(a.q),                           \
                                         static_cast<const T*>(a.k_cache),                     \

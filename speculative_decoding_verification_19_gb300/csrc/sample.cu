@@ -70,6 +70,14 @@ constexpr int kUnroll = 4;
 constexpr int kLongRun = 5 * kWarp;  // vectors; above it the walk is shared
 constexpr size_t kMaxSharedBytes = 224 * 1024;  // static and dynamic, of an SM's CTAs
 
+// Lets launches of `kern` ask for up to `most` bytes of dynamic shared memory.
+// The limit is the same in every call: it belongs to the kernel, and another
+// thread's call may stand between this one's setting and its launch.
+template <typename K>
+cudaError_t allow_shared(K kern, size_t most) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 // 2^(j/32) as hi + lo
 __device__ const float2 kPow2[32] = {
     {0x1p+0f, 0.f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f},
@@ -1872,8 +1880,7 @@ static cudaError_t launch_t(const SampleArgs& a, cudaStream_t st, int* launches)
     const bool fits = bytes + sizeof(MarkedShared) <= kMaxSharedBytes;
     auto kern = fits ? sample_marked_kernel<T, true> : sample_marked_kernel<T, false>;
     const size_t smem = fits ? bytes : 0;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_shared(kern, fits ? kMaxSharedBytes - sizeof(MarkedShared) : 0);
     if (e != cudaSuccess) return e;
     ClusterLaunch L(min(kMarkedClusters, a.rows), C, kThreads, smem, st);
     ++*launches;
@@ -1909,8 +1916,7 @@ static cudaError_t launch_t(const SampleArgs& a, cudaStream_t st, int* launches)
   const int warp_vecs = vecs_of(C);
   auto kern = fits ? sample_kernel<T, true> : sample_kernel<T, false>;
   const size_t smem = (fits ? (size_t)kWarps * warp_vecs * 16 : 0) + list;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = allow_shared(kern, fits ? kMaxSharedBytes - sizeof(Shared) : list);
   if (e != cudaSuccess) return e;
   ClusterLaunch L(a.rows, C, kThreads, smem, st);
   ++*launches;
