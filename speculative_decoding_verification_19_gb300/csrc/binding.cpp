@@ -117,7 +117,8 @@ double real(PyObject* o) {
 }
 
 // Runs `call(stream)` on the device and the given stream (an address, or None
-// for the device's current one).
+// for the device's current one).  The call runs without the interpreter's lock:
+// it may call the C ABI alone, and touches no tensor (which could throw).
 template <typename F>
 PyObject* launch(int device, PyObject* stream, F call) {
   void* st;
@@ -268,6 +269,8 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (type != at::kBFloat16 && type != at::kFloat)
       throw Refused(std::string("logits: unsupported dtype ") + c10::toString(type));
     const int64_t rows = x.size(0), V = x.size(1);
+    const int64_t stride = rows > 1 ? x.stride(0) : V;
+    const void* logits = x.data_ptr();
     void* T = dense(a[1], "temperature", at::kFloat, dev, {rows});
     void* u = dense(a[2], "uniform", at::kFloat, dev, {rows});
     void* tok = dense(a[3], "out_tokens", at::kInt, dev, {rows});
@@ -279,7 +282,7 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* mp = dense_or_none(a[8], "min_p", at::kFloat, dev, {rows});
     if (rows > INT32_MAX || V > INT32_MAX) throw Refused("logits: too large");
     return launch(dev, a[9], [&](void* st) {
-      return spec_sample(x.data_ptr(), rows > 1 ? x.stride(0) : V, (int32_t)rows, (int32_t)V,
+      return spec_sample(logits, stride, (int32_t)rows, (int32_t)V,
                          type == at::kBFloat16 ? SPEC_BF16 : SPEC_F32, as<float>(T), as<int32_t>(k),
                          as<float>(p), as<float>(mp), as<float>(u), as<int32_t>(tok),
                          as<float>(prob), ws, bytes, st);

@@ -134,3 +134,18 @@ def test_cuda_core_attention_from_several_host_threads():
         return prepare, call, lambda s: (s["out"], s["lse"])
 
     in_threads([job(65, None), job(128, None), job(66, None), job(90, 50)], 300)
+
+
+def test_tensors_without_memory_are_refused():
+    """A tensor that only stands for others (inside vmap) has no address."""
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    one, tok = torch.ones(2, device="cuda"), torch.zeros(2, dtype=I32, device="cuda")
+
+    def call(x):
+        sv.spec_sample(x, one, one * 0.5, tok, None, ws)
+        return x
+
+    with pytest.raises((RuntimeError, ValueError)):
+        torch.func.vmap(call)(torch.zeros(3, 2, 64, device="cuda"))
+    call(torch.zeros(2, 64, device="cuda"))
+    assert sv.device_status(ws) == 0
