@@ -11,7 +11,11 @@ dropped.  The pages do not say how blocks are handed out.  Readings taken:
   the sinks and of the positions that its first new row can still see;
 * a request gets its pages if the ring holds what it and every request before
   it ask for; else it takes none and does not run;
-* length -1 means that the request has ended.
+* length -1 means that the request has ended;
+* a ring or table entry that is no block id (a corrupt state) serves no row and
+  is given to nobody: the request that would take it or write to it does not
+  run (its rows are -1, it keeps its pages), the entry reads -1 in the table,
+  and what is returned to the ring are block ids alone.
 
 Written page by page with sets; no interval arithmetic.
 """
@@ -85,6 +89,14 @@ def oracle_block_tables(ctx_lens, row_start, parent, rows, block_table, span, po
                 for p in need:
                     table[b, p] = ring[(head + taken) % nb]
                     taken += 1
+                    if not 0 <= table[b, p] < nb:
+                        table[b, p] = -1
+                        status |= 1 << BOUNDS
+                        served = False
+                for t in range(ctx, ctx + r1 - r0):
+                    if not 0 <= table[b, t // block] < nb:
+                        status |= 1 << BOUNDS
+                        served = False
         if code is not None:
             status |= 1 << code
         else:
@@ -105,9 +117,12 @@ def oracle_block_tables(ctx_lens, row_start, parent, rows, block_table, span, po
                 positions[r] = ctx + (i if parent is None else depth)
     for b, lo2, hi2 in new_state:
         sp[b] = lo2, hi2
-    for j, i in enumerate(returned):
-        ring[(head + count + j) % nb] = i
-    state = np.array([(head + taken) % nb, count - taken + len(returned)], dtype=np.int32)
+    back = [i for i in returned if 0 <= i < nb]
+    if len(back) < len(returned):
+        status |= 1 << BOUNDS
+    for j in range(len(returned)):
+        ring[(head + count + j) % nb] = back[j] if j < len(back) else -1
+    state = np.array([(head + taken) % nb, count - taken + len(back)], dtype=np.int32)
     if not pool_ok:
         state = np.array(pool_state, dtype=np.int32)
     return dict(block_table=table, span=sp, pool=ring, pool_state=state, slots=slots,

@@ -28,6 +28,12 @@
 // first CTA) and then does its share of the items: pages given back, pages
 // taken, rows.  Spans, ring state and verdicts are written by the CTA that
 // arrives last, when every CTA has read the old ones.
+//
+// An entry of a table or of the ring that is no block id (a corrupt state) must
+// not reach another request.  A CTA that meets one says so with its arrival, and
+// only then does the last CTA look through the pages that the requests take or
+// write, refuse the requests with such a page, and close the gaps among the ids
+// given back; a sound state pays for nothing but the flag.
 #include "block_tables.cuh"
 
 namespace specv {
@@ -48,10 +54,13 @@ struct Shared {
   int row0[kThreads + 1];  // first row of each request
   int ctx[kThreads];
   int lo[kThreads], hi[kThreads], lo2[kThreads], hi2[kThreads];
-  int good[kThreads];  // 2: rows get slots, 1: a request without rows to serve, 0: unchanged
+  // 2: rows get slots, 1: a request without rows to serve, 0: unchanged; 3: of
+  // the first kind, but one of its pages is no block
+  int good[kThreads];
   int64_t warp_need[kWarps];
   int warp_give[kWarps], warp_take[kWarps];
   int last;
+  int corrupt;  // an entry that is no block id was met
 };
 
 // What the rounds carry from request to request.
@@ -210,6 +219,44 @@ __device__ __forceinline__ int find(const int* pre, int n, int x) {
   return lo;
 }
 
+// Whether every page that request r of the round takes, or that its rows are
+// written to, is a block (the table after the call; read past L1, as other CTAs
+// wrote it).
+__device__ __noinline__ bool pages_sound(const Shared& sh, const PageArgs& a, int base, int r,
+                                         int sp) {
+  const int32_t* table = a.block_table + (int64_t)(base + r) * a.d.max_blocks;
+  auto sound = [&](int p0, int p1) {
+    bool good = true;
+    for (int p = p0; p < p1; ++p) {
+      const int id = __ldcg(table + p);
+      good &= id >= 0 && id < a.d.num_blocks;
+    }
+    return good;
+  };
+  const int hi = sh.hi[r], hi2 = sh.hi2[r];
+  return sound(hi, min(sp, hi2)) && sound(take_from(hi, sh.lo2[r], sp), hi2) &&
+         (sh.row0[r + 1] == sh.row0[r] || sound(sh.ctx[r] / kBlock, hi2));
+}
+
+// Moves the block ids among the `given` entries behind the ring's first `count`
+// together, in their order, and clears the places left over (one warp).
+// Returns how many ids there are.
+__device__ __noinline__ int close_gaps(int32_t* pool, int head, int count, int given, int nb) {
+  const int lane = threadIdx.x % kWarp;
+  const int64_t first = (int64_t)head + count;
+  int kept = 0;
+  for (int j0 = 0; j0 < given; j0 += kWarp) {
+    const int id = j0 + lane < given ? __ldcg(pool + (first + j0 + lane) % nb) : -1;
+    const bool good = id >= 0 && id < nb;
+    const unsigned mask = __ballot_sync(0xffffffffu, good);  // every lane has read
+    if (good) pool[(first + kept + __popc(mask & ((1u << lane) - 1))) % nb] = id;
+    kept += __popc(mask);
+    __syncwarp();
+  }
+  for (int j = kept + lane; j < given; j += kWarp) pool[(first + j) % nb] = -1;
+  return kept;
+}
+
 __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint32_t* arrivals,
                                                                 uint32_t* status) {
   __shared__ Shared sh;
@@ -221,6 +268,13 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
   const int head = a.pool_state[0], count = a.pool_state[1];
   const bool pool_ok = head >= 0 && head < nb && count >= 0 && count <= nb;
   if (!pool_ok && blockIdx.x == 0 && tid == 0) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
+  if (tid == 0) sh.corrupt = 0;  // plan_round's barriers stand before its uses
+  auto is_block = [&](int id) {
+    if (id >= 0 && id < nb) return true;
+    raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
+    sh.corrupt = 1;
+    return false;
+  };
   const int gt = blockIdx.x * kThreads + tid, gn = gridDim.x * kThreads;
   bool rows_ok = true;  // one entry out of order leaves no row certain
   if (a.row_start != nullptr && B > kThreads) {
@@ -245,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
       int32_t* entry = a.block_table + (int64_t)(base + r) * mb + p;
       const int id = *entry;
       const int64_t g = (int64_t)count + carry.give + j;
-      if (id < 0 || id >= nb || g >= nb) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
+      if (is_block(id) && g >= nb) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
       if (g < nb) a.pool[(head + g) % nb] = id;
       *entry = -1;
     }
@@ -256,8 +310,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
       const int k = j - sh.take_pre[r];
       const int p = k < low ? hi + k : take_from(hi, sh.lo2[r], sp) + k - low;
       const int id = a.pool[((int64_t)head + carry.take + j) % nb];
-      if (id < 0 || id >= nb) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
-      a.block_table[(int64_t)(base + r) * mb + p] = id;
+      a.block_table[(int64_t)(base + r) * mb + p] = is_block(id) ? id : -1;
     }
     // rows: slot and position; an entry of a page taken by this call is read
     // from the ring, not from the table that another CTA may be writing
@@ -279,8 +332,7 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
                                   : take_low(hi, sh.hi2[r], sp) + p - take_from(hi, sh.lo2[r], sp);
           id = a.pool[((int64_t)head + carry.take + sh.take_pre[r] + rank) % nb];
         }
-        if (id >= 0 && id < nb) slot = (int64_t)id * kBlock + t % kBlock;
-        else raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
+        if (is_block(id)) slot = (int64_t)id * kBlock + t % kBlock;
         pos = t;
         if (a.parent != nullptr) {
           // depth: steps to the root (checked above: every step goes down)
@@ -297,20 +349,36 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
     carry.give += n_give;
     __syncthreads();  // the round's records are read
   }
-  // ---- the new page state, by the last CTA to arrive
+  // ---- the new page state, by the last CTA to arrive (arrivals in the lower
+  // half of the word, those with a corrupt entry in the upper)
   if (gridDim.x > 1) {
     if (tid == 0) {
       __threadfence();
-      sh.last = atomicAdd(arrivals, 1u) == gridDim.x - 1;
+      const uint32_t before = atomicAdd(arrivals, sh.corrupt ? 0x10001u : 1u);
+      sh.last = (before & 0xffffu) == gridDim.x - 1;
+      if (before >> 16) sh.corrupt = 1;
     }
     __syncthreads();
     if (!sh.last) return;
     __threadfence();
   }
+  const bool corrupt = sh.corrupt;
   Carry again{0, 0, 0};
   for (int base = 0; base < B; base += kThreads) {
     if (B > kThreads) plan_round(sh, a, base, sp, pool_ok, count, rows_ok, again, status, false);
     const int b = base + tid;
+    if (corrupt) {
+      const int n = min(kThreads, B - base);
+      if (b < B && sh.good[tid] == 2 && !pages_sound(sh, a, base, tid, sp)) sh.good[tid] = 3;
+      __syncthreads();
+      for (int r = 0; r < n; ++r) {
+        if (sh.good[r] != 3) continue;
+        for (int row = sh.row0[r] + tid; row < sh.row0[r + 1]; row += kThreads) {
+          a.slots[row] = -1;
+          a.positions[row] = -1;
+        }
+      }
+    }
     if (b < B) {
       if (a.ok != nullptr) a.ok[b] = sh.good[tid] == 2;
       a.span[2 * (int64_t)b] = sh.lo2[tid];
@@ -318,10 +386,12 @@ __global__ void __launch_bounds__(kThreads) block_tables_kernel(PageArgs a, uint
     }
     __syncthreads();
   }
+  int given = (int)min((int64_t)carry.give, (int64_t)nb - count);
+  if (corrupt && pool_ok && tid < kWarp) given = close_gaps(a.pool, head, count, given, nb);
   if (tid == 0) {
     if (pool_ok) {
       a.pool_state[0] = (int)(((int64_t)head + carry.take) % nb);
-      a.pool_state[1] = (int)min((int64_t)count + carry.give, (int64_t)nb) - carry.take;
+      a.pool_state[1] = count + given - carry.take;
     }
     if (gridDim.x > 1) *arrivals = 0;
   }
