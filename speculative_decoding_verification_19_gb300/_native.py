@@ -198,8 +198,12 @@ def _done(fn: str, result: int) -> int:
 def spec_verify_attn(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens,
                      parent, out, lse, dims: SpecDims, ws, stream=None, window=None,
                      sinks=0) -> int:
-    """spec_verify_attn; with a window (and sinks) spec_verify_attn_window."""
-    if window is not None:
+    """spec_verify_attn; with a window (and sinks) spec_verify_attn_window.  A
+    window of None or 0 is none, as in spec_block_tables."""
+    if window is None or window == 0:
+        if sinks:
+            raise ValueError("sinks: a window is wanted with them")
+    else:
         return _done("spec_verify_attn_window", _bind().verify_attn_window(
             q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, out, lse, dims, ws,
             window, sinks, None if stream is None else stream.cuda_stream))
@@ -239,7 +243,9 @@ def spec_block_tables(ctx_lens, row_start, parent, block_table, span, pool, pool
                       positions, ok, dims: SpecDims, ws, window=0, sinks=0, stream=None) -> int:
     """Block tables, slot map and positions of a step's new rows from the
     requests' lengths; pages come from and go back to a ring of free ids
-    (block_table, span, pool and pool_state are updated in place)."""
+    (block_table, span, pool and pool_state are updated in place).  A window of
+    None or 0 is none: every page is held."""
+    window = 0 if window is None else window
     return _done("spec_block_tables", _bind().block_tables(
         ctx_lens, row_start, parent, block_table, span, pool, pool_state, slots, positions, ok, dims,
         ws, window, sinks, None if stream is None else stream.cuda_stream))
