@@ -180,6 +180,13 @@ struct Law {
   }
 };
 
+// w / z, rounded once (the quotient of the high words, and its remainder).
+__device__ __forceinline__ float df_quotient(dfloat w, dfloat z) {
+  const float q = w.hi / z.hi;
+  const float rest = fmaf(-q, z.hi, w.hi) + fmaf(-q, z.lo, w.lo);
+  return q + rest / z.hi;
+}
+
 // A weight as a 42-bit fixed-point fraction, in three limbs of 14 bits, none
 // negative (the limbs of 2^17 weights add up in 32 bits).
 __device__ __forceinline__ void fixed_limbs(dfloat w, uint32_t (&l)[3]) {
@@ -670,7 +677,7 @@ __device__ void exact_draw(DrawShared& sh, const Slice<T, kSmem>& sl, const Law&
     tie_base = __shfl_sync(0xffffffffu, before, warp);
   }
   int last = -1;        // this lane's last kept token so far
-  float last_w = 0.f;
+  dfloat last_w = df_make(0.f);
   for (int v0 = v_lo; v0 < v_hi; v0 += kWarp) {
     const int v = v0 + lane;
     float x[kVec];
@@ -707,7 +714,7 @@ __device__ void exact_draw(DrawShared& sh, const Slice<T, kSmem>& sl, const Law&
       }
       if (w[i].hi > 0.f) {
         last = v * kVec + i;
-        last_w = w[i].hi;
+        last_w = w[i];
       }
       sum = df_add(sum, w[i]);
     }
@@ -718,17 +725,17 @@ __device__ void exact_draw(DrawShared& sh, const Slice<T, kSmem>& sl, const Law&
       if (lane == __ffs(past) - 1) {
         dfloat c = df_sub(incl, sum);
         int at = -1;
-        float wt = 0.f;
+        dfloat wt = df_make(0.f);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           if ((at < 0 || !df_gt(c, thr)) && w[i].hi > 0.f) {
             c = df_add(c, w[i]);
             at = v * kVec + i;
-            wt = w[i].hi;
+            wt = w[i];
           }
         }
         a.out_tokens[row] = first + at - sl.off;
-        if (a.out_prob != nullptr) a.out_prob[row] = wt / df_to_f(Z);
+        if (a.out_prob != nullptr) a.out_prob[row] = df_quotient(wt, Z);
       }
       return;
     }
@@ -739,7 +746,7 @@ __device__ void exact_draw(DrawShared& sh, const Slice<T, kSmem>& sl, const Law&
   const int top = __reduce_max_sync(0xffffffffu, last);
   if (last == top && top >= 0) {
     a.out_tokens[row] = first + top - sl.off;
-    if (a.out_prob != nullptr) a.out_prob[row] = last_w / df_to_f(Z);
+    if (a.out_prob != nullptr) a.out_prob[row] = df_quotient(last_w, Z);
   }
 }
 
@@ -805,6 +812,13 @@ __device__ __forceinline__ void fixed_pair(dfloat w, uint32_t& hi, uint32_t& lo)
   hi = (uint32_t)a;
   lo = (uint32_t)__float2int_rn(r * 0x1p40f);
 }
+
+// Sum of such fractions as a double-float.
+__device__ __forceinline__ dfloat pair_sum(long long z) {
+  const float hi = (float)z;
+  return dfloat{hi * 0x1p-40f, (float)(z - (long long)hi) * 0x1p-40f};
+}
+
 __device__ __forceinline__ long long pair_value(uint32_t hi, uint32_t lo) {
   return ((long long)hi << 20) + lo;
 }
@@ -941,7 +955,7 @@ __device__ void short_draw(Shared& sh, const uint2* list, const Law& law, int C,
   const long long past = __double2ll_rd((double)u * (double)z);
   if (part == 0 && kept > 0 && before <= past && past < before + kept) {
     a.out_tokens[row] = (int)idx;
-    if (a.out_prob != nullptr) a.out_prob[row] = w.hi / ((float)z * 0x1p-40f);
+    if (a.out_prob != nullptr) a.out_prob[row] = df_quotient(w, pair_sum(z));
   }
 }
 
@@ -1051,7 +1065,7 @@ __device__ void list_draw(Shared& sh, const uint2* list, const Law& law, int C, 
     if (((active >> q) & 1u) && back[q] == s.key) {
       a.out_tokens[row] = (int)idx[q];
       if (a.out_prob != nullptr)
-        a.out_prob[row] = law.weight(x[q]).hi / ((float)z * 0x1p-40f);
+        a.out_prob[row] = df_quotient(law.weight(x[q]), pair_sum(z));
     }
   }
 }
@@ -1704,22 +1718,21 @@ __global__ void __launch_bounds__(kPlainThreads, 5)
       dfloat cum = df_sub(upto, sum[j]);
       if (sum[j].hi > 0.f && df_gt(upto, thr) && !df_gt(cum, thr)) {  // one thread at most
         int at = -1;
-        float wt = 0.f;
-        dfloat before = cum;
+        dfloat wt = df_make(0.f), before = cum;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
           if ((at < 0 || !df_gt(cum, thr)) && w[j][i].hi > 0.f) {
             before = cum;
             cum = df_add(cum, w[j][i]);
             at = i;
-            wt = w[j][i].hi;
+            wt = w[j][i];
           }
         }
         const float gap = fminf(df_to_f(df_sub(thr, before)), df_to_f(df_sub(cum, thr)));
         if (gap > sh.pick_err) {
           for (int q = 0; q < C; ++q) *cluster.map_shared_rank(&sh.sure, q) = 1;
           a.out_tokens[row] = (v0 + j * kWarp) * kVec + at - whole.off;
-          if (a.out_prob != nullptr) a.out_prob[row] = wt / df_to_f(Z);
+          if (a.out_prob != nullptr) a.out_prob[row] = df_quotient(wt, Z);
         }
       }
     }
