@@ -536,8 +536,14 @@ spec_status spec_qk_norm_rope(const void* q, const void* k, const void* v, int64
  *   ws, ws_bytes  at least 16 bytes (its first word is the status word)
  * V up to 2^20.  A bad parameter (SPEC_ERR_INVALID_ARG) or a row with NaN,
  * +inf or only -inf (SPEC_ERR_NONFINITE) gives token -1 and probability 0.
- * Sums are held to about 2^-40, so the token is the definition's unless u * Z
- * lies that close to a step.  rows = 0 does nothing.  Of the workspace the
+ * Accuracy (T up to 2^100): a weight is held to 2^-28.9 of its value at worst and
+ * 2^-31.5 on average; where the draw is among a row's few largest tokens also to
+ * 2^-41 of the largest weight, the masses that top_p compares to 2^-41 or 2^-43
+ * of it a token; sums add 2^-40.  So the token is the definition's unless u * Z
+ * lies within 2^-28 * Z of a step, or a filter's cut that close to its target.
+ * Without filters the Z of out_prob is off by up to 2^-20 of its value (about 2^-24
+ * in practice), with them as above.
+ * rows = 0 does nothing.  Of the workspace the
  * second word counts rows that needed a second look, modulo 2^32; its value
  * does not matter, and calls that overlap may share it.
  */

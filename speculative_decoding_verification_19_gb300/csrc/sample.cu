@@ -13,14 +13,18 @@
 // A kept set is {x > tau} and the first c tokens equal to tau, so the filters
 // come down to a threshold and a count.
 //
-// Rounding.  The token is a whole number that hangs on a comparison of sums,
-// so the sums are held to about 2^-40 of their value, not to fp32's 2^-24
-// (with 150k tokens every second row has a step of C within fp32's error of
-// u Z).  Weights come as double-floats (fp32 pairs; exact to about 2^-32 of
-// each weight): the exponential by table and polynomial (P. T. P. Tang,
+// Rounding.  The token is a whole number that hangs on a comparison of sums;
+// with 150k tokens every second row has a step of C within fp32's error of
+// u Z.  Sums add 2^-40 of their value at most.  Weights come as double-floats
+// (fp32 pairs): the exponential by table and polynomial (P. T. P. Tang,
 // "Table-driven implementation of the exponential function", ACM TOMS 1989),
-// 2^(j/32) from the table and four terms of the series for the rest, sums as
-// double-floats.  GB300's fp64 rate is a hundredth of its fp32 rate, so
+// 2^(j/32) from the table and four terms of the series for the rest r.  They
+// are off by 2^-28.9 of their value at worst, 2^-31.5 on average: r (up to 2^-6)
+// is one fp32 number, 2^-31 off, or 2^-30 just above 2^-6; so is the series, whose
+// last product and sum round 2^-31 each; and the table's low word is not
+// multiplied by it, 2^-31.5.  With a few tokens a step of C is off by as much; with
+// many the errors average out.  (T above 2^100 loses more: log2(e) / T has no low
+// word left there.)  GB300's fp64 rate is a hundredth of its fp32 rate, so
 // nothing here is a per-element fp64 operation.  Masses that the filters
 // compare are 42-bit fixed-point integers: their sums do not depend on the
 // order of the atomics that form them.
@@ -156,7 +160,7 @@ struct Law {
       : m(max), c_hi(1.44269502f / T), pow2(table) {
     c_lo = (fmaf(-c_hi, T, 1.44269502f) + 1.92596303e-8f) / T;
   }
-  // exp((x - m) / T) as a double-float; 0 below 2^-120
+  // exp((x - m) / T) as a double-float, off by 2^-28.9 of it at most; 0 below 2^-120
   __device__ __forceinline__ dfloat weight(float x) const {
     const dfloat d = df_two_sum(x, -m);
     const float y = __fmul_rn(d.hi, c_hi);

@@ -53,3 +53,35 @@ def test_probabilities_are_rounded_once(n, V, k, min_p):
     p = w.gather(1, tok[:, None])[:, 0] / w.sum(1)
     err = ((prob - p).abs() / p).max().item()
     assert err <= PROB, err * 2 ** 24
+
+
+@pytest.mark.parametrize("path", ["plain", "runs", "list"])
+def test_tokens_beside_a_step(path):
+    """Two tokens and a uniform number next to the step between them, on either
+    side: the definition's token wherever it is more than 2^-28 away."""
+    rng = np.random.default_rng(40)
+    n = 20000
+    x = np.zeros((n, 2 if path != "list" else 3), np.float32)
+    x[:, 0] = -rng.uniform(0, 5, n)
+    x[:, 2:] = -300.0
+    T = rng.choice([0.3, 0.7, 1.0, 1.7], n).astype(np.float32)
+    first = np.exp(x[:, 0].astype(np.longdouble) / T.astype(np.longdouble))
+    step = first / (1 + first)
+    near = step.astype(np.float32)
+    kw = {}
+    if path == "runs":
+        kw["min_p"] = torch.full((n,), 1e-20, device="cuda")
+    if path == "list":
+        kw["top_k"] = torch.full((n,), 2, dtype=I32, device="cuda")
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    sure = 0
+    for u in (np.nextafter(near, np.float32(0)), near, np.nextafter(near, np.float32(1))):
+        u = np.minimum(u, np.float32(1 - 2.0 ** -24))
+        tok, _ = draw(dev(x), dev(T), dev(u), **kw)
+        want = (step <= u.astype(np.longdouble)).astype(np.int64)  # the first with C > u Z
+        clear = np.abs(step - u.astype(np.longdouble)) > 2.0 ** -28
+        assert np.array_equal(tok.cpu().numpy()[clear], want[clear])
+        sure += clear.mean()
+    # of the three sides; a count of the inputs alone (steps below 2^-4 have their
+    # neighbours within 2^-28): 1.342
+    assert sure > 1.3
