@@ -482,8 +482,9 @@ spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
  *   y = x * rsqrt(mean(x^2) + eps) * weight       (no norm without a weight)
  *   (a, b) -> (a cos - b sin, b cos + a sin), angle t * inv_freq[j], for the
  *   pairs (j, j + rot_dim/2), or (2j, 2j + 1) if interleaved, j < rot_dim/2
- * in fp32 (angles reduced exactly), rounded once; values of q and k have to be
- * finite.  rows = 0 does nothing.
+ * in fp32 (angles reduced exactly), rounded once; elements past rot_dim do not
+ * turn, and without a weight keep their bits.  Values of q and k that turn, or
+ * that a norm is taken of, have to be finite.  rows = 0 does nothing.
  *
  *   q [rows, Hq, D], k, v [rows, Hkv, D]  kv_dtype   rows q_stride, k_stride,
  *                 v_stride elements apart (multiples of 16 bytes), heads dense:

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(RopeArgs a, S
           const float s = __shfl_sync(0xffffffffu, s2[j & 1], ((j0 + j) >> 1) & 31);
           const bool first = kInter ? (i & 1) == 0 : e0 < half;
           wc[i] = turned ? c : 1.f;
-          ws[i] = turned ? (first ? -s : s) : 0.f;
+          ws[i] = turned ? (first ? -s : s) : -0.f;
           if (norm) {
             wc[i] *= to_f32(w[e0 + i]);
             ws[i] *= to_f32(w[kInter ? mate + (i ^ 1) : mate + i]);
@@ -174,13 +174,14 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(RopeArgs a, S
         unpack16(raw[k], x);
         if (kInter) {
 #pragma unroll
-          for (int i = 0; i < kVec; ++i) xp[i] = x[i ^ 1];
+          for (int i = 0; i < kVec; ++i) xp[i] = turned ? x[i ^ 1] : 0.f;
         } else {
           uint4 o;
           o.x = __shfl_sync(0xffffffffu, raw[k].x, partner);
           o.y = __shfl_sync(0xffffffffu, raw[k].y, partner);
           o.z = __shfl_sync(0xffffffffu, raw[k].z, partner);
           o.w = __shfl_sync(0xffffffffu, raw[k].w, partner);
+          if (!turned) o = make_uint4(0, 0, 0, 0);
           unpack16(o, xp);
         }
         float r = 1.f;
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(RopeArgs a, S
           for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
           r = rsqrtf(ss * (1.f / D) + a.eps);
         }
+        // what does not turn: 0 * -0 + x, which is x also for infinities and zeros
 #pragma unroll
         for (int i = 0; i < kVec; ++i) y[i] = fmaf(xp[i], ws[i], x[i] * wc[i]) * r;
         if (hh >= h1) continue;
