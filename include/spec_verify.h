@@ -209,7 +209,10 @@ spec_status spec_verify_attn(const void* q, const void* k_new,
  * read and may be anything, and so may the table entries of pages that hold
  * only such positions (spec_block_tables returns those pages).  Keys and
  * values that some row of a request sees have to be finite.  A window of the whole context
- * gives spec_verify_attn's results, up to the order of the sums.
+ * gives spec_verify_attn's results, up to the order of the sums and the bf16
+ * rounding of the probabilities, which the tensor cores take relative to the
+ * running maximum (as without a window: an output is off by up to 2^-8 of
+ * sum p |v| before it is rounded; the CUDA cores hold probabilities in fp32).
  */
 spec_status spec_verify_attn_window(const void* q, const void* k_new, const void* v_new,
                                     void* k_cache, void* v_cache, const int32_t* block_table,

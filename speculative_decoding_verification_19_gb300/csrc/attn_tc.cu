@@ -66,6 +66,17 @@
 // 9 rows, window 2048: 71 us for 0.24 GB; with one or two pairs a CTA the
 // start, the plan (6 us) and the merge of split pairs are half of it.
 //
+// Rounding.  Scores, maxima, row sums and O are fp32.  The probabilities are
+// rounded to bf16 for P V, whose two operands have one type, and the row sum
+// takes them unrounded: an output is off by up to 2^-8 of sum p |v| before its
+// own rounding, 0.0023 of its size (2-norm) against fp64 where probabilities in
+// fp32 leave 0.0017, the output's rounding.  A second product with what the
+// rounding leaves (P in twice the columns, so three S buffers instead of four)
+// brings the 0.0017, but each tile then issues eight PV MMAs instead of four:
+// 128 requests of 5 rows with a window of 4096 take 580 us instead of 388, 32 of
+// 9 rows 96 instead of 69.  So the probabilities stay bf16, with and without a
+// window; CUDA cores (SPEC_ATTN_CUDA_CORES) hold them in fp32.
+//
 // TMEM: S0..S3 cols [0,64) .. [192,256), O [256,384), P0..P3 (bf16 pairs of
 // S0..S3) [384,416) .. [480,512).  Four S buffers let Q K^T of tile t wait
 // only for P V of tile t-4: the hand-off chain QK -> softmax -> PV -> QK of a
