@@ -481,7 +481,11 @@ spec_status spec_block_tables(const int32_t* ctx_lens, const int32_t* row_start,
  * rotation in one pass; keys and values to the paged cache by slot.
  *
  * The queries and keys that spec_verify_attn takes, with their position
- * encoding applied.  For a head x at position t:
+ * encoding applied.  A verify step passes no slots: spec_verify_attn appends the
+ * new rows itself.  The cache is written here for rows that other attention
+ * reads, a prompt's prefill for instance, as are the ragged rows of
+ * spec_block_tables (the verify calls take M rows of every request, at most 128
+ * per KV head).  For a head x at position t:
  *   y = x * rsqrt(mean(x^2) + eps) * weight       (no norm without a weight)
  *   (a, b) -> (a cos - b sin, b cos + a sin), angle t * inv_freq[j], for the
  *   pairs (j, j + rot_dim/2), or (2j, 2j + 1) if interleaved, j < rot_dim/2
@@ -520,7 +524,11 @@ spec_status spec_qk_norm_rope(const void* q, const void* k, const void* v, int64
  * temperature, top-k, top-p and min-p.
  *
  * The draft's own draws, and plain decoding (gamma 0, the fallback of
- * spec_ctrl_update).  The law of a row is softmax(x / T) (page 1 §3.3)
+ * spec_ctrl_update).  Drafts have to be drawn by the law that the verify tests
+ * them against: with the temperature alone for spec_reject_sample, with its
+ * top_k and top_p for spec_reject_sample_filtered, and without min_p, which the
+ * verify does not know (its outputs would not follow the target's law).  min_p
+ * is for plain decoding.  The law of a row is softmax(x / T) (page 1 §3.3)
  * restricted as in spec_reject_sample_filtered (the first top_k tokens by
  * logit, the smaller index first among equal ones; of those the shortest
  * prefix whose mass reaches top_p times theirs) and then to the tokens of at

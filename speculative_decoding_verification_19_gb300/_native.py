@@ -256,7 +256,8 @@ def spec_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k
                       v_cache=None, stream=None) -> int:
     """RMS norm of every query and key head and the position rotation
     (2 * len(inv_freq) values of each head turn); with slots, the keys and
-    values also go to the paged cache."""
+    values also go to the paged cache (a prefill; a verify step passes none, as
+    spec_verify_attn appends its rows itself)."""
     return _done("spec_qk_norm_rope", _bind().qk_norm_rope(
         q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out, dims, ws, eps, interleaved,
         slots, k_cache, v_cache, None if stream is None else stream.cuda_stream))
@@ -265,7 +266,8 @@ def spec_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k
 def spec_sample(logits, temperature, uniform, out_tokens, out_prob, ws, top_k=None, top_p=None,
                 min_p=None, stream=None) -> int:
     """One token per row of logits [rows, V] (any row stride) from given
-    uniforms, with temperature, top-k, top-p and min-p."""
+    uniforms, with temperature, top-k, top-p and min-p.  Drafts that the verify
+    tests are drawn without min-p, which its laws do not have."""
     return _done("spec_sample", _bind().sample(
         logits, temperature, uniform, out_tokens, out_prob, ws, top_k, top_p, min_p,
         None if stream is None else stream.cuda_stream))
