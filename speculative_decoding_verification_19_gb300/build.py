@@ -3,8 +3,8 @@
 Each .cu under csrc/ is compiled to an object in parallel, then linked into
 speculative_decoding_verification_19_gb300/libspecverify.so, and
 csrc/binding.cpp (the step operators' argument checks) into _specbind.so
-beside it.  Everything is rebuilt when any source or header changed (content
-hash stamp).
+beside it; where the latter cannot be built the library is there all the same.
+Everything is rebuilt when any source or header changed (content hash stamp).
 """
 from __future__ import annotations
 
@@ -98,13 +98,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         bind = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        tmp = LIB + ".tmp"
+        cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        # the library stands by itself: without Python's and torch's headers the C
+        # ABI and its ctypes calls are there, and no binding of an older library
+        os.replace(tmp, LIB)
+        if os.path.exists(BIND):
+            os.remove(BIND)
         bind_obj = bind.result()
-    tmp = LIB + ".tmp"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
     # the binding finds the library beside it and torch's libraries loaded
     tmp = BIND + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, bind_obj, "-L" + PKG, "-l:" + os.path.basename(LIB),
