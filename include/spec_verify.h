@@ -464,9 +464,10 @@ spec_status spec_reject_sample_noalloc(const void* target_logits,
  * leaves every request unchanged, and so does a row_start that does not ascend
  * within [0, rows] (SPEC_ERR_INVALID_ARG; all of slots and positions are -1
  * then).  An entry of the table or the ring that is no block id raises
- * SPEC_ERR_DEVICE_BOUNDS and spreads to no other request: one that would take it,
- * or whose rows would be written to it, does not run (rows of -1, ok 0; it keeps
- * its pages, the entry as -1), and returned to the ring are block ids alone.
+ * SPEC_ERR_DEVICE_BOUNDS when it is met and spreads to no other request: one that
+ * takes it (the table then holds -1), or whose rows would be written to it, does
+ * not run (rows of -1, ok 0; it keeps its pages), and returned to the ring are
+ * block ids alone.
  * rows and B * max_blocks are at most 2^30.  Calls that share a page
  * state or a workspace must not overlap.
  */

@@ -13,9 +13,9 @@ dropped.  The pages do not say how blocks are handed out.  Readings taken:
   it ask for; else it takes none and does not run;
 * length -1 means that the request has ended;
 * a ring or table entry that is no block id (a corrupt state) serves no row and
-  is given to nobody: the request that would take it or write to it does not
-  run (its rows are -1, it keeps its pages), the entry reads -1 in the table,
-  and what is returned to the ring are block ids alone.
+  is given to nobody: the request that takes it (the table then holds -1) or
+  would write to it does not run (its rows are -1, it keeps its pages), and what
+  is returned to the ring are block ids alone.
 
 Written page by page with sets; no interval arithmetic.
 """

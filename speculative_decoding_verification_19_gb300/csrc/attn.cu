@@ -319,7 +319,9 @@ __global__ void __launch_bounds__(kSimtThreads) attn_split_kernel(
 // the call, 35 of them here, where the kernel above with a window took 100 of
 // 147; it waits for shared memory (46% of the issue slots used).  Tiles of 64
 // keys, two a lane, need a third fewer loads of the queries and leave registers
-// for two CTAs an SM instead of three: 52 us.
+// for two CTAs an SM instead of three: 52 us.  Three CTAs leave 80 registers, and
+// the instances of 8 rows a warp spill (136 bytes of stores a thread for fp32
+// heads of 64, 672 for heads of 128).
 constexpr int kWinWarps = 8;
 constexpr int kWinThreads = kWinWarps * kWarp;
 

@@ -25,7 +25,7 @@
 // weight into them: w_a cos and w_b sin stay in registers, which leaves few
 // enough of them for 32 warps an SM with four loads each in flight.
 // 16384 rows of 64 + 8 bf16 heads of 128 with the cache written (705 MB):
-// 117 us (104 at the copy rate); 178 us with the weights and both kinds of
+// 118 us (104 at the copy rate); 178 us with the weights and both kinds of
 // heads in one loop at 16 warps an SM.
 // (Packed fp32 pairs for the products took 135 us: pairing the unpacked halves
 // costs more than the packed instructions save.)

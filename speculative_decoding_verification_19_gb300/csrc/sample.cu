@@ -48,7 +48,7 @@
 //       holds u Z walks its run in order
 // Measured (queued calls, us): 640 rows of 152064 bf16 logits, temperature
 // alone, 72 (195 MB: 29 at the copy rate; the stream 50, the marked rows 21);
-// 33 rows of 32001 fp32 logits with mixed filters 27 (44 by the selects over
+// 33 rows of 32001 fp32 logits with mixed filters 26 to 31 (44 by the selects over
 // the cluster alone); one row of 32000: 9 without filters, 13 with top-k 50,
 // 18 with top-p 0.9; 33 rows of 128256 bf16 logits with a top-p that keeps
 // 30000 tokens 80.  A filtered row is bound by its chain of barriers, not by
