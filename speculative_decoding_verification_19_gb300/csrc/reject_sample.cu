@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kRsThreads) rs_rowstats_kernel(
 #pragma unroll
     for (int v = 0; v < kStatVecs; ++v) {
       const int64_t e = e0 + ((int64_t)v * kWarp + lane) * EPV;
-      raw[v] = (e + EPV <= V) ? __ldg(reinterpret_cast<const uint4*>(rp + e)) : make_uint4(0, 0, 0, 0);
+      raw[v] = (e + EPV <= V) ? load16(reinterpret_cast<const uint4*>(rp + e)) : make_uint4(0, 0, 0, 0);
     }
   };
 
@@ -1056,8 +1056,8 @@ __device__ __forceinline__ float lane_weights(const T* trow, const T* drow, int6
 #pragma unroll
   for (int v = 0; v < kStatVecs; ++v) {
     const bool in = e + (v + 1) * EPV <= V;  // rows are whole 16-byte vectors
-    raw_t[v] = in ? __ldg(reinterpret_cast<const uint4*>(trow + e) + v) : make_uint4(0, 0, 0, 0);
-    raw_d[v] = (in && nrej > 0) ? __ldg(reinterpret_cast<const uint4*>(drow + e) + v)
+    raw_t[v] = in ? load16(reinterpret_cast<const uint4*>(trow + e) + v) : make_uint4(0, 0, 0, 0);
+    raw_d[v] = (in && nrej > 0) ? load16(reinterpret_cast<const uint4*>(drow + e) + v)
                                 : make_uint4(0, 0, 0, 0);
   }
   float s = 0.f;
@@ -1943,8 +1943,8 @@ __device__ void tail_block_draw(const T* trow, const T* drow, int64_t e0, int V,
   float w[EPV];
   float ts = 0.f;
   if (e < V) {
-    const uint4 xt = __ldg(reinterpret_cast<const uint4*>(trow + e));
-    const uint4 xd = __ldg(reinterpret_cast<const uint4*>(drow + e));
+    const uint4 xt = load16(reinterpret_cast<const uint4*>(trow + e));
+    const uint4 xd = load16(reinterpret_cast<const uint4*>(drow + e));
     float ft[EPV], fd[EPV];
     unpack16(xt, ft);
     unpack16(xd, fd);

@@ -133,7 +133,7 @@ template <typename T, bool kAligned>
 __device__ __forceinline__ void load_vec(const T* row, int64_t e, int V, float (&f)[16 / sizeof(T)]) {
   constexpr int EPV = 16 / sizeof(T);
   if (kAligned && e + EPV <= V) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4*>(row + e));
+    const uint4 r = load16(reinterpret_cast<const uint4*>(row + e));
     unpack16(r, f);
   } else {
 #pragma unroll

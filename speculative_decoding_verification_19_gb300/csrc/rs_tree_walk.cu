@@ -215,8 +215,8 @@ __device__ void tw_slice_runs(const T* trow, const T* drow, int64_t v0, int64_t 
 #pragma unroll
     for (int k = 0; k < kTwBatch; ++k) {
       const int64_t v = base + (int64_t)k * kTwThreads;
-      xt[k] = v < v1 ? __ldg(reinterpret_cast<const uint4*>(trow) + v) : make_uint4(0, 0, 0, 0);
-      xd[k] = (drow != nullptr && v < v1) ? __ldg(reinterpret_cast<const uint4*>(drow) + v)
+      xt[k] = v < v1 ? load16(reinterpret_cast<const uint4*>(trow) + v) : make_uint4(0, 0, 0, 0);
+      xd[k] = (drow != nullptr && v < v1) ? load16(reinterpret_cast<const uint4*>(drow) + v)
                                           : make_uint4(0, 0, 0, 0);
     }
     // the batch: its maximum and first argmax, then its sum against that
@@ -281,8 +281,8 @@ __device__ void tw_slice_mass(const T* trow, const T* drow, int64_t v0, int64_t 
 #pragma unroll
     for (int k = 0; k < kTwBatch; ++k) {
       const int64_t v = base + (int64_t)k * kTwThreads;
-      xt[k] = v < v1 ? __ldg(reinterpret_cast<const uint4*>(trow) + v) : make_uint4(0, 0, 0, 0);
-      xd[k] = v < v1 ? __ldg(reinterpret_cast<const uint4*>(drow) + v) : make_uint4(0, 0, 0, 0);
+      xt[k] = v < v1 ? load16(reinterpret_cast<const uint4*>(trow) + v) : make_uint4(0, 0, 0, 0);
+      xd[k] = v < v1 ? load16(reinterpret_cast<const uint4*>(drow) + v) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < kTwBatch; ++k) {
@@ -329,8 +329,8 @@ __device__ void tw_slice_draw(const T* trow, const T* drow, int64_t v0, int64_t 
     float w[EPV];
     float ts = 0.f;
     if (v < v1) {
-      const uint4 xt = __ldg(reinterpret_cast<const uint4*>(trow) + v);
-      const uint4 xd = nrej > 0 ? __ldg(reinterpret_cast<const uint4*>(drow) + v)
+      const uint4 xt = load16(reinterpret_cast<const uint4*>(trow) + v);
+      const uint4 xd = nrej > 0 ? load16(reinterpret_cast<const uint4*>(drow) + v)
                                 : make_uint4(0, 0, 0, 0);
       float ft[EPV], fd[EPV];
       unpack16(xt, ft);
@@ -391,8 +391,8 @@ __device__ void tw_slice_draw(const T* trow, const T* drow, int64_t v0, int64_t 
   // slice (found by one more look at its last positive vector)
   if (tid == 0 && sh.last_pos >= 0) {
     const int64_t v = sh.last_pos / EPV;
-    const uint4 xt = __ldg(reinterpret_cast<const uint4*>(trow) + v);
-    const uint4 xd = nrej > 0 ? __ldg(reinterpret_cast<const uint4*>(drow) + v)
+    const uint4 xt = load16(reinterpret_cast<const uint4*>(trow) + v);
+    const uint4 xd = nrej > 0 ? load16(reinterpret_cast<const uint4*>(drow) + v)
                               : make_uint4(0, 0, 0, 0);
     float ft[EPV], fd[EPV];
     unpack16(xt, ft);

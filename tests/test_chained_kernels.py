@@ -8,6 +8,7 @@ before the write.  Any call of a step may stand before any other, so the rule
 holds for every input of every kernel that waits: block tables and slots come
 from spec_block_tables, queries, keys and cache rows from spec_qk_norm_rope,
 tokens from spec_sample, logits from spec_lm_head, lengths from kv_commit.
+For the same reason nothing is read by an explicit load of the read-only path.
 Checked in the source: a race shows on a GPU by luck alone.
 """
 import glob
@@ -46,6 +47,14 @@ def kernels(path):
             continue  # a declaration
         brace = text.index("{", stop)
         yield name[1], text[at + name.end():stop - 1], text[brace:closing(text, brace, "{}")]
+
+
+@pytest.mark.parametrize("path", SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))),
+                         ids=os.path.basename)
+def test_no_loads_of_the_read_only_path(path):
+    with open(path) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    assert not re.findall(r"__ldg\b|ld\.global\.nc", text)
 
 
 def test_the_kernels_are_found():

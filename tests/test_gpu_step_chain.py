@@ -140,3 +140,50 @@ def test_steps_back_to_back(impl, window, sinks, cached):
         graph.replay()
         for k in names:
             assert torch.equal(s[k], alone[k]), k
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_logits_of_the_head_read_by_the_next_call(tree):
+    """LM heads into one logits buffer, then the decisions and the draft's draws
+    that read it, many times with other hidden states, queued back to back: the
+    results of the calls one at a time."""
+    from synth import random_tree
+
+    steps, B, M, H, V = 8, 4, 8, 256, 8192
+    g = torch.Generator(device="cuda").manual_seed(32)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=g).to(BF)  # noqa: E731
+    hidden, w = rand(steps, 2, B * M, H), rand(2, V, H) * 0.1
+    parent = None
+    if tree:
+        parent = to_dev(np.stack([random_tree(np.random.default_rng(b), 3, 3, M) for b in range(B)]),
+                        I32)
+    T, u = torch.ones(B * M, device="cuda"), torch.rand(B * M, device="cuda", generator=g)
+    k = torch.full((B,), 40, dtype=I32, device="cuda")
+    dims = sv.make_dims(B=B, M=M, V=V)
+
+    def run(between):
+        ws = sv.workspace(dims)
+        target, draft = torch.zeros(2, B, M, V, dtype=BF, device="cuda")
+        out = []
+        for i in range(steps):
+            e = lambda *s: torch.zeros(*s, dtype=I32, device="cuda")  # noqa: E731
+            drawn, toks, path, acc = e(B, M), e(B, M), e(B, M), e(B)
+            sv.spec_lm_head(hidden[i, 1], w[1], draft.view(B * M, V), ws)
+            between()
+            sv.spec_sample(draft.view(B * M, V), T, u, drawn.view(-1), None, ws)
+            between()
+            sv.spec_lm_head(hidden[i, 0], w[0], target.view(B * M, V), ws)
+            between()
+            kw = {} if i % 2 else dict(top_k=k)  # without a filter, and with one
+            sv.spec_reject_sample(target, draft, drawn, parent, T[:B], 3, i, toks, path, acc, None,
+                                  dims, ws, **kw)
+            between()
+            out += [drawn, toks, path, acc]
+        torch.cuda.synchronize()
+        assert sv.device_status(ws) == 0
+        return out
+
+    alone = run(torch.cuda.synchronize)
+    for _ in range(20):
+        for a, b in zip(run(lambda: None), alone):
+            assert torch.equal(a, b)
