@@ -144,7 +144,10 @@ size_t spec_workspace_size(const spec_dims* dims);
  * kv_commit.  spec_reject_sample, its filtered form and
  * spec_reject_sample_lm_head keep counters at places that depend on dims: a
  * workspace that they use serves one spec_dims, or is zeroed again before a
- * call of theirs that follows one of other dims. */
+ * call of theirs that follows one of other dims.  Calls that may run at the same
+ * time (on two streams, in two graphs) have a workspace each; only
+ * spec_qk_norm_rope, spec_sample, spec_lm_head and kv_commit, which keep nothing
+ * in it but the status word and a count, may share one. */
 spec_status spec_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream` and read the device status word: bit (1 << code) is
