@@ -20,6 +20,9 @@
  *   spec_qk_norm_rope   per-head norm and position rotation of the queries and
  *                       keys that spec_verify_attn takes;
  *   spec_verify_attn_window  verify attention with a sliding window and sinks;
+ *   spec_verify_attn_prefix  verify attention of requests that begin alike;
+ *   spec_page_bounds, spec_page_score, spec_page_select, spec_verify_attn_pages
+ *                       verify attention over the pages that matter;
  *   spec_sample         the draft's own draws, and plain decoding.
  *
  * Conventions shared by every call
@@ -139,15 +142,17 @@ size_t spec_workspace_size(const spec_dims* dims);
  * `stream`.
  *
  * Calls of different dims may take turns on one workspace (of the largest
- * one's size) if they are spec_verify_attn, spec_verify_attn_window,
+ * one's size) if they are spec_verify_attn and its forms (_window, _prefix,
+ * _pages), spec_page_bounds, spec_page_score, spec_page_select,
  * spec_block_tables, spec_qk_norm_rope, spec_sample, spec_lm_head and
  * kv_commit.  spec_reject_sample, its filtered form and
  * spec_reject_sample_lm_head keep counters at places that depend on dims: a
  * workspace that they use serves one spec_dims, or is zeroed again before a
  * call of theirs that follows one of other dims.  Calls that may run at the same
  * time (on two streams, in two graphs) have a workspace each; only
- * spec_qk_norm_rope, spec_sample, spec_lm_head and kv_commit, which keep nothing
- * in it but the status word and a count, may share one. */
+ * spec_qk_norm_rope, spec_page_bounds, spec_page_score, spec_page_select,
+ * spec_sample, spec_lm_head and kv_commit, which keep nothing in it but the
+ * status word and a count, may share one. */
 spec_status spec_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream` and read the device status word: bit (1 << code) is
@@ -222,6 +227,126 @@ spec_status spec_verify_attn_window(const void* q, const void* k_new, const void
                                     const int32_t* ctx_lens, const int32_t* parent, int32_t window,
                                     int32_t sinks, void* out, float* lse, const spec_dims* dims,
                                     void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * spec_verify_attn_prefix -- spec_verify_attn of requests that begin alike.
+ *
+ * Page 2 §3.3: a prefix that is cached is not computed again; page 2 §4.3 and
+ * page 3 share its pages between requests.  Where every request of the batch
+ * begins with the same pages (a system prompt, a document that many questions
+ * go to, several samples of one prompt) their keys and values are read once for
+ * the whole batch here, not once a request.
+ *
+ *   prefix_table [prefix_len / 16] int32   the shared pages: position t <
+ *                 prefix_len of every request lives in block
+ *                 prefix_table[t/16], slot t%16
+ *   prefix_len    a multiple of 16, at least 16 and less than max_blocks * 16
+ * Other arguments and results as in spec_verify_attn, with the rounding of
+ * spec_verify_attn_window.  block_table has the requests' whole tables; its
+ * entries below prefix_len / 16 are not read.  A request whose ctx is less than
+ * prefix_len fails (SPEC_ERR_INVALID_ARG: caches untouched, out = 0, lse = -inf),
+ * and so does every request if an entry of prefix_table is no block id
+ * (SPEC_ERR_DEVICE_BOUNDS).  The shared pages are never written: the pages that
+ * the new rows go to must not be among them.
+ */
+spec_status spec_verify_attn_prefix(const void* q, const void* k_new, const void* v_new,
+                                    void* k_cache, void* v_cache, const int32_t* block_table,
+                                    const int32_t* ctx_lens, const int32_t* parent,
+                                    const int32_t* prefix_table, int32_t prefix_len, void* out,
+                                    float* lse, const spec_dims* dims, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/*
+ * spec_page_bounds -- least and largest coordinates of the keys of each page.
+ *
+ * The four calls from here on read only some pages of a long context (page 2
+ * §1.2: a step is bound by what it reads).  Before a step, spec_page_bounds
+ * brings the bounds of the pages that the last step changed up to date,
+ * spec_page_score gives every whole page a score for the step's queries,
+ * spec_page_select picks pages, and spec_verify_attn_pages reads those.
+ *
+ *   from_lens [B] int32 or NULL (all 0), >= 0   cached tokens whose pages' bounds
+ *                 hold: for every page p of request b with from_lens[b] / 16
+ *                 <= p and 16 p < ctx_lens[b] the bounds of its keys at
+ *                 positions below ctx_lens[b] are written
+ *   ctx_lens [B] int32   cached tokens (<= 0: nothing to do)
+ *   k_cache, block_table as in spec_verify_attn; table entries of other pages
+ *                 are not read
+ *   bounds [num_blocks, Hkv, 2, D] kv_dtype (in/out)   minima, then maxima,
+ *                 per block; other blocks keep theirs
+ *   ws, ws_bytes  at least 16 bytes (its first word is the status word)
+ * After kv_commit, from_lens are the context lengths before the step.  Blocks
+ * that several requests share may be met by several.  Keys have to be finite.
+ * A request with a negative from_lens (SPEC_ERR_INVALID_ARG) or ctx_lens past
+ * its table (SPEC_ERR_CAPACITY) is left out; so is a page whose entry is no
+ * block id (SPEC_ERR_DEVICE_BOUNDS).
+ */
+spec_status spec_page_bounds(const void* k_cache, const int32_t* block_table,
+                             const int32_t* from_lens, const int32_t* ctx_lens, void* bounds,
+                             const spec_dims* dims, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * spec_page_score -- how large a score a page's keys can have.
+ *
+ *   scores[b][h][p] = max over the rows i and query heads that read KV head h of
+ *                     sum_d max(q_d * lo_d, q_d * hi_d)
+ * with the page's bounds lo, hi: no row has a larger product q . k with a key
+ * of the page (softmax_scale is not applied).  Sums in fp32.
+ *   q [B, M, Hq, D] kv_dtype, bounds as in spec_page_bounds
+ *   scores [B, Hkv, max_blocks] float   -inf for p >= ctx_lens[b] / 16: pages
+ *                 that are not whole are always read
+ *   ws, ws_bytes  at least 16 bytes (its first word is the status word)
+ * A page whose table entry is no block id gets -inf (SPEC_ERR_DEVICE_BOUNDS), and
+ * so do all pages of a request whose ctx_lens passes its table
+ * (SPEC_ERR_CAPACITY) or is negative.
+ */
+spec_status spec_page_score(const void* q, const void* bounds, const int32_t* block_table,
+                            const int32_t* ctx_lens, float* scores, const spec_dims* dims, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * spec_page_select -- the pages of each request and KV head to be read.
+ *
+ * Of the F = ctx_lens[b] / 16 whole pages the first `first`, the last `last`
+ * and then those of largest score, the lower page first among equal scores,
+ * until there are n_pages (all F if there are no more than that).
+ *   scores [B, Hkv, max_blocks] float   those of pages from F on are not read;
+ *                 -0 equals 0; NaN counts as the lowest value
+ *                 (SPEC_ERR_NONFINITE)
+ *   n_pages >= 1, first, last >= 0, first + last <= n_pages
+ *   pages [B, Hkv, n_pages] int32   places in the block table, ascending; -1
+ *                 behind the last
+ *   counts [B] int32   min(F, n_pages); 0 for a negative ctx_lens or one past
+ *                 the table (SPEC_ERR_CAPACITY)
+ *   ws, ws_bytes  at least 16 bytes (its first word is the status word)
+ * Of dims, B, Hkv and max_blocks count (the others have to be valid).
+ */
+spec_status spec_page_select(const float* scores, const int32_t* ctx_lens, int32_t n_pages,
+                             int32_t first, int32_t last, int32_t* pages, int32_t* counts,
+                             const spec_dims* dims, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * spec_verify_attn_pages -- spec_verify_attn over selected pages.
+ *
+ * Of the cached positions every row sees those in the pages that its KV head
+ * has selected and those from (ctx / 16) * 16 on (the last, partial page); the
+ * new rows as in spec_verify_attn.
+ *
+ *   pages [B, Hkv, n_pages] int32, counts [B] int32   as spec_page_select
+ *                 writes them: counts[b] places in the block table for each KV
+ *                 head, strictly ascending, below ctx / 16 (0 of them: the last
+ *                 page and the new rows alone)
+ * Other arguments and results as in spec_verify_attn, with the rounding of
+ * spec_verify_attn_window.  Table entries and keys and values of other pages are
+ * not read and may be anything.  A request whose list breaks the rules fails
+ * (SPEC_ERR_INVALID_ARG: caches untouched, out = 0, lse = -inf).
+ */
+spec_status spec_verify_attn_pages(const void* q, const void* k_new, const void* v_new,
+                                   void* k_cache, void* v_cache, const int32_t* block_table,
+                                   const int32_t* ctx_lens, const int32_t* parent,
+                                   const int32_t* pages, const int32_t* counts, int32_t n_pages,
+                                   void* out, float* lse, const spec_dims* dims, void* ws,
+                                   size_t ws_bytes, void* stream);
 
 /*
  * spec_reject_sample -- accept / reject / resample of the drafts.

@@ -26,6 +26,8 @@ Modules:
                  compaction
   pages          block tables, slot map and positions from request lengths
   rope           per-head norm and position rotation
+  select         bounds, scores and selection of pages, attention over selected
+                 pages and behind a shared prefix
   sample         sampling with temperature, top-k, top-p and min-p
 
 Parity status: every function here is pinned by tests under tests/ against
@@ -61,3 +63,10 @@ from .lm_head import oracle_lm_head  # noqa: F401
 from .pages import oracle_block_tables  # noqa: F401
 from .rope import oracle_norm_rope  # noqa: F401
 from .sample import oracle_sample  # noqa: F401
+from .select import (  # noqa: F401
+    oracle_page_bounds,
+    oracle_page_score,
+    oracle_page_select,
+    oracle_verify_attn_pages,
+    oracle_verify_attn_prefix,
+)

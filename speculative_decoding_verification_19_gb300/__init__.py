@@ -4,7 +4,8 @@ The compute lives in libspecverify.so (hand-written CUDA for sm_103a, C ABI
 in include/spec_verify.h).  This package is its thin Python binding:
 
   spec_verify_attn    KV append + masked verify attention over a paged cache
-                      (with a sliding window and sinks on request)
+                      (on request with a sliding window and sinks, behind a
+                      prefix that the batch shares, or over selected pages)
   spec_reject_sample  temperature softmax, accept/reject, residual/bonus draw
                       (greedy at temperature 0; top-k / top-p restricted laws)
   spec_lm_head        LM-head logits on the tensor cores
@@ -16,6 +17,12 @@ around it, what a serving step needs before and beside it:
   spec_block_tables   block tables, slot map and positions from the lengths
   spec_qk_norm_rope   per-head norm and position rotation of queries and keys
   spec_sample         temperature / top-k / top-p / min-p sampling
+
+and which pages of a long cache each KV head reads:
+
+  spec_page_bounds    least and largest coordinates of each page's keys
+  spec_page_score     how large a score a page's keys can have
+  spec_page_select    the first, the last and the best pages
 
 plus helpers to size and initialise the caller-owned workspace and to read
 the device status word.
@@ -41,6 +48,9 @@ from ._native import (  # noqa: F401
     philox_block,
     spec_block_tables,
     spec_lm_head,
+    spec_page_bounds,
+    spec_page_score,
+    spec_page_select,
     spec_qk_norm_rope,
     spec_reject_sample,
     spec_reject_sample_lm_head,

@@ -35,6 +35,8 @@ EXPORTS = (
     "spec_ctrl_default_config", "spec_ctrl_init", "spec_ctrl_update", "spec_ctrl_metrics",
     "spec_step_stats",
     "spec_verify_attn_window", "spec_block_tables", "spec_qk_norm_rope", "spec_sample",
+    "spec_verify_attn_prefix", "spec_verify_attn_pages", "spec_page_bounds", "spec_page_score",
+    "spec_page_select",
 )
 
 
@@ -106,6 +108,16 @@ def lib() -> ctypes.CDLL:
     L.spec_qk_norm_rope.restype = i32
     L.spec_sample.argtypes = [vp, i64, i32, i32, i32] + [vp] * 7 + [vp, sz, vp]
     L.spec_sample.restype = i32
+    L.spec_verify_attn_prefix.argtypes = [vp] * 9 + [i32, vp, vp, pd, vp, sz, vp]
+    L.spec_verify_attn_prefix.restype = i32
+    L.spec_verify_attn_pages.argtypes = [vp] * 10 + [i32, vp, vp, pd, vp, sz, vp]
+    L.spec_verify_attn_pages.restype = i32
+    L.spec_page_bounds.argtypes = [vp] * 5 + [pd, vp, sz, vp]
+    L.spec_page_bounds.restype = i32
+    L.spec_page_score.argtypes = [vp] * 5 + [pd, vp, sz, vp]
+    L.spec_page_score.restype = i32
+    L.spec_page_select.argtypes = [vp, vp, i32, i32, i32, vp, vp, pd, vp, sz, vp]
+    L.spec_page_select.restype = i32
     L.spec_philox_block.argtypes = [ctypes.POINTER(u64)] * 3
     L.spec_philox_block.restype = None
     L.spec_status_string.argtypes = [i32]
@@ -197,16 +209,29 @@ def _done(fn: str, result: int) -> int:
 
 def spec_verify_attn(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens,
                      parent, out, lse, dims: SpecDims, ws, stream=None, window=None,
-                     sinks=0) -> int:
-    """spec_verify_attn; with a window (and sinks) spec_verify_attn_window.  A
+                     sinks=0, prefix=None, pages=None, page_counts=None) -> int:
+    """spec_verify_attn; with a window (and sinks) spec_verify_attn_window, with
+    `prefix` (block ids of the pages that all requests begin with, [n] int32)
+    spec_verify_attn_prefix, with `pages` and `page_counts` (a selection by
+    spec_page_select) spec_verify_attn_pages; one of the three at most.  A
     window of None or 0 is none, as in spec_block_tables."""
-    if window is None or window == 0:
-        if sinks:
-            raise ValueError("sinks: a window is wanted with them")
-    else:
-        return _done("spec_verify_attn_window", _bind().verify_attn_window(
-            q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, out, lse, dims, ws,
-            window, sinks, None if stream is None else stream.cuda_stream))
+    windowed = window is not None and window != 0
+    if sinks and not windowed:
+        raise ValueError("sinks: a window is wanted with them")
+    if (pages is None) != (page_counts is None):
+        raise ValueError("pages and page_counts: both are wanted, or neither")
+    if windowed + (prefix is not None) + (pages is not None) > 1:
+        raise ValueError("window, prefix and pages: one of them at most")
+    st = None if stream is None else stream.cuda_stream
+    args = (q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, out, lse, dims, ws)
+    if windowed:
+        return _done("spec_verify_attn_window",
+                     _bind().verify_attn_window(*args, window, sinks, st))
+    if prefix is not None:
+        return _done("spec_verify_attn_prefix", _bind().verify_attn_prefix(*args, prefix, st))
+    if pages is not None:
+        return _done("spec_verify_attn_pages",
+                     _bind().verify_attn_pages(*args, pages, page_counts, st))
     code = lib().spec_verify_attn(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
         _ptr(block_table), _ptr(ctx_lens), _ptr(parent), _ptr(out), _ptr(lse),
@@ -249,6 +274,33 @@ def spec_block_tables(ctx_lens, row_start, parent, block_table, span, pool, pool
     return _done("spec_block_tables", _bind().block_tables(
         ctx_lens, row_start, parent, block_table, span, pool, pool_state, slots, positions, ok, dims,
         ws, window, sinks, None if stream is None else stream.cuda_stream))
+
+
+def spec_page_bounds(k_cache, block_table, from_lens, ctx_lens, bounds, dims: SpecDims, ws,
+                     stream=None) -> int:
+    """Least and largest coordinates of the keys of every page from position
+    from_lens (None: 0) to ctx_lens, to bounds [num_blocks, Hkv, 2, D]."""
+    return _done("spec_page_bounds", _bind().page_bounds(
+        k_cache, block_table, from_lens, ctx_lens, bounds, dims, ws,
+        None if stream is None else stream.cuda_stream))
+
+
+def spec_page_score(q, bounds, block_table, ctx_lens, scores, dims: SpecDims, ws,
+                    stream=None) -> int:
+    """How large a score the keys of each whole page can have with any query
+    that reads the KV head, to scores [B, Hkv, max_blocks]."""
+    return _done("spec_page_score", _bind().page_score(
+        q, bounds, block_table, ctx_lens, scores, dims, ws,
+        None if stream is None else stream.cuda_stream))
+
+
+def spec_page_select(scores, ctx_lens, pages, page_counts, dims: SpecDims, ws, first=0, last=0,
+                     stream=None) -> int:
+    """The pages of each request and KV head to be read: the `first` and the
+    `last` whole ones and those of largest score, pages.shape[2] together."""
+    return _done("spec_page_select", _bind().page_select(
+        scores, ctx_lens, pages, page_counts, dims, ws, first, last,
+        None if stream is None else stream.cuda_stream))
 
 
 def spec_qk_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, k_out,

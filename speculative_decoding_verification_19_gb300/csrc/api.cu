@@ -10,6 +10,7 @@
 #include "kv_commit.cuh"
 #include "philox.cuh"
 #include "lm_head.cuh"
+#include "page_select.cuh"
 #include "qk_norm_rope.cuh"
 #include "reject_sample.cuh"
 #include "sample.cuh"
@@ -61,6 +62,13 @@ WsLayout workspace_layout(const spec_dims& d) {
   const size_t tc_bytes = d.Hkv > 0 ? sizeof(float) * attn_tc_part_floats(d) : 0;
   if (tc_bytes > L.attn_bytes) L.attn_bytes = tc_bytes;
   L.attn_off = take(L.attn_bytes);
+  if (group > 0 && L.rows <= kMaxNodes) {  // calls of more rows are refused
+    L.view_ctx_off = take(sizeof(int32_t) * (size_t)d.B);
+    if (d.max_blocks > 0)
+      L.view_table_off = take(sizeof(int32_t) * (size_t)d.B * d.Hkv * d.max_blocks);
+    L.own_part_off = take(sizeof(float) * (size_t)d.B * d.Hkv * L.rows * tc_part_stride(d.D));
+    L.pfx_part_off = take(sizeof(float) * prefix_part_floats(d));
+  }
   L.rs_chunk = rs_chunk_elems(d.logits_dtype);
   L.rs_chunks = (int)ceil_div64(d.V, L.rs_chunk);
   L.rs_bytes = sizeof(RowStat) * (size_t)d.B * 2 * d.M * L.rs_chunks;
@@ -149,9 +157,9 @@ spec_status spec_get_device_status(void* ws, void* stream, int32_t* flags, int32
 
 static spec_status attn_common(const void* q, const void* k_new, const void* v_new, void* k_cache,
                                void* v_cache, const int32_t* block_table, const int32_t* ctx_lens,
-                               const int32_t* parent, int32_t window, int32_t sinks, void* out,
-                               float* lse, const spec_dims* dims, void* ws, size_t ws_bytes,
-                               void* stream) {
+                               const int32_t* parent, int32_t window, int32_t sinks,
+                               AttnView view, void* out, float* lse, const spec_dims* dims,
+                               void* ws, size_t ws_bytes, void* stream) {
   g_launches = 0;
   spec_status s = check_common(dims);
   if (s != SPEC_OK) return s;
@@ -200,7 +208,27 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
   a.scale = dims->softmax_scale != 0.f ? dims->softmax_scale : 1.0f / sqrtf((float)dims->D);
   a.window = window;
   a.sinks = sinks;
+  a.view = view;
   a.ws = ws;
+  if (view.mode != kViewNone) {
+    char* w = static_cast<char*>(ws);
+    a.view.ctx = reinterpret_cast<int32_t*>(w + lay.view_ctx_off);
+    if (view.mode == kViewPrefix) {
+      const int pp = view.prefix_len / kBlock;
+      a.view.table = block_table + pp;
+      a.view.stride_b = dims->max_blocks;
+      a.view.stride_h = 0;
+      a.view.entries = dims->max_blocks - pp;
+    } else {
+      // the selected pages, then those of the context's last partial page and
+      // the new rows; together no more than the context and the new rows have
+      const int64_t most = (int64_t)view.n_pages + ceil_div(kBlock - 1 + dims->M, kBlock);
+      a.view.entries = most < dims->max_blocks ? (int)most : dims->max_blocks;
+      a.view.table = reinterpret_cast<int32_t*>(w + lay.view_table_off);
+      a.view.stride_h = a.view.entries;
+      a.view.stride_b = (int64_t)dims->Hkv * a.view.entries;
+    }
+  }
   int launches = 0;
   const cudaError_t e = use_tc ? attn_launch_tc(a, lay, static_cast<cudaStream_t>(stream), &launches)
                                : attn_launch_simt(a, lay, static_cast<cudaStream_t>(stream), &launches);
@@ -212,8 +240,8 @@ spec_status spec_verify_attn(const void* q, const void* k_new, const void* v_new
                              void* v_cache, const int32_t* block_table, const int32_t* ctx_lens,
                              const int32_t* parent, void* out, float* lse, const spec_dims* dims,
                              void* ws, size_t ws_bytes, void* stream) {
-  return attn_common(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, 0, 0, out,
-                     lse, dims, ws, ws_bytes, stream);
+  return attn_common(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, 0, 0,
+                     AttnView{}, out, lse, dims, ws, ws_bytes, stream);
 }
 
 spec_status spec_verify_attn_window(const void* q, const void* k_new, const void* v_new,
@@ -229,8 +257,105 @@ spec_status spec_verify_attn_window(const void* q, const void* k_new, const void
   if (cap > INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
   const int32_t most = cap > 0 ? (int32_t)cap : 1;
   return attn_common(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent,
-                     window < most ? window : most, sinks < most ? sinks : most, out, lse, dims, ws,
-                     ws_bytes, stream);
+                     window < most ? window : most, sinks < most ? sinks : most, AttnView{}, out,
+                     lse, dims, ws, ws_bytes, stream);
+}
+
+spec_status spec_verify_attn_prefix(const void* q, const void* k_new, const void* v_new,
+                                    void* k_cache, void* v_cache, const int32_t* block_table,
+                                    const int32_t* ctx_lens, const int32_t* parent,
+                                    const int32_t* prefix_table, int32_t prefix_len, void* out,
+                                    float* lse, const spec_dims* dims, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  g_launches = 0;
+  if (dims == nullptr || !prefix_table) return SPEC_ERR_INVALID_ARG;
+  const int64_t cap = (int64_t)dims->max_blocks * kBlock;
+  if (cap > INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
+  if (prefix_len < kBlock || prefix_len % kBlock != 0 || prefix_len >= cap)
+    return SPEC_ERR_INVALID_ARG;
+  AttnView v = {};
+  v.mode = kViewPrefix;
+  v.prefix_table = prefix_table;
+  v.prefix_len = prefix_len;
+  return attn_common(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, 0, 0, v, out,
+                     lse, dims, ws, ws_bytes, stream);
+}
+
+spec_status spec_verify_attn_pages(const void* q, const void* k_new, const void* v_new,
+                                   void* k_cache, void* v_cache, const int32_t* block_table,
+                                   const int32_t* ctx_lens, const int32_t* parent,
+                                   const int32_t* pages, const int32_t* counts, int32_t n_pages,
+                                   void* out, float* lse, const spec_dims* dims, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  if (dims == nullptr || !pages || !counts || n_pages < 1) return SPEC_ERR_INVALID_ARG;
+  if ((int64_t)dims->max_blocks * kBlock > INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
+  AttnView v = {};
+  v.mode = kViewPages;
+  v.pages = pages;
+  v.counts = counts;
+  v.n_pages = n_pages;
+  return attn_common(q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, 0, 0, v, out,
+                     lse, dims, ws, ws_bytes, stream);
+}
+
+// Checks that the calls on pages' bounds and scores share; of the workspace
+// they use the status word alone.
+static spec_status check_pages(const spec_dims* d, void* ws, size_t ws_bytes) {
+  spec_status s = check_common(d);
+  if (s != SPEC_OK) return s;
+  if ((s = check_kv(d)) != SPEC_OK) return s;
+  if ((int64_t)d->max_blocks * kBlock > INT32_MAX / 2 || d->Hkv > 65535) return SPEC_ERR_UNSUPPORTED;
+  if (ws == nullptr || ws_bytes < 16 || !aligned16(ws)) return SPEC_ERR_INVALID_ARG;
+  return SPEC_OK;
+}
+
+spec_status spec_page_bounds(const void* k_cache, const int32_t* block_table,
+                             const int32_t* from_lens, const int32_t* ctx_lens, void* bounds,
+                             const spec_dims* dims, void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  const spec_status s = check_pages(dims, ws, ws_bytes);
+  if (s != SPEC_OK) return s;
+  if (!k_cache || !block_table || !ctx_lens || !bounds) return SPEC_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(bounds)) return SPEC_ERR_INVALID_ARG;
+  const BoundsArgs a = {k_cache, block_table, from_lens, ctx_lens, bounds, *dims,
+                        static_cast<uint32_t*>(ws)};
+  int launches = 0;
+  const cudaError_t e = page_bounds_launch(a, static_cast<cudaStream_t>(stream), &launches);
+  g_launches = launches;
+  return from_cuda(e);
+}
+
+spec_status spec_page_score(const void* q, const void* bounds, const int32_t* block_table,
+                            const int32_t* ctx_lens, float* scores, const spec_dims* dims, void* ws,
+                            size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  const spec_status s = check_pages(dims, ws, ws_bytes);
+  if (s != SPEC_OK) return s;
+  if (!q || !bounds || !block_table || !ctx_lens || !scores) return SPEC_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(bounds)) return SPEC_ERR_INVALID_ARG;
+  const ScoreArgs a = {q, bounds, block_table, ctx_lens, scores, *dims, static_cast<uint32_t*>(ws)};
+  int launches = 0;
+  const cudaError_t e = page_score_launch(a, static_cast<cudaStream_t>(stream), &launches);
+  g_launches = launches;
+  return from_cuda(e);
+}
+
+spec_status spec_page_select(const float* scores, const int32_t* ctx_lens, int32_t n_pages,
+                             int32_t first, int32_t last, int32_t* pages, int32_t* counts,
+                             const spec_dims* dims, void* ws, size_t ws_bytes, void* stream) {
+  g_launches = 0;
+  const spec_status s = check_pages(dims, ws, ws_bytes);
+  if (s != SPEC_OK) return s;
+  if (!scores || !ctx_lens || !pages || !counts) return SPEC_ERR_INVALID_ARG;
+  if (n_pages < 1 || first < 0 || last < 0 || (int64_t)first + last > n_pages)
+    return SPEC_ERR_INVALID_ARG;
+  const SelectArgs a = {scores, ctx_lens, n_pages, first, last, pages, counts, *dims,
+                        static_cast<uint32_t*>(ws)};
+  int launches = 0;
+  const cudaError_t e = page_select_launch(a, static_cast<cudaStream_t>(stream), &launches);
+  g_launches = launches;
+  return from_cuda(e);
 }
 
 static spec_status reject_common(const void* target_logits, const void* draft_logits,

@@ -17,7 +17,8 @@
 //                      key range); all group*M query rows that read the KV
 //                      head are handled together, so every K/V byte is read
 //                      once per range.  Online softmax in base 2.
-//   attn_win_split_kernel  the same over a sliding window and sinks.
+//   attn_win_split_kernel  the same over a sliding window and sinks, or over a
+//                      view of the request (AttnView).
 //   attn_combine_kernel  merges the per-range partials by log-sum-exp, a warp
 //                      per row.
 #include <math.h>
@@ -34,7 +35,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) kv_append_kernel(
     const T* k_new, const T* v_new, T* k_cache, T* v_cache, const int32_t* block_table,
     const int32_t* ctx_lens, const int32_t* parent, spec_dims d, int window, int sinks,
-    ulonglong2* anc_ws, int32_t* depth_ws, int32_t* __restrict__ req_ok,
+    AttnView view, ulonglong2* anc_ws, int32_t* depth_ws, int32_t* __restrict__ req_ok,
     uint32_t* __restrict__ status) {
   pdl_trigger();
   pdl_wait();  // the inputs and the cache may come from the previous kernel
@@ -49,8 +50,12 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
   const bool cap_ok = ctx >= 0 && L <= cap;
   // block ids of every page the request reads or writes (with a window, not
   // of the pages between the sinks and it)
-  int bad_block = 0;
-  if (cap_ok) {
+  int bad_block = 0, bad_view = 0;
+  if (cap_ok && view.mode != kViewNone) {
+    const int bad = view_check(view, d, bt, b, ctx, blockIdx.y == 0);
+    bad_view = bad & 1;
+    bad_block = bad & 2;
+  } else if (cap_ok) {
     const int pages = (int)ceil_div64(L, kBlock);
     for (int p = tid; p < pages; p += blockDim.x) {
       const int id = bt[p];
@@ -70,10 +75,11 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
     }
   }
   bad_block = __syncthreads_or(bad_block);
-  bad_topo = __syncthreads_or(bad_topo);
+  bad_topo = __syncthreads_or(bad_topo | bad_view);
   const bool ok = cap_ok && !bad_block && !bad_topo;
   if (tid == 0 && blockIdx.y == 0) {
     req_ok[b] = ok ? 1 : 0;
+    if (ok && view.mode != kViewNone) view.ctx[b] = view_ctx(view, b, ctx);
     if (!cap_ok) raise_status(status, SPEC_ERR_CAPACITY);
     if (bad_block) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
     if (bad_topo) raise_status(status, SPEC_ERR_INVALID_ARG);
@@ -122,6 +128,7 @@ constexpr int kSimtWarps = kSimtThreads / kWarp;
 constexpr int kMaxRows = 128;  // new rows per request (tree nodes)
 constexpr int kMinWinSplit = 64;  // fewest keys of a range with a window
 constexpr int kWinCtas = 3 * 152;
+constexpr int kNoWindow = 1 << 30;  // positions stay below it
 
 size_t attn_simt_smem_bytes(int R, int D) {
   return sizeof(float) * ((size_t)R * D + kTileKeys * (D + 4) + kTileKeys * D + (size_t)R * kTileKeys) +
@@ -342,8 +349,8 @@ __device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, uns
 
 template <typename T, int D, int RPW>
 __global__ void __launch_bounds__(kWinThreads, RPW <= 8 ? 3 : (D == 64 ? 2 : 1)) attn_win_split_kernel(
-    const T* q, const T* k_cache, const T* v_cache, const int32_t* block_table,
-    const int32_t* ctx_lens, const ulonglong2* anc_ws, const int32_t* depth_ws,
+    const T* q, const T* k_cache, const T* v_cache, const int32_t* table, int64_t stride_b,
+    int64_t stride_h, const int32_t* ctx_lens, const ulonglong2* anc_ws, const int32_t* depth_ws,
     const int32_t* req_ok, spec_dims d, int window, int sinks, float qscale,
     int split_keys, int max_splits, float* __restrict__ part) {
   constexpr int DPL = D / kWarp;  // d values per lane in the PV step
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(kWinThreads, RPW <= 8 ? 3 : (D == 64 ? 2 : 1))
   constexpr int kVecPerKey = D / kVec;
   constexpr int kItems = kTileKeys * kVecPerKey / kWinThreads;  // 16-byte vectors of a thread
   static_assert(kItems >= 1, "a tile has at least one vector per thread");
-  const int32_t* bt = block_table + (int64_t)b * d.max_blocks;
+  const int32_t* bt = table + b * stride_b + h * stride_h;
   uint4 kr[kItems], vr[kItems];
   // vectors of the tile at t0; keys past the range and keys that no row sees
   // (their pages may not be held, their values may be anything) are zero
@@ -607,25 +614,37 @@ cudaError_t kv_append_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_
     e = cudaLaunchKernelEx(&L.cfg, kv_append_kernel<T>, static_cast<const T*>(a.k_new),
                            static_cast<const T*>(a.v_new), static_cast<T*>(a.k_cache),
                            static_cast<T*>(a.v_cache), a.block_table, a.ctx_lens, a.parent, d,
-                           a.window, a.sinks, anc, depth, req_ok, status);
+                           a.window, a.sinks, a.view, anc, depth, req_ok, status);
   } else {
     e = cudaLaunchKernelEx(&L.cfg, kv_append_kernel<float>, static_cast<const float*>(a.k_new),
                            static_cast<const float*>(a.v_new), static_cast<float*>(a.k_cache),
                            static_cast<float*>(a.v_cache), a.block_table, a.ctx_lens, a.parent,
-                           d, a.window, a.sinks, anc, depth, req_ok, status);
+                           d, a.window, a.sinks, a.view, anc, depth, req_ok, status);
   }
   ++*launches;
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T>
-static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, int* launches) {
+static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaStream_t st,
+                               int* launches) {
+  AttnArgs a = args;
+  if (a.view.mode != kViewNone) {  // the windowed kernel with a window past every view
+    a.window = kNoWindow;
+    a.sinks = 0;
+  }
   const spec_dims& d = a.d;
   const int R = (d.Hq / d.Hkv) * d.M;
   int32_t* req_ok = reinterpret_cast<int32_t*>(static_cast<char*>(a.ws) + lay.attn_ok_off);
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + lay.attn_off);
 
-  kv_append_launch(a, lay, st, launches);
+  cudaError_t e = kv_append_launch(a, lay, st, launches);
+  if (e != cudaSuccess) return e;
+  const bool viewed = a.view.mode != kViewNone;
+  const int32_t* table = viewed ? a.view.table : a.block_table;
+  const int64_t stride_b = viewed ? a.view.stride_b : d.max_blocks;
+  const int64_t stride_h = viewed ? a.view.stride_h : 0;
+  const int32_t* ctx = viewed ? a.view.ctx : a.ctx_lens;
 
   const size_t smem = attn_simt_smem_bytes(R, d.D);
   // Key ranges: the layout's, or, with a window, of the fewer keys that a
@@ -634,7 +653,8 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
   // 128), in whole tiles, no more ranges than the partials' workspace holds.
   int split_keys = lay.split_keys, splits = lay.max_splits;
   if (a.window > 0) {
-    const int64_t most = min((int64_t)d.max_blocks * kBlock,
+    const int64_t entries = viewed ? a.view.entries : d.max_blocks;
+    const int64_t most = min(entries * kBlock,
                              (int64_t)ceil_div(a.sinks, kTileKeys) * kTileKeys + a.window + d.M +
                                  kTileKeys);
     const int64_t want = max((int64_t)kMinWinSplit, (int64_t)d.B * d.Hkv * most / kWinCtas);
@@ -647,7 +667,6 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
   const int32_t* depth =
       reinterpret_cast<const int32_t*>(static_cast<char*>(a.ws) + lay.win_depth_off);
   const float qscale = a.scale * 1.4426950408889634f;
-  cudaError_t e = cudaSuccess;
 #define SPECV_SIMT(DD, RPW)                                                                   \
   do {                                                                                        \
     auto k = attn_split_kernel<T, DD, RPW>;                                                   \
@@ -669,7 +688,7 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
     PdlLaunch L(grid, dim3(kWinThreads), win_smem, st);                                       \
     e = cudaLaunchKernelEx(&L.cfg, k, static_cast<const T*>(a.q),                             \
                            static_cast<const T*>(a.k_cache), static_cast<const T*>(a.v_cache),\
-                           a.block_table, a.ctx_lens, anc, depth, (const int32_t*)req_ok, d,  \
+                           table, stride_b, stride_h, ctx, anc, depth, (const int32_t*)req_ok, d, \
                            a.window, a.sinks, qscale, split_keys, splits, part);              \
     if (e != cudaSuccess) return e;                                                           \
   } while (0)
@@ -706,10 +725,17 @@ static cudaError_t launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStrea
 #undef SPECV_WIN
 #undef SPECV_SIMT
   ++*launches;
+  if (a.view.mode == kViewPrefix) {
+    PrefixPlan plan;
+    e = prefix_launch(a, lay, st, &plan, launches);
+    if (e != cudaSuccess) return e;
+    const OwnPart own = {part, splits, d.D + 1, split_keys, ctx, req_ok};
+    return prefix_merge_launch(a, lay, plan, own, st, launches);
+  }
 
   {
     PdlLaunch L(dim3(d.Hkv, ceil_div(R, 8), d.B), dim3(256), 0, st);
-    e = cudaLaunchKernelEx(&L.cfg, attn_combine_kernel<T>, (const float*)part, a.ctx_lens,
+    e = cudaLaunchKernelEx(&L.cfg, attn_combine_kernel<T>, (const float*)part, ctx,
                            (const int32_t*)req_ok, d, a.window, a.sinks, split_keys, splits,
                            static_cast<T*>(a.out), a.lse);
     if (e != cudaSuccess) return e;

@@ -5,6 +5,35 @@
 
 namespace specv {
 
+// A request as the attention kernels see it where they do not read the whole
+// context.  They run on a view: ctx cached keys in blocks of a table of its own,
+// then the M new rows, as if that were the request; only the append and the
+// checks go by the request itself.
+//   kViewPrefix  the first prefix_len positions are the batch's shared prefix
+//                and read elsewhere: ctx is less by prefix_len, the table starts
+//                prefix_len / 16 entries later
+//   kViewPages   the selected whole pages of each KV head, then the pages from
+//                the last (partial) one of the context on; the request check
+//                writes a table of block ids for every KV head
+enum { kViewNone = 0, kViewPrefix = 1, kViewPages = 2 };
+struct AttnView {
+  int mode;
+  const int32_t* prefix_table;  // [prefix_len / 16]
+  int prefix_len;
+  const int32_t* pages;   // [B, Hkv, n_pages], ascending
+  const int32_t* counts;  // [B]
+  int n_pages;
+  const int32_t* table;   // block of page p of the view: table[b * stride_b + h * stride_h + p]
+  int64_t stride_b, stride_h;
+  int entries;            // pages of a view at most
+  int32_t* ctx;           // [B] cached keys of the views
+};
+// Cached keys of a request's view (the request itself has been checked).
+__device__ __forceinline__ int view_ctx(const AttnView& v, int b, int ctx) {
+  if (v.mode == kViewPrefix) return ctx - v.prefix_len;
+  return __ldcg(v.counts + b) * kBlock + ctx % kBlock;
+}
+
 struct AttnArgs {
   const void* q;
   const void* k_new;
@@ -19,6 +48,7 @@ struct AttnArgs {
   spec_dims d;
   float scale;
   int window, sinks;  // window 0: every cached position is visible
+  AttnView view;      // mode kViewNone: the requests themselves
   void* ws;
 };
 
@@ -67,7 +97,79 @@ __device__ __forceinline__ void win_row_mask(const int32_t* par, int n, int ctx,
   *depth = at;
 }
 
+// Checks of a view that needs the whole CTA (the request's length has been
+// checked): bit 0 a bad argument, bit 1 a bad block id among the pages that the
+// view holds, for this thread's share.  `write`: the table of block ids is
+// written (kViewPages; entries that are no block id stay out of it).
+__device__ __forceinline__ int view_check(const AttnView& v, const spec_dims& d, const int32_t* bt,
+                                          int b, int ctx, bool write) {
+  const int pages = (int)ceil_div64((int64_t)ctx + d.M, kBlock);
+  int bad = 0;
+  if (v.mode == kViewPrefix) {
+    if (ctx < v.prefix_len) return 1;
+    const int pp = v.prefix_len / kBlock;
+#pragma unroll 4
+    for (int p = threadIdx.x; p < pages; p += blockDim.x) {
+      const int id = __ldcg(p < pp ? v.prefix_table + p : bt + p);
+      if (id < 0 || id >= d.num_blocks) bad |= 2;
+    }
+    return bad;
+  }
+  const int n = __ldcg(v.counts + b), full = ctx / kBlock;
+  if (n < 0 || n > v.n_pages || n > full) return 1;
+  int32_t* table = const_cast<int32_t*>(v.table) + (int64_t)b * v.stride_b;
+  const int len = n + pages - full;  // pages of the view: at most `pages`
+  for (int e = threadIdx.x; e < d.Hkv * len; e += blockDim.x) {
+    const int h = e / len, j = e - h * len;
+    int p = full + j - n;
+    if (j < n) {
+      const int32_t* list = v.pages + ((int64_t)b * d.Hkv + h) * v.n_pages + j;
+      p = __ldcg(list);
+      if (p < 0 || p >= full || (j > 0 && __ldcg(list - 1) >= p)) {
+        bad |= 1;
+        continue;
+      }
+    }
+    const int id = __ldcg(bt + p);
+    if (id < 0 || id >= d.num_blocks) bad |= 2;
+    else if (write) table[h * v.stride_h + j] = id;
+  }
+  return bad;
+}
+
+// One pass over the keys of a shared prefix, for all rows of the batch that
+// read a KV head: rows b * R + i * group + g of the head, in tiles.  A partial
+// is a slot of tile rows of tc_part_stride(D) floats: the normalised output,
+// then the log2-sum-exp at index D.
+struct PrefixPlan {
+  int tile;        // rows of a tile
+  int tiles;       // tiles of a KV head
+  int key_tiles;   // key tiles of the prefix
+  int ctas;        // CTAs that share all (head, tile, key tile) items evenly, in this order; a
+                   // unit (head, tile) u has its partials in slots u + c of the CTAs c that ran
+                   // some of it.  0: every unit has `splits` ranges of keys, in slots
+                   // u * splits + s
+  int splits;
+};
+// The CTA of plan p that runs item x.
+__host__ __device__ __forceinline__ int prefix_cta(const PrefixPlan& p, int64_t items, int64_t x) {
+  return (int)(((x + 1) * p.ctas - 1) / items);
+}
+
+// What the merge needs of the attention over a request's own keys.
+struct OwnPart {
+  const float* part;  // row r of split s of (request, head) pair: part[((pair * splits + s) * R + r) * stride]
+  int splits, stride, split_keys;
+  const int32_t* ctx;     // of the views
+  const int32_t* ok;      // [B] nonzero: the request has passed its checks
+};
+
 size_t attn_simt_smem_bytes(int R, int D);
+size_t prefix_part_floats(const spec_dims& d);
+cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, PrefixPlan* plan,
+                          int* launches);
+cudaError_t prefix_merge_launch(const AttnArgs& a, const WsLayout& lay, const PrefixPlan& plan,
+                                const OwnPart& own, cudaStream_t st, int* launches);
 size_t attn_tc_part_floats(const spec_dims& d);
 cudaError_t kv_append_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, int* launches);
 cudaError_t attn_launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, int* launches);

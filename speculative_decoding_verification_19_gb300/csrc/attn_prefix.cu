@@ -1,0 +1,371 @@
+// Attention of a whole batch over a prefix that its requests share.
+//
+// softmax(q K^T) V over the keys of the prefix and over a request's own keys
+// are two partial sums of one softmax: with their log2-sum-exps l_1, l_2 the
+// output is (2^l_1 o_1 + 2^l_2 o_2) / (2^l_1 + 2^l_2).  The prefix' keys are
+// the same for every request, so all B * group * M rows that read a KV head are
+// one product with them (page 2 §3.3: the cached prefix is reused, here by the
+// whole batch): its keys and values are read once, not once a request.  A
+// request's own keys go through the verify attention (attn.cu, attn_tc.cu).
+//
+// Kernels in this file:
+//   prefix_simt_kernel   the prefix on CUDA cores (fp32, heads of 64)
+//   prefix_merge_kernel  the partials of a row, a warp per row
+#include <math.h>
+
+#include "attn.cuh"
+#include "common.cuh"
+
+namespace specv {
+
+// ---------------------------------------------------------------------------
+// the prefix on CUDA cores
+// ---------------------------------------------------------------------------
+// A CTA runs 64 rows of a KV head over a range of key tiles.  Both products
+// are register tiles of 8 rows per thread: scores 8 x kKeys / 16, outputs
+// 8 x D / 16, with the operands that the rows index (queries, probabilities)
+// transposed in shared memory, so that a thread's 8 rows are two 16-byte loads
+// that 16 lanes share.  fp32 throughout, two rows a packed FMA.
+constexpr int kPfxRows = 64, kPfxThreads = 128;
+constexpr int kPfxSlots = 4 * 152;  // ranges of all units together, at least the units
+
+template <int D>
+struct PfxTile {
+  // 64 keys with heads of 64 (69 KB: three CTAs an SM), 32 with heads of 128
+  // (80 KB: two)
+  static constexpr int kKeys = D == 64 ? 64 : 32;
+  static constexpr int kLd = kPfxRows + 4;   // padded rows of the transposed tiles
+  static constexpr int kLdK = kKeys + 4;
+  static constexpr size_t smem = sizeof(float) * ((size_t)D * kLd + D * kLdK + kKeys * D + kKeys * kLd);
+};
+
+__device__ __forceinline__ unsigned long long pair_of(float a, float b) {
+  return (unsigned long long)__float_as_uint(a) | ((unsigned long long)__float_as_uint(b) << 32);
+}
+__device__ __forceinline__ float lo_of(unsigned long long x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_of(unsigned long long x) {
+  return __uint_as_float((uint32_t)(x >> 32));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
+                                                   unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPfxThreads) prefix_simt_kernel(
+    const T* q, const T* k_cache, const T* v_cache, const int32_t* table, int prefix_len,
+    spec_dims d, float qscale, PrefixPlan plan, float* __restrict__ part) {
+  using Tile = PfxTile<D>;
+  constexpr int kKeys = Tile::kKeys, kLd = Tile::kLd, kLdK = Tile::kLdK;
+  constexpr int KPT = kKeys / 16;  // keys of a thread
+  constexpr int CPT = D / 16;      // output columns of a thread
+  constexpr int kVec = 16 / sizeof(T), kVecRow = D / kVec;
+  extern __shared__ __align__(16) float smem[];
+  float* qt = smem;             // [D][kLd]   queries, scaled
+  float* kt = qt + D * kLd;     // [D][kLdK]  keys
+  float* vs = kt + D * kLdK;    // [kKeys][D] values, key j * 16 + x at 4-key group x (kSlot)
+  float* pt = vs + kKeys * D;   // [kKeys][kLd] probabilities, the same order of keys
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int s = blockIdx.x % plan.splits, tile = blockIdx.x / plan.splits, h = blockIdx.y;
+  const int group = d.Hq / d.Hkv, R = group * d.M;
+  const int rows = d.B * R;
+  pdl_trigger();
+  pdl_wait();  // the queries and the cache may come from the previous kernels
+
+  for (int e = tid; e < kPfxRows * kVecRow; e += kPfxThreads) {
+    const int r = e % kPfxRows, vi = e / kPfxRows;
+    const int gr = tile * kPfxRows + r;
+    float f[kVec];
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) f[c] = 0.f;
+    if (gr < rows) {
+      const int b = gr / R, rr = gr - b * R, i = rr / group;
+      const int64_t at = (((int64_t)b * d.M + i) * d.Hq + h * group + rr - i * group) * D;
+      unpack16(reinterpret_cast<const uint4*>(q + at)[vi], f);
+    }
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) qt[(vi * kVec + c) * kLd + r] = f[c] * qscale;
+  }
+
+  unsigned long long o[4][CPT];  // row pairs x columns
+  float m[8], l[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) o[r][c] = 0ull;
+
+  const int j0 = (int)((int64_t)s * plan.key_tiles / plan.splits);
+  const int j1 = (int)((int64_t)(s + 1) * plan.key_tiles / plan.splits);
+  for (int j = j0; j < j1; ++j) {
+    __syncthreads();  // the last tile is consumed
+    for (int e = tid; e < kKeys * kVecRow; e += kPfxThreads) {
+      // two neighbouring vectors of 16 keys a warp: whole sectors from global
+      // memory, no bank conflicts in the transposed stores
+      const int vi = (e & 1) | ((e / (2 * kKeys)) << 1), kk = (e >> 1) % kKeys;
+      const int t = j * kKeys + kk;
+      float kf[kVec], vf[kVec];
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) kf[c] = vf[c] = 0.f;
+      if (t < prefix_len) {
+        const int id = __ldcg(table + t / kBlock);
+        // no block id: the request check fails every request
+        const int64_t blk = (uint32_t)id < (uint32_t)d.num_blocks ? id : 0;
+        const int64_t base = ((blk * d.Hkv + h) * kBlock + t % kBlock) * D;
+        unpack16(reinterpret_cast<const uint4*>(k_cache + base)[vi], kf);
+        unpack16(reinterpret_cast<const uint4*>(v_cache + base)[vi], vf);
+      }
+      const int slot = (kk % KPT) * 16 + kk / KPT;  // key kk is number kk % KPT of thread kk / KPT
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) kt[(vi * kVec + c) * kLdK + kk] = kf[c];
+#pragma unroll
+      for (int c = 0; c < kVec; c += 4)
+        *reinterpret_cast<float4*>(vs + slot * D + vi * kVec + c) =
+            make_float4(vf[c], vf[c + 1], vf[c + 2], vf[c + 3]);
+    }
+    __syncthreads();
+
+    unsigned long long sc[4][KPT];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) sc[r][k] = 0ull;
+#pragma unroll 4
+    for (int dd = 0; dd < D; ++dd) {
+      const ulonglong2 qa = *reinterpret_cast<const ulonglong2*>(qt + dd * kLd + ty * 8);
+      const ulonglong2 qb = *reinterpret_cast<const ulonglong2*>(qt + dd * kLd + ty * 8 + 4);
+      const unsigned long long qv[4] = {qa.x, qa.y, qb.x, qb.y};
+      float kv[KPT];
+      if constexpr (KPT == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(kt + dd * kLdK + tx * 4);
+        kv[0] = x.x; kv[1] = x.y; kv[2] = x.z; kv[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(kt + dd * kLdK + tx * 2);
+        kv[0] = x.x; kv[1] = x.y;
+      }
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) {
+        const unsigned long long kk = pair_of(kv[k], kv[k]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sc[r][k] = fma2(qv[r], kk, sc[r][k]);
+      }
+    }
+    // softmax: the 16 threads of a row group share its rows
+    const int left = prefix_len - j * kKeys - tx * KPT;  // this thread's keys below it are real
+    float p[8][KPT];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      float mt = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) {
+        const float x = (r & 1) ? hi_of(sc[r / 2][k]) : lo_of(sc[r / 2][k]);
+        p[r][k] = k < left ? x : -INFINITY;
+        mt = fmaxf(mt, p[r][k]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));
+      const float mn = fmaxf(m[r], mt);  // finite: a tile has at least one key
+      const float corr = fast_exp2(m[r] - mn);
+      m[r] = mn;
+      l[r] *= corr;
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) {
+        p[r][k] = fast_exp2(p[r][k] - mn);
+        l[r] += p[r][k];  // this thread's keys; the 16 are summed at the end
+      }
+      // rescale the row's outputs
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        const float a = lo_of(o[r / 2][c]), b2 = hi_of(o[r / 2][c]);
+        o[r / 2][c] = (r & 1) ? pair_of(a, b2 * corr) : pair_of(a * corr, b2);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+      float* row = pt + (k * 16 + tx) * kLd + ty * 8;
+      *reinterpret_cast<float4*>(row) = make_float4(p[0][k], p[1][k], p[2][k], p[3][k]);
+      *reinterpret_cast<float4*>(row + 4) = make_float4(p[4][k], p[5][k], p[6][k], p[7][k]);
+    }
+    __syncwarp();  // a row group's probabilities stay inside its warp
+#pragma unroll 4
+    for (int k = 0; k < kKeys; ++k) {
+      const ulonglong2 pa = *reinterpret_cast<const ulonglong2*>(pt + k * kLd + ty * 8);
+      const ulonglong2 pb = *reinterpret_cast<const ulonglong2*>(pt + k * kLd + ty * 8 + 4);
+      const unsigned long long pv[4] = {pa.x, pa.y, pb.x, pb.y};
+#pragma unroll
+      for (int c4 = 0; c4 < CPT / 4; ++c4) {
+        const float4 v4 = *reinterpret_cast<const float4*>(vs + k * D + c4 * 64 + tx * 4);
+        const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const unsigned long long v2 = pair_of(vv[c], vv[c]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[r][c4 * 4 + c] = fma2(pv[r], v2, o[r][c4 * 4 + c]);
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  const int S = tc_part_stride(D);
+  const int64_t unit = (int64_t)h * plan.tiles + tile;
+  float* pbase = part + (unit * plan.splits + s) * plan.tile * (int64_t)S;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    float sum = l[r];
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+    const int row = ty * 8 + r;
+    if (row >= plan.tile || tile * kPfxRows + row >= rows) continue;
+    const float inv = 1.f / sum;
+    float* prow = pbase + (int64_t)row * S;
+#pragma unroll
+    for (int c4 = 0; c4 < CPT / 4; ++c4) {
+      float f[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        f[c] = ((r & 1) ? hi_of(o[r / 2][c4 * 4 + c]) : lo_of(o[r / 2][c4 * 4 + c])) * inv;
+      *reinterpret_cast<float4*>(prow + c4 * 64 + tx * 4) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+    if (tx == 0) prow[D] = m[r] + log2f(sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// merge
+// ---------------------------------------------------------------------------
+// A warp per row: the log2-sum-exps of its partials first, then their outputs
+// with the weights that these give.
+template <typename T>
+__global__ void __launch_bounds__(256) prefix_merge_kernel(
+    OwnPart own, const float* prefix, PrefixPlan plan, int64_t items, spec_dims d,
+    T* __restrict__ out, float* __restrict__ lse) {
+  pdl_trigger();
+  pdl_wait();  // the partials come from the previous kernels
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int h = blockIdx.y, D = d.D;
+  const int group = d.Hq / d.Hkv, R = group * d.M;
+  const int64_t gr = (int64_t)blockIdx.x * (blockDim.x / kWarp) + warp;
+  if (gr >= (int64_t)d.B * R) return;
+  const int b = (int)(gr / R), r = (int)(gr - (int64_t)b * R), i = r / group;
+  const int64_t at = ((int64_t)b * d.M + i) * d.Hq + h * group + r - i * group;
+  T* orow = out + at * D;
+  if (!__ldcg(own.ok + b)) {  // the request has failed its checks
+    for (int c = lane; c < D; c += kWarp) orow[c] = from_f32<T>(0.f);
+    if (lse != nullptr && lane == 0) lse[at] = -INFINITY;
+    return;
+  }
+  const int n_own = own.splits == 1 ? 1 : ceil_div(__ldcg(own.ctx + b) + d.M, own.split_keys);
+  const int64_t own_step = (int64_t)R * own.stride;
+  const float* own_row = own.part + (((int64_t)b * d.Hkv + h) * own.splits * R + r) * own.stride;
+  const int tile = (int)(gr / plan.tile);
+  const int64_t unit = (int64_t)h * plan.tiles + tile;
+  const int S = tc_part_stride(D);
+  int64_t slot;
+  int n_pfx;
+  if (plan.ctas > 0) {
+    const int c0 = prefix_cta(plan, items, unit * plan.key_tiles);
+    const int c1 = prefix_cta(plan, items, (unit + 1) * plan.key_tiles - 1);
+    slot = unit + c0;
+    n_pfx = c1 - c0 + 1;
+  } else {
+    slot = unit * plan.splits;
+    n_pfx = plan.splits;
+  }
+  const int64_t pfx_step = (int64_t)plan.tile * S;
+  const float* pfx_row = prefix + slot * pfx_step + (gr - (int64_t)tile * plan.tile) * S;
+  const int n = n_own + n_pfx;
+  auto row_of = [&](int s) { return s < n_own ? own_row + s * own_step : pfx_row + (s - n_own) * pfx_step; };
+  float mx = -INFINITY;
+  for (int s = lane; s < n; s += kWarp) mx = fmaxf(mx, __ldcg(row_of(s) + D));
+  mx = warp_max(mx);
+  float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float* p = row_of(s);
+    const float w = exp2f(__ldcg(p + D) - mx);
+    sum += w;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c * kWarp < D) acc[c] = fmaf(w, __ldcg(p + lane + c * kWarp), acc[c]);
+  }
+  const float inv = 1.f / sum;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (c * kWarp < D) orow[lane + c * kWarp] = from_f32<T>(acc[c] * inv);
+  if (lse != nullptr && lane == 0) lse[at] = (mx + log2f(sum)) * 0.69314718055994530942f;
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+static PrefixPlan simt_plan(const spec_dims& d, int prefix_len) {
+  PrefixPlan p;
+  const int64_t rows = (int64_t)d.B * (d.Hq / d.Hkv) * d.M;
+  const int keys = d.D == 64 ? PfxTile<64>::kKeys : PfxTile<128>::kKeys;
+  p.tile = (int)(rows < kPfxRows ? rows : kPfxRows);
+  p.tiles = (int)ceil_div64(rows, kPfxRows);
+  p.key_tiles = ceil_div(prefix_len, keys);
+  p.ctas = 0;
+  const int64_t units = (int64_t)d.Hkv * p.tiles;
+  int64_t splits = kPfxSlots / units;
+  if (splits > p.key_tiles) splits = p.key_tiles;
+  p.splits = splits < 1 ? 1 : (int)splits;
+  return p;
+}
+
+size_t prefix_part_floats(const spec_dims& d) {
+  const int64_t rows = (int64_t)d.B * (d.Hq / d.Hkv) * d.M;
+  const int64_t units = (int64_t)d.Hkv * ceil_div64(rows, kPfxRows);
+  const int64_t slots = units > kPfxSlots ? units : kPfxSlots;
+  return (size_t)slots * (size_t)(rows < kPfxRows ? rows : kPfxRows) * tc_part_stride(d.D);
+}
+
+template <typename T>
+static cudaError_t launch_simt(const AttnArgs& a, const PrefixPlan& p, float* part, cudaStream_t st) {
+  auto kern = a.d.D == 64 ? prefix_simt_kernel<T, 64> : prefix_simt_kernel<T, 128>;
+  const size_t smem = a.d.D == 64 ? PfxTile<64>::smem : PfxTile<128>::smem;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  PdlLaunch L(dim3(p.splits * p.tiles, a.d.Hkv), dim3(kPfxThreads), smem, st);
+  return cudaLaunchKernelEx(&L.cfg, kern, static_cast<const T*>(a.q),
+                            static_cast<const T*>(a.k_cache), static_cast<const T*>(a.v_cache),
+                            a.view.prefix_table, a.view.prefix_len, a.d,
+                            a.scale * 1.4426950408889634f, p, part);
+}
+
+cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, PrefixPlan* plan,
+                          int* launches) {
+  float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + lay.pfx_part_off);
+  *plan = simt_plan(a.d, a.view.prefix_len);
+  const cudaError_t e = a.d.kv_dtype == SPEC_BF16 ? launch_simt<__nv_bfloat16>(a, *plan, part, st)
+                                                  : launch_simt<float>(a, *plan, part, st);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+cudaError_t prefix_merge_launch(const AttnArgs& a, const WsLayout& lay, const PrefixPlan& plan,
+                                const OwnPart& own, cudaStream_t st, int* launches) {
+  const spec_dims& d = a.d;
+  const float* part = reinterpret_cast<const float*>(static_cast<char*>(a.ws) + lay.pfx_part_off);
+  const int64_t rows = (int64_t)d.B * (d.Hq / d.Hkv) * d.M;
+  const int64_t items = (int64_t)d.Hkv * plan.tiles * plan.key_tiles;
+  PdlLaunch L(dim3((unsigned)ceil_div64(rows, 8), d.Hkv), dim3(256), 0, st);
+  cudaError_t e;
+  if (d.kv_dtype == SPEC_BF16)
+    e = cudaLaunchKernelEx(&L.cfg, prefix_merge_kernel<__nv_bfloat16>, own, part, plan, items, d,
+                           static_cast<__nv_bfloat16*>(a.out), a.lse);
+  else
+    e = cudaLaunchKernelEx(&L.cfg, prefix_merge_kernel<float>, own, part, plan, items, d,
+                           static_cast<float*>(a.out), a.lse);
+  if (e == cudaSuccess) ++*launches;
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace specv

@@ -131,6 +131,7 @@ constexpr int kSegCost = 3;
 // 152 CTAs (17 partials to merge a pair), 22 with 4, 21 with 8, 23 with 12, 29
 // with 24 (no pair split); window 4096: 40, 30, 28 and 33 with 4, 8, 12, 24.
 constexpr int kWinMinCost = 8;
+constexpr int kPlain = 0, kWindow = 1, kViewed = 2;  // what the kernels' kMode instances run on
 constexpr int kPrepThreads = 256;
 constexpr int kPlanReqs = 1024;  // requests whose plan arrays fit the prep kernel's shared memory
 
@@ -299,16 +300,20 @@ __device__ __forceinline__ void store32_bf16(__nv_bfloat16* dst, const uint32_t 
 // kWide: more than 64 new rows per request (128-bit ancestor masks); the
 // narrow kernel keeps one 64-bit word per row.  kShort: the wait limit is
 // short (ptx::mbar_wait_t).
-// kWin: a sliding window and sinks (masks and depths of the new rows come from
-// the prep kernel for chains too).
-template <bool kWide, bool kShort, bool kWin>
+// kMode: kWindow, a sliding window and sinks (masks and depths of the new rows
+// come from the prep kernel for chains too); kViewed, the attention runs on the
+// requests' views (AttnView: ctx and the tables are the views', rq[b].w is the
+// request's own ctx) and, for a shared prefix, leaves every row's normalised
+// fp32 output and log2-sum-exp in own_part for the merge instead of out and lse.
+template <bool kWide, bool kShort, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __nv_bfloat16* k_new,
     const __nv_bfloat16* v_new, __nv_bfloat16* k_cache, __nv_bfloat16* v_cache,
     const int32_t* block_table, const int4* rq, const int4* starts, const ulonglong2* anc_ws,
-    const int* depth_ws, int window, int sinks, int* pairs, spec_dims d, float qscale2,
-    float* part, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-    uint32_t* __restrict__ status) {
+    const int* depth_ws, int window, int sinks, AttnView view, int* pairs, spec_dims d,
+    float qscale2, float* part, float* own_part, __nv_bfloat16* __restrict__ out,
+    float* __restrict__ lse, uint32_t* __restrict__ status) {
+  constexpr bool kWin = kMode == kWindow, kView = kMode == kViewed;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -398,8 +403,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
       const int h = (rem / 16) % Hkv;
       const int ch = rem % 16;
       const int4 r = __ldcg(rq + b);  // (ctx, tiles, ...): no tiles means the request failed its checks
-      const int64_t tpos = (int64_t)r.x + pi;
-      if (r.y == 0 || tpos >= ceil_div64((int64_t)r.x + M, kBlock) * kBlock) continue;
+      const int ctx = kView ? r.w : r.x;
+      const int64_t tpos = (int64_t)ctx + pi;
+      if (r.y == 0 || tpos >= ceil_div64((int64_t)ctx + M, kBlock) * kBlock) continue;
       const int64_t dst = (((int64_t)block_table[(int64_t)b * d.max_blocks + tpos / kBlock] * Hkv + h) *
                                kBlock + tpos % kBlock) * 128 + ch * 8;
       uint4 kv = make_uint4(0, 0, 0, 0), vv = make_uint4(0, 0, 0, 0);
@@ -446,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     cu.start(st0, st1, rq, B, sinks);
     int seg = -1, L = 0;
     int wb = -1, ww = -1, nb = -1, nw = -1;  // window held in ids and window loaded into nids
+    int wh = -1, nh = -1;                    // their heads (kView: tables of heads differ)
+    const int entries = kView ? view.entries : d.max_blocks;
     int ids[kPages] = {0, 0, 0, 0}, nids[kPages] = {0, 0, 0, 0};
     int64_t t = 0;
     int q_issued = 0;  // Q loads issued (warp 10, lane 0)
@@ -474,37 +482,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
         }
       }
       const int w = cu.tile >> 5;
-      if (cu.b != wb || w != ww) {  // next window of 32 tiles
-        if (cu.b == nb && w == nw) {
+      if (cu.b != wb || w != ww || (kView && cu.h != wh)) {  // next window of 32 tiles
+        if (cu.b == nb && w == nw && (!kView || cu.h == nh)) {
 #pragma unroll
           for (int p = 0; p < kPages; ++p) ids[p] = nids[p];
         } else {
           const int page0 = cu.page_of((w << 5) + lane);
-          const int32_t* bt = block_table + (int64_t)cu.b * d.max_blocks;
+          const int32_t* bt = kView ? view.table + cu.b * view.stride_b + cu.h * view.stride_h
+                                    : block_table + (int64_t)cu.b * d.max_blocks;
 #pragma unroll
-          for (int p = 0; p < kPages; ++p) ids[p] = (page0 + p < d.max_blocks) ? bt[page0 + p] : 0;
+          for (int p = 0; p < kPages; ++p) ids[p] = (page0 + p < entries) ? bt[page0 + p] : 0;
         }
         wb = cu.b;
         ww = w;
+        wh = cu.h;
         // the next window with other ids: the pair's next window, else the
         // first of the next head (same ids when the pair has one window:
         // then the next request's first)
         if ((w + 1) * 32 < cu.nt) {
           nb = cu.b;
           nw = w + 1;
+          nh = cu.h;
         } else {
-          nb = (cu.h + 1 < Hkv && w > 0) ? cu.b : cu.next_b;
+          const bool same = cu.h + 1 < Hkv && (kView || w > 0);
+          nb = same ? cu.b : cu.next_b;
           nw = 0;
+          nh = same ? cu.h + 1 : 0;
         }
-        if (nb == wb && nw == ww) {
+        if (!kView && nb == wb && nw == ww) {
 #pragma unroll
           for (int p = 0; p < kPages; ++p) nids[p] = ids[p];
         } else if (nb < B) {
           const int nj = (nw << 5) + lane;
           const int page0 = nb == cu.b ? cu.page_of(nj) : cu.next_page_of(nj);
-          const int32_t* bt = block_table + (int64_t)nb * d.max_blocks;
+          const int32_t* bt = kView ? view.table + nb * view.stride_b + nh * view.stride_h
+                                    : block_table + (int64_t)nb * d.max_blocks;
 #pragma unroll
-          for (int p = 0; p < kPages; ++p) nids[p] = (page0 + p < d.max_blocks) ? bt[page0 + p] : 0;
+          for (int p = 0; p < kPages; ++p) nids[p] = (page0 + p < entries) ? bt[page0 + p] : 0;
         }
       }
       const int pg = cu.page();
@@ -1028,9 +1042,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
                   o[4 * j + 3] = __float_as_uint(fmaf(w, v[j].w, a * __uint_as_float(o[4 * j + 3])));
                 }
               }
-              if (real) store32_bf16(orow + cc2 * 32, o, ls > 0.f ? 1.f / ls : 0.f);
+              const float inv = ls > 0.f ? 1.f / ls : 0.f;
+              if (kView && own_part != nullptr) {
+                if (real) {
+                  float* prow = own_part + (pair * R + row) * (int64_t)S + half * 64 + cc2 * 32;
+#pragma unroll
+                  for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4*>(prow + j) = make_float4(
+                        __uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
+                        __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                }
+              } else if (real) {
+                store32_bf16(orow + cc2 * 32, o, inv);
+              }
             }
-            if (real && half == 0 && lrow != nullptr)
+            if (kView && own_part != nullptr) {
+              if (real && half == 0)
+                own_part[(pair * R + row) * (int64_t)S + d.D] = ls > 0.f ? mx + log2f(ls) : -INFINITY;
+            } else if (real && half == 0 && lrow != nullptr)
               *lrow = ls > 0.f ? (mx + log2f(ls)) * 0.69314718055994530942f : -INFINITY;
           }
           ptx::tc_fence_before();
@@ -1105,15 +1134,16 @@ __device__ __forceinline__ void block_scan(int64_t& a, int64_t& c, int& m, int64
 // plans the split of the tiles.  With a window (kWin) only the pages of the
 // sinks and of the window are checked, only their tiles are counted, and
 // every new row gets its depth and the mask of the ancestors it sees.
-template <bool kWin>
+template <int kMode>
 __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     const int32_t* block_table, const int32_t* ctx_lens,
-    const int32_t* parent, spec_dims d, int window, int sinks, int G,
+    const int32_t* parent, spec_dims d, int window, int sinks, AttnView view, int G,
     int32_t* __restrict__ depth_ws, int32_t* __restrict__ ntiles,
     int64_t* __restrict__ pre, int4* __restrict__ rq, int4* __restrict__ starts,
     int* __restrict__ pairs, ulonglong2* __restrict__ anc_ws,
     uint32_t* __restrict__ arrivals, __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
     uint32_t* __restrict__ status) {
+  constexpr bool kWin = kMode == kWindow, kView = kMode == kViewed;
   __shared__ int s_last;
   __shared__ int64_t s_a[kPrepThreads / kWarp], s_c[kPrepThreads / kWarp];
   __shared__ int s_m[kPrepThreads / kWarp];
@@ -1135,15 +1165,20 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
 #pragma unroll
   for (int k = 0; k < kPrepPages; ++k) {
     const int p = tid + k * kPrepThreads;
-    ids[k] = !kWin && p < d.max_blocks ? __ldcg(bt + p) : 0;
+    ids[k] = kMode == kPlain && p < d.max_blocks ? __ldcg(bt + p) : 0;
   }
   const int ctx = __ldcg(ctx_lens + b);
   const int64_t L = (int64_t)ctx + M;
   const int64_t cap = (int64_t)d.max_blocks * kBlock;
 
   const bool cap_ok = ctx >= 0 && L <= cap;
-  int bad_block = 0;
-  if (cap_ok) {
+  int bad_block = 0, bad_view = 0;
+  if (kView && cap_ok) {
+    const int bad = view_check(view, d, bt, b, ctx, true);
+    bad_view = bad & 1;
+    bad_block = bad & 2;
+  }
+  if (!kView && cap_ok) {
     const int pages = (int)ceil_div64(L, kBlock);
     if (kWin) {
       const int sp = min(ceil_div(sinks, kBlock), pages);
@@ -1175,7 +1210,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     }
   }
   bad_block = __syncthreads_or(bad_block);
-  bad_topo = __syncthreads_or(bad_topo);
+  bad_topo = __syncthreads_or(bad_topo | bad_view);
   const bool ok = cap_ok && !bad_block && !bad_topo;
   // tile counts of the request's (request, head) pairs start at zero
   for (int h = tid; h < Hkv; h += blockDim.x) pairs[(int64_t)b * Hkv + h] = 0;
@@ -1202,7 +1237,8 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     if (!cap_ok) raise_status(status, SPEC_ERR_CAPACITY);
     if (bad_block) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
     if (bad_topo) raise_status(status, SPEC_ERR_INVALID_ARG);
-    ntiles[b] = ok ? (int)ceil_div64(ceil_div64(L, kBlock) -
+    const int64_t keys = kView && ok ? (int64_t)view_ctx(view, b, ctx) + M : L;
+    ntiles[b] = ok ? (int)ceil_div64(ceil_div64(keys, kBlock) -
                                          (kWin ? win_skip_pages(ctx, window, sinks) : 0),
                                      kPages)
                    : 0;
@@ -1238,7 +1274,8 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
   for (int base = 0; base < B; base += blockDim.x) {
     const int r = base + tid;
     const int nt = r < B ? __ldcg(ntiles + r) : 0;
-    const int cx = r < B ? ctx_lens[r] : 0;
+    const int own = r < B ? ctx_lens[r] : 0;
+    const int cx = kView && nt > 0 ? view_ctx(view, r, own) : own;
     int64_t vt = (int64_t)nt * Hkv, vc = nt > 0 ? (int64_t)Hkv * (nt + kSegCost) : 0;
     int vm = nt > 0 ? r : -1;
     int64_t tt, tcst;
@@ -1248,7 +1285,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     if (r < B) {
       tpre[r] = carry_t + vt;
       cpre[r] = carry_c + vc;
-      rq[r] = make_int4(cx, nt, B, kWin ? win_skip_pages(cx, window, sinks) : 0);
+      rq[r] = make_int4(cx, nt, B, kWin ? win_skip_pages(cx, window, sinks) : own);
       if (small) {
         s_nt[r] = nt;
         s_ctx[r] = cx;
@@ -1266,10 +1303,10 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     __syncthreads();
   }
   const int64_t T = carry_t, Ctot = carry_c;
-  // With a window a small batch has few tiles: each CTA then takes at least
+  // With a window or a view a small batch has few tiles: each CTA then takes at least
   // kWinMinCost of the cost, because every further CTA of a pair is a partial
   // that the pair's first CTA reads in turn.
-  const int Ge = kWin ? (int)max((int64_t)1, min((int64_t)G, Ctot / kWinMinCost)) : G;
+  const int Ge = kMode != kPlain ? (int)max((int64_t)1, min((int64_t)G, Ctot / kWinMinCost)) : G;
   if (tid == 0) {
     tpre[B] = T;
     cpre[B] = Ctot;
@@ -1395,21 +1432,31 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
   if (e != cudaSuccess) return e;
   const int G = sms < kMaxAttnCtas ? sms : kMaxAttnCtas;
 
+  const bool viewed = a.view.mode != kViewNone, behind = a.view.mode == kViewPrefix;
+  float* own_part = reinterpret_cast<float*>(ws + lay.own_part_off);
+  PrefixPlan plan = {};
   {
     PdlLaunch L(dim3(d.B), dim3(kPrepThreads), 0, st);
-    e = cudaLaunchKernelEx(&L.cfg, a.window > 0 ? attn_prep_kernel<true> : attn_prep_kernel<false>,
-                           a.block_table, a.ctx_lens, a.parent, d, a.window, a.sinks, G, depth, ntiles, pre, rq, starts, pairs, anc, arrivals,
+    e = cudaLaunchKernelEx(&L.cfg,
+                           viewed         ? attn_prep_kernel<kViewed>
+                           : a.window > 0 ? attn_prep_kernel<kWindow>
+                                          : attn_prep_kernel<kPlain>,
+                           a.block_table, a.ctx_lens, a.parent, d, a.window, a.sinks, a.view, G,
+                           depth, ntiles, pre, rq, starts, pairs, anc, arrivals,
                            static_cast<__nv_bfloat16*>(a.out), a.lse, status);
     if (e != cudaSuccess) return e;
   }
   ++*launches;
+  if (behind) {
+    e = prefix_launch(a, lay, st, &plan, launches);
+    if (e != cudaSuccess) return e;
+  }
   const bool wide = d.M > 64, short_wait = wait_limit_cycles(d) < ptx::kShortWait;
-  auto kern = wide ? (short_wait ? attn_tc_kernel<true, true, false> : attn_tc_kernel<true, false, false>)
-                   : (short_wait ? attn_tc_kernel<false, true, false>
-                                 : attn_tc_kernel<false, false, false>);
-  if (a.window > 0)
-    kern = wide ? (short_wait ? attn_tc_kernel<true, true, true> : attn_tc_kernel<true, false, true>)
-                : (short_wait ? attn_tc_kernel<false, true, true> : attn_tc_kernel<false, false, true>);
+#define SPECV_TC(mode)                                                                          \
+  (wide ? (short_wait ? attn_tc_kernel<true, true, mode> : attn_tc_kernel<true, false, mode>)    \
+        : (short_wait ? attn_tc_kernel<false, true, mode> : attn_tc_kernel<false, false, mode>))
+  auto kern = viewed ? SPECV_TC(kViewed) : a.window > 0 ? SPECV_TC(kWindow) : SPECV_TC(kPlain);
+#undef SPECV_TC
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   const float qscale2 = a.scale * 1.4426950408889634f;
@@ -1422,10 +1469,16 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
                            static_cast<__nv_bfloat16*>(a.v_cache), a.block_table,
                            (const int4*)rq, (const int4*)starts,
                            a.parent != nullptr || a.window > 0 ? (const ulonglong2*)anc : nullptr,
-                           (const int*)depth, a.window, a.sinks, pairs, d, qscale2, part, static_cast<__nv_bfloat16*>(a.out), a.lse, status);
+                           (const int*)depth, a.window, a.sinks, a.view, pairs, d, qscale2, part,
+                           behind ? own_part : nullptr, static_cast<__nv_bfloat16*>(a.out), a.lse,
+                           status);
     if (e != cudaSuccess) return e;
   }
   ++*launches;
+  if (behind) {
+    const OwnPart own = {own_part, 1, tc_part_stride(d.D), INT32_MAX, a.view.ctx, ntiles};
+    return prefix_merge_launch(a, lay, plan, own, st, launches);
+  }
   return cudaGetLastError();
 }
 

@@ -155,32 +155,146 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F body) {
   return nullptr;
 }
 
+// The tensors that the forms of the verify attention share.
+struct AttnTensors {
+  int dev;
+  spec_dims d;
+  void *q, *kn, *vn, *kc, *vc, *bt, *ctx, *par, *out, *lse, *ws;
+  size_t bytes;
+};
 // q, k_new, v_new, k_cache, v_cache, block_table, ctx_lens, parent, out, lse,
-// dims, ws, window, sinks, stream
+// dims, ws
+AttnTensors attn_tensors(PyObject* const* a) {
+  AttnTensors t;
+  t.dev = device_of(a[0], "q");
+  t.d = dims_of(a[10]);
+  const spec_dims& d = t.d;
+  const auto kv = kv_type(d);
+  const int64_t B = d.B, M = d.M, Hq = d.Hq, Hkv = d.Hkv, D = d.D;
+  const Shape cache = {d.num_blocks, Hkv, d.block, D};
+  t.q = dense(a[0], "q", kv, t.dev, {B, M, Hq, D});
+  t.kn = dense(a[1], "k_new", kv, t.dev, {B, M, Hkv, D});
+  t.vn = dense(a[2], "v_new", kv, t.dev, {B, M, Hkv, D});
+  t.kc = dense(a[3], "k_cache", kv, t.dev, cache);
+  t.vc = dense(a[4], "v_cache", kv, t.dev, cache);
+  t.bt = dense(a[5], "block_table", at::kInt, t.dev, {B, d.max_blocks});
+  t.ctx = dense(a[6], "ctx_lens", at::kInt, t.dev, {B});
+  t.par = dense_or_none(a[7], "parent", at::kInt, t.dev, {B, M});
+  t.out = dense(a[8], "out", kv, t.dev, {B, M, Hq, D});
+  t.lse = dense_or_none(a[9], "lse", at::kFloat, t.dev, {B, M, Hq});
+  t.ws = workspace(a[11], t.dev, &t.bytes);
+  return t;
+}
+
+// the tensors of the verify attention, window, sinks, stream
 PyObject* verify_attn_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 15, [&] {
-    const int dev = device_of(a[0], "q");
-    const spec_dims d = dims_of(a[10]);
-    const auto kv = kv_type(d);
-    const int64_t B = d.B, M = d.M, Hq = d.Hq, Hkv = d.Hkv, D = d.D;
-    const Shape cache = {d.num_blocks, Hkv, d.block, D};
-    void* q = dense(a[0], "q", kv, dev, {B, M, Hq, D});
-    void* kn = dense(a[1], "k_new", kv, dev, {B, M, Hkv, D});
-    void* vn = dense(a[2], "v_new", kv, dev, {B, M, Hkv, D});
-    void* kc = dense(a[3], "k_cache", kv, dev, cache);
-    void* vc = dense(a[4], "v_cache", kv, dev, cache);
-    void* bt = dense(a[5], "block_table", at::kInt, dev, {B, d.max_blocks});
-    void* ctx = dense(a[6], "ctx_lens", at::kInt, dev, {B});
-    void* par = dense_or_none(a[7], "parent", at::kInt, dev, {B, M});
-    void* out = dense(a[8], "out", kv, dev, {B, M, Hq, D});
-    void* lse = dense_or_none(a[9], "lse", at::kFloat, dev, {B, M, Hq});
-    size_t bytes;
-    void* ws = workspace(a[11], dev, &bytes);
+    const AttnTensors t = attn_tensors(a);
     const int32_t window = (int32_t)whole(a[12]), sinks = (int32_t)whole(a[13]);
-    return launch(dev, a[14], [&](void* st) {
-      return spec_verify_attn_window(q, kn, vn, kc, vc, as<int32_t>(bt), as<int32_t>(ctx),
-                                     as<int32_t>(par), window, sinks, out, as<float>(lse), &d, ws,
-                                     bytes, st);
+    return launch(t.dev, a[14], [&](void* st) {
+      return spec_verify_attn_window(t.q, t.kn, t.vn, t.kc, t.vc, as<int32_t>(t.bt),
+                                     as<int32_t>(t.ctx), as<int32_t>(t.par), window, sinks, t.out,
+                                     as<float>(t.lse), &t.d, t.ws, t.bytes, st);
+    });
+  });
+}
+
+// the tensors of the verify attention, prefix, stream
+PyObject* verify_attn_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 14, [&] {
+    const AttnTensors t = attn_tensors(a);
+    const int64_t pages = tensor(a[12], "prefix").numel();
+    void* prefix = dense(a[12], "prefix", at::kInt, t.dev, {pages});
+    if (pages > INT32_MAX / 16) throw Refused("prefix: too many pages");
+    return launch(t.dev, a[13], [&](void* st) {
+      return spec_verify_attn_prefix(t.q, t.kn, t.vn, t.kc, t.vc, as<int32_t>(t.bt),
+                                     as<int32_t>(t.ctx), as<int32_t>(t.par), as<int32_t>(prefix),
+                                     (int32_t)(16 * pages), t.out, as<float>(t.lse), &t.d, t.ws,
+                                     t.bytes, st);
+    });
+  });
+}
+
+// Pages per KV head of a selection [B, Hkv, n].
+int64_t selected(PyObject* o) {
+  const at::Tensor& t = tensor(o, "pages");
+  if (t.dim() != 3) throw Refused("pages: [B, Hkv, n] is wanted");
+  if (t.size(2) > INT32_MAX) throw Refused("pages: too many");
+  return t.size(2);
+}
+
+// the tensors of the verify attention, pages, page_counts, stream
+PyObject* verify_attn_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&] {
+    const AttnTensors t = attn_tensors(a);
+    const int64_t np = selected(a[12]);
+    void* pages = dense(a[12], "pages", at::kInt, t.dev, {t.d.B, t.d.Hkv, np});
+    void* counts = dense(a[13], "page_counts", at::kInt, t.dev, {t.d.B});
+    return launch(t.dev, a[14], [&](void* st) {
+      return spec_verify_attn_pages(t.q, t.kn, t.vn, t.kc, t.vc, as<int32_t>(t.bt),
+                                    as<int32_t>(t.ctx), as<int32_t>(t.par), as<int32_t>(pages),
+                                    as<int32_t>(counts), (int32_t)np, t.out, as<float>(t.lse), &t.d,
+                                    t.ws, t.bytes, st);
+    });
+  });
+}
+
+// k_cache, block_table, from_lens, ctx_lens, bounds, dims, ws, stream
+PyObject* page_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&] {
+    const int dev = device_of(a[0], "k_cache");
+    const spec_dims d = dims_of(a[5]);
+    const auto kv = kv_type(d);
+    void* kc = dense(a[0], "k_cache", kv, dev, {d.num_blocks, d.Hkv, d.block, d.D});
+    void* bt = dense(a[1], "block_table", at::kInt, dev, {d.B, d.max_blocks});
+    void* from = dense_or_none(a[2], "from_lens", at::kInt, dev, {d.B});
+    void* ctx = dense(a[3], "ctx_lens", at::kInt, dev, {d.B});
+    void* bounds = dense(a[4], "bounds", kv, dev, {d.num_blocks, d.Hkv, 2, d.D});
+    size_t bytes;
+    void* ws = workspace(a[6], dev, &bytes);
+    return launch(dev, a[7], [&](void* st) {
+      return spec_page_bounds(kc, as<int32_t>(bt), as<int32_t>(from), as<int32_t>(ctx), bounds, &d,
+                              ws, bytes, st);
+    });
+  });
+}
+
+// q, bounds, block_table, ctx_lens, scores, dims, ws, stream
+PyObject* page_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&] {
+    const int dev = device_of(a[0], "q");
+    const spec_dims d = dims_of(a[5]);
+    const auto kv = kv_type(d);
+    void* q = dense(a[0], "q", kv, dev, {d.B, d.M, d.Hq, d.D});
+    void* bounds = dense(a[1], "bounds", kv, dev, {d.num_blocks, d.Hkv, 2, d.D});
+    void* bt = dense(a[2], "block_table", at::kInt, dev, {d.B, d.max_blocks});
+    void* ctx = dense(a[3], "ctx_lens", at::kInt, dev, {d.B});
+    void* scores = dense(a[4], "scores", at::kFloat, dev, {d.B, d.Hkv, d.max_blocks});
+    size_t bytes;
+    void* ws = workspace(a[6], dev, &bytes);
+    return launch(dev, a[7], [&](void* st) {
+      return spec_page_score(q, bounds, as<int32_t>(bt), as<int32_t>(ctx), as<float>(scores), &d, ws,
+                             bytes, st);
+    });
+  });
+}
+
+// scores, ctx_lens, pages, page_counts, dims, ws, first, last, stream
+PyObject* page_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&] {
+    const int dev = device_of(a[0], "scores");
+    const spec_dims d = dims_of(a[4]);
+    const int64_t np = selected(a[2]);
+    void* scores = dense(a[0], "scores", at::kFloat, dev, {d.B, d.Hkv, d.max_blocks});
+    void* ctx = dense(a[1], "ctx_lens", at::kInt, dev, {d.B});
+    void* pages = dense(a[2], "pages", at::kInt, dev, {d.B, d.Hkv, np});
+    void* counts = dense(a[3], "page_counts", at::kInt, dev, {d.B});
+    size_t bytes;
+    void* ws = workspace(a[5], dev, &bytes);
+    const int32_t first = (int32_t)whole(a[6]), last = (int32_t)whole(a[7]);
+    return launch(dev, a[8], [&](void* st) {
+      return spec_page_select(as<float>(scores), as<int32_t>(ctx), (int32_t)np, first, last,
+                              as<int32_t>(pages), as<int32_t>(counts), &d, ws, bytes, st);
     });
   });
 }
@@ -291,8 +405,11 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define SPECV_FN(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {SPECV_FN(verify_attn_window), SPECV_FN(block_tables),
-                         SPECV_FN(qk_norm_rope), SPECV_FN(sample), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {SPECV_FN(verify_attn_window), SPECV_FN(verify_attn_prefix),
+                         SPECV_FN(verify_attn_pages),  SPECV_FN(block_tables),
+                         SPECV_FN(qk_norm_rope),       SPECV_FN(page_bounds),
+                         SPECV_FN(page_score),         SPECV_FN(page_select),
+                         SPECV_FN(sample),             {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_specbind", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,410 @@
+// Which pages of a long cache a verify step reads.
+//
+// Page 1 §2.1 has every query see the whole context; at long contexts most of
+// a softmax' mass lies in a few pages.  For a page whose keys have least and
+// largest coordinates lo, hi, no query q has a score above
+//   sum_d max(q_d lo_d, q_d hi_d) = q+ . hi + q- . lo,   q+ = max(q, 0), q- = min(q, 0)
+// with any of its keys.  Bounds of 2 D numbers a page and KV head stand for 16
+// D of keys, and the pages with the largest bounds are read.
+//
+//   page_bounds_kernel   lo and hi of the pages that a step has filled
+//   page_score_kernel    the bound of every page, the largest over the rows
+//                        that read the KV head
+//   page_select_kernel   the first and last pages and those of largest score
+#include <math.h>
+
+#include "page_select.cuh"
+
+namespace specv {
+
+// ---------------------------------------------------------------------------
+// bounds
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void widen(uint4& lo, uint4& hi, const uint4& v, float) {
+  float a[4], b[4], c[4];
+  unpack16(lo, a);
+  unpack16(hi, b);
+  unpack16(v, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = fminf(a[i], c[i]);
+    b[i] = fmaxf(b[i], c[i]);
+  }
+  lo = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
+  hi = make_uint4(__float_as_uint(b[0]), __float_as_uint(b[1]), __float_as_uint(b[2]), __float_as_uint(b[3]));
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void widen(uint4& lo, uint4& hi, const uint4& v, __nv_bfloat16) {
+  lo = make_uint4(min2(lo.x, v.x), min2(lo.y, v.y), min2(lo.z, v.z), min2(lo.w, v.w));
+  hi = make_uint4(max2(hi.x, v.x), max2(hi.y, v.y), max2(hi.z, v.z), max2(hi.w, v.w));
+}
+__device__ __forceinline__ uint4 shfl_xor16(const uint4& v, int m) {
+  return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                    __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
+}
+
+// A warp per page and KV head: 16 rows of D keys in 16-byte vectors, minima and
+// maxima in registers, then across the lanes that hold the same columns.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) page_bounds_kernel(const T* k_cache,
+                                                          const int32_t* block_table,
+                                                          const int32_t* from_lens,
+                                                          const int32_t* ctx_lens, spec_dims d,
+                                                          T* bounds, uint32_t* status) {
+  constexpr int kVecRow = D * (int)sizeof(T) / 16;  // vectors of a row: 8, 16 or 32
+  constexpr int kLoads = kVecRow / 2;               // of a lane
+  constexpr int kRowsPer = kWarp / kVecRow;         // rows of one load of the warp
+  pdl_trigger();
+  pdl_wait();  // the cache and the lengths may come from the previous kernels
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int b = blockIdx.y;
+  const int ctx = __ldcg(ctx_lens + b);
+  if (ctx <= 0) return;
+  const int from = from_lens != nullptr ? __ldcg(from_lens + b) : 0;
+  if (from < 0 || ctx > (int64_t)d.max_blocks * kBlock) {
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+      raise_status(status, from < 0 ? SPEC_ERR_INVALID_ARG : SPEC_ERR_CAPACITY);
+    return;
+  }
+  const int p0 = from / kBlock, p1 = ceil_div(ctx, kBlock);
+  const int64_t n = (int64_t)(p1 - p0) * d.Hkv;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / kWarp);
+  for (int64_t w = (int64_t)blockIdx.x * (blockDim.x / kWarp) + warp; w < n; w += step) {
+    const int p = p0 + (int)(w / d.Hkv), h = (int)(w % d.Hkv);
+    const int id = __ldcg(block_table + (int64_t)b * d.max_blocks + p);
+    if (id < 0 || id >= d.num_blocks) {
+      if (lane == 0) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
+      continue;
+    }
+    const int last = min(kBlock, ctx - p * kBlock) - 1;  // rows past it repeat it
+    const int64_t blk = (int64_t)id * d.Hkv + h;
+    const uint4* keys = reinterpret_cast<const uint4*>(k_cache + blk * kBlock * D);
+    const int r0 = lane / kVecRow, c = lane % kVecRow;
+    uint4 v[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) v[i] = __ldcg(keys + min(r0 + i * kRowsPer, last) * kVecRow + c);
+    uint4 lo = v[0], hi = v[0];
+#pragma unroll
+    for (int i = 1; i < kLoads; ++i) widen(lo, hi, v[i], T());
+#pragma unroll
+    for (int m = kVecRow; m < kWarp; m <<= 1) {
+      const uint4 a = shfl_xor16(lo, m), e = shfl_xor16(hi, m);
+      uint4 t = a;
+      widen(lo, t, a, T());
+      t = e;
+      widen(t, hi, e, T());
+    }
+    uint4* dst = reinterpret_cast<uint4*>(bounds + blk * 2 * D);
+    if (lane < kVecRow) dst[lane] = lo;
+    if (kVecRow == kWarp) dst[kVecRow + lane] = hi;
+    else if (lane >= kVecRow && lane < 2 * kVecRow) dst[lane] = hi;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// scores
+// ---------------------------------------------------------------------------
+// A CTA per 64 pages of a KV head; the product q+ . hi + q- . lo in register
+// tiles of RPT rows x 4 pages, the rows' maximum in registers, then across the
+// eight row groups.
+constexpr int kScorePages = 64, kScoreThreads = 128;
+
+template <int D, int RPT>
+constexpr size_t score_smem() {
+  return sizeof(float) * ((size_t)2 * D * (kScorePages + 4) + (size_t)D * (8 * RPT + 4) +
+                          8 * kScorePages);
+}
+
+template <typename T, int D, int RPT>
+__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
+    const T* q, const T* bounds, const int32_t* block_table, const int32_t* ctx_lens, spec_dims d,
+    float* __restrict__ scores, uint32_t* __restrict__ status) {
+  constexpr int kLd = kScorePages + 4, kRows = 8 * RPT, kLdQ = kRows + 4;
+  constexpr int kVec = 16 / sizeof(T), kVecRow = D / kVec;
+  extern __shared__ __align__(16) float smem[];
+  float* lo = smem;               // [D][kLd]
+  float* hi = lo + D * kLd;       // [D][kLd]
+  float* qs = hi + D * kLd;       // [D][kLdQ]
+  float* red = qs + D * kLdQ;     // [8][kScorePages]
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int h = blockIdx.y, b = blockIdx.z, page0 = blockIdx.x * kScorePages;
+  const int group = d.Hq / d.Hkv, R = group * d.M;
+  pdl_trigger();
+  pdl_wait();  // the queries, bounds and lengths may come from the previous kernels
+  const int ctx = __ldcg(ctx_lens + b);
+  const bool fits = ctx <= (int64_t)d.max_blocks * kBlock;
+  const int full = fits && ctx > 0 ? ctx / kBlock : 0;
+  if (!fits && page0 == 0 && h == 0 && tid == 0) raise_status(status, SPEC_ERR_CAPACITY);
+  float* out = scores + ((int64_t)b * d.Hkv + h) * d.max_blocks;
+  if (page0 >= full) {
+    for (int p = page0 + tid; p < min(page0 + kScorePages, d.max_blocks); p += kScoreThreads)
+      out[p] = -INFINITY;
+    return;
+  }
+  for (int e = tid; e < kScorePages * 2 * kVecRow; e += kScoreThreads) {
+    const int p = e % kScorePages, vi = e / kScorePages;  // vectors of lo, then of hi
+    float f[kVec];
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) f[c] = 0.f;
+    if (page0 + p < full) {
+      const int id = __ldcg(block_table + (int64_t)b * d.max_blocks + page0 + p);
+      if (id >= 0 && id < d.num_blocks)
+        unpack16(__ldcg(reinterpret_cast<const uint4*>(bounds + ((int64_t)id * d.Hkv + h) * 2 * D) + vi), f);
+    }
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) lo[(vi * kVec + c) * kLd + p] = f[c];
+  }
+  float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  for (int r0 = 0; r0 < R; r0 += kRows) {
+    __syncthreads();
+    for (int e = tid; e < kRows * kVecRow; e += kScoreThreads) {
+      const int r = e % kRows, vi = e / kRows;
+      const int rr = min(r0 + r, R - 1), i = rr / group;  // rows past the last repeat it
+      float f[kVec];
+      unpack16(__ldcg(reinterpret_cast<const uint4*>(
+                          q + (((int64_t)b * d.M + i) * d.Hq + h * group + rr - i * group) * D) + vi), f);
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) qs[(vi * kVec + c) * kLdQ + r] = f[c];
+    }
+    __syncthreads();
+    float acc[RPT][4];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[r][k] = 0.f;
+#pragma unroll 2
+    for (int dd = 0; dd < D; ++dd) {
+      const float4 a = *reinterpret_cast<const float4*>(lo + dd * kLd + tx * 4);
+      const float4 c = *reinterpret_cast<const float4*>(hi + dd * kLd + tx * 4);
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) {
+        const float qv = qs[dd * kLdQ + ty * RPT + r];
+        const float qp = fmaxf(qv, 0.f), qn = fminf(qv, 0.f);
+        acc[r][0] = fmaf(qp, c.x, fmaf(qn, a.x, acc[r][0]));
+        acc[r][1] = fmaf(qp, c.y, fmaf(qn, a.y, acc[r][1]));
+        acc[r][2] = fmaf(qp, c.z, fmaf(qn, a.z, acc[r][2]));
+        acc[r][3] = fmaf(qp, c.w, fmaf(qn, a.w, acc[r][3]));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) best[k] = fmaxf(best[k], acc[r][k]);
+  }
+  *reinterpret_cast<float4*>(red + ty * kScorePages + tx * 4) =
+      make_float4(best[0], best[1], best[2], best[3]);
+  __syncthreads();
+  if (tid < kScorePages && page0 + tid < d.max_blocks) {
+    float m = red[tid];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) m = fmaxf(m, red[k * kScorePages + tid]);
+    bool there = page0 + tid < full;
+    if (there) {
+      const int id = __ldcg(block_table + (int64_t)b * d.max_blocks + page0 + tid);
+      if (id < 0 || id >= d.num_blocks) {
+        there = false;
+        raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
+      }
+    }
+    out[page0 + tid] = there ? m : -INFINITY;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// selection
+// ---------------------------------------------------------------------------
+// A CTA per (request, KV head).  Scores become keys whose order is the scores';
+// the key of the last page taken is found digit by digit from the top (four
+// histograms of 256 counts), then one pass over the pages in order writes those
+// above it and the first of those equal to it.
+constexpr int kSelThreads = 256;
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+  // -0 counts as 0; NaN as the lowest value of all
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kSelThreads) page_select_kernel(
+    const float* scores, const int32_t* ctx_lens, int n_pages, int first, int last, spec_dims d,
+    int32_t* __restrict__ pages, int32_t* __restrict__ counts, uint32_t* __restrict__ status) {
+  __shared__ int s_hist[256];
+  __shared__ int s_digit, s_want;
+  __shared__ int s_gt[kSelThreads / kWarp], s_eq[kSelThreads / kWarp];
+  const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
+  const int h = blockIdx.x, b = blockIdx.y;
+  pdl_trigger();
+  pdl_wait();  // the scores and lengths may come from the previous kernels
+  const int ctx = __ldcg(ctx_lens + b);
+  const bool fits = ctx <= (int64_t)d.max_blocks * kBlock;
+  const int full = fits && ctx > 0 ? ctx / kBlock : 0;
+  const int count = min(full, n_pages);
+  int32_t* list = pages + ((int64_t)b * d.Hkv + h) * n_pages;
+  if (tid == 0 && h == 0) {
+    counts[b] = count;
+    if (!fits) raise_status(status, SPEC_ERR_CAPACITY);
+  }
+  for (int j = count + tid; j < n_pages; j += kSelThreads) list[j] = -1;
+  const float* x = scores + ((int64_t)b * d.Hkv + h) * d.max_blocks;
+  if (full <= n_pages) {  // every page
+    for (int j = tid; j < count; j += kSelThreads) list[j] = j;
+    return;
+  }
+  // pages first .. full - last - 1 compete for `want` places
+  const int c0 = first, c1 = full - last, want0 = n_pages - first - last;
+  uint32_t prefix = 0;
+  int want = want0, bad = 0;
+  for (int shift = 24; shift >= 0 && want0 > 0; shift -= 8) {
+    for (int i = tid; i < 256; i += kSelThreads) s_hist[i] = 0;
+    __syncthreads();
+    for (int p = c0 + tid; p < c1; p += kSelThreads) {
+      const float v = __ldcg(x + p);
+      bad |= v != v;
+      const uint32_t k = order_key(v);
+      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
+        atomicAdd(&s_hist[(k >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // lane j has the digits 255 - 8 j and the seven below
+      int c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c[i] = s_hist[255 - 8 * lane - i];
+        sum += c[i];
+      }
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      before -= sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before < want && want <= before + c[i]) {
+          s_digit = 255 - 8 * lane - i;
+          s_want = want - before;
+        }
+        before += c[i];
+      }
+    }
+    __syncthreads();
+    prefix |= (uint32_t)s_digit << shift;
+    want = s_want;
+  }
+  if (__syncthreads_or(bad) && tid == 0) raise_status(status, SPEC_ERR_NONFINITE);
+  // pages in order: taken are the first and the last, keys above `prefix`, and
+  // the first `want` of those equal to it
+  int done = 0, equal = 0;  // pages written, equal keys met
+  for (int base = 0; base < full; base += kSelThreads) {
+    const int p = base + tid;
+    bool take = false, eq = false;
+    if (p < full) {
+      if (p < c0 || p >= c1) {
+        take = true;
+      } else if (want0 > 0) {
+        const uint32_t k = order_key(__ldcg(x + p));
+        take = k > prefix;
+        eq = k == prefix;
+      }
+    }
+    const uint32_t below = (1u << lane) - 1;
+    const uint32_t em = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) s_eq[warp] = __popc(em);
+    __syncthreads();
+    int eb = equal + __popc(em & below), et = 0;
+    for (int w = 0; w < kSelThreads / kWarp; ++w) {
+      if (w < warp) eb += s_eq[w];
+      et += s_eq[w];
+    }
+    take |= eq && eb < want;
+    const uint32_t tm = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) s_gt[warp] = __popc(tm);
+    __syncthreads();
+    int tb = done + __popc(tm & below), tt = 0;
+    for (int w = 0; w < kSelThreads / kWarp; ++w) {
+      if (w < warp) tb += s_gt[w];
+      tt += s_gt[w];
+    }
+    if (take && tb < n_pages) list[tb] = p;
+    done += tt;
+    equal += et;
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+template <typename T>
+static cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t st) {
+  const spec_dims& d = a.d;
+  // one warp a (page, head); no more CTAs a request than its table has work for,
+  // eight CTAs an SM over the batch
+  const int64_t most = ceil_div64((int64_t)d.max_blocks * d.Hkv, 8);
+  int64_t x = ceil_div64(8 * 152, d.B);
+  if (x > most) x = most;
+  PdlLaunch L(dim3((unsigned)x, d.B), dim3(256), 0, st);
+  return cudaLaunchKernelEx(&L.cfg, d.D == 64 ? page_bounds_kernel<T, 64> : page_bounds_kernel<T, 128>,
+                            static_cast<const T*>(a.k_cache), a.block_table, a.from_lens,
+                            a.ctx_lens, d, static_cast<T*>(a.bounds), a.status);
+}
+
+cudaError_t page_bounds_launch(const BoundsArgs& a, cudaStream_t st, int* launches) {
+  const cudaError_t e = a.d.kv_dtype == SPEC_BF16 ? launch_bounds<__nv_bfloat16>(a, st)
+                                                  : launch_bounds<float>(a, st);
+  if (e == cudaSuccess) ++*launches;
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int D, int RPT>
+static cudaError_t launch_score(const ScoreArgs& a, cudaStream_t st) {
+  const spec_dims& d = a.d;
+  auto k = page_score_kernel<T, D, RPT>;
+  constexpr size_t smem = score_smem<D, RPT>();
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  PdlLaunch L(dim3(ceil_div(d.max_blocks, kScorePages), d.Hkv, d.B), dim3(kScoreThreads), smem, st);
+  return cudaLaunchKernelEx(&L.cfg, k, static_cast<const T*>(a.q), static_cast<const T*>(a.bounds),
+                            a.block_table, a.ctx_lens, d, a.scores, a.status);
+}
+
+template <typename T, int D>
+static cudaError_t launch_score(const ScoreArgs& a, cudaStream_t st) {
+  const int R = (a.d.Hq / a.d.Hkv) * a.d.M;
+  if (R <= 8) return launch_score<T, D, 1>(a, st);
+  if (R <= 16) return launch_score<T, D, 2>(a, st);
+  if (R <= 32) return launch_score<T, D, 4>(a, st);
+  return launch_score<T, D, 8>(a, st);
+}
+
+cudaError_t page_score_launch(const ScoreArgs& a, cudaStream_t st, int* launches) {
+  cudaError_t e;
+  if (a.d.kv_dtype == SPEC_BF16)
+    e = a.d.D == 64 ? launch_score<__nv_bfloat16, 64>(a, st) : launch_score<__nv_bfloat16, 128>(a, st);
+  else
+    e = a.d.D == 64 ? launch_score<float, 64>(a, st) : launch_score<float, 128>(a, st);
+  if (e == cudaSuccess) ++*launches;
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t page_select_launch(const SelectArgs& a, cudaStream_t st, int* launches) {
+  PdlLaunch L(dim3(a.d.Hkv, a.d.B), dim3(kSelThreads), 0, st);
+  cudaError_t e = cudaLaunchKernelEx(&L.cfg, page_select_kernel, a.scores, a.ctx_lens, a.n_pages,
+                                     a.first, a.last, a.d, a.pages, a.counts, a.status);
+  if (e == cudaSuccess) ++*launches;
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace specv

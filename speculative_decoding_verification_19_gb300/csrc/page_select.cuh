@@ -1,0 +1,40 @@
+// Internal interface between the C ABI layer and the page-selection kernels.
+#pragma once
+
+#include "common.cuh"
+
+namespace specv {
+
+struct BoundsArgs {
+  const void* k_cache;
+  const int32_t* block_table;
+  const int32_t* from_lens;  // NULL: from the first page on
+  const int32_t* ctx_lens;
+  void* bounds;
+  spec_dims d;
+  uint32_t* status;
+};
+struct ScoreArgs {
+  const void* q;
+  const void* bounds;
+  const int32_t* block_table;
+  const int32_t* ctx_lens;
+  float* scores;
+  spec_dims d;
+  uint32_t* status;
+};
+struct SelectArgs {
+  const float* scores;
+  const int32_t* ctx_lens;
+  int n_pages, first, last;
+  int32_t* pages;
+  int32_t* counts;
+  spec_dims d;
+  uint32_t* status;
+};
+
+cudaError_t page_bounds_launch(const BoundsArgs& a, cudaStream_t st, int* launches);
+cudaError_t page_score_launch(const ScoreArgs& a, cudaStream_t st, int* launches);
+cudaError_t page_select_launch(const SelectArgs& a, cudaStream_t st, int* launches);
+
+}  // namespace specv
