@@ -165,7 +165,15 @@ struct OwnPart {
 };
 
 size_t attn_simt_smem_bytes(int R, int D);
+// CTAs of the prefix kernel on tensor cores never exceed this (its partials are
+// sized for it).
+constexpr int kMaxPrefixCtas = 160;
+
 size_t prefix_part_floats(const spec_dims& d);
+bool prefix_tc_ok(const spec_dims& d);
+size_t prefix_tc_part_floats(const spec_dims& d);
+cudaError_t prefix_tc_launch(const AttnArgs& a, float* part, uint32_t* status, cudaStream_t st,
+                             PrefixPlan* plan);
 cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, PrefixPlan* plan,
                           int* launches);
 cudaError_t prefix_merge_launch(const AttnArgs& a, const WsLayout& lay, const PrefixPlan& plan,

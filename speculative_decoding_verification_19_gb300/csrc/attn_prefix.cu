@@ -9,7 +9,8 @@
 // request's own keys go through the verify attention (attn.cu, attn_tc.cu).
 //
 // Kernels in this file:
-//   prefix_simt_kernel   the prefix on CUDA cores (fp32, heads of 64)
+//   prefix_simt_kernel   the prefix on CUDA cores (fp32; bf16 goes to the tensor
+//                        cores, attn_prefix_tc.cu, unless CUDA cores are asked for)
 //   prefix_merge_kernel  the partials of a row, a warp per row
 #include <math.h>
 
@@ -324,7 +325,9 @@ size_t prefix_part_floats(const spec_dims& d) {
   const int64_t rows = (int64_t)d.B * (d.Hq / d.Hkv) * d.M;
   const int64_t units = (int64_t)d.Hkv * ceil_div64(rows, kPfxRows);
   const int64_t slots = units > kPfxSlots ? units : kPfxSlots;
-  return (size_t)slots * (size_t)(rows < kPfxRows ? rows : kPfxRows) * tc_part_stride(d.D);
+  const size_t simt = (size_t)slots * (size_t)(rows < kPfxRows ? rows : kPfxRows) * tc_part_stride(d.D);
+  const size_t tc = prefix_tc_part_floats(d);
+  return simt > tc ? simt : tc;
 }
 
 template <typename T>
@@ -343,8 +346,15 @@ static cudaError_t launch_simt(const AttnArgs& a, const PrefixPlan& p, float* pa
 cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, PrefixPlan* plan,
                           int* launches) {
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + lay.pfx_part_off);
+  uint32_t* status = reinterpret_cast<uint32_t*>(static_cast<char*>(a.ws) + lay.status_off);
+  cudaError_t e;
+  if (prefix_tc_ok(a.d) && a.d.attn_impl != SPEC_ATTN_CUDA_CORES) {
+    e = prefix_tc_launch(a, part, status, st, plan);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+  }
   *plan = simt_plan(a.d, a.view.prefix_len);
-  const cudaError_t e = a.d.kv_dtype == SPEC_BF16 ? launch_simt<__nv_bfloat16>(a, *plan, part, st)
+  e = a.d.kv_dtype == SPEC_BF16 ? launch_simt<__nv_bfloat16>(a, *plan, part, st)
                                                   : launch_simt<float>(a, *plan, part, st);
   if (e == cudaSuccess) ++*launches;
   return e;

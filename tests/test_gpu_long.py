@@ -133,6 +133,8 @@ PREFIX = [  # ctx, P, M, Hq, Hkv, D, dt, tree, impl
     ([48, 49, 63, 64], 48, 1, 8, 2, 128, BF, False, CORES),
     ([2000, 2001, 2100], 2000, 9, 8, 2, 128, BF, True, CORES),
     ([80, 81], 80, 7, 3, 3, 64, BF, False, AUTO),
+    ([80, 81], 80, 7, 3, 3, 64, BF, False, CORES),
+    ([3008] * 3, 3008, 128, 1, 1, 64, BF, False, AUTO),       # a unit with one tile of rows
     ([1600, 1900, 1616], 1600, 16, 8, 2, 64, BF, True, AUTO),
     ([80, 95], 80, 3, 4, 2, 128, F32, False, AUTO),
     ([1040] * 9, 1040, 16, 2, 1, 128, F32, True, AUTO),
