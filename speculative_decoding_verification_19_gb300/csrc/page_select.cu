@@ -9,7 +9,8 @@
 //
 //   page_bounds_kernel   lo and hi of the pages that a step has filled
 //   page_score_kernel    the bound of every page, the largest over the rows
-//                        that read the KV head
+//                        that read the KV head (fp32, and more than 128 rows;
+//                        bf16 goes to the tensor cores, page_score_tc.cu)
 //   page_select_kernel   the first and last pages and those of largest score
 #include <math.h>
 
@@ -223,9 +224,15 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
 // selection
 // ---------------------------------------------------------------------------
 // A CTA per (request, KV head).  Scores become keys whose order is the scores';
-// the key of the last page taken is found digit by digit from the top (four
-// histograms of 256 counts), then one pass over the pages in order writes those
-// above it and the first of those equal to it.
+// the key of the last page taken is found digit by digit from the top of the
+// competing keys' range (histograms of 256 counts; the range, because scores of
+// one row share their exponents), then those above it and the first of those
+// equal to it are written in the pages' order.
+//
+// Keys stay in registers, page i * threads + t in thread t, so a row is read once.
+// What is left is a chain of some twenty barriers: 128 requests x 8 heads of 8192
+// pages at most, 18 MB: 9 us, one request 5 us, where four passes over memory with
+// the leading digits in few bins took 61 and 11.
 constexpr int kSelThreads = 256;
 
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -235,16 +242,48 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) page_select_kernel(
+// Exclusive prefix of s[0 .. n) in place by the first warp; the sum in s[n].
+__device__ __forceinline__ void scan_counts(int* s, int n) {
+  const int lane = threadIdx.x;
+  int carry = 0;
+  for (int base = 0; base < n; base += kWarp) {
+    const int own = base + lane < n ? s[base + lane] : 0;
+    int x = own;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (base + lane < n) s[base + lane] = carry + x - own;
+    carry += __shfl_sync(0xffffffffu, x, kWarp - 1);
+  }
+  if (lane == 0) s[n] = carry;
+}
+
+// kKeys: keys of a thread (0: any number, read again for every pass).
+template <int kThreads, int kKeys>
+__global__ void __launch_bounds__(kThreads) page_select_kernel(
     const float* scores, const int32_t* ctx_lens, int n_pages, int first, int last, spec_dims d,
     int32_t* __restrict__ pages, int32_t* __restrict__ counts, uint32_t* __restrict__ status) {
+  constexpr int kWarps = kThreads / kWarp;
+  constexpr int kHeld = kKeys > 0 ? kKeys : 1;
+  constexpr int kRun = kKeys > 0 ? kKeys : 8;  // rounds of pages between two scans
   __shared__ int s_hist[256];
-  __shared__ int s_digit, s_want;
-  __shared__ int s_gt[kSelThreads / kWarp], s_eq[kSelThreads / kWarp];
+  __shared__ int s_digit, s_want, s_all;
+  __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
+  __shared__ int s_cnt[kRun * kWarps + 1];
   const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
   const int h = blockIdx.x, b = blockIdx.y;
   pdl_trigger();
   pdl_wait();  // the scores and lengths may come from the previous kernels
+  const float* x = scores + ((int64_t)b * d.Hkv + h) * d.max_blocks;
+  // all of the row's places are there: the loads need not wait for the length
+  float v[kHeld];
+#pragma unroll
+  for (int i = 0; i < kKeys; ++i) {
+    const int p = i * kThreads + tid;
+    v[i] = p < d.max_blocks ? __ldcg(x + p) : 0.f;
+  }
   const int ctx = __ldcg(ctx_lens + b);
   const bool fits = ctx <= (int64_t)d.max_blocks * kBlock;
   const int full = fits && ctx > 0 ? ctx / kBlock : 0;
@@ -254,25 +293,66 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(
     counts[b] = count;
     if (!fits) raise_status(status, SPEC_ERR_CAPACITY);
   }
-  for (int j = count + tid; j < n_pages; j += kSelThreads) list[j] = -1;
-  const float* x = scores + ((int64_t)b * d.Hkv + h) * d.max_blocks;
+  for (int j = count + tid; j < n_pages; j += kThreads) list[j] = -1;
   if (full <= n_pages) {  // every page
-    for (int j = tid; j < count; j += kSelThreads) list[j] = j;
+    for (int j = tid; j < count; j += kThreads) list[j] = j;
     return;
   }
-  // pages first .. full - last - 1 compete for `want` places
-  const int c0 = first, c1 = full - last, want0 = n_pages - first - last;
-  uint32_t prefix = 0;
-  int want = want0, bad = 0;
-  for (int shift = 24; shift >= 0 && want0 > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelThreads) s_hist[i] = 0;
+  // pages c0 .. c1 - 1 compete for `want` places
+  const int c0 = first, c1 = full - last;
+  int want = n_pages - first - last;
+  const int rounds = kKeys > 0 ? kKeys : ceil_div(full, kThreads);
+  // key of this thread's i-th page, and whether it competes
+  auto key_of = [&](int i, bool* in) {
+    const int p = i * kThreads + tid;
+    *in = p >= c0 && p < c1;
+    return *in ? order_key(kKeys > 0 ? v[i] : __ldcg(x + p)) : 0u;
+  };
+  uint32_t lo = 0xffffffffu, hi = 0;
+  int bad = 0;
+#pragma unroll
+  for (int i = 0; i < rounds; ++i) {
+    bool in;
+    const uint32_t k = key_of(i, &in);
+    if (in) {
+      lo = min(lo, k);
+      hi = max(hi, k);
+      bad |= k == 0u;
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    s_lo[warp] = lo;
+    s_hi[warp] = hi;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) raise_status(status, SPEC_ERR_NONFINITE);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    lo = min(lo, s_lo[w]);
+    hi = max(hi, s_hi[w]);
+  }
+  // Taken are the keys above `edge` and the first `want` of those equal to it.
+  // `edge` is known down to bit `shift` (relative to lo).
+  uint32_t edge = lo;
+  int shift = 32 - __clz(hi - lo);  // 0 if all are equal
+  if (want == 0) {
+    edge = hi;  // nothing is above it
+    shift = 0;
+  }
+  while (shift > 0) {
+    const int bits = min(8, shift);
+    const uint32_t above = shift < 32 ? (edge - lo) >> shift : 0u;
+    shift -= bits;
+    if (tid < 256) s_hist[tid] = 0;
     __syncthreads();
-    for (int p = c0 + tid; p < c1; p += kSelThreads) {
-      const float v = __ldcg(x + p);
-      bad |= v != v;
-      const uint32_t k = order_key(v);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)))
-        atomicAdd(&s_hist[(k >> shift) & 255u], 1);
+#pragma unroll
+    for (int i = 0; i < rounds; ++i) {
+      bool in;
+      const uint32_t k = key_of(i, &in) - lo;
+      if (in && (shift + bits >= 32 || (k >> (shift + bits)) == above))
+        atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1);
     }
     __syncthreads();
     if (warp == 0) {
@@ -295,52 +375,72 @@ __global__ void __launch_bounds__(kSelThreads) page_select_kernel(
         if (before < want && want <= before + c[i]) {
           s_digit = 255 - 8 * lane - i;
           s_want = want - before;
+          s_all = want == before + c[i];
         }
         before += c[i];
       }
     }
     __syncthreads();
-    prefix |= (uint32_t)s_digit << shift;
+    edge += (uint32_t)s_digit << shift;
     want = s_want;
-  }
-  if (__syncthreads_or(bad) && tid == 0) raise_status(status, SPEC_ERR_NONFINITE);
-  // pages in order: taken are the first and the last, keys above `prefix`, and
-  // the first `want` of those equal to it
-  int done = 0, equal = 0;  // pages written, equal keys met
-  for (int base = 0; base < full; base += kSelThreads) {
-    const int p = base + tid;
-    bool take = false, eq = false;
-    if (p < full) {
-      if (p < c0 || p >= c1) {
-        take = true;
-      } else if (want0 > 0) {
-        const uint32_t k = order_key(__ldcg(x + p));
-        take = k > prefix;
-        eq = k == prefix;
+    if (s_all) {
+      // every key of this digit is taken: those from `edge` on.  (edge is a sum of
+      // digits below hi - lo, so edge - 1 wraps only for edge = lo = 0, where NaN
+      // is the lowest key and all are taken as equal or above.)
+      if (edge > 0u) {
+        --edge;
+        want = 0;
+        break;
       }
     }
-    const uint32_t below = (1u << lane) - 1;
-    const uint32_t em = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_eq[warp] = __popc(em);
-    __syncthreads();
-    int eb = equal + __popc(em & below), et = 0;
-    for (int w = 0; w < kSelThreads / kWarp; ++w) {
-      if (w < warp) eb += s_eq[w];
-      et += s_eq[w];
+  }
+  // write them in the pages' order, kRun rounds of pages at a time
+  int done = 0, equal = 0;
+  for (int r0 = 0; r0 < rounds; r0 += kRun) {
+    uint32_t take = 0, eq = 0;  // bit i: round r0 + i
+    if (want > 0) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        bool in = false;
+        const uint32_t k = r0 + i < rounds ? key_of(r0 + i, &in) : 0u;
+        const bool e = in && k == edge;
+        const uint32_t m = __ballot_sync(0xffffffffu, e);
+        if (lane == 0) s_cnt[i * kWarps + warp] = __popc(m);
+        eq |= (e ? 1u : 0u) << i;
+      }
+      __syncthreads();
+      if (warp == 0) scan_counts(s_cnt, kRun * kWarps);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const uint32_t m = __ballot_sync(0xffffffffu, (eq >> i) & 1u);
+        if (((eq >> i) & 1u) &&
+            equal + s_cnt[i * kWarps + warp] + __popc(m & ((1u << lane) - 1u)) < want)
+          take |= 1u << i;
+      }
+      equal += s_cnt[kRun * kWarps];
+      __syncthreads();
     }
-    take |= eq && eb < want;
-    const uint32_t tm = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) s_gt[warp] = __popc(tm);
-    __syncthreads();
-    int tb = done + __popc(tm & below), tt = 0;
-    for (int w = 0; w < kSelThreads / kWarp; ++w) {
-      if (w < warp) tb += s_gt[w];
-      tt += s_gt[w];
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const int p = (r0 + i) * kThreads + tid;
+      bool in = false;
+      const uint32_t k = r0 + i < rounds ? key_of(r0 + i, &in) : 0u;
+      if (p < full && (in ? k > edge : true)) take |= 1u << i;
+      const uint32_t m = __ballot_sync(0xffffffffu, (take >> i) & 1u);
+      if (lane == 0) s_cnt[i * kWarps + warp] = __popc(m);
     }
-    if (take && tb < n_pages) list[tb] = p;
-    done += tt;
-    equal += et;
     __syncthreads();
+    if (warp == 0) scan_counts(s_cnt, kRun * kWarps);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const uint32_t m = __ballot_sync(0xffffffffu, (take >> i) & 1u);
+      const int at = done + s_cnt[i * kWarps + warp] + __popc(m & ((1u << lane) - 1u));
+      if (((take >> i) & 1u) && at < n_pages) list[at] = (r0 + i) * kThreads + tid;
+    }
+    done += s_cnt[kRun * kWarps];
+    if (r0 + kRun < rounds) __syncthreads();
   }
 }
 
@@ -390,6 +490,7 @@ static cudaError_t launch_score(const ScoreArgs& a, cudaStream_t st) {
 }
 
 cudaError_t page_score_launch(const ScoreArgs& a, cudaStream_t st, int* launches) {
+  if (page_score_tc_ok(a.d)) return page_score_tc_launch(a, st, launches);
   cudaError_t e;
   if (a.d.kv_dtype == SPEC_BF16)
     e = a.d.D == 64 ? launch_score<__nv_bfloat16, 64>(a, st) : launch_score<__nv_bfloat16, 128>(a, st);
@@ -399,10 +500,22 @@ cudaError_t page_score_launch(const ScoreArgs& a, cudaStream_t st, int* launches
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int kThreads, int kKeys>
+static cudaError_t launch_select(const SelectArgs& a, cudaStream_t st) {
+  PdlLaunch L(dim3(a.d.Hkv, a.d.B), dim3(kThreads), 0, st);
+  return cudaLaunchKernelEx(&L.cfg, page_select_kernel<kThreads, kKeys>, a.scores, a.ctx_lens,
+                            a.n_pages, a.first, a.last, a.d, a.pages, a.counts, a.status);
+}
+
 cudaError_t page_select_launch(const SelectArgs& a, cudaStream_t st, int* launches) {
-  PdlLaunch L(dim3(a.d.Hkv, a.d.B), dim3(kSelThreads), 0, st);
-  cudaError_t e = cudaLaunchKernelEx(&L.cfg, page_select_kernel, a.scores, a.ctx_lens, a.n_pages,
-                                     a.first, a.last, a.d, a.pages, a.counts, a.status);
+  // the smallest instance whose registers hold the longest row
+  const int n = a.d.max_blocks;
+  const cudaError_t e = n <= 4 * kSelThreads    ? launch_select<kSelThreads, 4>(a, st)
+                        : n <= 8 * kSelThreads  ? launch_select<kSelThreads, 8>(a, st)
+                        : n <= 16 * kSelThreads ? launch_select<kSelThreads, 16>(a, st)
+                        : n <= 32 * kSelThreads ? launch_select<kSelThreads, 32>(a, st)
+                        : n <= 32 * 1024        ? launch_select<1024, 32>(a, st)
+                                                : launch_select<1024, 0>(a, st);
   if (e == cudaSuccess) ++*launches;
   return e != cudaSuccess ? e : cudaGetLastError();
 }

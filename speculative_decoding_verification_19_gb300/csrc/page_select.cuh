@@ -35,6 +35,8 @@ struct SelectArgs {
 
 cudaError_t page_bounds_launch(const BoundsArgs& a, cudaStream_t st, int* launches);
 cudaError_t page_score_launch(const ScoreArgs& a, cudaStream_t st, int* launches);
+bool page_score_tc_ok(const spec_dims& d);
+cudaError_t page_score_tc_launch(const ScoreArgs& a, cudaStream_t st, int* launches);
 cudaError_t page_select_launch(const SelectArgs& a, cudaStream_t st, int* launches);
 
 }  // namespace specv
