@@ -10,11 +10,13 @@
 //
 // The tiles of 128 pages of all (request, KV head) pairs, in this order, are
 // shared evenly among one CTA per SM.  Per CTA, warp-specialised:
-//   warps 4, 5  copy a tile's bounds (512 bytes a page for D = 128) by 16-byte
-//               cp.async into a ring, in the 128-byte-swizzled operand layout
-//   warp 7      builds (q-, q+) of a pair
-//   warp 6      issues the MMAs into two TMEM buffers in turn
-//   warps 0..3  maxima and scores
+//   warps 4..7   copy a tile's bounds (512 bytes a page for D = 128) by 16-byte
+//                cp.async into a ring, in the 128-byte-swizzled operand layout;
+//                a tile's block ids are on their way while the last one is copied
+//   warps 9, 10  build (q-, q+) of a pair, one pair ahead where shared memory has
+//                room for two
+//   warp 8       issues the MMAs into two TMEM buffers in turn
+//   warps 0..3   maxima and scores
 #include <math.h>
 
 #include "page_select.cuh"
@@ -24,20 +26,20 @@ namespace specv {
 namespace score {
 
 constexpr int kPages = 128;
-constexpr int kThreads = 256;
-constexpr int kCopyWarp = 4, kCopyThreads = 64, kMmaWarp = 6, kQueryWarp = 7;
+constexpr int kThreads = 384;
+constexpr int kCopyWarp = 4, kCopyThreads = 128, kMmaWarp = 8, kQueryWarp = 9, kQueryThreads = 64;
 constexpr int kMaxStages = 4;
 constexpr int kHalfBytes = kPages * 128;  // 64 columns of 128 pages
 constexpr size_t kSmemMost = 224 * 1024;
 
 struct __align__(8) Bars {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t acc_full[2], acc_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  int issued[2];        // stages that each copy warp issued
+  int issued[4];        // stages that each copy warp issued
   int64_t first, last;  // the CTA's tiles
   int64_t before;       // tiles of the requests before `b`
   int b;                // the request that holds its first tile
@@ -86,8 +88,8 @@ struct Walk {
 template <int D, bool kShort>
 __global__ void __launch_bounds__(kThreads, 1) page_score_tc_kernel(
     const __nv_bfloat16* q, const __nv_bfloat16* bounds, const int32_t* block_table,
-    const int32_t* ctx_lens, spec_dims d, int N, int n_stages, float* __restrict__ scores,
-    uint32_t* __restrict__ status) {
+    const int32_t* ctx_lens, spec_dims d, int N, int n_stages, int n_q,
+    float* __restrict__ scores, uint32_t* __restrict__ status) {
   constexpr int kHalves = 2 * D / 64;
   constexpr int kStageBytes = kHalves * kHalfBytes;
   constexpr int kChunks = kHalves * 8;  // 16-byte chunks of a page's bounds
@@ -110,9 +112,9 @@ __global__ void __launch_bounds__(kThreads, 1) page_score_tc_kernel(
       ptx::mbar_init(ptx::smem_u32(&bars->full[s]), kCopyThreads);
       ptx::mbar_init(ptx::smem_u32(&bars->empty[s]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(&bars->q_full), kWarp);
-    ptx::mbar_init(ptx::smem_u32(&bars->q_empty), 1);
     for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&bars->q_full[i]), kQueryThreads);
+      ptx::mbar_init(ptx::smem_u32(&bars->q_empty[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars->acc_full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars->acc_empty[i]), 4);
     }
@@ -179,26 +181,32 @@ __global__ void __launch_bounds__(kThreads, 1) page_score_tc_kernel(
   ptx::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp >= kCopyWarp && warp < kCopyWarp + 2) {
+  if (warp >= kCopyWarp && warp < kCopyWarp + 4) {
     // --------------------------------------------------------------- copies
     const int ct = (warp - kCopyWarp) * kWarp + lane;
-    const int c = ct % kChunks;      // chunk of a page's bounds
+    const int c = ct % kChunks;                    // chunk of a page's bounds
     constexpr int kStep = kCopyThreads / kChunks;  // pages of one round of the threads
     const int p0 = ct / kChunks;
     const uint32_t so = (uint32_t)(c >> 3) * kHalfBytes;
     int st = 0, at = 0;
     uint32_t round = 0;
     bool ok = true;
-    for (Walk w(*bars, ctx_lens, d); w.more() && ok; w.next()) {
+    int ids[kPages / kWarp], nids[kPages / kWarp];  // lane j: blocks of pages j, 32 + j, ...
+    auto look_up = [&](const Walk& w, int(&to)[kPages / kWarp]) {
       const int32_t* bt = block_table + (int64_t)w.b * d.max_blocks + w.tile * kPages;
-      const int np = min(kPages, w.full - w.tile * kPages);
-      int ids[kPages / kWarp];  // lane j: blocks of pages j, 32 + j, ...
+      const int np = w.full - w.tile * kPages;
 #pragma unroll
-      for (int k = 0; k < kPages / kWarp; ++k) {
-        const int p = k * kWarp + lane;
-        const int id = p < np ? __ldcg(bt + p) : -1;
-        ids[k] = id < d.num_blocks ? id : -1;
-      }
+      for (int k = 0; k < kPages / kWarp; ++k)
+        to[k] = k * kWarp + lane < np ? __ldcg(bt + k * kWarp + lane) : -1;
+    };
+    Walk w(*bars, ctx_lens, d);
+    if (w.more()) look_up(w, nids);
+    while (w.more() && ok) {
+      const int h = w.h;
+#pragma unroll
+      for (int k = 0; k < kPages / kWarp; ++k) ids[k] = nids[k] < d.num_blocks ? nids[k] : -1;
+      w.next();
+      if (w.more()) look_up(w, nids);
       ok = ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->empty[at]), round ^ 1u, abort, wait);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_score_tc_kernel(
           const int id = __shfl_sync(0xffffffffu, ids[k], r + p0);
           const bool there = id >= 0;  // else zeros
           const __nv_bfloat16* src =
-              bounds + ((int64_t)(there ? id : 0) * d.Hkv + w.h) * 2 * D + c * 8;
+              bounds + ((int64_t)(there ? id : 0) * d.Hkv + h) * 2 * D + c * 8;
           ptx::cp_async16_fill(sb + (uint32_t)p * 128u + ((uint32_t)((c & 7) ^ (p & 7)) << 4), src,
                                there ? 16u : 0u);
         }
@@ -225,62 +233,75 @@ __global__ void __launch_bounds__(kThreads, 1) page_score_tc_kernel(
     // every copy lands before the CTA may exit, also when a wait gave up
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0) bars->issued[warp - kCopyWarp] = st;
-    asm volatile("bar.sync 1, 64;" ::: "memory");
+    asm volatile("bar.sync 1, 128;" ::: "memory");
     if (ct == 0) {
-      const int both = min(bars->issued[0], bars->issued[1]);
-      for (int u = both > n_stages ? both - n_stages : 0; u < both; ++u)
+      const int all = min(min(bars->issued[0], bars->issued[1]), min(bars->issued[2], bars->issued[3]));
+      for (int u = all > n_stages ? all - n_stages : 0; u < all; ++u)
         ptx::mbar_drain(ptx::smem_u32(&bars->full[u % n_stages]), (uint32_t)((u / n_stages) & 1),
                         kDefaultWaitCycles);
     }
-  } else if (warp == kQueryWarp) {
+  } else if (warp >= kQueryWarp && warp < kQueryWarp + 2) {
     // -------------------------------------------------------------- queries
+    const int qt = (warp - kQueryWarp) * kWarp + lane;
     int pairs = 0;
     for (Walk w(*bars, ctx_lens, d); w.more(); w.next()) {
       if (!w.first(x0)) continue;
+      const int buf = pairs % n_q;
       if (!__all_sync(0xffffffffu,
-                      ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->q_empty),
-                                               (uint32_t)((pairs & 1) ^ 1), abort, wait)))
+                      ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->q_empty[buf]),
+                                               (uint32_t)((pairs / n_q) & 1) ^ 1u, abort, wait)))
         break;
       ++pairs;
-      for (int e = lane; e < N * (D / 8); e += kWarp) {
-        const int n = e / (D / 8), c = e % (D / 8);
-        uint4 neg = make_uint4(0, 0, 0, 0), pos = neg;
-        if (n < R) {
-          const int i = n / group;
-          const uint4 v = __ldcg(reinterpret_cast<const uint4*>(
-                                     q + (((int64_t)w.b * d.M + i) * d.Hq + w.h * group + n - i * group) * D) + c);
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      uint8_t* to = qbuf + (size_t)buf * kHalves * N * 128;
+      constexpr int kVec = D / 8, kAtOnce = 6;
+      for (int e0 = qt; e0 < N * kVec; e0 += kAtOnce * kQueryThreads) {
+        uint4 v[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int e = e0 + u * kQueryThreads, n = e / kVec, c = e % kVec, i = n / group;
+          v[u] = make_uint4(0, 0, 0, 0);
+          if (n < R)
+            v[u] = __ldcg(reinterpret_cast<const uint4*>(
+                              q + (((int64_t)w.b * d.M + i) * d.Hq + w.h * group + n - i * group) * D) + c);
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int e = e0 + u * kQueryThreads, n = e / kVec, c = e % kVec;
+          if (n >= N) break;
+          const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
           uint32_t lo[4], hi[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             asm("min.bf16x2 %0, %1, %2;" : "=r"(lo[k]) : "r"(x[k]), "r"(0u));
             asm("max.bf16x2 %0, %1, %2;" : "=r"(hi[k]) : "r"(x[k]), "r"(0u));
           }
-          neg = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          pos = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          const uint32_t o = (uint32_t)(c >> 3) * (uint32_t)N * 128u + (uint32_t)n * 128u +
+                             ((uint32_t)((c & 7) ^ (n & 7)) << 4);
+          *reinterpret_cast<uint4*>(to + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);  // meets lo
+          *reinterpret_cast<uint4*>(to + (kHalves / 2) * N * 128 + o) =
+              make_uint4(hi[0], hi[1], hi[2], hi[3]);
         }
-        const uint32_t o = (uint32_t)(c >> 3) * (uint32_t)N * 128u + (uint32_t)n * 128u +
-                           ((uint32_t)((c & 7) ^ (n & 7)) << 4);
-        *reinterpret_cast<uint4*>(qbuf + o) = neg;  // meets lo
-        *reinterpret_cast<uint4*>(qbuf + (kHalves / 2) * N * 128 + o) = pos;
       }
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(ptx::smem_u32(&bars->q_full));
+      ptx::mbar_arrive(ptx::smem_u32(&bars->q_full[buf]));
     }
   } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------------- MMAs
     if (lane == 0) {
       const uint64_t da0 = ptx::sdesc_sw128(ptx::smem_u32(smem), 16, 1024);
-      const uint64_t db = ptx::sdesc_sw128(ptx::smem_u32(qbuf), 16, 1024);
+      const uint64_t db0 = ptx::sdesc_sw128(ptx::smem_u32(qbuf), 16, 1024);
       const uint32_t id = ptx::idesc_bf16_f32(128, N, false, false);
-      int at = 0, pairs = 0;
+      int at = 0, pairs = 0, qb = 0;
       uint32_t round = 0, t = 0;
       for (Walk w(*bars, ctx_lens, d); w.more(); w.next(), ++t) {
         if (w.first(x0)) {
-          if (!ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->q_full), (uint32_t)(pairs & 1), abort, wait))
+          qb = pairs % n_q;
+          if (!ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->q_full[qb]), (uint32_t)((pairs / n_q) & 1),
+                                        abort, wait))
             break;
           ++pairs;
         }
+        const uint64_t db = db0 + (uint64_t)((qb * kHalves * N * 128) >> 4);
         if (!ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->full[at]), round, abort, wait)) break;
         const int buf = t & 1;
         if (!ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->acc_empty[buf]), ((t >> 1) & 1) ^ 1u, abort,
@@ -295,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) page_score_tc_kernel(
                       db + (uint64_t)(((k >> 2) * N * 128 + (k & 3) * 32) >> 4), id, k > 0 ? 1u : 0u);
         ptx::mma_commit(ptx::smem_u32(&bars->acc_full[buf]));
         ptx::mma_commit(ptx::smem_u32(&bars->empty[at]));
-        if (w.last()) ptx::mma_commit(ptx::smem_u32(&bars->q_empty));
+        if (w.last()) ptx::mma_commit(ptx::smem_u32(&bars->q_empty[qb]));
         if (++at == n_stages) {
           at = 0;
           round ^= 1u;
@@ -368,9 +389,12 @@ cudaError_t page_score_tc_launch(const ScoreArgs& a, cudaStream_t st, int* launc
   const spec_dims& d = a.d;
   const int N = ceil_div((d.Hq / d.Hkv) * d.M, 16) * 16;
   const size_t stage = (size_t)(2 * d.D / 64) * kHalfBytes, qbytes = (size_t)N * 4 * d.D;
-  int n_stages = (int)((kSmemMost - qbytes) / stage);
+  // two buffers of queries where two stages (128 KB of bounds on their way) fit
+  // beside them
+  const int n_q = 2 * qbytes + 2 * stage <= kSmemMost ? 2 : 1;
+  int n_stages = (int)((kSmemMost - n_q * qbytes) / stage);
   if (n_stages > kMaxStages) n_stages = kMaxStages;
-  const size_t smem = n_stages * stage + qbytes + 1024;
+  const size_t smem = n_stages * stage + n_q * qbytes + 1024;
   const bool short_wait = wait_limit_cycles(d) < ptx::kShortWait;
   auto kern = d.D == 64 ? (short_wait ? page_score_tc_kernel<64, true> : page_score_tc_kernel<64, false>)
                         : (short_wait ? page_score_tc_kernel<128, true> : page_score_tc_kernel<128, false>);
@@ -385,7 +409,7 @@ cudaError_t page_score_tc_launch(const ScoreArgs& a, cudaStream_t st, int* launc
   PdlLaunch L(dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), smem, st);
   e = cudaLaunchKernelEx(&L.cfg, kern, static_cast<const __nv_bfloat16*>(a.q),
                          static_cast<const __nv_bfloat16*>(a.bounds), a.block_table, a.ctx_lens, d,
-                         N, n_stages, a.scores, a.status);
+                         N, n_stages, n_q, a.scores, a.status);
   if (e == cudaSuccess) ++*launches;
   return e != cudaSuccess ? e : cudaGetLastError();
 }

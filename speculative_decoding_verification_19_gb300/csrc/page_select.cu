@@ -242,22 +242,28 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix of s[0 .. n) in place by the first warp; the sum in s[n].
-__device__ __forceinline__ void scan_counts(int* s, int n) {
-  const int lane = threadIdx.x;
-  int carry = 0;
-  for (int base = 0; base < n; base += kWarp) {
-    const int own = base + lane < n ? s[base + lane] : 0;
-    int x = own;
+// Exclusive prefix of one count per thread over the CTA (s: a place per warp and
+// one for the sum, which is returned too).
+template <int kWarps>
+__device__ __forceinline__ int cta_prefix(int own, int* s, int* sum) {
+  const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+  int x = own;
 #pragma unroll
-    for (int o = 1; o < kWarp; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (base + lane < n) s[base + lane] = carry + x - own;
-    carry += __shfl_sync(0xffffffffu, x, kWarp - 1);
+  for (int o = 1; o < kWarp; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  if (lane == 0) s[n] = carry;
+  if (lane == kWarp - 1) s[warp] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int y = s[w];
+    before += w < warp ? y : 0;
+    all += y;
+  }
+  *sum = all;
+  return before + x - own;
 }
 
 // kKeys: keys of a thread (0: any number, read again for every pass).
@@ -267,11 +273,15 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
     int32_t* __restrict__ pages, int32_t* __restrict__ counts, uint32_t* __restrict__ status) {
   constexpr int kWarps = kThreads / kWarp;
   constexpr int kHeld = kKeys > 0 ? kKeys : 1;
-  constexpr int kRun = kKeys > 0 ? kKeys : 8;  // rounds of pages between two scans
+  constexpr int kRun = kKeys > 0 ? kKeys : 32;  // rounds of pages between two scans: at most
+                                                // one word of 32 pages a thread
+  constexpr int kList = 1024;
   __shared__ int s_hist[256];
-  __shared__ int s_digit, s_want, s_all;
+  __shared__ int s_digit, s_want, s_count, s_n;
   __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
-  __shared__ int s_cnt[kRun * kWarps + 1];
+  __shared__ int s_sum[2][kWarps];
+  __shared__ uint32_t s_above[kRun * kWarps], s_equal[kRun * kWarps];
+  __shared__ uint32_t s_list[kList];
   const int tid = threadIdx.x, warp = tid / kWarp, lane = tid % kWarp;
   const int h = blockIdx.x, b = blockIdx.y;
   pdl_trigger();
@@ -301,17 +311,26 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
   // pages c0 .. c1 - 1 compete for `want` places
   const int c0 = first, c1 = full - last;
   int want = n_pages - first - last;
-  const int rounds = kKeys > 0 ? kKeys : ceil_div(full, kThreads);
+  const int rounds = ceil_div(full, kThreads);
   // key of this thread's i-th page, and whether it competes
   auto key_of = [&](int i, bool* in) {
     const int p = i * kThreads + tid;
     *in = p >= c0 && p < c1;
     return *in ? order_key(kKeys > 0 ? v[i] : __ldcg(x + p)) : 0u;
   };
+  // rounds of keys: unrolled where they are in registers
+  auto each = [&](auto body) {
+    if constexpr (kKeys > 0) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (i < rounds) body(i);
+    } else {
+      for (int i = 0; i < rounds; ++i) body(i);
+    }
+  };
   uint32_t lo = 0xffffffffu, hi = 0;
   int bad = 0;
-#pragma unroll
-  for (int i = 0; i < rounds; ++i) {
+  each([&](int i) {
     bool in;
     const uint32_t k = key_of(i, &in);
     if (in) {
@@ -319,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
       hi = max(hi, k);
       bad |= k == 0u;
     }
-  }
+  });
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
@@ -341,18 +360,23 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
     edge = hi;  // nothing is above it
     shift = 0;
   }
+  int listed = -1;  // keys in s_list: all that are still open (-1: no list yet)
   while (shift > 0) {
-    const int bits = min(8, shift);
-    const uint32_t above = shift < 32 ? (edge - lo) >> shift : 0u;
+    const int bits = min(8, shift), top = shift;
+    const uint32_t above = top < 32 ? (edge - lo) >> top : 0u;
     shift -= bits;
     if (tid < 256) s_hist[tid] = 0;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < rounds; ++i) {
-      bool in;
-      const uint32_t k = key_of(i, &in) - lo;
-      if (in && (shift + bits >= 32 || (k >> (shift + bits)) == above))
-        atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1);
+    auto digit = [&](uint32_t k) { atomicAdd(&s_hist[(k >> shift) & ((1u << bits) - 1u)], 1); };
+    if (listed >= 0) {
+      for (int e = tid; e < listed; e += kThreads)
+        if ((s_list[e] >> top) == above) digit(s_list[e]);
+    } else {
+      each([&](int i) {
+        bool in;
+        const uint32_t k = key_of(i, &in) - lo;
+        if (in && (top >= 32 || (k >> top) == above)) digit(k);
+      });
     }
     __syncthreads();
     if (warp == 0) {
@@ -375,71 +399,73 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
         if (before < want && want <= before + c[i]) {
           s_digit = 255 - 8 * lane - i;
           s_want = want - before;
-          s_all = want == before + c[i];
+          s_count = c[i];
         }
         before += c[i];
       }
+      if (lane == 0) s_n = 0;
     }
     __syncthreads();
     edge += (uint32_t)s_digit << shift;
     want = s_want;
-    if (s_all) {
-      // every key of this digit is taken: those from `edge` on.  (edge is a sum of
-      // digits below hi - lo, so edge - 1 wraps only for edge = lo = 0, where NaN
-      // is the lowest key and all are taken as equal or above.)
-      if (edge > 0u) {
-        --edge;
-        want = 0;
-        break;
-      }
+    const int open = s_count;  // keys with the digits of `edge` so far
+    if (want == open && edge > 0u) {
+      // all of them are taken: the keys from `edge` on.  (edge = 0 only where NaN
+      // is among the keys; it goes on digit by digit.)
+      --edge;
+      want = 0;
+      break;
+    }
+    if (listed < 0 && shift > 0 && open <= kList) {  // the later digits of these alone
+      const uint32_t now = (edge - lo) >> shift;
+      each([&](int i) {
+        bool in;
+        const uint32_t k = key_of(i, &in) - lo;
+        if (in && (k >> shift) == now) s_list[atomicAdd(&s_n, 1)] = k;
+      });
+      listed = open;
+      __syncthreads();
     }
   }
-  // write them in the pages' order, kRun rounds of pages at a time
+  // words of 32 pages in order: those above the edge (and the first and last
+  // pages), those equal to it
   int done = 0, equal = 0;
   for (int r0 = 0; r0 < rounds; r0 += kRun) {
-    uint32_t take = 0, eq = 0;  // bit i: round r0 + i
+    auto word = [&](int i) {
+      const int p = i * kThreads + tid;
+      bool in;
+      const uint32_t k = key_of(i, &in);
+      const uint32_t m = __ballot_sync(0xffffffffu, p < full && (!in || k > edge));
+      const uint32_t e = __ballot_sync(0xffffffffu, in && k == edge);
+      if (lane == 0) {
+        s_above[(i - r0) * kWarps + warp] = m;
+        s_equal[(i - r0) * kWarps + warp] = e;
+      }
+    };
+    if constexpr (kKeys > 0) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (i < rounds) word(i);
+    } else {
+      for (int i = r0; i < min(rounds, r0 + kRun); ++i) word(i);
+    }
+    __syncthreads();
+    const bool mine = tid < kRun * kWarps && r0 * kWarps + tid < rounds * kWarps;
+    uint32_t m = mine ? s_above[tid] : 0u, e = mine && want > 0 ? s_equal[tid] : 0u;
+    int sum;
     if (want > 0) {
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        bool in = false;
-        const uint32_t k = r0 + i < rounds ? key_of(r0 + i, &in) : 0u;
-        const bool e = in && k == edge;
-        const uint32_t m = __ballot_sync(0xffffffffu, e);
-        if (lane == 0) s_cnt[i * kWarps + warp] = __popc(m);
-        eq |= (e ? 1u : 0u) << i;
+      const int before = equal + cta_prefix<kWarps>(__popc(e), s_sum[0], &sum);
+      equal += sum;
+      for (int left = want - before; e != 0 && left > 0; --left) {  // the lowest of them
+        m |= e & (0u - e);
+        e &= e - 1u;
       }
-      __syncthreads();
-      if (warp == 0) scan_counts(s_cnt, kRun * kWarps);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const uint32_t m = __ballot_sync(0xffffffffu, (eq >> i) & 1u);
-        if (((eq >> i) & 1u) &&
-            equal + s_cnt[i * kWarps + warp] + __popc(m & ((1u << lane) - 1u)) < want)
-          take |= 1u << i;
-      }
-      equal += s_cnt[kRun * kWarps];
-      __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const int p = (r0 + i) * kThreads + tid;
-      bool in = false;
-      const uint32_t k = r0 + i < rounds ? key_of(r0 + i, &in) : 0u;
-      if (p < full && (in ? k > edge : true)) take |= 1u << i;
-      const uint32_t m = __ballot_sync(0xffffffffu, (take >> i) & 1u);
-      if (lane == 0) s_cnt[i * kWarps + warp] = __popc(m);
-    }
-    __syncthreads();
-    if (warp == 0) scan_counts(s_cnt, kRun * kWarps);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const uint32_t m = __ballot_sync(0xffffffffu, (take >> i) & 1u);
-      const int at = done + s_cnt[i * kWarps + warp] + __popc(m & ((1u << lane) - 1u));
-      if (((take >> i) & 1u) && at < n_pages) list[at] = (r0 + i) * kThreads + tid;
-    }
-    done += s_cnt[kRun * kWarps];
+    int at = done + cta_prefix<kWarps>(__popc(m), s_sum[1], &sum);
+    done += sum;
+    const int page0 = r0 * kThreads + tid * kWarp;
+    for (; m != 0; m &= m - 1u, ++at)
+      if (at < n_pages) list[at] = page0 + __ffs(m) - 1;
     if (r0 + kRun < rounds) __syncthreads();
   }
 }
@@ -514,6 +540,7 @@ cudaError_t page_select_launch(const SelectArgs& a, cudaStream_t st, int* launch
                         : n <= 8 * kSelThreads  ? launch_select<kSelThreads, 8>(a, st)
                         : n <= 16 * kSelThreads ? launch_select<kSelThreads, 16>(a, st)
                         : n <= 32 * kSelThreads ? launch_select<kSelThreads, 32>(a, st)
+                        : n <= 32 * 512         ? launch_select<512, 32>(a, st)
                         : n <= 32 * 1024        ? launch_select<1024, 32>(a, st)
                                                 : launch_select<1024, 0>(a, st);
   if (e == cudaSuccess) ++*launches;
