@@ -229,17 +229,24 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
 // one row share their exponents), then those above it and the first of those
 // equal to it are written in the pages' order.
 //
-// Keys stay in registers, page i * threads + t in thread t, so a row is read once.
-// What is left is a chain of some twenty barriers: 128 requests x 8 heads of 8192
-// pages at most, 18 MB: 9 us, one request 5 us, where four passes over memory with
-// the leading digits in few bins took 61 and 11.
+// Keys stay in shared memory, so a row is read once, and all passes go over it
+// with many warps an SM (keys in registers, 32 a thread: half the warps, unrolled
+// code past the instruction cache, 26 to 42 us where this takes 25).
+// What is left is a chain of some fifteen barriers and about 40 instructions a key:
+// 128 requests x 8 heads of 8192 pages at most, 18 MB: 25 us, one request 4.7 us,
+// where four passes over memory with the leading digits in few bins took 61 and 11.
 constexpr int kSelThreads = 256;
 
 __device__ __forceinline__ uint32_t order_key(float x) {
-  // -0 counts as 0; NaN as the lowest value of all
-  if (x != x) return 0u;
+  // -0 counts as 0; NaN as the lowest value of all (no number has a key of 0 or 1)
+  if (x != x) return 1u;
   const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// Bits 0 .. n - 1 of a word.
+__device__ __forceinline__ uint32_t first_bits(int n) {
+  return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
 // Exclusive prefix of one count per thread over the CTA (s: a place per warp and
@@ -266,16 +273,16 @@ __device__ __forceinline__ int cta_prefix(int own, int* s, int* sum) {
   return before + x - own;
 }
 
-// kKeys: keys of a thread (0: any number, read again for every pass).
-template <int kThreads, int kKeys>
+// kHeld: the keys fit shared memory (else they are read again for every pass).
+template <int kThreads, bool kHeld>
 __global__ void __launch_bounds__(kThreads) page_select_kernel(
     const float* scores, const int32_t* ctx_lens, int n_pages, int first, int last, spec_dims d,
     int32_t* __restrict__ pages, int32_t* __restrict__ counts, uint32_t* __restrict__ status) {
   constexpr int kWarps = kThreads / kWarp;
-  constexpr int kHeld = kKeys > 0 ? kKeys : 1;
-  constexpr int kRun = kKeys > 0 ? kKeys : 32;  // rounds of pages between two scans: at most
-                                                // one word of 32 pages a thread
+  constexpr int kRun = 32;    // rounds of pages between two scans: a word of 32 pages a thread
+  constexpr int kAtOnce = 8;  // loads of a thread on their way
   constexpr int kList = 1024;
+  extern __shared__ uint32_t s_keys[];  // 0 for pages that do not compete
   __shared__ int s_hist[256];
   __shared__ int s_digit, s_want, s_count, s_n;
   __shared__ uint32_t s_lo[kWarps], s_hi[kWarps];
@@ -287,12 +294,12 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
   pdl_trigger();
   pdl_wait();  // the scores and lengths may come from the previous kernels
   const float* x = scores + ((int64_t)b * d.Hkv + h) * d.max_blocks;
-  // all of the row's places are there: the loads need not wait for the length
-  float v[kHeld];
+  // all of the row's places are there: the first loads need not wait for the length
+  float v[kAtOnce];
 #pragma unroll
-  for (int i = 0; i < kKeys; ++i) {
+  for (int i = 0; i < kAtOnce; ++i) {
     const int p = i * kThreads + tid;
-    v[i] = p < d.max_blocks ? __ldcg(x + p) : 0.f;
+    v[i] = kHeld && p < d.max_blocks ? __ldcg(x + p) : 0.f;
   }
   const int ctx = __ldcg(ctx_lens + b);
   const bool fits = ctx <= (int64_t)d.max_blocks * kBlock;
@@ -312,44 +319,53 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
   const int c0 = first, c1 = full - last;
   int want = n_pages - first - last;
   const int rounds = ceil_div(full, kThreads);
-  // key of this thread's i-th page, and whether it competes
-  auto key_of = [&](int i, bool* in) {
+  auto make_key = [&](int i, float score) {
     const int p = i * kThreads + tid;
-    *in = p >= c0 && p < c1;
-    return *in ? order_key(kKeys > 0 ? v[i] : __ldcg(x + p)) : 0u;
+    return p >= c0 && p < c1 ? order_key(score) : 0u;
   };
-  // rounds of keys: unrolled where they are in registers
-  auto each = [&](auto body) {
-    if constexpr (kKeys > 0) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (i < rounds) body(i);
-    } else {
-      for (int i = 0; i < rounds; ++i) body(i);
-    }
+  // the key of this thread's i-th page
+  auto key_of = [&](int i) {
+    const int p = i * kThreads + tid;
+    if constexpr (kHeld) return s_keys[p];
+    else return make_key(i, p < full ? __ldcg(x + p) : 0.f);
   };
   uint32_t lo = 0xffffffffu, hi = 0;
-  int bad = 0;
-  each([&](int i) {
-    bool in;
-    const uint32_t k = key_of(i, &in);
-    if (in) {
-      lo = min(lo, k);
-      hi = max(hi, k);
-      bad |= k == 0u;
+  auto see = [&](uint32_t k) {
+    lo = min(lo, k - 1u);  // 0 becomes the largest value
+    hi = max(hi, k);
+  };
+  if constexpr (kHeld) {
+    for (int i0 = 0; i0 < rounds; i0 += kAtOnce) {
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int p = (i0 + i) * kThreads + tid;
+        if (i0 > 0) v[i] = p < full ? __ldcg(x + p) : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (i0 + i < rounds) {
+          const uint32_t k = make_key(i0 + i, v[i]);
+          s_keys[(i0 + i) * kThreads + tid] = k;
+          see(k);
+        }
     }
-  });
-  lo = __reduce_min_sync(0xffffffffu, lo);
+  } else {
+#pragma unroll 4
+    for (int i = 0; i < rounds; ++i) see(key_of(i));
+  }
+  const int bad = lo == 0u;
+  lo += 1u;
+  // (no competing page in this thread: lo wraps to 0)
+  lo = __reduce_min_sync(0xffffffffu, lo - 1u) + 1u;
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
     s_lo[warp] = lo;
     s_hi[warp] = hi;
   }
-  bad = __syncthreads_or(bad);
-  if (bad && tid == 0) raise_status(status, SPEC_ERR_NONFINITE);
+  if (__syncthreads_or(bad) && tid == 0) raise_status(status, SPEC_ERR_NONFINITE);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    lo = min(lo, s_lo[w]);
+    lo = min(lo - 1u, s_lo[w] - 1u) + 1u;
     hi = max(hi, s_hi[w]);
   }
   // Taken are the keys above `edge` and the first `want` of those equal to it.
@@ -372,11 +388,11 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
       for (int e = tid; e < listed; e += kThreads)
         if ((s_list[e] >> top) == above) digit(s_list[e]);
     } else {
-      each([&](int i) {
-        bool in;
-        const uint32_t k = key_of(i, &in) - lo;
-        if (in && (top >= 32 || (k >> top) == above)) digit(k);
-      });
+#pragma unroll 4
+      for (int i = 0; i < rounds; ++i) {
+        const uint32_t k = key_of(i);
+        if (k != 0u && (top >= 32 || ((k - lo) >> top) == above)) digit(k - lo);
+      }
     }
     __syncthreads();
     if (warp == 0) {
@@ -409,20 +425,18 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
     edge += (uint32_t)s_digit << shift;
     want = s_want;
     const int open = s_count;  // keys with the digits of `edge` so far
-    if (want == open && edge > 0u) {
-      // all of them are taken: the keys from `edge` on.  (edge = 0 only where NaN
-      // is among the keys; it goes on digit by digit.)
+    if (want == open) {  // all of them are taken: the keys from `edge` on (keys are above 0)
       --edge;
       want = 0;
       break;
     }
     if (listed < 0 && shift > 0 && open <= kList) {  // the later digits of these alone
       const uint32_t now = (edge - lo) >> shift;
-      each([&](int i) {
-        bool in;
-        const uint32_t k = key_of(i, &in) - lo;
-        if (in && (k >> shift) == now) s_list[atomicAdd(&s_n, 1)] = k;
-      });
+#pragma unroll 4
+      for (int i = 0; i < rounds; ++i) {
+        const uint32_t k = key_of(i);
+        if (k != 0u && ((k - lo) >> shift) == now) s_list[atomicAdd(&s_n, 1)] = k - lo;
+      }
       listed = open;
       __syncthreads();
     }
@@ -432,26 +446,24 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
   int done = 0, equal = 0;
   for (int r0 = 0; r0 < rounds; r0 += kRun) {
     auto word = [&](int i) {
-      const int p = i * kThreads + tid;
-      bool in;
-      const uint32_t k = key_of(i, &in);
-      const uint32_t m = __ballot_sync(0xffffffffu, p < full && (!in || k > edge));
-      const uint32_t e = __ballot_sync(0xffffffffu, in && k == edge);
+      const uint32_t k = key_of(i);
+      const uint32_t m = __ballot_sync(0xffffffffu, k > edge);
+      const uint32_t e = __ballot_sync(0xffffffffu, k == edge);
       if (lane == 0) {
         s_above[(i - r0) * kWarps + warp] = m;
         s_equal[(i - r0) * kWarps + warp] = e;
       }
     };
-    if constexpr (kKeys > 0) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (i < rounds) word(i);
-    } else {
-      for (int i = r0; i < min(rounds, r0 + kRun); ++i) word(i);
-    }
+#pragma unroll 4
+    for (int i = r0; i < min(rounds, r0 + kRun); ++i) word(i);
     __syncthreads();
     const bool mine = tid < kRun * kWarps && r0 * kWarps + tid < rounds * kWarps;
-    uint32_t m = mine ? s_above[tid] : 0u, e = mine && want > 0 ? s_equal[tid] : 0u;
+    const int page0 = r0 * kThreads + tid * kWarp;
+    uint32_t m = 0, e = 0;
+    if (mine) {
+      m = s_above[tid] | first_bits(c0 - page0) | (first_bits(full - page0) & ~first_bits(c1 - page0));
+      e = want > 0 ? s_equal[tid] : 0u;
+    }
     int sum;
     if (want > 0) {
       const int before = equal + cta_prefix<kWarps>(__popc(e), s_sum[0], &sum);
@@ -463,7 +475,6 @@ __global__ void __launch_bounds__(kThreads) page_select_kernel(
     }
     int at = done + cta_prefix<kWarps>(__popc(m), s_sum[1], &sum);
     done += sum;
-    const int page0 = r0 * kThreads + tid * kWarp;
     for (; m != 0; m &= m - 1u, ++at)
       if (at < n_pages) list[at] = page0 + __ffs(m) - 1;
     if (r0 + kRun < rounds) __syncthreads();
@@ -526,23 +537,29 @@ cudaError_t page_score_launch(const ScoreArgs& a, cudaStream_t st, int* launches
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int kThreads, int kKeys>
+constexpr int kSelMost = 48 * 1024;  // keys that fit shared memory
+
+template <int kThreads, bool kHeld>
 static cudaError_t launch_select(const SelectArgs& a, cudaStream_t st) {
-  PdlLaunch L(dim3(a.d.Hkv, a.d.B), dim3(kThreads), 0, st);
-  return cudaLaunchKernelEx(&L.cfg, page_select_kernel<kThreads, kKeys>, a.scores, a.ctx_lens,
-                            a.n_pages, a.first, a.last, a.d, a.pages, a.counts, a.status);
+  auto k = page_select_kernel<kThreads, kHeld>;
+  // whole rounds of the threads
+  const size_t smem = kHeld ? sizeof(uint32_t) * ceil_div(a.d.max_blocks, kThreads) * kThreads : 0;
+  if (kHeld) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)(sizeof(uint32_t) * kSelMost));
+    if (e != cudaSuccess) return e;
+  }
+  PdlLaunch L(dim3(a.d.Hkv, a.d.B), dim3(kThreads), smem, st);
+  return cudaLaunchKernelEx(&L.cfg, k, a.scores, a.ctx_lens, a.n_pages, a.first, a.last, a.d,
+                            a.pages, a.counts, a.status);
 }
 
 cudaError_t page_select_launch(const SelectArgs& a, cudaStream_t st, int* launches) {
-  // the smallest instance whose registers hold the longest row
+  // few threads a row where there are many rows' worth of warps anyway
   const int n = a.d.max_blocks;
-  const cudaError_t e = n <= 4 * kSelThreads    ? launch_select<kSelThreads, 4>(a, st)
-                        : n <= 8 * kSelThreads  ? launch_select<kSelThreads, 8>(a, st)
-                        : n <= 16 * kSelThreads ? launch_select<kSelThreads, 16>(a, st)
-                        : n <= 32 * kSelThreads ? launch_select<kSelThreads, 32>(a, st)
-                        : n <= 32 * 512         ? launch_select<512, 32>(a, st)
-                        : n <= 32 * 1024        ? launch_select<1024, 32>(a, st)
-                                                : launch_select<1024, 0>(a, st);
+  const cudaError_t e = n <= 16 * 1024    ? launch_select<kSelThreads, true>(a, st)
+                        : n <= kSelMost   ? launch_select<1024, true>(a, st)
+                                          : launch_select<1024, false>(a, st);
   if (e == cudaSuccess) ++*launches;
   return e != cudaSuccess ? e : cudaGetLastError();
 }

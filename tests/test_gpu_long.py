@@ -399,7 +399,7 @@ def select_check(x, ctx, n, first, last, status=0):
 
 SELECT = [(1, 1, 1, 0, 0), (1, 40, 1, 1, 0), (3, 40, 5, 1, 2), (2, 300, 64, 1, 4), (5, 256, 17, 0, 17),
           (2, 257, 16, 16, 0), (3, 1000, 999, 3, 5), (2, 3000, 100, 0, 0), (2, 9000, 1000, 4, 17),
-          (1, 40000, 33, 1, 1), (4, 20, 500, 2, 3)]
+          (1, 40000, 33, 1, 1), (4, 20, 500, 2, 3), (1, 17000, 12000, 1, 1), (1, 60000, 700, 2, 5)]
 
 
 @pytest.mark.parametrize("B,mb,n,first,last", SELECT)
