@@ -155,6 +155,27 @@ spec_status spec_get_device_status(void* ws, void* stream, int32_t* flags, int32
   return SPEC_OK;
 }
 
+// Whether every request reads a shared prefix itself (its pages come from L2 after
+// the first), rather than one pass over it for the batch with a merge after it.
+// The pass and the merge cost 10 to 25 us, the other grows with the requests.
+// Measured, us, requests / one pass (B, Hkv, group, M, prefix):
+//   tensor cores, by B * Hkv * prefix: 262144 keys 39 / 42 (4, 8, 4, 1, 8192), 38 / 47
+//   (16, 8, 4, 5, 2048), 46 / 52 (64, 8, 8, 1, 512); 524288 64 / 62 (64, 1, 4, 9,
+//   8192); 786432 81 / 60 (4, 8, 4, 1, 24576), 78 / 76 (16, 2, 8, 1, 24576)
+//   fp32 on CUDA cores, where the products cost too, by keys times rows per KV head:
+//   0.52 M 33 / 41 (16, 2, 8, 1, 2048), 1.05 M 69 / 61 (8, 4, 1, 64, 512), 66 / 81 (4,
+//   8, 4, 1, 8192), 1.3 M 53 / 49 (16, 8, 4, 5, 512), 2.1 M 89 / 55 (64, 8, 8, 1, 512)
+//   bf16 heads of 64, the pass on tensor cores and the rest on CUDA cores, likewise:
+//   66 K 21 / 22 (1, 8, 4, 1, 2048), 23 / 21 (4, 8, 4, 1, 512), 131 K 42 / 33 (4, 1, 8, 8,
+//   512), 0.52 M 33 / 28 (16, 2, 8, 1, 2048)
+static bool prefix_in_requests(const spec_dims& d, int prefix_len, bool tc) {
+  const int64_t keys = (int64_t)d.B * d.Hkv * prefix_len;
+  if (tc) return keys <= 400000;
+  const int64_t products = keys * (d.Hq / d.Hkv) * d.M;
+  if (d.attn_impl != SPEC_ATTN_CUDA_CORES && prefix_tc_ok(d)) return products <= 100000;
+  return d.B == 1 || products <= 800000;
+}
+
 static spec_status attn_common(const void* q, const void* k_new, const void* v_new, void* k_cache,
                                void* v_cache, const int32_t* block_table, const int32_t* ctx_lens,
                                const int32_t* parent, int32_t window, int32_t sinks,
@@ -192,6 +213,8 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
   } else {
     return SPEC_ERR_INVALID_ARG;
   }
+  if (view.mode == kViewPrefix && prefix_in_requests(*dims, view.prefix_len, use_tc))
+    view.mode = kViewWhole;
   const WsLayout lay = workspace_layout(*dims);
   AttnArgs a;
   a.q = q;
@@ -219,6 +242,11 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
       a.view.stride_b = dims->max_blocks;
       a.view.stride_h = 0;
       a.view.entries = dims->max_blocks - pp;
+    } else if (view.mode == kViewWhole) {
+      a.view.table = reinterpret_cast<int32_t*>(w + lay.view_table_off);
+      a.view.stride_b = dims->max_blocks;
+      a.view.stride_h = 0;
+      a.view.entries = dims->max_blocks;
     } else {
       // the selected pages, then those of the context's last partial page and
       // the new rows; together no more than the context and the new rows have
@@ -289,7 +317,9 @@ spec_status spec_verify_attn_pages(const void* q, const void* k_new, const void*
                                    size_t ws_bytes, void* stream) {
   g_launches = 0;
   if (dims == nullptr || !pages || !counts || n_pages < 1) return SPEC_ERR_INVALID_ARG;
-  if ((int64_t)dims->max_blocks * kBlock > INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
+  if ((int64_t)dims->max_blocks * kBlock > INT32_MAX / 2 ||
+      (int64_t)dims->max_blocks * dims->Hkv > INT32_MAX / 2)
+    return SPEC_ERR_UNSUPPORTED;
   AttnView v = {};
   v.mode = kViewPages;
   v.pages = pages;

@@ -12,10 +12,13 @@ namespace specv {
 //   kViewPrefix  the first prefix_len positions are the batch's shared prefix
 //                and read elsewhere: ctx is less by prefix_len, the table starts
 //                prefix_len / 16 entries later
+//   kViewWhole   the same requests where reading the prefix once is not worth a
+//                pass of its own: ctx as it is, the request check writes a table
+//                of the shared pages and the request's own
 //   kViewPages   the selected whole pages of each KV head, then the pages from
 //                the last (partial) one of the context on; the request check
 //                writes a table of block ids for every KV head
-enum { kViewNone = 0, kViewPrefix = 1, kViewPages = 2 };
+enum { kViewNone = 0, kViewPrefix = 1, kViewWhole = 2, kViewPages = 3 };
 struct AttnView {
   int mode;
   const int32_t* prefix_table;  // [prefix_len / 16]
@@ -26,11 +29,12 @@ struct AttnView {
   const int32_t* table;   // block of page p of the view: table[b * stride_b + h * stride_h + p]
   int64_t stride_b, stride_h;
   int entries;            // pages of a view at most
-  int32_t* ctx;           // [B] cached keys of the views
+  int32_t* ctx;           // [B] cached keys of the views (CUDA cores)
 };
 // Cached keys of a request's view (the request itself has been checked).
 __device__ __forceinline__ int view_ctx(const AttnView& v, int b, int ctx) {
   if (v.mode == kViewPrefix) return ctx - v.prefix_len;
+  if (v.mode == kViewWhole) return ctx;
   return __ldcg(v.counts + b) * kBlock + ctx % kBlock;
 }
 
@@ -100,39 +104,55 @@ __device__ __forceinline__ void win_row_mask(const int32_t* par, int n, int ctx,
 // Checks of a view that needs the whole CTA (the request's length has been
 // checked): bit 0 a bad argument, bit 1 a bad block id among the pages that the
 // view holds, for this thread's share.  `write`: the table of block ids is
-// written (kViewPages; entries that are no block id stay out of it).
+// written (kViewWhole and kViewPages; entries that are no block id stay out of it).
 __device__ __forceinline__ int view_check(const AttnView& v, const spec_dims& d, const int32_t* bt,
                                           int b, int ctx, bool write) {
   const int pages = (int)ceil_div64((int64_t)ctx + d.M, kBlock);
   int bad = 0;
-  if (v.mode == kViewPrefix) {
+  int32_t* table = const_cast<int32_t*>(v.table) + (int64_t)b * v.stride_b;
+  if (v.mode != kViewPages) {
     if (ctx < v.prefix_len) return 1;
     const int pp = v.prefix_len / kBlock;
 #pragma unroll 4
     for (int p = threadIdx.x; p < pages; p += blockDim.x) {
       const int id = __ldcg(p < pp ? v.prefix_table + p : bt + p);
       if (id < 0 || id >= d.num_blocks) bad |= 2;
+      else if (write && v.mode == kViewWhole) table[p] = id;
     }
     return bad;
   }
   const int n = __ldcg(v.counts + b), full = ctx / kBlock;
   if (n < 0 || n > v.n_pages || n > full) return 1;
-  int32_t* table = const_cast<int32_t*>(v.table) + (int64_t)b * v.stride_b;
   const int len = n + pages - full;  // pages of the view: at most `pages`
-  for (int e = threadIdx.x; e < d.Hkv * len; e += blockDim.x) {
-    const int h = e / len, j = e - h * len;
-    int p = full + j - n;
-    if (j < n) {
-      const int32_t* list = v.pages + ((int64_t)b * d.Hkv + h) * v.n_pages + j;
-      p = __ldcg(list);
-      if (p < 0 || p >= full || (j > 0 && __ldcg(list - 1) >= p)) {
-        bad |= 1;
-        continue;
+  constexpr int kAtOnce = 4;  // chains of loads (list, block table) of a thread side by side
+  for (int e0 = threadIdx.x; e0 < d.Hkv * len; e0 += kAtOnce * blockDim.x) {
+    int p[kAtOnce], before[kAtOnce], id[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int e = e0 + u * blockDim.x, h = e / len, j = e - h * len;
+      p[u] = full + j - n;
+      before[u] = -1;
+      if (j < n && h < d.Hkv) {
+        const int32_t* list = v.pages + ((int64_t)b * d.Hkv + h) * v.n_pages + j;
+        p[u] = __ldcg(list);
+        if (j > 0) before[u] = __ldcg(list - 1);
       }
     }
-    const int id = __ldcg(bt + p);
-    if (id < 0 || id >= d.num_blocks) bad |= 2;
-    else if (write) table[h * v.stride_h + j] = id;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int e = e0 + u * blockDim.x, h = e / len, j = e - h * len;
+      id[u] = 0;
+      if (h >= d.Hkv) continue;
+      if (j < n && (p[u] < 0 || p[u] >= full || before[u] >= p[u])) bad |= 1;
+      else id[u] = __ldcg(bt + p[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int e = e0 + u * blockDim.x, h = e / len, j = e - h * len;
+      if (h >= d.Hkv) continue;
+      if (id[u] < 0 || id[u] >= d.num_blocks) bad |= 2;
+      else if (write) table[h * v.stride_h + j] = id[u];
+    }
   }
   return bad;
 }
@@ -153,7 +173,8 @@ struct PrefixPlan {
 };
 // The CTA of plan p that runs item x.
 __host__ __device__ __forceinline__ int prefix_cta(const PrefixPlan& p, int64_t items, int64_t x) {
-  return (int)(((x + 1) * p.ctas - 1) / items);
+  const int64_t n = (x + 1) * p.ctas - 1;
+  return (n | items) >> 32 == 0 ? (int)((uint32_t)n / (uint32_t)items) : (int)(n / items);
 }
 
 // What the merge needs of the attention over a request's own keys.

@@ -28,7 +28,10 @@ namespace specv {
 // transposed in shared memory, so that a thread's 8 rows are two 16-byte loads
 // that 16 lanes share.  fp32 throughout, two rows a packed FMA.
 constexpr int kPfxRows = 64, kPfxThreads = 128;
-constexpr int kPfxSlots = 4 * 152;  // ranges of all units together, at least the units
+// Ranges of all units together, at least the units: one wave of the CTAs that an
+// SM holds (16 requests of 16 rows, 8 heads of 64, 2000 positions in 608 ranges, a
+// third of them in a second wave: 46 us for the kernel).
+__host__ __device__ constexpr int pfx_slots(int D) { return (D == 64 ? 3 : 2) * 152; }
 
 template <int D>
 struct PfxTile {
@@ -241,60 +244,65 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_simt_kernel(
 // ---------------------------------------------------------------------------
 // merge
 // ---------------------------------------------------------------------------
-// A warp per row: the log2-sum-exps of its partials first, then their outputs
-// with the weights that these give.
+// A warp per row: a lane has the log2-sum-exp of a partial, then all have columns
+// of the outputs and the lanes' weights in turn.
 template <typename T>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(
     OwnPart own, const float* prefix, PrefixPlan plan, int64_t items, spec_dims d,
     T* __restrict__ out, float* __restrict__ lse) {
   pdl_trigger();
-  pdl_wait();  // the partials come from the previous kernels
   const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
   const int h = blockIdx.y, D = d.D;
   const int group = d.Hq / d.Hkv, R = group * d.M;
-  const int64_t gr = (int64_t)blockIdx.x * (blockDim.x / kWarp) + warp;
-  if (gr >= (int64_t)d.B * R) return;
-  const int b = (int)(gr / R), r = (int)(gr - (int64_t)b * R), i = r / group;
+  const int64_t gr64 = (int64_t)blockIdx.x * (blockDim.x / kWarp) + warp;
+  if (gr64 >= (int64_t)d.B * R) return;
+  const int gr = (int)gr64;  // B and R have 16 and 8 bits at most
+  const int b = gr / R, r = gr - b * R, i = r / group;
   const int64_t at = ((int64_t)b * d.M + i) * d.Hq + h * group + r - i * group;
+  const int tile = gr / plan.tile;
+  const int64_t unit = (int64_t)h * plan.tiles + tile;
+  const int S = tc_part_stride(D);
+  int64_t slot = unit * plan.splits;
+  int n_pfx = plan.splits;
+  if (plan.ctas > 0) {
+    const int c0 = prefix_cta(plan, items, unit * plan.key_tiles);
+    slot = unit + c0;
+    n_pfx = prefix_cta(plan, items, (unit + 1) * plan.key_tiles - 1) - c0 + 1;
+  }
+  const int own_step = R * own.stride, pfx_step = plan.tile * S;
+  const float* own_row = own.part + (((int64_t)b * d.Hkv + h) * own.splits * R + r) * own.stride;
+  const float* pfx_row = prefix + slot * pfx_step + (int64_t)(gr - tile * plan.tile) * S;
+  pdl_wait();  // the partials come from the previous kernels
+  const int ok = __ldcg(own.ok + b);
+  const int n_own = own.splits == 1 ? 1 : ceil_div(__ldcg(own.ctx + b) + d.M, own.split_keys);
   T* orow = out + at * D;
-  if (!__ldcg(own.ok + b)) {  // the request has failed its checks
+  if (!ok) {  // the request has failed its checks
     for (int c = lane; c < D; c += kWarp) orow[c] = from_f32<T>(0.f);
     if (lse != nullptr && lane == 0) lse[at] = -INFINITY;
     return;
   }
-  const int n_own = own.splits == 1 ? 1 : ceil_div(__ldcg(own.ctx + b) + d.M, own.split_keys);
-  const int64_t own_step = (int64_t)R * own.stride;
-  const float* own_row = own.part + (((int64_t)b * d.Hkv + h) * own.splits * R + r) * own.stride;
-  const int tile = (int)(gr / plan.tile);
-  const int64_t unit = (int64_t)h * plan.tiles + tile;
-  const int S = tc_part_stride(D);
-  int64_t slot;
-  int n_pfx;
-  if (plan.ctas > 0) {
-    const int c0 = prefix_cta(plan, items, unit * plan.key_tiles);
-    const int c1 = prefix_cta(plan, items, (unit + 1) * plan.key_tiles - 1);
-    slot = unit + c0;
-    n_pfx = c1 - c0 + 1;
-  } else {
-    slot = unit * plan.splits;
-    n_pfx = plan.splits;
-  }
-  const int64_t pfx_step = (int64_t)plan.tile * S;
-  const float* pfx_row = prefix + slot * pfx_step + (gr - (int64_t)tile * plan.tile) * S;
-  const int n = n_own + n_pfx;
-  auto row_of = [&](int s) { return s < n_own ? own_row + s * own_step : pfx_row + (s - n_own) * pfx_step; };
-  float mx = -INFINITY;
-  for (int s = lane; s < n; s += kWarp) mx = fmaxf(mx, __ldcg(row_of(s) + D));
-  mx = warp_max(mx);
-  float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const float* p = row_of(s);
-    const float w = exp2f(__ldcg(p + D) - mx);
-    sum += w;
+  float mx = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  auto row_of = [&](int s) {
+    return s < n_own ? own_row + (int64_t)s * own_step : pfx_row + (int64_t)(s - n_own) * pfx_step;
+  };
+  for (int s0 = 0; s0 < n_own + n_pfx; s0 += kWarp) {
+    const int n = min(kWarp, n_own + n_pfx - s0);
+    const float l = lane < n ? __ldcg(row_of(s0 + lane) + D) : -INFINITY;
+    const float mn = fmaxf(mx, warp_max(l));
+    const float w = mn == -INFINITY ? 0.f : exp2f(l - mn);
+    const float a = mx == -INFINITY ? 0.f : exp2f(mx - mn);
+    sum = sum * a + warp_sum(w);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c * kWarp < D) acc[c] = fmaf(w, __ldcg(p + lane + c * kWarp), acc[c]);
+    for (int c = 0; c < 4; ++c) acc[c] *= a;
+    mx = mn;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float* p = row_of(s0 + s) + lane;
+      const float ws = __shfl_sync(0xffffffffu, w, s);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c * kWarp < D) acc[c] = fmaf(ws, __ldcg(p + c * kWarp), acc[c]);
+    }
   }
   const float inv = 1.f / sum;
 #pragma unroll
@@ -315,7 +323,7 @@ static PrefixPlan simt_plan(const spec_dims& d, int prefix_len) {
   p.key_tiles = ceil_div(prefix_len, keys);
   p.ctas = 0;
   const int64_t units = (int64_t)d.Hkv * p.tiles;
-  int64_t splits = kPfxSlots / units;
+  int64_t splits = pfx_slots(d.D) / units;
   if (splits > p.key_tiles) splits = p.key_tiles;
   p.splits = splits < 1 ? 1 : (int)splits;
   return p;
@@ -324,7 +332,7 @@ static PrefixPlan simt_plan(const spec_dims& d, int prefix_len) {
 size_t prefix_part_floats(const spec_dims& d) {
   const int64_t rows = (int64_t)d.B * (d.Hq / d.Hkv) * d.M;
   const int64_t units = (int64_t)d.Hkv * ceil_div64(rows, kPfxRows);
-  const int64_t slots = units > kPfxSlots ? units : kPfxSlots;
+  const int64_t slots = units > pfx_slots(d.D) ? units : pfx_slots(d.D);
   const size_t simt = (size_t)slots * (size_t)(rows < kPfxRows ? rows : kPfxRows) * tc_part_stride(d.D);
   const size_t tc = prefix_tc_part_floats(d);
   return simt > tc ? simt : tc;

@@ -147,6 +147,17 @@ def test_prefix(ctx, P, M, Hq, Hkv, D, dt, tree, impl):
     prefix_step(ctx, P, M, Hq, Hkv, D, dt, P + M, tree=tree, impl=impl)
 
 
+@pytest.mark.parametrize("ctx,P,M,Hq,Hkv,D,dt,impl", [
+    ([12800 + 7 * b for b in range(17)], 12800, 2, 14, 2, 128, BF, TC),     # one pass, 119 rows
+    ([8208] * 50, 8208, 1, 8, 1, 128, BF, TC),                              # 400 rows of a head
+    ([8000 + b for b in range(60)], 8000, 5, 1, 1, 128, BF, TC),            # a third unit's tile
+    ([4000 + 3 * b for b in range(3)], 4000, 40, 6, 2, 64, BF, AUTO),
+    ([16400 + 3 * b for b in range(13)], 16400, 2, 3, 3, 128, F32, AUTO)])
+def test_prefix_in_one_pass(ctx, P, M, Hq, Hkv, D, dt, impl):
+    """Sizes at which the prefix is read once in a pass of its own."""
+    prefix_step(ctx, P, M, Hq, Hkv, D, dt, 4, impl=impl)
+
+
 @pytest.mark.parametrize("impl", [CORES, TC])
 def test_prefix_batches_of_many_rows(impl):
     """257 requests, rows that fill tiles unevenly."""
