@@ -195,6 +195,65 @@ def test_prefix_requests_that_fail(dt, D, impl):
     assert torch.all(st.out[3] == 0) and torch.all(torch.isfinite(st.lse[:3]))
 
 
+@pytest.mark.parametrize("dt,D,M,Hq", [(BF, 128, 4, 4), (BF, 64, 2, 6), (F32, 64, 4, 2)])
+def test_prefix_in_one_pass_requests_that_fail(dt, D, M, Hq):
+    """Failing requests among others where the prefix has a pass of its own."""
+    P, B = 3216, 64
+    st = Step([P + 3 * b for b in range(B)], M, Hq, 2, D, dt, 9, shared=P // 16, tree=True)
+    ctx, table = st.ctx.copy(), st.table.copy()
+    ctx[3], ctx[17], ctx[40] = P - 1, -1, 16 * st.mb - M + 1
+    table[B - 1, P // 16] = -5
+    st.parent[30, 1] = 1
+    before = (st.kc.clone(), st.vc.clone())
+    assert st.call(table=table, ctx=ctx, prefix=to_dev(st.shared, I32)) == INVALID | CAPACITY | BAD_ID
+    bad = np.isin(np.arange(B), [3, 17, 30, 40, B - 1])
+    assert torch.all(st.out[torch.from_numpy(bad)] == 0)
+    assert torch.all(st.lse[torch.from_numpy(bad)] == -float("inf"))
+    live = ~bad
+    args = (st.q[live], st.k, st.v, st.table[live], st.ctx[live], st.kn[live])
+    ref = oracle_verify_attn(*args, st.vn[live], parent=st.parent[live])
+    size = oracle_verify_attn(*args[:2], np.abs(st.v), *args[3:], np.abs(st.vn[live]),
+                              parent=st.parent[live])[0]
+    keep = torch.from_numpy(live).cuda()
+    st.out, st.lse = st.out[keep], st.lse[keep]
+    st.check(ref, size)
+    st.check_cache(ref)
+    shared = st.shared.copy()
+    shared[-1] = st.nb
+    st.kc.copy_(before[0])
+    st.vc.copy_(before[1])
+    assert st.call(prefix=to_dev(shared, I32)) & BAD_ID
+    assert torch.all(st.out == 0) and torch.all(st.lse == -float("inf"))
+    assert torch.equal(st.kc, before[0]) and torch.equal(st.vc, before[1])
+
+
+@pytest.mark.parametrize("dt,D", [(BF, 128), (F32, 64)])
+def test_prefix_scores_that_grow(dt, D):
+    """Keys whose scores grow along the prefix, far and in steps, so that the
+    running maximum moves in every tile, and a row of queries that are zero."""
+    P, B = 3216, 64
+    st = Step([P + b for b in range(B)], 4, 8, 2, D, dt, 5, shared=P // 16)
+    lift = np.zeros((st.nb, 2, 16, 1))
+    for j, blk in enumerate(st.shared):
+        lift[blk] = (16 * j + np.arange(16)[:, None]) / P
+    st.k = typed((st.k * 0.1 + lift * 6.0 * np.sign(st.q[0, 0, ::4])[None, :, None, :]).astype(np.float32), dt)
+    st.q = typed((st.q * 0.3 + 0.7 * np.sign(st.q[0, 0, ::4]).repeat(4, 0)).astype(np.float32), dt)
+    st.q[3, 1, 5] = 0
+    st.kc = to_dev(st.k, dt)
+    assert st.call(prefix=to_dev(st.shared, I32)) == 0
+    args = (st.q, st.k, st.v, st.table, st.ctx, st.kn)
+    ref = oracle_verify_attn(*args, st.vn)
+    size = oracle_verify_attn(*args[:2], np.abs(st.v), *args[3:], np.abs(st.vn))[0]
+    err = np.abs(st.out.double().cpu().numpy() - ref[0])
+    # scores up to s = 6 * 0.7 * 128 / sqrt(128) = 48 and more: fp32 sums of D terms
+    # are off by D * 2^-24 of them, and so are the weights, relatively
+    s = np.abs(ref[1]).max() + 10
+    w = 2 * D * 2.0 ** -24 * s * 4
+    tol = (2.0 ** -8 * 1.02 * (size + np.abs(ref[0])) if dt == BF else 0) + w * size + 2.0 ** -16
+    assert np.all(err <= tol), float((err / tol).max())
+    assert np.max(np.abs(st.lse.cpu().numpy() - ref[1])) <= w + 1e-5
+
+
 def test_prefix_agrees_with_the_plain_call_and_itself():
     """The same numbers as without the sharing up to roundings, the same bits
     from the same call twice, and without an lse."""
@@ -505,6 +564,36 @@ def test_decoding_over_selected_pages(dt, D, impl):
         assert np.array_equal(ctx.cpu().numpy(), st.ctx)
 
 
+@pytest.mark.parametrize("dt,D", [(BF, 128), (BF, 64), (F32, 64)])
+def test_prefix_in_one_pass_captured(dt, D):
+    """The pass of its own in a graph, the prefix' pages and lengths replaced."""
+    P, B = 3216, 64
+    st = Step([P + b % 9 for b in range(B)], 2, 4, 2, D, dt, 5, shared=P // 16)
+    q, kn, vn = (to_dev(x, dt) for x in (st.q, st.kn, st.vn))
+    table, ctx, shared = (to_dev(x, I32) for x in (st.table, st.ctx, st.shared))
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.spec_verify_attn(q, kn, vn, st.kc, st.vc, table, ctx, None, out, lse, st.dims, st.ws,
+                            prefix=shared)
+    for turn in range(2):
+        if turn:
+            st.shared = st.shared[::-1].copy()
+            st.table[:, :P // 16] = st.shared
+            shared.copy_(to_dev(st.shared, I32))
+            st.ctx = np.minimum(st.ctx, P + 5)
+            ctx.copy_(to_dev(st.ctx, I32))
+        st.kc.copy_(to_dev(st.k, dt))
+        st.vc.copy_(to_dev(st.v, dt))
+        g.replay()
+        args = (st.q, st.k, st.v, st.table, st.ctx, st.kn)
+        ref = oracle_verify_attn(*args, st.vn)
+        size = oracle_verify_attn(*args[:2], np.abs(st.v), *args[3:], np.abs(st.vn))[0]
+        st.out, st.lse = out, lse
+        st.check(ref, size)
+        st.check_cache(ref)
+
+
 @pytest.mark.parametrize("form", ["prefix", "pages"])
 @pytest.mark.parametrize("dt,D", [(BF, 128), (F32, 64)])
 def test_captured_and_replayed(form, dt, D):
@@ -544,6 +633,80 @@ def test_captured_and_replayed(form, dt, D):
         st.out, st.lse = out[live], lse[live]
         st.check(ref, size)
         st.check_cache(ref)
+
+
+def test_waits_that_run_out():
+    """A wait limit of 1000 clocks: the calls end, with their results or with the
+    status of a wait that gave up, and after the workspace is zeroed they are right."""
+    st = Step([3216 + b for b in range(64)], 4, 8, 2, 128, BF, 5, shared=201)
+    full = st.dims
+    args = (st.q, st.k, st.v, st.table, st.ctx, st.kn)
+    ref = oracle_verify_attn(*args, st.vn)
+    size = oracle_verify_attn(*args[:2], np.abs(st.v), *args[3:], np.abs(st.vn))[0]
+    pair = typed(np.sort(st.rng.standard_normal((st.nb, 2, 2, 128)), axis=2).astype(np.float32), BF)
+    scores = torch.empty(64, 2, st.mb, device="cuda")
+    want, s = oracle_page_score(st.q, pair, st.table, st.ctx)
+    there = np.isfinite(want)
+    for limit in (1, 0):
+        st.dims = sv.make_dims(B=64, M=4, Hq=8, Hkv=2, D=128, max_blocks=st.mb, num_blocks=st.nb,
+                               kv_dtype=BF, wait_limit_kcycles=limit)
+        st.ws.zero_()
+        status = st.call(prefix=to_dev(st.shared, I32))
+        assert status in (0, 1 << 7) and (limit == 1 or status == 0)
+        if status == 0:
+            st.check(ref, size)
+        st.ws.zero_()
+        sv.spec_page_score(to_dev(st.q, BF), to_dev(pair, BF), to_dev(st.table, I32),
+                           to_dev(st.ctx, I32), scores, st.dims, st.ws)
+        status = sv.device_status(st.ws)
+        assert status in (0, 1 << 7) and (limit == 1 or status == 0)
+        if status == 0:
+            got = scores.double().cpu().numpy()
+            assert np.all(np.abs(got[there] - want[there]) <= 2 * 128 * 2.0 ** -24 * s[there])
+    st.dims = full
+
+
+def test_calls_on_two_streams():
+    """Bounds, scores and selection of two batches side by side share a workspace;
+    the attention forms have one each."""
+    steps = [Step([900 + 40 * b for b in range(9)], 3, 4, 2, 128, BF, seed, shared=4) for seed in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    inputs = [[to_dev(x, BF) for x in (st.q, st.kn, st.vn)] +
+              [to_dev(x, I32) for x in (st.table, st.ctx, st.shared)] for st in steps]
+    outs = [dict(bounds=torch.zeros(st.nb, 2, 2, 128, dtype=BF, device="cuda"),
+                 scores=torch.empty(9, 2, st.mb, device="cuda"),
+                 pages=torch.empty(9, 2, 7, dtype=I32, device="cuda"),
+                 counts=torch.empty(9, dtype=I32, device="cuda"),
+                 out=torch.empty_like(i[0]), lse=torch.empty(9, 3, 4, device="cuda"),
+                 out2=torch.empty_like(i[0]), lse2=torch.empty(9, 3, 4, device="cuda"))
+            for st, i in zip(steps, inputs)]
+    torch.cuda.synchronize()
+    for turn in range(5):
+        for st, s, i, o in zip(steps, streams, inputs, outs):
+            q, kn, vn, table, ctx, shared = i
+            sv.spec_page_bounds(st.kc, table, None, ctx, o["bounds"], st.dims, ws, stream=s)
+            sv.spec_page_score(q, o["bounds"], table, ctx, o["scores"], st.dims, ws, stream=s)
+            sv.spec_page_select(o["scores"], ctx, o["pages"], o["counts"], st.dims, ws, first=1,
+                                last=1, stream=s)
+            sv.spec_verify_attn(q, kn, vn, st.kc, st.vc, table, ctx, None, o["out"], o["lse"], st.dims,
+                                st.ws, pages=o["pages"], page_counts=o["counts"], stream=s)
+            sv.spec_verify_attn(q, kn, vn, st.kc, st.vc, table, ctx, None, o["out2"], o["lse2"],
+                                st.dims, st.ws, prefix=shared, stream=s)
+    torch.cuda.synchronize()
+    assert sv.device_status(ws) == 0
+    for st, o in zip(steps, outs):
+        want = oracle_page_bounds(st.k, st.table, None, st.ctx, np.zeros(o["bounds"].shape))
+        assert np.array_equal(o["bounds"].double().cpu().numpy(), want)
+        sel, cnt = oracle_page_select(o["scores"].double().cpu().numpy(), st.ctx, 7, 1, 1)
+        assert np.array_equal(o["pages"].cpu().numpy(), sel)
+        args = (st.q, st.k, st.v, st.table, st.ctx, st.kn)
+        sizes = (st.q, st.k, np.abs(st.v), st.table, st.ctx, st.kn)
+        st.out, st.lse = o["out"], o["lse"]
+        st.check(oracle_verify_attn_pages(*args, st.vn, sel, cnt),
+                 oracle_verify_attn_pages(*sizes, np.abs(st.vn), sel, cnt)[0])
+        st.out, st.lse = o["out2"], o["lse2"]
+        st.check(oracle_verify_attn(*args, st.vn), oracle_verify_attn(*sizes, np.abs(st.vn))[0])
 
 
 def test_forms_take_turns_on_one_workspace():
