@@ -247,7 +247,7 @@ spec_status spec_verify_attn_window(const void* q, const void* k_new, const void
  * prefix_len fails (SPEC_ERR_INVALID_ARG: caches untouched, out = 0, lse = -inf),
  * and so does every request if an entry of prefix_table is no block id
  * (SPEC_ERR_DEVICE_BOUNDS).  The shared pages are never written: the pages that
- * the new rows go to must not be among them.
+ * the new rows go to must not be among them.  dims->softmax_scale is not negative.
  */
 spec_status spec_verify_attn_prefix(const void* q, const void* k_new, const void* v_new,
                                     void* k_cache, void* v_cache, const int32_t* block_table,
@@ -275,8 +275,9 @@ spec_status spec_verify_attn_prefix(const void* q, const void* k_new, const void
  *   bounds [num_blocks, Hkv, 2, D] kv_dtype (in/out)   minima, then maxima,
  *                 per block; other blocks keep theirs
  *   ws, ws_bytes  at least 16 bytes (its first word is the status word)
- * After kv_commit, from_lens are the context lengths before the step.  Blocks
- * that several requests share may be met by several.  Keys have to be finite.
+ * After kv_commit, from_lens are the context lengths before the step.  Whole
+ * blocks that several requests share may be met by several.  Keys have to be
+ * finite.
  * A request with a negative from_lens (SPEC_ERR_INVALID_ARG) or ctx_lens past
  * its table (SPEC_ERR_CAPACITY) is left out; so is a page whose entry is no
  * block id (SPEC_ERR_DEVICE_BOUNDS).
@@ -311,9 +312,9 @@ spec_status spec_page_score(const void* q, const void* bounds, const int32_t* bl
  * and then those of largest score, the lower page first among equal scores,
  * until there are n_pages (all F if there are no more than that).
  *   scores [B, Hkv, max_blocks] float   those of pages from F on are not read;
- *                 -0 equals 0; NaN counts as the lowest value
- *                 (SPEC_ERR_NONFINITE)
- *   n_pages >= 1, first, last >= 0, first + last <= n_pages
+ *                 -0 equals 0; NaN counts as the lowest value and, among the
+ *                 pages that compete, raises SPEC_ERR_NONFINITE
+ *   n_pages 1 .. 2^30, first, last >= 0, first + last <= n_pages
  *   pages [B, Hkv, n_pages] int32   places in the block table, ascending; -1
  *                 behind the last
  *   counts [B] int32   min(F, n_pages); 0 for a negative ctx_lens or one past
@@ -340,6 +341,7 @@ spec_status spec_page_select(const float* scores, const int32_t* ctx_lens, int32
  * spec_verify_attn_window.  Table entries and keys and values of other pages are
  * not read and may be anything.  A request whose list breaks the rules fails
  * (SPEC_ERR_INVALID_ARG: caches untouched, out = 0, lse = -inf).
+ * dims->softmax_scale is not negative.
  */
 spec_status spec_verify_attn_pages(const void* q, const void* k_new, const void* v_new,
                                    void* k_cache, void* v_cache, const int32_t* block_table,

@@ -289,6 +289,18 @@ spec_status spec_verify_attn_window(const void* q, const void* k_new, const void
                      lse, dims, ws, ws_bytes, stream);
 }
 
+// What the forms of the attention on views ask of dims beyond attn_common.
+static spec_status check_view(const spec_dims* d) {
+  if (d == nullptr) return SPEC_ERR_INVALID_ARG;
+  if (!(d->softmax_scale >= 0.f) || !(d->softmax_scale < INFINITY)) return SPEC_ERR_INVALID_ARG;
+  // positions, and a request's (KV head, page) pairs, stay 32-bit; KV heads are a
+  // grid's second extent
+  if ((int64_t)d->max_blocks * kBlock > INT32_MAX / 2 || d->Hkv > 65535 ||
+      (int64_t)d->max_blocks * d->Hkv > INT32_MAX / 2)
+    return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
 spec_status spec_verify_attn_prefix(const void* q, const void* k_new, const void* v_new,
                                     void* k_cache, void* v_cache, const int32_t* block_table,
                                     const int32_t* ctx_lens, const int32_t* parent,
@@ -296,10 +308,10 @@ spec_status spec_verify_attn_prefix(const void* q, const void* k_new, const void
                                     float* lse, const spec_dims* dims, void* ws, size_t ws_bytes,
                                     void* stream) {
   g_launches = 0;
-  if (dims == nullptr || !prefix_table) return SPEC_ERR_INVALID_ARG;
-  const int64_t cap = (int64_t)dims->max_blocks * kBlock;
-  if (cap > INT32_MAX / 2) return SPEC_ERR_UNSUPPORTED;
-  if (prefix_len < kBlock || prefix_len % kBlock != 0 || prefix_len >= cap)
+  const spec_status s = check_view(dims);
+  if (s != SPEC_OK) return s;
+  if (!prefix_table || prefix_len < kBlock || prefix_len % kBlock != 0 ||
+      prefix_len >= (int64_t)dims->max_blocks * kBlock)
     return SPEC_ERR_INVALID_ARG;
   AttnView v = {};
   v.mode = kViewPrefix;
@@ -316,10 +328,10 @@ spec_status spec_verify_attn_pages(const void* q, const void* k_new, const void*
                                    void* out, float* lse, const spec_dims* dims, void* ws,
                                    size_t ws_bytes, void* stream) {
   g_launches = 0;
-  if (dims == nullptr || !pages || !counts || n_pages < 1) return SPEC_ERR_INVALID_ARG;
-  if ((int64_t)dims->max_blocks * kBlock > INT32_MAX / 2 ||
-      (int64_t)dims->max_blocks * dims->Hkv > INT32_MAX / 2)
-    return SPEC_ERR_UNSUPPORTED;
+  const spec_status s = check_view(dims);
+  if (s != SPEC_OK) return s;
+  if (!pages || !counts || n_pages < 1) return SPEC_ERR_INVALID_ARG;
+  if (n_pages > kSelectMostPages) return SPEC_ERR_UNSUPPORTED;
   AttnView v = {};
   v.mode = kViewPages;
   v.pages = pages;
@@ -380,6 +392,7 @@ spec_status spec_page_select(const float* scores, const int32_t* ctx_lens, int32
   if (!scores || !ctx_lens || !pages || !counts) return SPEC_ERR_INVALID_ARG;
   if (n_pages < 1 || first < 0 || last < 0 || (int64_t)first + last > n_pages)
     return SPEC_ERR_INVALID_ARG;
+  if (n_pages > kSelectMostPages) return SPEC_ERR_UNSUPPORTED;
   const SelectArgs a = {scores, ctx_lens, n_pages, first, last, pages, counts, *dims,
                         static_cast<uint32_t*>(ws)};
   int launches = 0;

@@ -5,6 +5,8 @@
 
 namespace specv {
 
+constexpr int kSelectMostPages = 1 << 30;  // places of a list (counts stay 32-bit)
+
 struct BoundsArgs {
   const void* k_cache;
   const int32_t* block_table;

@@ -151,6 +151,8 @@ def test_prefix(ctx, P, M, Hq, Hkv, D, dt, tree, impl):
     ([12800 + 7 * b for b in range(17)], 12800, 2, 14, 2, 128, BF, TC),     # one pass, 119 rows
     ([8208] * 50, 8208, 1, 8, 1, 128, BF, TC),                              # 400 rows of a head
     ([8000 + b for b in range(60)], 8000, 5, 1, 1, 128, BF, TC),            # a third unit's tile
+    ([12816, 12817, 12830, 12900], 12816, 1, 8, 8, 128, BF, TC),            # four rows of a head
+    ([64 + b % 20 for b in range(6500)], 64, 1, 1, 1, 128, BF, TC),         # less than a key tile
     ([4000 + 3 * b for b in range(3)], 4000, 40, 6, 2, 64, BF, AUTO),
     ([16400 + 3 * b for b in range(13)], 16400, 2, 3, 3, 128, F32, AUTO)])
 def test_prefix_in_one_pass(ctx, P, M, Hq, Hkv, D, dt, impl):
@@ -225,6 +227,25 @@ def test_prefix_in_one_pass_requests_that_fail(dt, D, M, Hq):
     assert st.call(prefix=to_dev(shared, I32)) & BAD_ID
     assert torch.all(st.out == 0) and torch.all(st.lse == -float("inf"))
     assert torch.equal(st.kc, before[0]) and torch.equal(st.vc, before[1])
+
+
+@pytest.mark.parametrize("D,impl", [(128, TC), (128, CORES), (64, AUTO)])
+def test_attention_scale(D, impl):
+    """A scale of the caller's, in every way of reading."""
+    for P, B in ((64, 3), (3216, 64)):
+        st = Step([P + b for b in range(B)], 4, 8, 2, D, BF, 5, shared=P // 16, impl=impl)
+        st.dims.softmax_scale = 0.05
+        assert st.call(prefix=to_dev(st.shared, I32)) == 0
+        args = (st.q, st.k, st.v, st.table, st.ctx, st.kn)
+        ref = oracle_verify_attn(*args, st.vn, scale=0.05)
+        size = oracle_verify_attn(*args[:2], np.abs(st.v), *args[3:], np.abs(st.vn), scale=0.05)[0]
+        st.check(ref, size)
+    pages, cnt = choose(st.rng, st.ctx, 2, 9)
+    assert st.call(pages=to_dev(pages, I32), page_counts=to_dev(cnt, I32)) == 0
+    ref = oracle_verify_attn_pages(*args, st.vn, pages, cnt, scale=0.05)
+    size = oracle_verify_attn_pages(*args[:2], np.abs(st.v), *args[3:], np.abs(st.vn), pages, cnt,
+                                    scale=0.05)[0]
+    st.check(ref, size)
 
 
 @pytest.mark.parametrize("dt,D", [(BF, 128), (F32, 64)])

@@ -88,6 +88,18 @@ def test_page_calls_arguments(lib):
     assert score(lib, q=ctypes.c_void_p(4104)) == INVALID
 
 
+@pytest.mark.parametrize("scale", [-0.1, float("nan"), float("inf")])
+def test_scales(lib, scale):
+    assert prefix(lib, d=dims(softmax_scale=scale)) == INVALID
+    assert pages(lib, d=dims(softmax_scale=scale)) == INVALID
+
+
+def test_lists_past_32_bit_counts(lib):
+    assert select(lib, (1 << 30) + 1) == UNSUPPORTED and pages(lib, n=(1 << 30) + 1) == UNSUPPORTED
+    wide = dims(Hq=1 << 12, Hkv=1 << 12, max_blocks=1 << 19, M=1)
+    assert pages(lib, d=wide) == UNSUPPORTED and prefix(lib, d=wide) == UNSUPPORTED
+
+
 def test_workspace_has_room_for_a_prefix(lib):
     # partials of the prefix: at least a slot of every 256 rows of a KV head
     d = dims(B=128, M=5, Hq=64, Hkv=8, max_blocks=2049)
