@@ -31,16 +31,17 @@ constexpr int kPfxRows = 64, kPfxThreads = 128;
 // Ranges of all units together, at least the units: one wave of the CTAs that an
 // SM holds (16 requests of 16 rows, 8 heads of 64, 2000 positions in 608 ranges, a
 // third of them in a second wave: 46 us for the kernel).
-__host__ __device__ constexpr int pfx_slots(int D) { return (D == 64 ? 3 : 2) * 152; }
+__host__ __device__ constexpr int pfx_slots(int D) { return (D == 64 ? 4 : 3) * 152; }
 
 template <int D>
 struct PfxTile {
-  // 64 keys with heads of 64 (69 KB: three CTAs an SM), 32 with heads of 128
-  // (80 KB: two)
+  // 64 keys with heads of 64 (51 KB: four CTAs an SM), 32 with heads of 128 (70 KB:
+  // three); the probabilities go where the keys were
   static constexpr int kKeys = D == 64 ? 64 : 32;
   static constexpr int kLd = kPfxRows + 4;   // padded rows of the transposed tiles
   static constexpr int kLdK = kKeys + 4;
-  static constexpr size_t smem = sizeof(float) * ((size_t)D * kLd + D * kLdK + kKeys * D + kKeys * kLd);
+  static constexpr size_t smem = sizeof(float) * ((size_t)D * kLd + D * kLdK + kKeys * D);
+  static_assert(kKeys * kLd <= D * kLdK, "the probabilities fit the keys' place");
 };
 
 __device__ __forceinline__ unsigned long long pair_of(float a, float b) {
@@ -58,7 +59,7 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kPfxThreads) prefix_simt_kernel(
+__global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kernel(
     const T* q, const T* k_cache, const T* v_cache, const int32_t* table, int prefix_len,
     spec_dims d, float qscale, PrefixPlan plan, float* __restrict__ part) {
   using Tile = PfxTile<D>;
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_simt_kernel(
   float* qt = smem;             // [D][kLd]   queries, scaled
   float* kt = qt + D * kLd;     // [D][kLdK]  keys
   float* vs = kt + D * kLdK;    // [kKeys][D] values, key j * 16 + x at 4-key group x (kSlot)
-  float* pt = vs + kKeys * D;   // [kKeys][kLd] probabilities, the same order of keys
+  float* pt = kt;               // [kKeys][kLd] probabilities, the same order of keys
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int s = blockIdx.x % plan.splits, tile = blockIdx.x / plan.splits, h = blockIdx.y;
   const int group = d.Hq / d.Hkv, R = group * d.M;
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(kPfxThreads) prefix_simt_kernel(
         for (int r = 0; r < 4; ++r) sc[r][k] = fma2(qv[r], kk, sc[r][k]);
       }
     }
+    __syncthreads();  // the keys are consumed
     // softmax: the 16 threads of a row group share its rows
     const int left = prefix_len - j * kKeys - tx * KPT;  // this thread's keys below it are real
     float p[8][KPT];

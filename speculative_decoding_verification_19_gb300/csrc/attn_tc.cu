@@ -1305,8 +1305,13 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
   const int64_t T = carry_t, Ctot = carry_c;
   // With a window or a view a small batch has few tiles: each CTA then takes at least
   // kWinMinCost of the cost, because every further CTA of a pair is a partial
-  // that the pair's first CTA reads in turn.
-  const int Ge = kMode != kPlain ? (int)max((int64_t)1, min((int64_t)G, Ctot / kWinMinCost)) : G;
+  // that the pair's first CTA reads in turn; a view, which may be a whole long
+  // context, sqrt(2.3 n) for n tiles a pair at least (a partial costs that much more
+  // than a tile).
+  int64_t least = kWinMinCost;
+  if (kView && Ctot > T)
+    least = max(least, (int64_t)sqrtf(2.3f * (float)T * kSegCost / (float)(Ctot - T)));
+  const int Ge = kMode != kPlain ? (int)max((int64_t)1, min((int64_t)G, Ctot / least)) : G;
   if (tid == 0) {
     tpre[B] = T;
     cpre[B] = Ctot;
