@@ -658,7 +658,19 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
                              (int64_t)ceil_div(a.sinks, kTileKeys) * kTileKeys + a.window + d.M +
                                  kTileKeys);
     const int64_t want = max((int64_t)kMinWinSplit, (int64_t)d.B * d.Hkv * most / kWinCtas);
-    split_keys = (int)(ceil_div64(max(want, ceil_div64(most, lay.max_splits)), kTileKeys) * kTileKeys);
+    int64_t ranges = lay.max_splits;
+    if (viewed && a.view.mode != kViewPrefix) {
+      // a small batch's ranges need more partials than the layout has: there is
+      // room where a prefix' partials would go (2 requests of 36 rows, 8 heads of
+      // 128 fp32 values, 1270 keys: 98 us for the call with 5 ranges, 56 with 20)
+      const int64_t slots = (int64_t)(prefix_part_floats(d) / ((size_t)R * (d.D + 1)));
+      const int64_t more = slots / ((int64_t)d.B * d.Hkv);
+      if (more > ranges) {
+        ranges = more;
+        part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + lay.pfx_part_off);
+      }
+    }
+    split_keys = (int)(ceil_div64(max(want, ceil_div64(most, ranges)), kTileKeys) * kTileKeys);
     splits = (int)ceil_div64(most, split_keys);
   }
   const dim3 grid(splits, d.Hkv, d.B);

@@ -29,8 +29,9 @@ namespace specv {
 // that 16 lanes share.  fp32 throughout, two rows a packed FMA.
 constexpr int kPfxRows = 64, kPfxThreads = 128;
 // Ranges of all units together, at least the units: one wave of the CTAs that an
-// SM holds (16 requests of 16 rows, 8 heads of 64, 2000 positions in 608 ranges, a
-// third of them in a second wave: 46 us for the kernel).
+// SM holds.  As many ranges as that gives: a tile takes a lone CTA of an SM some 10
+// us (26 requests of one row, 8 heads of 64, 2208 positions: 57 us for the call with
+// a tile a range, 70 with two), its partial in the merge 0.3.
 __host__ __device__ constexpr int pfx_slots(int D) { return (D == 64 ? 4 : 3) * 152; }
 
 template <int D>
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[c] *= a;
     mx = mn;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < n; ++s) {
       const float* p = row_of(s0 + s) + lane;
       const float ws = __shfl_sync(0xffffffffu, w, s);

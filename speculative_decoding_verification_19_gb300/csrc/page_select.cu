@@ -114,30 +114,32 @@ __global__ void __launch_bounds__(256) page_bounds_kernel(const T* k_cache,
 // ---------------------------------------------------------------------------
 // scores
 // ---------------------------------------------------------------------------
-// A CTA per 64 pages of a KV head; the product q+ . hi + q- . lo in register
-// tiles of RPT rows x 4 pages, the rows' maximum in registers, then across the
-// eight row groups.
-constexpr int kScorePages = 64, kScoreThreads = 128;
+// A CTA per kTile pages of a KV head; the product q+ . hi + q- . lo in register
+// tiles of RPT rows x kTile / 16 pages, the rows' maximum in registers, then across
+// the eight row groups.  64 pages a CTA, or 16 where those would not fill the GPU
+// twice: 11 requests of 17 rows, 4 heads of 128 fp32 values, up to 310 pages 16 us
+// (25 with 64), 3 of 116 rows, one head of 64, up to 390 pages 12 us (20).
+constexpr int kScoreThreads = 128;
 
-template <int D, int RPT>
+template <int D, int RPT, int kTile>
 constexpr size_t score_smem() {
-  return sizeof(float) * ((size_t)2 * D * (kScorePages + 4) + (size_t)D * (8 * RPT + 4) +
-                          8 * kScorePages);
+  return sizeof(float) * ((size_t)2 * D * (kTile + 4) + (size_t)D * (8 * RPT + 4) + 8 * kTile);
 }
 
-template <typename T, int D, int RPT>
+template <typename T, int D, int RPT, int kTile>
 __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
     const T* q, const T* bounds, const int32_t* block_table, const int32_t* ctx_lens, spec_dims d,
     float* __restrict__ scores, uint32_t* __restrict__ status) {
-  constexpr int kLd = kScorePages + 4, kRows = 8 * RPT, kLdQ = kRows + 4;
+  constexpr int kLd = kTile + 4, kRows = 8 * RPT, kLdQ = kRows + 4, PPT = kTile / 16;
+  static_assert(PPT == 4 || PPT == 1, "a thread has four pages or one");
   constexpr int kVec = 16 / sizeof(T), kVecRow = D / kVec;
   extern __shared__ __align__(16) float smem[];
   float* lo = smem;               // [D][kLd]
   float* hi = lo + D * kLd;       // [D][kLd]
   float* qs = hi + D * kLd;       // [D][kLdQ]
-  float* red = qs + D * kLdQ;     // [8][kScorePages]
+  float* red = qs + D * kLdQ;     // [8][kTile]
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const int h = blockIdx.y, b = blockIdx.z, page0 = blockIdx.x * kScorePages;
+  const int h = blockIdx.y, b = blockIdx.z, page0 = blockIdx.x * kTile;
   const int group = d.Hq / d.Hkv, R = group * d.M;
   pdl_trigger();
   pdl_wait();  // the queries, bounds and lengths may come from the previous kernels
@@ -147,12 +149,12 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
   if (!fits && page0 == 0 && h == 0 && tid == 0) raise_status(status, SPEC_ERR_CAPACITY);
   float* out = scores + ((int64_t)b * d.Hkv + h) * d.max_blocks;
   if (page0 >= full) {
-    for (int p = page0 + tid; p < min(page0 + kScorePages, d.max_blocks); p += kScoreThreads)
+    for (int p = page0 + tid; p < min(page0 + kTile, d.max_blocks); p += kScoreThreads)
       out[p] = -INFINITY;
     return;
   }
-  for (int e = tid; e < kScorePages * 2 * kVecRow; e += kScoreThreads) {
-    const int p = e % kScorePages, vi = e / kScorePages;  // vectors of lo, then of hi
+  for (int e = tid; e < kTile * 2 * kVecRow; e += kScoreThreads) {
+    const int p = e % kTile, vi = e / kTile;  // vectors of lo, then of hi
     float f[kVec];
 #pragma unroll
     for (int c = 0; c < kVec; ++c) f[c] = 0.f;
@@ -164,7 +166,9 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
 #pragma unroll
     for (int c = 0; c < kVec; ++c) lo[(vi * kVec + c) * kLd + p] = f[c];
   }
-  float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float best[PPT];
+#pragma unroll
+  for (int k = 0; k < PPT; ++k) best[k] = -INFINITY;
   for (int r0 = 0; r0 < R; r0 += kRows) {
     __syncthreads();
     for (int e = tid; e < kRows * kVecRow; e += kScoreThreads) {
@@ -177,37 +181,43 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
       for (int c = 0; c < kVec; ++c) qs[(vi * kVec + c) * kLdQ + r] = f[c];
     }
     __syncthreads();
-    float acc[RPT][4];
+    float acc[RPT][PPT];
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[r][k] = 0.f;
+      for (int k = 0; k < PPT; ++k) acc[r][k] = 0.f;
 #pragma unroll 2
     for (int dd = 0; dd < D; ++dd) {
-      const float4 a = *reinterpret_cast<const float4*>(lo + dd * kLd + tx * 4);
-      const float4 c = *reinterpret_cast<const float4*>(hi + dd * kLd + tx * 4);
+      float a[PPT], c[PPT];
+      if constexpr (PPT == 4) {
+        const float4 a4 = *reinterpret_cast<const float4*>(lo + dd * kLd + tx * 4);
+        const float4 c4 = *reinterpret_cast<const float4*>(hi + dd * kLd + tx * 4);
+        a[0] = a4.x; a[1] = a4.y; a[2] = a4.z; a[3] = a4.w;
+        c[0] = c4.x; c[1] = c4.y; c[2] = c4.z; c[3] = c4.w;
+      } else {
+        a[0] = lo[dd * kLd + tx];
+        c[0] = hi[dd * kLd + tx];
+      }
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
         const float qv = qs[dd * kLdQ + ty * RPT + r];
         const float qp = fmaxf(qv, 0.f), qn = fminf(qv, 0.f);
-        acc[r][0] = fmaf(qp, c.x, fmaf(qn, a.x, acc[r][0]));
-        acc[r][1] = fmaf(qp, c.y, fmaf(qn, a.y, acc[r][1]));
-        acc[r][2] = fmaf(qp, c.z, fmaf(qn, a.z, acc[r][2]));
-        acc[r][3] = fmaf(qp, c.w, fmaf(qn, a.w, acc[r][3]));
+#pragma unroll
+        for (int k = 0; k < PPT; ++k) acc[r][k] = fmaf(qp, c[k], fmaf(qn, a[k], acc[r][k]));
       }
     }
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) best[k] = fmaxf(best[k], acc[r][k]);
+      for (int k = 0; k < PPT; ++k) best[k] = fmaxf(best[k], acc[r][k]);
   }
-  *reinterpret_cast<float4*>(red + ty * kScorePages + tx * 4) =
-      make_float4(best[0], best[1], best[2], best[3]);
+#pragma unroll
+  for (int k = 0; k < PPT; ++k) red[ty * kTile + tx * PPT + k] = best[k];
   __syncthreads();
-  if (tid < kScorePages && page0 + tid < d.max_blocks) {
+  if (tid < kTile && page0 + tid < d.max_blocks) {
     float m = red[tid];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) m = fmaxf(m, red[k * kScorePages + tid]);
+    for (int k = 1; k < 8; ++k) m = fmaxf(m, red[k * kTile + tid]);
     bool there = page0 + tid < full;
     if (there) {
       const int id = __ldcg(block_table + (int64_t)b * d.max_blocks + page0 + tid);
@@ -505,25 +515,31 @@ cudaError_t page_bounds_launch(const BoundsArgs& a, cudaStream_t st, int* launch
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <typename T, int D, int RPT>
+template <typename T, int D, int RPT, int kTile>
 static cudaError_t launch_score(const ScoreArgs& a, cudaStream_t st) {
   const spec_dims& d = a.d;
-  auto k = page_score_kernel<T, D, RPT>;
-  constexpr size_t smem = score_smem<D, RPT>();
+  auto k = page_score_kernel<T, D, RPT, kTile>;
+  constexpr size_t smem = score_smem<D, RPT, kTile>();
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  PdlLaunch L(dim3(ceil_div(d.max_blocks, kScorePages), d.Hkv, d.B), dim3(kScoreThreads), smem, st);
+  PdlLaunch L(dim3(ceil_div(d.max_blocks, kTile), d.Hkv, d.B), dim3(kScoreThreads), smem, st);
   return cudaLaunchKernelEx(&L.cfg, k, static_cast<const T*>(a.q), static_cast<const T*>(a.bounds),
                             a.block_table, a.ctx_lens, d, a.scores, a.status);
 }
 
-template <typename T, int D>
+template <typename T, int D, int kTile>
 static cudaError_t launch_score(const ScoreArgs& a, cudaStream_t st) {
   const int R = (a.d.Hq / a.d.Hkv) * a.d.M;
-  if (R <= 8) return launch_score<T, D, 1>(a, st);
-  if (R <= 16) return launch_score<T, D, 2>(a, st);
-  if (R <= 32) return launch_score<T, D, 4>(a, st);
-  return launch_score<T, D, 8>(a, st);
+  if (R <= 8) return launch_score<T, D, 1, kTile>(a, st);
+  if (R <= 16) return launch_score<T, D, 2, kTile>(a, st);
+  if (R <= 32) return launch_score<T, D, 4, kTile>(a, st);
+  return launch_score<T, D, 8, kTile>(a, st);
+}
+
+template <typename T, int D>
+static cudaError_t launch_score(const ScoreArgs& a, cudaStream_t st) {
+  const int64_t ctas = (int64_t)ceil_div(a.d.max_blocks, 64) * a.d.Hkv * a.d.B;
+  return ctas < 2 * 152 ? launch_score<T, D, 16>(a, st) : launch_score<T, D, 64>(a, st);
 }
 
 cudaError_t page_score_launch(const ScoreArgs& a, cudaStream_t st, int* launches) {

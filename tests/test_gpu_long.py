@@ -456,6 +456,25 @@ def test_score(dt, D, M, Hq, Hkv):
     assert np.all(err <= 2 * D * 2.0 ** -24 * size[there]), err.max()
 
 
+@pytest.mark.parametrize("dt,D", [(BF, 128), (BF, 64), (F32, 128), (F32, 64)])
+def test_score_of_many_requests(dt, D):
+    """Enough tiles of 64 pages to fill the GPU, several requests a CTA."""
+    B, M, Hq, Hkv = 21, 2, 24, 8
+    rng = np.random.default_rng(3)
+    ctx = rng.integers(0, 2100, B)
+    ctx[:3] = (2099, 0, 1024)
+    st = Step(ctx, M, Hq, Hkv, D, dt, 6)
+    pair = typed(np.sort(rng.standard_normal((st.nb, Hkv, 2, D)), axis=2).astype(np.float32), dt)
+    scores = torch.full((B, Hkv, st.mb), float("nan"), device="cuda")
+    sv.spec_page_score(to_dev(st.q, dt), to_dev(pair, dt), to_dev(st.table, I32), to_dev(ctx, I32),
+                       scores, st.dims, st.ws)
+    assert sv.device_status(st.ws) == 0
+    ref, size = oracle_page_score(st.q, pair, st.table, ctx)
+    got, there = scores.double().cpu().numpy(), np.isfinite(ref)
+    assert np.all(got[~there] == -np.inf)
+    assert np.all(np.abs(got[there] - ref[there]) <= 2 * D * 2.0 ** -24 * size[there])
+
+
 @pytest.mark.parametrize("dt,D", [(BF, 128), (F32, 64)])
 def test_score_of_pages_that_fail(dt, D):
     ctx = np.array([1200, 800])
