@@ -170,10 +170,9 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits for the phase of `parity`, with ptx::mbar_wait's rules for giving up.
-// (No function call: that and setmaxnreg do not go together.)  A poll suspends the
-// warp for up to a microsecond; with the default time the waiting warps' polls
-// took a third of the issue slots from the softmax.
+// Waits for the phase of `parity`, with ptx::mbar_wait's rules for giving up; a poll
+// suspends the warp for up to a microsecond.  (No function call: that and
+// setmaxnreg do not go together.)
 template <bool kShort>
 __device__ __forceinline__ bool await(const uint64_t* bar, uint32_t parity, volatile int* abort,
                                       uint64_t timeout_cycles) {

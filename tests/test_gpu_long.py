@@ -749,6 +749,43 @@ def test_calls_on_two_streams():
         st.check(oracle_verify_attn(*args, st.vn), oracle_verify_attn(*sizes, np.abs(st.vn))[0])
 
 
+@pytest.mark.parametrize("dt,D,Hkv,blocks", [(BF, 128, 8, 270_000), (F32, 64, 8, 530_000)])
+def test_blocks_past_32_bit_offsets(dt, D, Hkv, blocks):
+    """The same blocks at the far end of a cache of more than 2^32 values: the same
+    bits as in a small cache."""
+    P, B, M = 3216, 16, 3
+    st = Step([P + 7 * b for b in range(B)], M, 2 * Hkv, Hkv, D, dt, 5, shared=P // 16)
+    far = np.arange(st.nb)[::-1] + blocks - st.nb  # block i lives at far[i]
+    at = torch.from_numpy(far.copy()).cuda()
+    k = torch.empty(blocks, Hkv, 16, D, dtype=dt, device="cuda")
+    v = torch.empty(blocks, Hkv, 16, D, dtype=dt, device="cuda")
+    assert k.numel() > 2 ** 32
+    k[at], v[at] = st.kc, st.vc
+    near = dict(k=st.kc, v=st.vc, table=st.table, shared=st.shared, nb=st.nb)
+    away = dict(k=k, v=v, table=np.where(st.table >= 0, far[st.table], -1), shared=far[st.shared], nb=blocks)
+    lists, cnt = choose(st.rng, st.ctx, Hkv, 20)
+    got = []
+    for place in (near, away):
+        st.kc, st.vc, st.nb = place["k"], place["v"], place["nb"]
+        st.dims = sv.make_dims(B=B, M=M, Hq=2 * Hkv, Hkv=Hkv, D=D, max_blocks=st.mb, num_blocks=st.nb,
+                               kv_dtype=dt)
+        table, ctx = to_dev(place["table"], I32), to_dev(st.ctx, I32)
+        bounds = torch.zeros(st.nb, Hkv, 2, D, dtype=dt, device="cuda")
+        scores = torch.empty(B, Hkv, st.mb, device="cuda")
+        sv.spec_page_bounds(st.kc, table, None, ctx, bounds, st.dims, st.ws)
+        sv.spec_page_score(to_dev(st.q, dt), bounds, table, ctx, scores, st.dims, st.ws)
+        res = [scores]
+        short = to_dev(place["shared"][:9], I32)  # read by the requests; then in a pass of its own
+        for kw in (dict(prefix=short), dict(prefix=to_dev(place["shared"], I32)),
+                   dict(pages=to_dev(lists, I32), page_counts=to_dev(cnt, I32))):
+            assert st.call(table=place["table"], **kw) == 0
+            res += [st.out, st.lse]
+        used = at if place is away else torch.arange(near["nb"], device="cuda")
+        got.append(res + [x[used] for x in (st.kc, st.vc, bounds)])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_forms_take_turns_on_one_workspace():
     """Every form of the attention, one after another on the same workspace and
     another stream, as a step that mixes layers may."""
