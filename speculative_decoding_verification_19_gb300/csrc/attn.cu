@@ -646,6 +646,9 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
   const int64_t stride_h = viewed ? a.view.stride_h : 0;
   const int32_t* ctx = viewed ? a.view.ctx : a.ctx_lens;
 
+  // views of many rows: register tiles of 64 rows (attn_prefix.cu, with both sides'
+  // times), else the windowed kernel, a row to four a warp
+  const bool tiled = viewed && R > 32;
   const size_t smem = attn_simt_smem_bytes(R, d.D);
   // Key ranges: the layout's, or, with a window, of the fewer keys that a
   // request then has at most, for one wave of three CTAs per SM (the tree case
@@ -657,7 +660,10 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
     const int64_t most = min(entries * kBlock,
                              (int64_t)ceil_div(a.sinks, kTileKeys) * kTileKeys + a.window + d.M +
                                  kTileKeys);
-    const int64_t want = max((int64_t)kMinWinSplit, (int64_t)d.B * d.Hkv * most / kWinCtas);
+    const int64_t want =
+        max((int64_t)kMinWinSplit, tiled ? (int64_t)d.B * d.Hkv * ceil_div(R, 64) * most / view_ctas(d)
+                                         : (int64_t)d.B * d.Hkv * most / kWinCtas);
+    const int unit = tiled ? view_range_unit(d) : kTileKeys;
     int64_t ranges = lay.max_splits;
     if (viewed && a.view.mode != kViewPrefix) {
       // a small batch's ranges need more partials than the layout has: there is
@@ -670,7 +676,7 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
         part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + lay.pfx_part_off);
       }
     }
-    split_keys = (int)(ceil_div64(max(want, ceil_div64(most, ranges)), kTileKeys) * kTileKeys);
+    split_keys = (int)(ceil_div64(max(want, ceil_div64(most, ranges)), unit) * unit);
     splits = (int)ceil_div64(most, split_keys);
   }
   const dim3 grid(splits, d.Hkv, d.B);
@@ -705,7 +711,11 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
     if (e != cudaSuccess) return e;                                                           \
   } while (0)
   const int rpw = ceil_div(R, a.window > 0 ? kWinWarps : kSimtWarps);
-  if (a.window > 0) {
+  if (tiled) {
+    const ViewRanges own = {stride_b, stride_h, ctx, req_ok, anc, split_keys};
+    e = view_split_launch(a, own, splits, part, st);
+    if (e != cudaSuccess) return e;
+  } else if (a.window > 0) {
     const int pad = rpw <= 1 ? 1 : rpw <= 2 ? 2 : rpw <= 4 ? 4 : rpw <= 8 ? 8 : 16;
     const size_t win_smem = attn_win_smem_bytes(pad * kWinWarps, d.D);
     if (d.D == 128) {

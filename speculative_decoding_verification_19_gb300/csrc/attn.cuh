@@ -185,6 +185,19 @@ struct OwnPart {
   const int32_t* ok;      // [B] nonzero: the request has passed its checks
 };
 
+// Views of the requests in ranges of keys, for prefix_simt_kernel's tiles.
+struct ViewRanges {
+  int64_t stride_b, stride_h;
+  const int32_t* ctx;
+  const int32_t* ok;
+  const ulonglong2* anc;  // [B, M] ancestors-or-self
+  int split_keys;
+};
+int view_range_unit(const spec_dims& d);  // ranges are whole numbers of it
+int view_ctas(const spec_dims& d);        // CTAs of a wave
+cudaError_t view_split_launch(const AttnArgs& a, const ViewRanges& own, int splits, float* part,
+                              cudaStream_t st);
+
 size_t attn_simt_smem_bytes(int R, int D);
 // CTAs of the prefix kernel on tensor cores never exceed this (its partials are
 // sized for it).

@@ -10,7 +10,8 @@
 //
 // Kernels in this file:
 //   prefix_simt_kernel   the prefix on CUDA cores (fp32; bf16 goes to the tensor
-//                        cores, attn_prefix_tc.cu, unless CUDA cores are asked for)
+//                        cores, attn_prefix_tc.cu, unless CUDA cores are asked
+//                        for), and views of requests with many rows
 //   prefix_merge_kernel  the partials of a row, a warp per row
 #include <math.h>
 
@@ -41,7 +42,8 @@ struct PfxTile {
   static constexpr int kKeys = D == 64 ? 64 : 32;
   static constexpr int kLd = kPfxRows + 4;   // padded rows of the transposed tiles
   static constexpr int kLdK = kKeys + 4;
-  static constexpr size_t smem = sizeof(float) * ((size_t)D * kLd + D * kLdK + kKeys * D);
+  static constexpr size_t smem = sizeof(float) * ((size_t)D * kLd + D * kLdK + kKeys * D) +
+                                 sizeof(ulonglong2) * kPfxRows;
   static_assert(kKeys * kLd <= D * kLdK, "the probabilities fit the keys' place");
 };
 
@@ -59,10 +61,16 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
   return r;
 }
 
-template <typename T, int D>
+// kOwn: the same tiles over views of the requests (attn_win_split_kernel's work)
+// for more than 32 rows per KV head: 64 rows of a request, its view's keys in
+// ranges of split_keys, the new rows' masks from the append kernel.  8 trees of 64
+// rows, 8 heads of 64 fp32 values over 33 pages: 43 us for the call, 48 with the
+// windowed kernel; 13 requests of 36 rows, 4 heads of 128 over 45 pages 63 us, 77.
+// Up to 32 rows a tile would be half empty.
+template <typename T, int D, bool kOwn>
 __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kernel(
     const T* q, const T* k_cache, const T* v_cache, const int32_t* table, int prefix_len,
-    spec_dims d, float qscale, PrefixPlan plan, float* __restrict__ part) {
+    spec_dims d, float qscale, PrefixPlan plan, ViewRanges own, float* __restrict__ part) {
   using Tile = PfxTile<D>;
   constexpr int kKeys = Tile::kKeys, kLd = Tile::kLd, kLdK = Tile::kLdK;
   constexpr int KPT = kKeys / 16;  // keys of a thread
@@ -71,14 +79,32 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
   extern __shared__ __align__(16) float smem[];
   float* qt = smem;             // [D][kLd]   queries, scaled
   float* kt = qt + D * kLd;     // [D][kLdK]  keys
-  float* vs = kt + D * kLdK;    // [kKeys][D] values, key j * 16 + x at 4-key group x (kSlot)
+  float* vs = kt + D * kLdK;    // [kKeys][D] values, a thread's keys 16 rows apart
   float* pt = kt;               // [kKeys][kLd] probabilities, the same order of keys
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int s = blockIdx.x % plan.splits, tile = blockIdx.x / plan.splits, h = blockIdx.y;
   const int group = d.Hq / d.Hkv, R = group * d.M;
-  const int rows = d.B * R;
+  const int rows = kOwn ? R : d.B * R;
   pdl_trigger();
-  pdl_wait();  // the queries and the cache may come from the previous kernels
+  pdl_wait();  // the queries, the cache and the views may come from the previous kernels
+  const int own_b = kOwn ? blockIdx.z : 0;
+  int ctx = prefix_len, k0, k1;  // cached keys, and the range of keys
+  ulonglong2* anc = reinterpret_cast<ulonglong2*>(vs + kKeys * D);  // masks of the rows (kOwn)
+  if constexpr (kOwn) {
+    if (!__ldcg(own.ok + own_b)) return;
+    ctx = __ldcg(own.ctx + own_b);
+    k0 = s * own.split_keys;
+    k1 = min(k0 + own.split_keys, ctx + d.M);
+    if (k0 >= k1) return;
+    table += own_b * own.stride_b + h * own.stride_h;
+    for (int r = tid; r < kPfxRows; r += kPfxThreads) {
+      const int i = min(tile * kPfxRows + r, R - 1) / group;
+      anc[r] = own.anc[(int64_t)own_b * d.M + i];
+    }
+  } else {
+    k0 = (int)((int64_t)s * plan.key_tiles / plan.splits) * kKeys;
+    k1 = min((int)((int64_t)(s + 1) * plan.key_tiles / plan.splits) * kKeys, prefix_len);
+  }
 
   for (int e = tid; e < kPfxRows * kVecRow; e += kPfxThreads) {
     const int r = e % kPfxRows, vi = e / kPfxRows;
@@ -87,7 +113,7 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
 #pragma unroll
     for (int c = 0; c < kVec; ++c) f[c] = 0.f;
     if (gr < rows) {
-      const int b = gr / R, rr = gr - b * R, i = rr / group;
+      const int b = kOwn ? own_b : gr / R, rr = kOwn ? gr : gr - b * R, i = rr / group;
       const int64_t at = (((int64_t)b * d.M + i) * d.Hq + h * group + rr - i * group) * D;
       unpack16(reinterpret_cast<const uint4*>(q + at)[vi], f);
     }
@@ -107,19 +133,17 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
 #pragma unroll
     for (int c = 0; c < CPT; ++c) o[r][c] = 0ull;
 
-  const int j0 = (int)((int64_t)s * plan.key_tiles / plan.splits);
-  const int j1 = (int)((int64_t)(s + 1) * plan.key_tiles / plan.splits);
-  for (int j = j0; j < j1; ++j) {
+  for (int t0 = k0; t0 < k1; t0 += kKeys) {
     __syncthreads();  // the last tile is consumed
     for (int e = tid; e < kKeys * kVecRow; e += kPfxThreads) {
       // two neighbouring vectors of 16 keys a warp: whole sectors from global
       // memory, no bank conflicts in the transposed stores
       const int vi = (e & 1) | ((e / (2 * kKeys)) << 1), kk = (e >> 1) % kKeys;
-      const int t = j * kKeys + kk;
+      const int t = t0 + kk;
       float kf[kVec], vf[kVec];
 #pragma unroll
       for (int c = 0; c < kVec; ++c) kf[c] = vf[c] = 0.f;
-      if (t < prefix_len) {
+      if (t < k1) {
         const int id = __ldcg(table + t / kBlock);
         // no block id: the request check fails every request
         const int64_t blk = (uint32_t)id < (uint32_t)d.num_blocks ? id : 0;
@@ -164,7 +188,8 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
     }
     __syncthreads();  // the keys are consumed
     // softmax: the 16 threads of a row group share its rows
-    const int left = prefix_len - j * kKeys - tx * KPT;  // this thread's keys below it are real
+    const int left = k1 - t0 - tx * KPT;  // this thread's keys below it are real
+    const bool masked = kOwn && t0 + kKeys > ctx;  // the tile reaches the new rows
     float p[8][KPT];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -172,18 +197,26 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
 #pragma unroll
       for (int k = 0; k < KPT; ++k) {
         const float x = (r & 1) ? hi_of(sc[r / 2][k]) : lo_of(sc[r / 2][k]);
-        p[r][k] = k < left ? x : -INFINITY;
+        bool see = k < left;
+        if (masked && see) {
+          const int n = t0 + tx * KPT + k - ctx;  // new row, < M as the key is real
+          const ulonglong2 m2 = anc[ty * 8 + r];
+          see = n < 0 || ((n < 64 ? m2.x : m2.y) >> (n & 63)) & 1ull;
+        }
+        p[r][k] = see ? x : -INFINITY;
         mt = fmaxf(mt, p[r][k]);
       }
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, w));
-      const float mn = fmaxf(m[r], mt);  // finite: a tile has at least one key
-      const float corr = fast_exp2(m[r] - mn);
+      const float mn = fmaxf(m[r], mt);
+      // a tile of a prefix has a key for every row; one of new rows may have none yet
+      const float ref = kOwn && mn == -INFINITY ? 0.f : mn;
+      const float corr = fast_exp2(m[r] - ref);
       m[r] = mn;
       l[r] *= corr;
 #pragma unroll
       for (int k = 0; k < KPT; ++k) {
-        p[r][k] = fast_exp2(p[r][k] - mn);
+        p[r][k] = fast_exp2(p[r][k] - ref);
         l[r] += p[r][k];  // this thread's keys; the 16 are summed at the end
       }
       // rescale the row's outputs
@@ -220,9 +253,10 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
     __syncwarp();
   }
 
-  const int S = tc_part_stride(D);
-  const int64_t unit = (int64_t)h * plan.tiles + tile;
-  float* pbase = part + (unit * plan.splits + s) * plan.tile * (int64_t)S;
+  const int S = kOwn ? D + 1 : tc_part_stride(D);
+  float* pbase =
+      kOwn ? part + ((((int64_t)own_b * d.Hkv + h) * plan.splits + s) * R + tile * kPfxRows) * (int64_t)S
+           : part + (((int64_t)h * plan.tiles + tile) * plan.splits + s) * plan.tile * (int64_t)S;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
     float sum = l[r];
@@ -230,7 +264,7 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
     for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
     const int row = ty * 8 + r;
     if (row >= plan.tile || tile * kPfxRows + row >= rows) continue;
-    const float inv = 1.f / sum;
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
     float* prow = pbase + (int64_t)row * S;
 #pragma unroll
     for (int c4 = 0; c4 < CPT / 4; ++c4) {
@@ -238,9 +272,14 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         f[c] = ((r & 1) ? hi_of(o[r / 2][c4 * 4 + c]) : lo_of(o[r / 2][c4 * 4 + c])) * inv;
-      *reinterpret_cast<float4*>(prow + c4 * 64 + tx * 4) = make_float4(f[0], f[1], f[2], f[3]);
+      if constexpr (kOwn) {  // rows of the merge's layout start anywhere
+#pragma unroll
+        for (int c = 0; c < 4; ++c) prow[c4 * 64 + tx * 4 + c] = f[c];
+      } else {
+        *reinterpret_cast<float4*>(prow + c4 * 64 + tx * 4) = make_float4(f[0], f[1], f[2], f[3]);
+      }
     }
-    if (tx == 0) prow[D] = m[r] + log2f(sum);
+    if (tx == 0) prow[D] = sum > 0.f ? m[r] + log2f(sum) : -INFINITY;
   }
 }
 
@@ -341,17 +380,31 @@ size_t prefix_part_floats(const spec_dims& d) {
   return simt > tc ? simt : tc;
 }
 
-template <typename T>
-static cudaError_t launch_simt(const AttnArgs& a, const PrefixPlan& p, float* part, cudaStream_t st) {
-  auto kern = a.d.D == 64 ? prefix_simt_kernel<T, 64> : prefix_simt_kernel<T, 128>;
+template <typename T, bool kOwn>
+static cudaError_t launch_simt(const AttnArgs& a, const PrefixPlan& p, const ViewRanges& own,
+                               float* part, cudaStream_t st) {
+  auto kern = a.d.D == 64 ? prefix_simt_kernel<T, 64, kOwn> : prefix_simt_kernel<T, 128, kOwn>;
   const size_t smem = a.d.D == 64 ? PfxTile<64>::smem : PfxTile<128>::smem;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  PdlLaunch L(dim3(p.splits * p.tiles, a.d.Hkv), dim3(kPfxThreads), smem, st);
+  PdlLaunch L(dim3(p.splits * p.tiles, a.d.Hkv, kOwn ? a.d.B : 1), dim3(kPfxThreads), smem, st);
   return cudaLaunchKernelEx(&L.cfg, kern, static_cast<const T*>(a.q),
                             static_cast<const T*>(a.k_cache), static_cast<const T*>(a.v_cache),
-                            a.view.prefix_table, a.view.prefix_len, a.d,
-                            a.scale * 1.4426950408889634f, p, part);
+                            kOwn ? a.view.table : a.view.prefix_table, kOwn ? 0 : a.view.prefix_len,
+                            a.d, a.scale * 1.4426950408889634f, p, own, part);
+}
+
+int view_range_unit(const spec_dims& d) { return d.D == 64 ? PfxTile<64>::kKeys : PfxTile<128>::kKeys; }
+int view_ctas(const spec_dims& d) { return pfx_slots(d.D); }
+
+cudaError_t view_split_launch(const AttnArgs& a, const ViewRanges& own, int splits, float* part,
+                              cudaStream_t st) {
+  PrefixPlan p = {};
+  p.tile = kPfxRows;
+  p.tiles = ceil_div((a.d.Hq / a.d.Hkv) * a.d.M, kPfxRows);
+  p.splits = splits;
+  return a.d.kv_dtype == SPEC_BF16 ? launch_simt<__nv_bfloat16, true>(a, p, own, part, st)
+                                   : launch_simt<float, true>(a, p, own, part, st);
 }
 
 cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, PrefixPlan* plan,
@@ -365,8 +418,8 @@ cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t s
     return e;
   }
   *plan = simt_plan(a.d, a.view.prefix_len);
-  e = a.d.kv_dtype == SPEC_BF16 ? launch_simt<__nv_bfloat16>(a, *plan, part, st)
-                                                  : launch_simt<float>(a, *plan, part, st);
+  e = a.d.kv_dtype == SPEC_BF16 ? launch_simt<__nv_bfloat16, false>(a, *plan, {}, part, st)
+                                : launch_simt<float, false>(a, *plan, {}, part, st);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

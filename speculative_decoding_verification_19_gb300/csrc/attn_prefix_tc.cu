@@ -29,8 +29,8 @@
 // 2048.  80 keys cost the products of S 51 cycles instead of 40 each (both
 // operands come from shared memory, 128 bytes a cycle).
 //
-// 64 requests of 5 rows, 64/8 heads, behind 32768 positions: about 280 us, 1.23
-// PFLOP/s, 0.64 of the measured bf16 rate; a tile of 80 keys takes some 2150 cycles
+// 64 requests of 5 rows, 64/8 heads, behind 32768 positions: 268 us, 1.28
+// PFLOP/s, 0.66 of the measured bf16 rate; a tile of 80 keys takes some 2150 cycles
 // of which the tensor cores work 1456.  Bound by the softmax' chain (loads of S 240
 // cycles, exponentials 1000, P's store 400, the next S 400) at two softmax warps a
 // scheduler.
