@@ -131,6 +131,7 @@ constexpr int kSegCost = 3;
 // 152 CTAs (17 partials to merge a pair), 22 with 4, 21 with 8, 23 with 12, 29
 // with 24 (no pair split); window 4096: 40, 30, 28 and 33 with 4, 8, 12, 24.
 constexpr int kWinMinCost = 8;
+constexpr int kGatherMinCost = 5;  // least cost of a CTA where view_merge_kernel merges (8: the same)
 constexpr int kPlain = 0, kWindow = 1, kViewed = 2;  // what the kernels' kMode instances run on
 constexpr int kPrepThreads = 256;
 constexpr int kPlanReqs = 1024;  // requests whose plan arrays fit the prep kernel's shared memory
@@ -305,12 +306,14 @@ __device__ __forceinline__ void store32_bf16(__nv_bfloat16* dst, const uint32_t 
 // requests' views (AttnView: ctx and the tables are the views', rq[b].w is the
 // request's own ctx) and, for a shared prefix, leaves every row's normalised
 // fp32 output and log2-sum-exp in own_part for the merge instead of out and lse.
+// gather (kViewed): every share of a split pair is left as a partial, for
+// view_merge_kernel.
 template <bool kWide, bool kShort, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __nv_bfloat16* k_new,
     const __nv_bfloat16* v_new, __nv_bfloat16* k_cache, __nv_bfloat16* v_cache,
     const int32_t* block_table, const int4* rq, const int4* starts, const ulonglong2* anc_ws,
-    const int* depth_ws, int window, int sinks, AttnView view, int* pairs, spec_dims d,
+    const int* depth_ws, int window, int sinks, AttnView view, int gather, int* pairs, spec_dims d,
     float qscale2, float* part, float* own_part, __nv_bfloat16* __restrict__ out,
     float* __restrict__ lse, uint32_t* __restrict__ status) {
   constexpr bool kWin = kMode == kWindow, kView = kMode == kViewed;
@@ -427,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
   // warp without a role, after the softmax warps have written the partial,
   // so that the fence before the count stalls no softmax warp.
   const int helper = n_sm_warps <= 2 ? kCopyWarpLargeR : (n_sm_warps == 3 ? 3 : -1);
-  if (warp == helper && lane == 0 && st0.w > 0) {
+  if (warp == helper && lane == 0 && st0.w > 0 && !(kView && gather)) {
     if (ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->ebar), 0, abort, wait)) {
       __threadfence();
       atomicAdd(pairs + (int64_t)st0.y * Hkv + st0.z, (int)min((int64_t)(st1.y - st0.w), g1 - g0));
@@ -939,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
           __nv_bfloat16* orow = out + (((int64_t)cu.b * M + i) * d.Hq + hq) * d.D + half * 64;
           float* lrow = lse != nullptr ? lse + ((int64_t)cu.b * M + i) * d.Hq + hq : nullptr;
           const int own = cu.tile - tile0 + 1;  // tiles of the pair run by this CTA
-          if (tile0 > 0) {
+          if (tile0 > 0 || (kView && gather && own < cu.nt)) {
             // ---- a later share of a split pair: a partial for the CTA that
             // ran the pair's first tile (unnormalised O of this half's 64
             // columns, the running maximum, this half's row sum, the tiles)
@@ -966,8 +969,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
               }
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->ebar));
-            if (helper < 0 && warp == 0 && lane == 0 &&
+            if (lane == 0 && !(kView && gather)) ptx::mbar_arrive(ptx::smem_u32(&bars->ebar));
+            if (helper < 0 && !(kView && gather) && warp == 0 && lane == 0 &&
                 ptx::mbar_wait_t<kShort>(ptx::smem_u32(&bars->ebar), 0, abort, wait)) {
               // every row of the partial is written (the barrier above); the
               // fence makes them visible GPU-wide before the tiles are counted
@@ -1137,7 +1140,7 @@ __device__ __forceinline__ void block_scan(int64_t& a, int64_t& c, int& m, int64
 template <int kMode>
 __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     const int32_t* block_table, const int32_t* ctx_lens,
-    const int32_t* parent, spec_dims d, int window, int sinks, AttnView view, int G,
+    const int32_t* parent, spec_dims d, int window, int sinks, AttnView view, int gather, int G,
     int32_t* __restrict__ depth_ws, int32_t* __restrict__ ntiles,
     int64_t* __restrict__ pre, int4* __restrict__ rq, int4* __restrict__ starts,
     int* __restrict__ pairs, ulonglong2* __restrict__ anc_ws,
@@ -1286,6 +1289,7 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
       tpre[r] = carry_t + vt;
       cpre[r] = carry_c + vc;
       rq[r] = make_int4(cx, nt, B, kWin ? win_skip_pages(cx, window, sinks) : own);
+      if (kView && gather) pre[r] = carry_t + vt;  // for the merge (tpre itself past kPlanReqs)
       if (small) {
         s_nt[r] = nt;
         s_ctx[r] = cx;
@@ -1307,9 +1311,11 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
   // kWinMinCost of the cost, because every further CTA of a pair is a partial
   // that the pair's first CTA reads in turn; a view, which may be a whole long
   // context, sqrt(2.3 n) for n tiles a pair at least (a partial costs that much more
-  // than a tile).
+  // than a tile).  Where a kernel of its own merges, partials cost little.
   int64_t least = kWinMinCost;
-  if (kView && Ctot > T)
+  if (kView && gather)
+    least = kGatherMinCost;
+  else if (kView && Ctot > T)
     least = max(least, (int64_t)sqrtf(2.3f * (float)T * kSegCost / (float)(Ctot - T)));
   const int Ge = kMode != kPlain ? (int)max((int64_t)1, min((int64_t)G, Ctot / least)) : G;
   if (tid == 0) {
@@ -1368,6 +1374,77 @@ __global__ void __launch_bounds__(kPrepThreads) attn_prep_kernel(
     const int4 rec = small ? make_int4(s_ctx[r], s_nt[r], s_next[r], 0) : rq[r];
     starts[2 * k + 1] = make_int4(rec.x, rec.y, rec.z, s_g0[k + 1]);
   }
+}
+
+// Merge of the split pairs of a small batch of views: a warp per row.  The CTAs
+// that ran the pair follow from their first tiles; one that ran it alone has
+// written its outputs.
+__global__ void __launch_bounds__(256) view_merge_kernel(const float* part, const int4* rq,
+                                                         const int64_t* pre, const int4* starts,
+                                                         int G, spec_dims d,
+                                                         __nv_bfloat16* __restrict__ out,
+                                                         float* __restrict__ lse) {
+  pdl_trigger();
+  const int warp = threadIdx.x / kWarp, lane = threadIdx.x % kWarp;
+  const int group = d.Hq / d.Hkv, R = group * d.M;
+  const int r = blockIdx.x * (blockDim.x / kWarp) + warp, h = blockIdx.y, b = blockIdx.z;
+  pdl_wait();  // the partials and the plan come from the previous kernels
+  if (r >= R) return;
+  const int nt = __ldcg(&rq[b].y);
+  if (nt == 0) return;  // the request has failed its checks
+  const int first = (int)(__ldcg(pre + b) + (int64_t)h * nt);  // the pair's first tile
+  int upto = 0, before = 0;  // CTAs that start at `first` or before, before its last tile's end
+  for (int k = lane; k < G; k += kWarp) {
+    const int g0 = __ldcg(&starts[2 * k].x);
+    upto += g0 <= first;
+    before += g0 < first + nt;
+  }
+  const int c0 = __reduce_add_sync(0xffffffffu, upto) - 1;
+  const int c1 = __reduce_add_sync(0xffffffffu, before) - 1;
+  if (c0 >= c1) return;
+  const int64_t pair = (int64_t)b * d.Hkv + h;
+  const int S = tc_part_stride(d.D);
+  float mx = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = c0; k0 <= c1; k0 += kWarp) {
+    const int n = min(kWarp, c1 + 1 - k0);
+    float m = -INFINITY, l = 0.f;
+    if (lane < n) {
+      const int g0 = __ldcg(&starts[2 * (k0 + lane)].x), g1 = __ldcg(&starts[2 * (k0 + lane) + 1].w);
+      if (g0 < g1) {  // else it had no tiles and wrote nothing
+        const float4 s =
+            __ldcg(reinterpret_cast<const float4*>(part + ((pair + k0 + lane) * R + r) * (int64_t)S + d.D));
+        m = s.x;
+        l = s.y + s.z;
+      }
+    }
+    const float mn = fmaxf(mx, warp_max(m));
+    const float w = m == -INFINITY ? 0.f : exp2f(m - mn);
+    const float a = mx == -INFINITY ? 0.f : exp2f(mx - mn);
+    sum = sum * a + warp_sum(w * l);
+    acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+    mx = mn;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      if (wk == 0.f) continue;  // nothing written, or nothing seen
+      const float4 v =
+          __ldcg(reinterpret_cast<const float4*>(part + ((pair + k0 + k) * R + r) * (int64_t)S) + lane);
+      acc.x = fmaf(wk, v.x, acc.x);
+      acc.y = fmaf(wk, v.y, acc.y);
+      acc.z = fmaf(wk, v.z, acc.z);
+      acc.w = fmaf(wk, v.w, acc.w);
+    }
+  }
+  const int i = r / group;
+  const int64_t at = ((int64_t)b * d.M + i) * d.Hq + h * group + r - i * group;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint2 o;
+  o.x = ptx::pack_bf16x2(acc.x * inv, acc.y * inv);
+  o.y = ptx::pack_bf16x2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(out + at * 128 + lane * 4) = o;
+  if (lse != nullptr && lane == 0)
+    lse[at] = sum > 0.f ? (mx + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
 // ---------------------------------------------------------------------------
@@ -1438,6 +1515,12 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
   const int G = sms < kMaxAttnCtas ? sms : kMaxAttnCtas;
 
   const bool viewed = a.view.mode != kViewNone, behind = a.view.mode == kViewPrefix;
+  // Few pairs of many tiles over a view: pairs are split finely and merged by a
+  // kernel of its own, where else a pair's first CTA merges.  us without / with: 4
+  // pairs of 201 tiles 43 / 34, 8 of 190 52 / 31, 8 of 65 31 / 25, 32 of 33 25 / 22, 36
+  // of up to 60 27 / 24; 64 pairs of 11 24 / 24, 144 of 34 39 / 42 and 45 / 53.
+  const int gather = viewed && !behind && 3 * (int64_t)d.B * d.Hkv <= G &&
+                     ceil_div(a.view.entries, kPages) > 2;
   float* own_part = reinterpret_cast<float*>(ws + lay.own_part_off);
   PrefixPlan plan = {};
   {
@@ -1446,8 +1529,8 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
                            viewed         ? attn_prep_kernel<kViewed>
                            : a.window > 0 ? attn_prep_kernel<kWindow>
                                           : attn_prep_kernel<kPlain>,
-                           a.block_table, a.ctx_lens, a.parent, d, a.window, a.sinks, a.view, G,
-                           depth, ntiles, pre, rq, starts, pairs, anc, arrivals,
+                           a.block_table, a.ctx_lens, a.parent, d, a.window, a.sinks, a.view,
+                           gather, G, depth, ntiles, pre, rq, starts, pairs, anc, arrivals,
                            static_cast<__nv_bfloat16*>(a.out), a.lse, status);
     if (e != cudaSuccess) return e;
   }
@@ -1474,7 +1557,7 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
                            static_cast<__nv_bfloat16*>(a.v_cache), a.block_table,
                            (const int4*)rq, (const int4*)starts,
                            a.parent != nullptr || a.window > 0 ? (const ulonglong2*)anc : nullptr,
-                           (const int*)depth, a.window, a.sinks, a.view, pairs, d, qscale2, part,
+                           (const int*)depth, a.window, a.sinks, a.view, gather, pairs, d, qscale2, part,
                            behind ? own_part : nullptr, static_cast<__nv_bfloat16*>(a.out), a.lse,
                            status);
     if (e != cudaSuccess) return e;
@@ -1483,6 +1566,14 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
   if (behind) {
     const OwnPart own = {own_part, 1, tc_part_stride(d.D), INT32_MAX, a.view.ctx, ntiles};
     return prefix_merge_launch(a, lay, plan, own, st, launches);
+  }
+  if (gather) {
+    PdlLaunch L(dim3(ceil_div(group * d.M, 8), d.Hkv, d.B), dim3(256), 0, st);
+    e = cudaLaunchKernelEx(&L.cfg, view_merge_kernel, (const float*)part, (const int4*)rq,
+                           (const int64_t*)pre, (const int4*)starts, G, d,
+                           static_cast<__nv_bfloat16*>(a.out), a.lse);
+    if (e != cudaSuccess) return e;
+    ++*launches;
   }
   return cudaGetLastError();
 }
