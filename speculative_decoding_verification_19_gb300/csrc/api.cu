@@ -162,18 +162,27 @@ spec_status spec_get_device_status(void* ws, void* stream, int32_t* flags, int32
 //   tensor cores, by B * Hkv * prefix: 262144 keys 39 / 42 (4, 8, 4, 1, 8192), 38 / 47
 //   (16, 8, 4, 5, 2048), 46 / 52 (64, 8, 8, 1, 512); 524288 64 / 62 (64, 1, 4, 9,
 //   8192); 786432 81 / 60 (4, 8, 4, 1, 24576), 78 / 76 (16, 2, 8, 1, 24576)
-//   fp32 on CUDA cores, where the products cost too, by keys times rows per KV head:
-//   0.52 M 33 / 41 (16, 2, 8, 1, 2048), 1.05 M 69 / 61 (8, 4, 1, 64, 512), 66 / 81 (4,
-//   8, 4, 1, 8192), 1.3 M 53 / 49 (16, 8, 4, 5, 512), 2.1 M 89 / 55 (64, 8, 8, 1, 512)
-//   bf16 heads of 64, the pass on tensor cores and the rest on CUDA cores, likewise:
-//   66 K 21 / 22 (1, 8, 4, 1, 2048), 23 / 21 (4, 8, 4, 1, 512), 131 K 42 / 33 (4, 1, 8, 8,
-//   512), 0.52 M 33 / 28 (16, 2, 8, 1, 2048)
+//   CUDA cores: the requests' reads cost 2.75 us for 10^6 elements of keys and 0.15 for
+//   10^6 products (more than 8 rows), the pass 21 or 29 us (heads of 64, 128) and 0.09
+//   for 10^6 products of whole tiles of 64 rows.  fp32, heads of 64: 21 / 29 (8, 8, 1,
+//   1, 512), 40 / 39 (8, 8, 1, 1, 2048), 41 / 50 (4, 8, 1, 1, 4096), 69 / 81 (2, 8, 1, 1,
+//   16384), 79 / 39 (64, 8, 1, 1, 512), 112 / 44 (26, 8, 1, 1, 2208); heads of 128: 38 / 52
+//   (16, 2, 4, 1, 2048), 41 / 61 (4, 8, 4, 1, 2048), 46 / 57 (8, 8, 4, 5, 512), 74 / 69 (16, 8,
+//   4, 5, 512), 77 / 48 (16, 8, 1, 1, 1024), 112 / 89 (4, 8, 4, 1, 8192), 147 / 55 (64, 8, 1, 1,
+//   512)
+//   bf16 heads of 64, the pass on tensor cores and the rest on CUDA cores, by keys and
+//   keys times rows: 17 / 19 (4, 8, 4, 1, 512), 20 / 20 (8, 8, 1, 1, 512), 25 / 30 (1, 2, 4, 1,
+//   4096), 27 / 22 (16, 8, 1, 1, 512), 39 / 24 (8, 8, 1, 1, 2048), 42 / 33 (4, 1, 8, 8, 512)
 static bool prefix_in_requests(const spec_dims& d, int prefix_len, bool tc) {
   const int64_t keys = (int64_t)d.B * d.Hkv * prefix_len;
   if (tc) return keys <= 400000;
-  const int64_t products = keys * (d.Hq / d.Hkv) * d.M;
-  if (d.attn_impl != SPEC_ATTN_CUDA_CORES && prefix_tc_ok(d)) return products <= 100000;
-  return d.B == 1 || products <= 800000;
+  const int64_t rows = (int64_t)(d.Hq / d.Hkv) * d.M;
+  if (d.attn_impl != SPEC_ATTN_CUDA_CORES && prefix_tc_ok(d))
+    return keys <= 40000 && keys * rows <= 100000;
+  const double tiles = 64.0 * (double)ceil_div64(d.B * rows, 64) * d.Hkv * prefix_len;
+  const double requests = d.D * 1e-6 * (2.75 * (double)keys + 0.15 * (double)(keys * rows));
+  const double pass = (d.D == 64 ? 21.0 : 29.0) + d.D * 1e-6 * 0.09 * tiles;
+  return d.B == 1 || requests <= pass;
 }
 
 static spec_status attn_common(const void* q, const void* k_new, const void* v_new, void* k_cache,

@@ -661,7 +661,7 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
                              (int64_t)ceil_div(a.sinks, kTileKeys) * kTileKeys + a.window + d.M +
                                  kTileKeys);
     const int64_t want =
-        max((int64_t)kMinWinSplit, tiled ? (int64_t)d.B * d.Hkv * ceil_div(R, 64) * most / view_ctas(d)
+        max((int64_t)kMinWinSplit, tiled ? (int64_t)d.B * d.Hkv * ceil_div(R, 64) * most / view_ctas()
                                          : (int64_t)d.B * d.Hkv * most / kWinCtas);
     const int unit = tiled ? view_range_unit(d) : kTileKeys;
     int64_t ranges = lay.max_splits;

@@ -194,7 +194,7 @@ struct ViewRanges {
   int split_keys;
 };
 int view_range_unit(const spec_dims& d);  // ranges are whole numbers of it
-int view_ctas(const spec_dims& d);        // CTAs of a wave
+int view_ctas();                          // CTAs of a wave
 cudaError_t view_split_launch(const AttnArgs& a, const ViewRanges& own, int splits, float* part,
                               cudaStream_t st);
 

@@ -17,6 +17,7 @@
 
 #include "attn.cuh"
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace specv {
 
@@ -24,27 +25,32 @@ namespace specv {
 // the prefix on CUDA cores
 // ---------------------------------------------------------------------------
 // A CTA runs 64 rows of a KV head over a range of key tiles.  Both products
-// are register tiles of 8 rows per thread: scores 8 x kKeys / 16, outputs
-// 8 x D / 16, with the operands that the rows index (queries, probabilities)
-// transposed in shared memory, so that a thread's 8 rows are two 16-byte loads
-// that 16 lanes share.  fp32 throughout, two rows a packed FMA.
+// are register tiles of 8 rows per thread: scores 8 x kKeys / 16, summed in two
+// halves (even and odd coordinates) so that a packed FMA takes what lies side by
+// side in memory, outputs 8 x D / 16, two rows a packed FMA, with the probabilities
+// transposed in shared memory.  The next keys are on their way (cp.async) from the
+// end of the scores on, the next values from the end of the products with these.
+// fp32 throughout.
 constexpr int kPfxRows = 64, kPfxThreads = 128;
+constexpr int kPfxCtas = 3;  // of an SM (68 KB with heads of 64, 74 KB with heads of 128)
 // Ranges of all units together, at least the units: one wave of the CTAs that an
-// SM holds.  As many ranges as that gives: a tile takes a lone CTA of an SM some 10
-// us (26 requests of one row, 8 heads of 64, 2208 positions: 57 us for the call with
-// a tile a range, 70 with two), its partial in the merge 0.3.
-__host__ __device__ constexpr int pfx_slots(int D) { return (D == 64 ? 4 : 3) * 152; }
+// SM holds, but no more than kPfxSplits lets: a partial in the merge costs 0.2 us, a
+// tile in a range some 8.  us with as many ranges as there are tiles / with half of
+// them: 8 tiles 29 / 35, 35 tiles 44 / 50, 64 tiles 52 / 44, 256 tiles (228 ranges, 128)
+// 95 / 69.
+constexpr int kPfxSlots = kPfxCtas * 152;
+constexpr int kPfxSplits = 40;  // ranges of a unit: at most the root of this times its tiles
 
 template <int D>
 struct PfxTile {
-  // 64 keys with heads of 64 (51 KB: four CTAs an SM), 32 with heads of 128 (70 KB:
-  // three); the probabilities go where the keys were
   static constexpr int kKeys = D == 64 ? 64 : 32;
-  static constexpr int kLd = kPfxRows + 4;   // padded rows of the transposed tiles
-  static constexpr int kLdK = kKeys + 4;
-  static constexpr size_t smem = sizeof(float) * ((size_t)D * kLd + D * kLdK + kKeys * D) +
-                                 sizeof(ulonglong2) * kPfxRows;
-  static_assert(kKeys * kLd <= D * kLdK, "the probabilities fit the keys' place");
+  static constexpr int kLd = kPfxRows + 4;  // padded rows of the transposed probabilities
+  static constexpr int kLdK = D + 4;        // 16 keys' vectors: two wavefronts
+  // eight rows of queries, then 16 bytes: the two row groups of a warp in other banks
+  static constexpr int kQ = kPfxRows * D + 4 * (kPfxRows / 8);
+  static constexpr size_t smem =
+      sizeof(float) * ((size_t)kQ + kKeys * kLdK + kKeys * D + kKeys * kLd) +
+      sizeof(ulonglong2) * kPfxRows;
 };
 
 __device__ __forceinline__ unsigned long long pair_of(float a, float b) {
@@ -63,12 +69,12 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
 
 // kOwn: the same tiles over views of the requests (attn_win_split_kernel's work)
 // for more than 32 rows per KV head: 64 rows of a request, its view's keys in
-// ranges of split_keys, the new rows' masks from the append kernel.  8 trees of 64
-// rows, 8 heads of 64 fp32 values over 33 pages: 43 us for the call, 48 with the
-// windowed kernel; 13 requests of 36 rows, 4 heads of 128 over 45 pages 63 us, 77.
-// Up to 32 rows a tile would be half empty.
+// ranges of split_keys, the new rows' masks from the append kernel.  13 requests of
+// 36 rows, 4 heads of 128 fp32 values over 45 pages: 61 us for the call, 77 with the
+// windowed kernel.  Up to 32 rows a tile would be half empty: 13 requests of 32 rows
+// 62 us, 53 with the windowed kernel; 8 of 32, 8 heads of 64 over 33 pages 48, 39.
 template <typename T, int D, bool kOwn>
-__global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kernel(
+__global__ void __launch_bounds__(kPfxThreads, kPfxCtas) prefix_simt_kernel(
     const T* q, const T* k_cache, const T* v_cache, const int32_t* table, int prefix_len,
     spec_dims d, float qscale, PrefixPlan plan, ViewRanges own, float* __restrict__ part) {
   using Tile = PfxTile<D>;
@@ -77,10 +83,10 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
   constexpr int CPT = D / 16;      // output columns of a thread
   constexpr int kVec = 16 / sizeof(T), kVecRow = D / kVec;
   extern __shared__ __align__(16) float smem[];
-  float* qt = smem;             // [D][kLd]   queries, scaled
-  float* kt = qt + D * kLd;     // [D][kLdK]  keys
-  float* vs = kt + D * kLdK;    // [kKeys][D] values, a thread's keys 16 rows apart
-  float* pt = kt;               // [kKeys][kLd] probabilities, the same order of keys
+  float* qs = smem;                // [64][D] queries, scaled, 16 bytes after every eighth
+  float* ks = qs + Tile::kQ;       // [kKeys][kLdK]
+  float* vs = ks + kKeys * kLdK;   // [kKeys][D]
+  float* pt = vs + kKeys * D;      // [kKeys][kLd] probabilities
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int s = blockIdx.x % plan.splits, tile = blockIdx.x / plan.splits, h = blockIdx.y;
   const int group = d.Hq / d.Hkv, R = group * d.M;
@@ -89,7 +95,7 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
   pdl_wait();  // the queries, the cache and the views may come from the previous kernels
   const int own_b = kOwn ? blockIdx.z : 0;
   int ctx = prefix_len, k0, k1;  // cached keys, and the range of keys
-  ulonglong2* anc = reinterpret_cast<ulonglong2*>(vs + kKeys * D);  // masks of the rows (kOwn)
+  ulonglong2* anc = reinterpret_cast<ulonglong2*>(pt + kKeys * kLd);  // masks of the rows (kOwn)
   if constexpr (kOwn) {
     if (!__ldcg(own.ok + own_b)) return;
     ctx = __ldcg(own.ctx + own_b);
@@ -106,8 +112,50 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
     k1 = min((int)((int64_t)(s + 1) * plan.key_tiles / plan.splits) * kKeys, prefix_len);
   }
 
+  // keys or values of the tile at t0 by 16-byte vectors, those past the range zero;
+  // block ids of its pages in id
+  constexpr int kTilePages = kKeys / kBlock;
+  auto ids_of = [&](int t0, int(&id)[kTilePages]) {
+#pragma unroll
+    for (int p = 0; p < kTilePages; ++p) {
+      id[p] = t0 + p * kBlock < k1 ? __ldcg(table + t0 / kBlock + p) : 0;
+      // no block id: the request check fails every request
+      if ((uint32_t)id[p] >= (uint32_t)d.num_blocks) id[p] = 0;
+    }
+  };
+  auto load = [&](const T* cache, int t0, const int(&id)[kTilePages], float* to, int ld) {
+    constexpr int kItems = kKeys * kVecRow / kPfxThreads;  // vectors of a thread
+    constexpr int kStep = kPfxThreads / kVecRow;           // keys of a round of the threads
+    const int vi = tid % kVecRow, kk0 = tid / kVecRow;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int kk = kk0 + i * kStep;
+      const bool there = t0 + kk < k1;
+      int blk = id[0];  // of page kk / 16
+#pragma unroll
+      for (int p = 1; p < kTilePages; ++p)
+        if (kk / kBlock == p) blk = id[p];
+      const T* src = cache + (((int64_t)blk * d.Hkv + h) * kBlock + kk % kBlock) * D + vi * kVec;
+      float* dst = to + kk * ld + vi * kVec;
+      if constexpr (sizeof(T) == 4) {
+        ptx::cp_async16_fill(ptx::smem_u32(dst), src, there ? 16u : 0u);
+      } else {
+        float f[kVec];
+        unpack16(there ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+        for (int c = 0; c < kVec; c += 4)
+          *reinterpret_cast<float4*>(dst + c) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int id[kTilePages];  // of the tile whose keys are to be loaded next, then its values
+  ids_of(k0, id);
+  load(k_cache, k0, id, ks, kLdK);
+  load(v_cache, k0, id, vs, D);
+
   for (int e = tid; e < kPfxRows * kVecRow; e += kPfxThreads) {
-    const int r = e % kPfxRows, vi = e / kPfxRows;
+    const int r = e / kVecRow, vi = e % kVecRow;
     const int gr = tile * kPfxRows + r;
     float f[kVec];
 #pragma unroll
@@ -117,8 +165,11 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
       const int64_t at = (((int64_t)b * d.M + i) * d.Hq + h * group + rr - i * group) * D;
       unpack16(reinterpret_cast<const uint4*>(q + at)[vi], f);
     }
+    float* to = qs + r * D + (r >> 3) * 4 + vi * kVec;
 #pragma unroll
-    for (int c = 0; c < kVec; ++c) qt[(vi * kVec + c) * kLd + r] = f[c] * qscale;
+    for (int c = 0; c < kVec; c += 4)
+      *reinterpret_cast<float4*>(to + c) = make_float4(f[c] * qscale, f[c + 1] * qscale,
+                                                       f[c + 2] * qscale, f[c + 3] * qscale);
   }
 
   unsigned long long o[4][CPT];  // row pairs x columns
@@ -134,61 +185,39 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
     for (int c = 0; c < CPT; ++c) o[r][c] = 0ull;
 
   for (int t0 = k0; t0 < k1; t0 += kKeys) {
-    __syncthreads();  // the last tile is consumed
-    for (int e = tid; e < kKeys * kVecRow; e += kPfxThreads) {
-      // two neighbouring vectors of 16 keys a warp: whole sectors from global
-      // memory, no bank conflicts in the transposed stores
-      const int vi = (e & 1) | ((e / (2 * kKeys)) << 1), kk = (e >> 1) % kKeys;
-      const int t = t0 + kk;
-      float kf[kVec], vf[kVec];
-#pragma unroll
-      for (int c = 0; c < kVec; ++c) kf[c] = vf[c] = 0.f;
-      if (t < k1) {
-        const int id = __ldcg(table + t / kBlock);
-        // no block id: the request check fails every request
-        const int64_t blk = (uint32_t)id < (uint32_t)d.num_blocks ? id : 0;
-        const int64_t base = ((blk * d.Hkv + h) * kBlock + t % kBlock) * D;
-        unpack16(reinterpret_cast<const uint4*>(k_cache + base)[vi], kf);
-        unpack16(reinterpret_cast<const uint4*>(v_cache + base)[vi], vf);
-      }
-      const int slot = (kk % KPT) * 16 + kk / KPT;  // key kk is number kk % KPT of thread kk / KPT
-#pragma unroll
-      for (int c = 0; c < kVec; ++c) kt[(vi * kVec + c) * kLdK + kk] = kf[c];
-#pragma unroll
-      for (int c = 0; c < kVec; c += 4)
-        *reinterpret_cast<float4*>(vs + slot * D + vi * kVec + c) =
-            make_float4(vf[c], vf[c + 1], vf[c + 2], vf[c + 3]);
-    }
-    __syncthreads();
+    const bool more = t0 + kKeys < k1;
+    if (more) ids_of(t0 + kKeys, id);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();  // the tile's keys are there
 
-    unsigned long long sc[4][KPT];
+    unsigned long long sc[8][KPT];  // row r, key k * 16 + tx
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
+    for (int r = 0; r < 8; ++r)
 #pragma unroll
       for (int k = 0; k < KPT; ++k) sc[r][k] = 0ull;
-#pragma unroll 4
-    for (int dd = 0; dd < D; ++dd) {
-      const ulonglong2 qa = *reinterpret_cast<const ulonglong2*>(qt + dd * kLd + ty * 8);
-      const ulonglong2 qb = *reinterpret_cast<const ulonglong2*>(qt + dd * kLd + ty * 8 + 4);
-      const unsigned long long qv[4] = {qa.x, qa.y, qb.x, qb.y};
-      float kv[KPT];
-      if constexpr (KPT == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(kt + dd * kLdK + tx * 4);
-        kv[0] = x.x; kv[1] = x.y; kv[2] = x.z; kv[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(kt + dd * kLdK + tx * 2);
-        kv[0] = x.x; kv[1] = x.y;
-      }
+    const float* qrow = qs + ty * 8 * D + ty * 4;
+    const float* krow = ks + tx * kLdK;
+#pragma unroll 2
+    for (int dd = 0; dd < D; dd += 4) {
+      ulonglong2 kv[KPT];
 #pragma unroll
-      for (int k = 0; k < KPT; ++k) {
-        const unsigned long long kk = pair_of(kv[k], kv[k]);
+      for (int k = 0; k < KPT; ++k)
+        kv[k] = *reinterpret_cast<const ulonglong2*>(krow + k * 16 * kLdK + dd);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sc[r][k] = fma2(qv[r], kk, sc[r][k]);
+      for (int r = 0; r < 8; ++r) {
+        const ulonglong2 qv = *reinterpret_cast<const ulonglong2*>(qrow + r * D + dd);
+#pragma unroll
+        for (int k = 0; k < KPT; ++k) {
+          sc[r][k] = fma2(qv.x, kv[k].x, sc[r][k]);
+          sc[r][k] = fma2(qv.y, kv[k].y, sc[r][k]);
+        }
       }
     }
     __syncthreads();  // the keys are consumed
+    if (more) load(k_cache, t0 + kKeys, id, ks, kLdK);
+    else asm volatile("cp.async.commit_group;" ::: "memory");
     // softmax: the 16 threads of a row group share its rows
-    const int left = k1 - t0 - tx * KPT;  // this thread's keys below it are real
+    const int left = k1 - t0 - tx;  // this thread's key k is real if k * 16 is below it
     const bool masked = kOwn && t0 + kKeys > ctx;  // the tile reaches the new rows
     float p[8][KPT];
 #pragma unroll
@@ -196,10 +225,10 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
       float mt = -INFINITY;
 #pragma unroll
       for (int k = 0; k < KPT; ++k) {
-        const float x = (r & 1) ? hi_of(sc[r / 2][k]) : lo_of(sc[r / 2][k]);
-        bool see = k < left;
+        const float x = lo_of(sc[r][k]) + hi_of(sc[r][k]);
+        bool see = k * 16 < left;
         if (masked && see) {
-          const int n = t0 + tx * KPT + k - ctx;  // new row, < M as the key is real
+          const int n = t0 + k * 16 + tx - ctx;  // new row, < M as the key is real
           const ulonglong2 m2 = anc[ty * 8 + r];
           see = n < 0 || ((n < 64 ? m2.x : m2.y) >> (n & 63)) & 1ull;
         }
@@ -232,7 +261,9 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
       *reinterpret_cast<float4*>(row) = make_float4(p[0][k], p[1][k], p[2][k], p[3][k]);
       *reinterpret_cast<float4*>(row + 4) = make_float4(p[4][k], p[5][k], p[6][k], p[7][k]);
     }
-    __syncwarp();  // a row group's probabilities stay inside its warp
+    // a row group's probabilities stay inside its warp; the tile's values are there
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
 #pragma unroll 4
     for (int k = 0; k < kKeys; ++k) {
       const ulonglong2 pa = *reinterpret_cast<const ulonglong2*>(pt + k * kLd + ty * 8);
@@ -250,7 +281,9 @@ __global__ void __launch_bounds__(kPfxThreads, D == 64 ? 4 : 3) prefix_simt_kern
         }
       }
     }
-    __syncwarp();
+    __syncthreads();  // the values are consumed
+    if (more) load(v_cache, t0 + kKeys, id, vs, D);
+    else asm volatile("cp.async.commit_group;" ::: "memory");
   }
 
   const int S = kOwn ? D + 1 : tc_part_stride(D);
@@ -365,8 +398,10 @@ static PrefixPlan simt_plan(const spec_dims& d, int prefix_len) {
   p.key_tiles = ceil_div(prefix_len, keys);
   p.ctas = 0;
   const int64_t units = (int64_t)d.Hkv * p.tiles;
-  int64_t splits = pfx_slots(d.D) / units;
+  int64_t splits = kPfxSlots / units;
   if (splits > p.key_tiles) splits = p.key_tiles;
+  const int most = (int)sqrt((double)kPfxSplits * p.key_tiles);
+  if (splits > most) splits = ceil_div(p.key_tiles, ceil_div(p.key_tiles, most));  // even ranges
   p.splits = splits < 1 ? 1 : (int)splits;
   return p;
 }
@@ -374,7 +409,7 @@ static PrefixPlan simt_plan(const spec_dims& d, int prefix_len) {
 size_t prefix_part_floats(const spec_dims& d) {
   const int64_t rows = (int64_t)d.B * (d.Hq / d.Hkv) * d.M;
   const int64_t units = (int64_t)d.Hkv * ceil_div64(rows, kPfxRows);
-  const int64_t slots = units > pfx_slots(d.D) ? units : pfx_slots(d.D);
+  const int64_t slots = units > kPfxSlots ? units : kPfxSlots;
   const size_t simt = (size_t)slots * (size_t)(rows < kPfxRows ? rows : kPfxRows) * tc_part_stride(d.D);
   const size_t tc = prefix_tc_part_floats(d);
   return simt > tc ? simt : tc;
@@ -395,7 +430,7 @@ static cudaError_t launch_simt(const AttnArgs& a, const PrefixPlan& p, const Vie
 }
 
 int view_range_unit(const spec_dims& d) { return d.D == 64 ? PfxTile<64>::kKeys : PfxTile<128>::kKeys; }
-int view_ctas(const spec_dims& d) { return pfx_slots(d.D); }
+int view_ctas() { return kPfxSlots; }
 
 cudaError_t view_split_launch(const AttnArgs& a, const ViewRanges& own, int splits, float* part,
                               cudaStream_t st) {
