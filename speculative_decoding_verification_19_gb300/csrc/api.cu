@@ -159,9 +159,12 @@ spec_status spec_get_device_status(void* ws, void* stream, int32_t* flags, int32
 // the first), rather than one pass over it for the batch with a merge after it.
 // The pass and the merge cost 10 to 25 us, the other grows with the requests.
 // Measured, us, requests / one pass (B, Hkv, group, M, prefix):
-//   tensor cores, by B * Hkv * prefix: 262144 keys 39 / 42 (4, 8, 4, 1, 8192), 38 / 47
-//   (16, 8, 4, 5, 2048), 46 / 52 (64, 8, 8, 1, 512); 524288 64 / 62 (64, 1, 4, 9,
-//   8192); 786432 81 / 60 (4, 8, 4, 1, 24576), 78 / 76 (16, 2, 8, 1, 24576)
+//   tensor cores: the requests' reads cost 82 us for 10^6 keys (heads of 128), the pass
+//   24 us and 0.8 for 10^9 operations of whole units of 256 rows.  38 / 62 (64, 1, 4, 1,
+//   4096), 42 / 51 (16, 8, 8, 5, 2048), 45 / 49 (64, 8, 8, 1, 512), 62 / 70 (2, 8, 4, 1,
+//   32768), 64 / 62 (64, 1, 4, 9, 8192), 64 / 66 (8, 8, 8, 9, 8192), 55 / 44 (16, 8, 4, 1,
+//   4096), 60 / 51 (64, 8, 4, 1, 1024), 81 / 60 (4, 8, 4, 1, 24576), 121 / 144 (1, 8, 4, 1,
+//   131072)
 //   CUDA cores: the requests' reads cost 2.75 us for 10^6 elements of keys and 0.15 for
 //   10^6 products (more than 8 rows), the pass 21 or 29 us (heads of 64, 128) and 0.09
 //   for 10^6 products of whole tiles of 64 rows.  fp32, heads of 64: 21 / 29 (8, 8, 1,
@@ -175,8 +178,11 @@ spec_status spec_get_device_status(void* ws, void* stream, int32_t* flags, int32
 //   4096), 27 / 22 (16, 8, 1, 1, 512), 39 / 24 (8, 8, 1, 1, 2048), 42 / 33 (4, 1, 8, 8, 512)
 static bool prefix_in_requests(const spec_dims& d, int prefix_len, bool tc) {
   const int64_t keys = (int64_t)d.B * d.Hkv * prefix_len;
-  if (tc) return keys <= 400000;
   const int64_t rows = (int64_t)(d.Hq / d.Hkv) * d.M;
+  if (tc) {
+    const double units = 256.0 * (double)ceil_div64(d.B * rows, 256) * d.Hkv * prefix_len;
+    return d.B == 1 || 82e-6 * (double)keys <= 24.0 + 0.8e-9 * 4.0 * d.D * units;
+  }
   if (d.attn_impl != SPEC_ATTN_CUDA_CORES && prefix_tc_ok(d))
     return keys <= 40000 && keys * rows <= 100000;
   const double tiles = 64.0 * (double)ceil_div64(d.B * rows, 64) * d.Hkv * prefix_len;

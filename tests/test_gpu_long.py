@@ -152,12 +152,23 @@ def test_prefix(ctx, P, M, Hq, Hkv, D, dt, tree, impl):
     ([8208] * 50, 8208, 1, 8, 1, 128, BF, TC),                              # 400 rows of a head
     ([8000 + b for b in range(60)], 8000, 5, 1, 1, 128, BF, TC),            # a third unit's tile
     ([12816, 12817, 12830, 12900], 12816, 1, 8, 8, 128, BF, TC),            # four rows of a head
+    ([14000, 14001, 14030, 14100], 14000, 1, 8, 8, 128, BF, TC),            # as many, a longer prefix
     ([64 + b % 20 for b in range(6500)], 64, 1, 1, 1, 128, BF, TC),         # less than a key tile
     ([4000 + 3 * b for b in range(3)], 4000, 40, 6, 2, 64, BF, AUTO),
     ([16400 + 3 * b for b in range(13)], 16400, 2, 3, 3, 128, F32, AUTO)])
 def test_prefix_in_one_pass(ctx, P, M, Hq, Hkv, D, dt, impl):
     """Sizes at which the prefix is read once in a pass of its own."""
     prefix_step(ctx, P, M, Hq, Hkv, D, dt, 4, impl=impl)
+
+
+@pytest.mark.parametrize("ctx,P,M,Hq,Hkv,D,dt,tree,impl", [
+    ([3216 + 5 * b for b in range(24)], 3216, 40, 4, 2, 64, F32, True, AUTO),  # own keys in tiles
+    ([1616 + b for b in range(30)], 1616, 3, 9, 3, 128, BF, False, CORES),     # 270 rows of a head
+    ([1008 + b % 3 for b in range(40)], 1008, 1, 8, 8, 64, BF, False, CORES),  # a last tile of 48
+    ([1040 + 9 * b for b in range(40)], 1040, 33, 2, 2, 128, F32, True, AUTO),
+    ([48 + b % 20 for b in range(8200)], 48, 1, 1, 1, 64, F32, False, AUTO)])  # less than a tile
+def test_prefix_in_one_pass_on_cuda_cores(ctx, P, M, Hq, Hkv, D, dt, tree, impl):
+    prefix_step(ctx, P, M, Hq, Hkv, D, dt, 6, tree=tree, impl=impl)
 
 
 @pytest.mark.parametrize("impl", [CORES, TC])
