@@ -660,9 +660,16 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
     const int64_t most = min(entries * kBlock,
                              (int64_t)ceil_div(a.sinks, kTileKeys) * kTileKeys + a.window + d.M +
                                  kTileKeys);
-    const int64_t want =
-        max((int64_t)kMinWinSplit, tiled ? (int64_t)d.B * d.Hkv * ceil_div(R, 64) * most / view_ctas()
-                                         : (int64_t)d.B * d.Hkv * most / kWinCtas);
+    // (tiles of rows: two waves where a CTA of one would have 160 keys or more, for what
+    // is uneven between requests: 20 requests of 64 rows, 8 heads of 128 fp32 values over
+    // 60 pages 208 us, 231 with one; 13 of 36 rows, 4 heads over 45 pages, 93 keys, 72
+    // with two waves, 62 with one)
+    int64_t want = (int64_t)d.B * d.Hkv * most / kWinCtas;
+    if (tiled) {
+      want = (int64_t)d.B * d.Hkv * ceil_div(R, 64) * most / view_ctas();
+      if (want >= 160) want /= 2;
+    }
+    if (want < kMinWinSplit) want = kMinWinSplit;
     const int unit = tiled ? view_range_unit(d) : kTileKeys;
     int64_t ranges = lay.max_splits;
     if (viewed && a.view.mode != kViewPrefix) {
