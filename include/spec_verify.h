@@ -292,7 +292,8 @@ spec_status spec_page_bounds(const void* k_cache, const int32_t* block_table,
  *   scores[b][h][p] = max over the rows i and query heads that read KV head h of
  *                     sum_d max(q_d * lo_d, q_d * hi_d)
  * with the page's bounds lo, hi: no row has a larger product q . k with a key
- * of the page (softmax_scale is not applied).  Sums in fp32.
+ * of the page, but for the rounding of the sums, which are in fp32
+ * (softmax_scale is not applied).
  *   q [B, M, Hq, D] kv_dtype, bounds as in spec_page_bounds
  *   scores [B, Hkv, max_blocks] float   -inf for p >= ctx_lens[b] / 16: pages
  *                 that are not whole are always read
@@ -311,7 +312,7 @@ spec_status spec_page_score(const void* q, const void* bounds, const int32_t* bl
  * Of the F = ctx_lens[b] / 16 whole pages the first `first`, the last `last`
  * and then those of largest score, the lower page first among equal scores,
  * until there are n_pages (all F if there are no more than that).
- *   scores [B, Hkv, max_blocks] float   those of pages from F on are not read;
+ *   scores [B, Hkv, max_blocks] float   those of pages from F on do not matter;
  *                 -0 equals 0; NaN counts as the lowest value and, among the
  *                 pages that compete, raises SPEC_ERR_NONFINITE
  *   n_pages 1 .. 2^30, first, last >= 0, first + last <= n_pages
