@@ -32,6 +32,95 @@ static int attn_split_keys(const spec_dims& d) {
   return (int)s;
 }
 
+// Whether every request reads a shared prefix itself (its pages come from L2 after
+// the first), rather than one pass over it for the batch with a merge after it.
+// The pass and the merge cost 10 to 25 us, the other grows with the requests.
+// Measured, us, requests / one pass (B, Hkv, group, M, prefix):
+//   tensor cores: the requests' reads cost 82 us for 10^6 keys (heads of 128), the pass
+//   24 us and 0.8 for 10^9 operations of whole units of 256 rows.  38 / 62 (64, 1, 4, 1,
+//   4096), 42 / 51 (16, 8, 8, 5, 2048), 45 / 49 (64, 8, 8, 1, 512), 62 / 70 (2, 8, 4, 1,
+//   32768), 64 / 62 (64, 1, 4, 9, 8192), 64 / 66 (8, 8, 8, 9, 8192), 55 / 44 (16, 8, 4, 1,
+//   4096), 60 / 51 (64, 8, 4, 1, 1024), 81 / 60 (4, 8, 4, 1, 24576), 121 / 144 (1, 8, 4, 1,
+//   131072)
+//   CUDA cores: the requests' reads cost 2.75 us for 10^6 elements of keys and 0.15 for
+//   10^6 products (more than 8 rows), the pass 21 or 29 us (heads of 64, 128) and 0.09
+//   for 10^6 products of whole tiles of 64 rows.  fp32, heads of 64: 21 / 29 (8, 8, 1,
+//   1, 512), 40 / 39 (8, 8, 1, 1, 2048), 41 / 50 (4, 8, 1, 1, 4096), 69 / 81 (2, 8, 1, 1,
+//   16384), 79 / 39 (64, 8, 1, 1, 512), 112 / 44 (26, 8, 1, 1, 2208); heads of 128: 38 / 52
+//   (16, 2, 4, 1, 2048), 41 / 61 (4, 8, 4, 1, 2048), 46 / 57 (8, 8, 4, 5, 512), 74 / 69 (16, 8,
+//   4, 5, 512), 77 / 48 (16, 8, 1, 1, 1024), 112 / 89 (4, 8, 4, 1, 8192), 147 / 55 (64, 8, 1, 1,
+//   512)
+//   bf16 heads of 64, the pass on tensor cores and the rest on CUDA cores, by keys and
+//   keys times rows: 17 / 19 (4, 8, 4, 1, 512), 20 / 20 (8, 8, 1, 1, 512), 25 / 30 (1, 2, 4, 1,
+//   4096), 27 / 22 (16, 8, 1, 1, 512), 39 / 24 (8, 8, 1, 1, 2048), 42 / 33 (4, 1, 8, 8, 512)
+static bool prefix_in_requests(const spec_dims& d, int64_t prefix_len, bool tc) {
+  const int64_t keys = (int64_t)d.B * d.Hkv * prefix_len;
+  const int64_t rows = (int64_t)(d.Hq / d.Hkv) * d.M;
+  if (tc) {
+    const double units = 256.0 * (double)ceil_div64(d.B * rows, 256) * d.Hkv * prefix_len;
+    return d.B == 1 || 82e-6 * (double)keys <= 24.0 + 0.8e-9 * 4.0 * d.D * units;
+  }
+  if (d.attn_impl != SPEC_ATTN_CUDA_CORES && prefix_tc_ok(d))
+    return keys <= 40000 && keys * rows <= 100000;
+  const double tiles = 64.0 * (double)ceil_div64(d.B * rows, 64) * d.Hkv * prefix_len;
+  const double requests = d.D * 1e-6 * (2.75 * (double)keys + 0.15 * (double)(keys * rows));
+  const double pass = (d.D == 64 ? 21.0 : 29.0) + d.D * 1e-6 * 0.09 * tiles;
+  return d.B == 1 || requests <= pass;
+}
+
+// The tensor-core attention takes the shape: bf16 heads of 128, up to 128 rows per KV
+// head, tiles of all pairs counted in 32 bits.
+static bool attn_tc_ok(const spec_dims& d) {
+  return d.kv_dtype == SPEC_BF16 && d.D == 128 && (d.Hq / d.Hkv) * d.M <= 128 &&
+         (int64_t)d.B * d.Hkv * ceil_div64((int64_t)d.max_blocks * kBlock, 64) <
+             ((int64_t)1 << 31);
+}
+
+// Where a call on views of this mode keeps what it needs (tc: on tensor cores).  The
+// partials' region of the calls without views is laid out for the most that either
+// path may take, so the rest of it mostly has room for everything; what it has no
+// room for goes behind all else (`behind`).
+static ViewPlaces view_places(const spec_dims& d, const WsLayout& L, int mode, bool tc,
+                              size_t behind) {
+  ViewPlaces v = {};
+  size_t free = L.attn_off, end = L.attn_off + L.attn_bytes;
+  auto take = [&](size_t bytes) {
+    size_t& from = free + bytes <= end ? free : behind;
+    const size_t o = from;
+    from = align_up(from + bytes, 256);
+    return o;
+  };
+  const size_t pairs = (size_t)d.B * d.Hkv;
+  if (tc) {
+    v.part = take(sizeof(float) * attn_tc_part_floats(d));
+  } else {
+    v.ranges = view_ranges_most(d, mode, L.max_splits);
+    v.part = take(sizeof(float) * pairs * v.ranges * L.rows * (d.D + 1));
+    v.ctx = take(sizeof(int32_t) * (size_t)d.B);
+  }
+  if (mode == kViewPrefix) {
+    if (tc) v.own = take(sizeof(float) * pairs * L.rows * tc_part_stride(d.D));
+    v.pfx = take(sizeof(float) * prefix_pass_floats(d));
+  } else {
+    v.table = take(sizeof(int32_t) * pairs * d.max_blocks);
+  }
+  v.end = behind;
+  return v;
+}
+
+// Bytes of the workspace with these dims' views.
+static size_t view_total(const spec_dims& d, const WsLayout& L) {
+  const bool tc = d.attn_impl != SPEC_ATTN_CUDA_CORES && attn_tc_ok(d);
+  size_t most = view_places(d, L, kViewPages, tc, L.plain).end;
+  // a pass over the prefix, unless even the longest one is read by the requests (the
+  // rule turns to the pass as a prefix grows, and never back)
+  if (!prefix_in_requests(d, ((int64_t)d.max_blocks - 1) * kBlock, tc)) {
+    const size_t end = view_places(d, L, kViewPrefix, tc, L.plain).end;
+    if (end > most) most = end;
+  }
+  return most;
+}
+
 WsLayout workspace_layout(const spec_dims& d) {
   WsLayout L;
   memset(&L, 0, sizeof(L));
@@ -62,13 +151,6 @@ WsLayout workspace_layout(const spec_dims& d) {
   const size_t tc_bytes = d.Hkv > 0 ? sizeof(float) * attn_tc_part_floats(d) : 0;
   if (tc_bytes > L.attn_bytes) L.attn_bytes = tc_bytes;
   L.attn_off = take(L.attn_bytes);
-  if (group > 0 && L.rows <= kMaxNodes) {  // calls of more rows are refused
-    L.view_ctx_off = take(sizeof(int32_t) * (size_t)d.B);
-    if (d.max_blocks > 0)
-      L.view_table_off = take(sizeof(int32_t) * (size_t)d.B * d.Hkv * d.max_blocks);
-    L.own_part_off = take(sizeof(float) * (size_t)d.B * d.Hkv * L.rows * tc_part_stride(d.D));
-    L.pfx_part_off = take(sizeof(float) * prefix_part_floats(d));
-  }
   L.rs_chunk = rs_chunk_elems(d.logits_dtype);
   L.rs_chunks = (int)ceil_div64(d.V, L.rs_chunk);
   L.rs_bytes = sizeof(RowStat) * (size_t)d.B * 2 * d.M * L.rs_chunks;
@@ -87,7 +169,9 @@ WsLayout workspace_layout(const spec_dims& d) {
     L.lm_cnt_off = take(sizeof(uint32_t) * 2 * (size_t)lm_units * 4);
   }
   off = rsf_layout(d, off, &L);
-  L.total = off;
+  L.plain = L.total = off;
+  if (group > 0 && L.rows <= kMaxNodes && d.max_blocks > 0)  // views of other dims are refused
+    L.total = view_total(d, L);
   return L;
 }
 
@@ -117,7 +201,7 @@ static spec_status check_kv(const spec_dims* d) {
 
 static spec_status check_ws(const spec_dims* d, void* ws, size_t ws_bytes) {
   if (ws == nullptr || !aligned16(ws)) return SPEC_ERR_INVALID_ARG;
-  if (ws_bytes < workspace_layout(*d).total) return SPEC_ERR_INVALID_ARG;
+  if (ws_bytes < workspace_layout(*d).plain) return SPEC_ERR_INVALID_ARG;
   return SPEC_OK;
 }
 
@@ -155,42 +239,6 @@ spec_status spec_get_device_status(void* ws, void* stream, int32_t* flags, int32
   return SPEC_OK;
 }
 
-// Whether every request reads a shared prefix itself (its pages come from L2 after
-// the first), rather than one pass over it for the batch with a merge after it.
-// The pass and the merge cost 10 to 25 us, the other grows with the requests.
-// Measured, us, requests / one pass (B, Hkv, group, M, prefix):
-//   tensor cores: the requests' reads cost 82 us for 10^6 keys (heads of 128), the pass
-//   24 us and 0.8 for 10^9 operations of whole units of 256 rows.  38 / 62 (64, 1, 4, 1,
-//   4096), 42 / 51 (16, 8, 8, 5, 2048), 45 / 49 (64, 8, 8, 1, 512), 62 / 70 (2, 8, 4, 1,
-//   32768), 64 / 62 (64, 1, 4, 9, 8192), 64 / 66 (8, 8, 8, 9, 8192), 55 / 44 (16, 8, 4, 1,
-//   4096), 60 / 51 (64, 8, 4, 1, 1024), 81 / 60 (4, 8, 4, 1, 24576), 121 / 144 (1, 8, 4, 1,
-//   131072)
-//   CUDA cores: the requests' reads cost 2.75 us for 10^6 elements of keys and 0.15 for
-//   10^6 products (more than 8 rows), the pass 21 or 29 us (heads of 64, 128) and 0.09
-//   for 10^6 products of whole tiles of 64 rows.  fp32, heads of 64: 21 / 29 (8, 8, 1,
-//   1, 512), 40 / 39 (8, 8, 1, 1, 2048), 41 / 50 (4, 8, 1, 1, 4096), 69 / 81 (2, 8, 1, 1,
-//   16384), 79 / 39 (64, 8, 1, 1, 512), 112 / 44 (26, 8, 1, 1, 2208); heads of 128: 38 / 52
-//   (16, 2, 4, 1, 2048), 41 / 61 (4, 8, 4, 1, 2048), 46 / 57 (8, 8, 4, 5, 512), 74 / 69 (16, 8,
-//   4, 5, 512), 77 / 48 (16, 8, 1, 1, 1024), 112 / 89 (4, 8, 4, 1, 8192), 147 / 55 (64, 8, 1, 1,
-//   512)
-//   bf16 heads of 64, the pass on tensor cores and the rest on CUDA cores, by keys and
-//   keys times rows: 17 / 19 (4, 8, 4, 1, 512), 20 / 20 (8, 8, 1, 1, 512), 25 / 30 (1, 2, 4, 1,
-//   4096), 27 / 22 (16, 8, 1, 1, 512), 39 / 24 (8, 8, 1, 1, 2048), 42 / 33 (4, 1, 8, 8, 512)
-static bool prefix_in_requests(const spec_dims& d, int prefix_len, bool tc) {
-  const int64_t keys = (int64_t)d.B * d.Hkv * prefix_len;
-  const int64_t rows = (int64_t)(d.Hq / d.Hkv) * d.M;
-  if (tc) {
-    const double units = 256.0 * (double)ceil_div64(d.B * rows, 256) * d.Hkv * prefix_len;
-    return d.B == 1 || 82e-6 * (double)keys <= 24.0 + 0.8e-9 * 4.0 * d.D * units;
-  }
-  if (d.attn_impl != SPEC_ATTN_CUDA_CORES && prefix_tc_ok(d))
-    return keys <= 40000 && keys * rows <= 100000;
-  const double tiles = 64.0 * (double)ceil_div64(d.B * rows, 64) * d.Hkv * prefix_len;
-  const double requests = d.D * 1e-6 * (2.75 * (double)keys + 0.15 * (double)(keys * rows));
-  const double pass = (d.D == 64 ? 21.0 : 29.0) + d.D * 1e-6 * 0.09 * tiles;
-  return d.B == 1 || requests <= pass;
-}
-
 static spec_status attn_common(const void* q, const void* k_new, const void* v_new, void* k_cache,
                                void* v_cache, const int32_t* block_table, const int32_t* ctx_lens,
                                const int32_t* parent, int32_t window, int32_t sinks,
@@ -210,10 +258,7 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
   // kernel choice: the tensor-core kernel whenever it supports the shape
   // (bf16, D = 128, up to 128 rows per KV head): even a few rows per KV head
   // run faster there than on CUDA cores; CUDA cores otherwise
-  const bool tc_ok = dims->kv_dtype == SPEC_BF16 && dims->D == 128 && R <= 128 &&
-                     (int64_t)dims->B * dims->Hkv *
-                             ceil_div64((int64_t)dims->max_blocks * kBlock, 64) <
-                         ((int64_t)1 << 31);
+  const bool tc_ok = attn_tc_ok(*dims);
   const bool simt_ok = R <= 128;
   bool use_tc;
   if (dims->attn_impl == SPEC_ATTN_TENSOR_CORES) {
@@ -231,6 +276,7 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
   if (view.mode == kViewPrefix && prefix_in_requests(*dims, view.prefix_len, use_tc))
     view.mode = kViewWhole;
   const WsLayout lay = workspace_layout(*dims);
+  if (view.mode != kViewNone && ws_bytes < lay.total) return SPEC_ERR_INVALID_ARG;
   AttnArgs a;
   a.q = q;
   a.k_new = k_new;
@@ -250,7 +296,8 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
   a.ws = ws;
   if (view.mode != kViewNone) {
     char* w = static_cast<char*>(ws);
-    a.view.ctx = reinterpret_cast<int32_t*>(w + lay.view_ctx_off);
+    a.at = view_places(*dims, lay, view.mode, use_tc, lay.plain);
+    a.view.ctx = reinterpret_cast<int32_t*>(w + a.at.ctx);
     if (view.mode == kViewPrefix) {
       const int pp = view.prefix_len / kBlock;
       a.view.table = block_table + pp;
@@ -258,7 +305,7 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
       a.view.stride_h = 0;
       a.view.entries = dims->max_blocks - pp;
     } else if (view.mode == kViewWhole) {
-      a.view.table = reinterpret_cast<int32_t*>(w + lay.view_table_off);
+      a.view.table = reinterpret_cast<int32_t*>(w + a.at.table);
       a.view.stride_b = dims->max_blocks;
       a.view.stride_h = 0;
       a.view.entries = dims->max_blocks;
@@ -267,7 +314,7 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
       // the new rows; together no more than the context and the new rows have
       const int64_t most = (int64_t)view.n_pages + ceil_div(kBlock - 1 + dims->M, kBlock);
       a.view.entries = most < dims->max_blocks ? (int)most : dims->max_blocks;
-      a.view.table = reinterpret_cast<int32_t*>(w + lay.view_table_off);
+      a.view.table = reinterpret_cast<int32_t*>(w + a.at.table);
       a.view.stride_h = a.view.entries;
       a.view.stride_b = (int64_t)dims->Hkv * a.view.entries;
     }

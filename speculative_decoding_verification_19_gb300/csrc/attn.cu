@@ -625,6 +625,46 @@ cudaError_t kv_append_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Views of many rows: register tiles of 64 rows (attn_prefix.cu, with both sides'
+// times), else the windowed kernel, a row to four a warp.
+static bool view_tiled(const spec_dims& d) { return (d.Hq / d.Hkv) * d.M > 32; }
+
+// Keys that a range of a view should have, of `most` at most.
+static int64_t view_range_keys(const spec_dims& d, int64_t most) {
+  const int R = (d.Hq / d.Hkv) * d.M;
+  int64_t want = (int64_t)d.B * d.Hkv * most / kWinCtas;
+  if (view_tiled(d)) {
+    // two waves where a CTA of one would have 160 keys or more, for what is uneven
+    // between requests: 20 requests of 64 rows, 8 heads of 128 fp32 values over 60
+    // pages 208 us, 231 with one; 13 of 36 rows, 4 heads over 45 pages, 93 keys, 72 with
+    // two waves, 62 with one
+    want = (int64_t)d.B * d.Hkv * ceil_div(R, 64) * most / view_ctas();
+    if (want >= 160) want /= 2;
+  }
+  // few long views: a key in a range costs some 0.04 us, a partial in the merge 0.15
+  // (fp32, one request and KV head, 30000 positions: 8 rows of 64 45 us, 88 without
+  // this, 64 rows of 128 105, 139; two requests of 4 rows of 128 82, 78)
+  want = max(want, (int64_t)sqrt((double)most / 0.27));
+  return max(want, (int64_t)kMinWinSplit);
+}
+
+// Ranges of a view that there is room for: the layout's, or for a small batch, whose
+// ranges need more partials than that, as many as the partials of a prefix would
+// take (2 requests of 36 rows, 8 heads of 128 fp32 values, 1270 keys: 98 us for the
+// call with 5 ranges, 56 with 20); but no more than a request that fills its table
+// is cut into.
+int view_ranges_most(const spec_dims& d, int mode, int max_splits) {
+  int64_t ranges = max_splits;
+  if (mode != kViewPrefix) {
+    const int R = (d.Hq / d.Hkv) * d.M;
+    const int64_t slots = (int64_t)(prefix_part_floats(d) / ((size_t)R * (d.D + 1)));
+    ranges = max(ranges, slots / ((int64_t)d.B * d.Hkv));
+  }
+  const int64_t most = (int64_t)d.max_blocks * kBlock;
+  const int64_t use = ceil_div64(most, view_range_keys(d, most));
+  return (int)min(ranges, use + use / 32 + 1);  // (whole keys a range: shorter tables may have more)
+}
+
 template <typename T>
 static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaStream_t st,
                                int* launches) {
@@ -646,9 +686,7 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
   const int64_t stride_h = viewed ? a.view.stride_h : 0;
   const int32_t* ctx = viewed ? a.view.ctx : a.ctx_lens;
 
-  // views of many rows: register tiles of 64 rows (attn_prefix.cu, with both sides'
-  // times), else the windowed kernel, a row to four a warp
-  const bool tiled = viewed && R > 32;
+  const bool tiled = viewed && view_tiled(d);
   const size_t smem = attn_simt_smem_bytes(R, d.D);
   // Key ranges: the layout's, or, with a window, of the fewer keys that a
   // request then has at most, for one wave of three CTAs per SM (the tree case
@@ -660,32 +698,13 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
     const int64_t most = min(entries * kBlock,
                              (int64_t)ceil_div(a.sinks, kTileKeys) * kTileKeys + a.window + d.M +
                                  kTileKeys);
-    // (tiles of rows: two waves where a CTA of one would have 160 keys or more, for what
-    // is uneven between requests: 20 requests of 64 rows, 8 heads of 128 fp32 values over
-    // 60 pages 208 us, 231 with one; 13 of 36 rows, 4 heads over 45 pages, 93 keys, 72
-    // with two waves, 62 with one)
-    int64_t want = (int64_t)d.B * d.Hkv * most / kWinCtas;
-    if (tiled) {
-      want = (int64_t)d.B * d.Hkv * ceil_div(R, 64) * most / view_ctas();
-      if (want >= 160) want /= 2;
-    }
-    // few long views: a key in a range costs some 0.04 us, a partial in the merge 0.15
-    // (fp32, one request and KV head, 30000 positions: 8 rows of 64 45 us, 88 without
-    // this, 64 rows of 128 105, 139; two requests of 4 rows of 128 82, 78)
-    if (viewed) want = max(want, (int64_t)sqrt((double)most / 0.27));
-    if (want < kMinWinSplit) want = kMinWinSplit;
+    const int64_t want = viewed ? view_range_keys(d, most)
+                                : max((int64_t)kMinWinSplit, (int64_t)d.B * d.Hkv * most / kWinCtas);
     const int unit = tiled ? view_range_unit(d) : kTileKeys;
     int64_t ranges = lay.max_splits;
-    if (viewed && a.view.mode != kViewPrefix) {
-      // a small batch's ranges need more partials than the layout has: there is
-      // room where a prefix' partials would go (2 requests of 36 rows, 8 heads of
-      // 128 fp32 values, 1270 keys: 98 us for the call with 5 ranges, 56 with 20)
-      const int64_t slots = (int64_t)(prefix_part_floats(d) / ((size_t)R * (d.D + 1)));
-      const int64_t more = slots / ((int64_t)d.B * d.Hkv);
-      if (more > ranges) {
-        ranges = more;
-        part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + lay.pfx_part_off);
-      }
+    if (viewed) {
+      ranges = a.at.ranges;
+      part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + a.at.part);
     }
     split_keys = (int)(ceil_div64(max(want, ceil_div64(most, ranges)), unit) * unit);
     splits = (int)ceil_div64(most, split_keys);
@@ -763,7 +782,7 @@ static cudaError_t launch_simt(const AttnArgs& args, const WsLayout& lay, cudaSt
     e = prefix_launch(a, lay, st, &plan, launches);
     if (e != cudaSuccess) return e;
     const OwnPart own = {part, splits, d.D + 1, split_keys, ctx, req_ok};
-    return prefix_merge_launch(a, lay, plan, own, st, launches);
+    return prefix_merge_launch(a, plan, own, st, launches);
   }
 
   {

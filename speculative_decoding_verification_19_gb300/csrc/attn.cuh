@@ -38,6 +38,18 @@ __device__ __forceinline__ int view_ctx(const AttnView& v, int b, int ctx) {
   return __ldcg(v.counts + b) * kBlock + ctx % kBlock;
 }
 
+// Places in the workspace of what a call on views keeps while it runs.  No two of
+// them overlap; they may lie where calls without a view have split-KV partials.
+struct ViewPlaces {
+  size_t part;    // partials of the requests' own keys, and the ranges that they have room for
+  int ranges;     // (CUDA cores)
+  size_t ctx;     // [B] int32 cached keys of every view (CUDA cores)
+  size_t table;   // [B, Hkv, <= max_blocks] int32 block ids (kViewWhole, kViewPages)
+  size_t own;     // [B*Hkv, rows] f32 rows of a request's own keys (kViewPrefix, tensor cores)
+  size_t pfx;     // f32 rows: partials of the prefix (kViewPrefix)
+  size_t end;     // bytes of the workspace up to the last of them
+};
+
 struct AttnArgs {
   const void* q;
   const void* k_new;
@@ -53,6 +65,7 @@ struct AttnArgs {
   float scale;
   int window, sinks;  // window 0: every cached position is visible
   AttnView view;      // mode kViewNone: the requests themselves
+  ViewPlaces at;      // of the view, if there is one
   void* ws;
 };
 
@@ -204,14 +217,16 @@ size_t attn_simt_smem_bytes(int R, int D);
 constexpr int kMaxPrefixCtas = 160;
 
 size_t prefix_part_floats(const spec_dims& d);
+size_t prefix_pass_floats(const spec_dims& d);
 bool prefix_tc_ok(const spec_dims& d);
+int view_ranges_most(const spec_dims& d, int mode, int max_splits);
 size_t prefix_tc_part_floats(const spec_dims& d);
 cudaError_t prefix_tc_launch(const AttnArgs& a, float* part, uint32_t* status, cudaStream_t st,
                              PrefixPlan* plan);
 cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, PrefixPlan* plan,
                           int* launches);
-cudaError_t prefix_merge_launch(const AttnArgs& a, const WsLayout& lay, const PrefixPlan& plan,
-                                const OwnPart& own, cudaStream_t st, int* launches);
+cudaError_t prefix_merge_launch(const AttnArgs& a, const PrefixPlan& plan, const OwnPart& own,
+                                cudaStream_t st, int* launches);
 size_t attn_tc_part_floats(const spec_dims& d);
 cudaError_t kv_append_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, int* launches);
 cudaError_t attn_launch_simt(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, int* launches);

@@ -406,13 +406,23 @@ static PrefixPlan simt_plan(const spec_dims& d, int prefix_len) {
   return p;
 }
 
-size_t prefix_part_floats(const spec_dims& d) {
+static size_t prefix_simt_part_floats(const spec_dims& d) {
   const int64_t rows = (int64_t)d.B * (d.Hq / d.Hkv) * d.M;
   const int64_t units = (int64_t)d.Hkv * ceil_div64(rows, kPfxRows);
   const int64_t slots = units > kPfxSlots ? units : kPfxSlots;
-  const size_t simt = (size_t)slots * (size_t)(rows < kPfxRows ? rows : kPfxRows) * tc_part_stride(d.D);
-  const size_t tc = prefix_tc_part_floats(d);
+  return (size_t)slots * (size_t)(rows < kPfxRows ? rows : kPfxRows) * tc_part_stride(d.D);
+}
+
+// Of either path; prefix_pass_floats: of the one that a pass with these dims takes.
+size_t prefix_part_floats(const spec_dims& d) {
+  const size_t simt = prefix_simt_part_floats(d), tc = prefix_tc_part_floats(d);
   return simt > tc ? simt : tc;
+}
+static bool prefix_on_tensor_cores(const spec_dims& d) {
+  return prefix_tc_ok(d) && d.attn_impl != SPEC_ATTN_CUDA_CORES;
+}
+size_t prefix_pass_floats(const spec_dims& d) {
+  return prefix_on_tensor_cores(d) ? prefix_tc_part_floats(d) : prefix_simt_part_floats(d);
 }
 
 template <typename T, bool kOwn>
@@ -444,10 +454,10 @@ cudaError_t view_split_launch(const AttnArgs& a, const ViewRanges& own, int spli
 
 cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t st, PrefixPlan* plan,
                           int* launches) {
-  float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + lay.pfx_part_off);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + a.at.pfx);
   uint32_t* status = reinterpret_cast<uint32_t*>(static_cast<char*>(a.ws) + lay.status_off);
   cudaError_t e;
-  if (prefix_tc_ok(a.d) && a.d.attn_impl != SPEC_ATTN_CUDA_CORES) {
+  if (prefix_on_tensor_cores(a.d)) {
     e = prefix_tc_launch(a, part, status, st, plan);
     if (e == cudaSuccess) ++*launches;
     return e;
@@ -459,10 +469,10 @@ cudaError_t prefix_launch(const AttnArgs& a, const WsLayout& lay, cudaStream_t s
   return e;
 }
 
-cudaError_t prefix_merge_launch(const AttnArgs& a, const WsLayout& lay, const PrefixPlan& plan,
-                                const OwnPart& own, cudaStream_t st, int* launches) {
+cudaError_t prefix_merge_launch(const AttnArgs& a, const PrefixPlan& plan, const OwnPart& own,
+                                cudaStream_t st, int* launches) {
   const spec_dims& d = a.d;
-  const float* part = reinterpret_cast<const float*>(static_cast<char*>(a.ws) + lay.pfx_part_off);
+  const float* part = reinterpret_cast<const float*>(static_cast<char*>(a.ws) + a.at.pfx);
   const int64_t rows = (int64_t)d.B * (d.Hq / d.Hkv) * d.M;
   const int64_t items = (int64_t)d.Hkv * plan.tiles * plan.key_tiles;
   PdlLaunch L(dim3((unsigned)ceil_div64(rows, 8), d.Hkv), dim3(256), 0, st);

@@ -1521,7 +1521,7 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
   // of up to 60 27 / 24; 64 pairs of 11 24 / 24, 144 of 34 39 / 42 and 45 / 53.
   const int gather = viewed && !behind && 3 * (int64_t)d.B * d.Hkv <= G &&
                      ceil_div(a.view.entries, kPages) > 2;
-  float* own_part = reinterpret_cast<float*>(ws + lay.own_part_off);
+  float* own_part = reinterpret_cast<float*>(ws + a.at.own);
   PrefixPlan plan = {};
   {
     PdlLaunch L(dim3(d.B), dim3(kPrepThreads), 0, st);
@@ -1565,7 +1565,7 @@ cudaError_t attn_launch_tc(const AttnArgs& a, const WsLayout& lay, cudaStream_t 
   ++*launches;
   if (behind) {
     const OwnPart own = {own_part, 1, tc_part_stride(d.D), INT32_MAX, a.view.ctx, ntiles};
-    return prefix_merge_launch(a, lay, plan, own, st, launches);
+    return prefix_merge_launch(a, plan, own, st, launches);
   }
   if (gather) {
     PdlLaunch L(dim3(ceil_div(group * d.M, 8), d.Hkv, d.B), dim3(256), 0, st);

@@ -153,11 +153,6 @@ struct WsLayout {
   size_t tc_sync_off;     // uint32 arrival count of the request-check kernel
   size_t win_depth_off;   // [B*M] int32 depth of every new row (windowed attention)
   size_t pg_sync_off;     // uint32 arrival count of the block-table kernel
-  size_t view_ctx_off;    // [B] int32 cached keys of every request's view (AttnView)
-  size_t view_table_off;  // [B, Hkv, <= max_blocks] int32 block ids of the views of selected pages
-  size_t own_part_off;    // [B*Hkv, rows] f32 rows: attention over a request's own keys behind
-                          // a shared prefix (tensor cores)
-  size_t pfx_part_off;    // f32 rows: partials of the shared prefix
   size_t attn_off;        // split-KV partials of either attention path (f32)
   size_t attn_bytes;
   int split_keys;         // keys per split (multiple of 16)
@@ -181,7 +176,8 @@ struct WsLayout {
   size_t rsf_req_off;     // [B] u32 rows finished per request
   size_t rsf_list_off;    // [B] 48-byte residual entries in the order posted
   size_t rsf_rescnt_off;  // [B] u32 residual units finished per request
-  size_t total;
+  size_t plain;           // bytes that the calls without a view need
+  size_t total;           // bytes that every call needs
 };
 
 WsLayout workspace_layout(const spec_dims& d);
