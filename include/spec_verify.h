@@ -294,7 +294,9 @@ spec_status spec_page_bounds(const void* k_cache, const int32_t* block_table,
  * with the page's bounds lo, hi: no row has a larger product q . k with a key
  * of the page, but for the rounding of the sums, which are in fp32
  * (softmax_scale is not applied).
- *   q [B, M, Hq, D] kv_dtype, bounds as in spec_page_bounds
+ *   q [B, M, Hq, D] kv_dtype, bounds as in spec_page_bounds; a NaN in the sum of a
+ *                 row (from a NaN or an infinite value in q) is the page's score, and
+ *                 raises SPEC_ERR_NONFINITE in spec_page_select where the page competes
  *   scores [B, Hkv, max_blocks] float   -inf for p >= ctx_lens[b] / 16: pages
  *                 that are not whole are always read
  *   ws, ws_bytes  at least 16 bytes (its first word is the status word)

@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1) page_score_tc_kernel(
           uint32_t lo[4], hi[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            asm("min.bf16x2 %0, %1, %2;" : "=r"(lo[k]) : "r"(x[k]), "r"(0u));
-            asm("max.bf16x2 %0, %1, %2;" : "=r"(hi[k]) : "r"(x[k]), "r"(0u));
+            asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(lo[k]) : "r"(x[k]), "r"(0u));
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(hi[k]) : "r"(x[k]), "r"(0u));
           }
           const uint32_t o = (uint32_t)(c >> 3) * (uint32_t)N * 128u + (uint32_t)n * 128u +
                              ((uint32_t)((c & 7) ^ (n & 7)) << 4);
@@ -344,26 +344,26 @@ __global__ void __launch_bounds__(kThreads, 1) page_score_tc_kernel(
                                                (t >> 1) & 1, abort, wait)))
         break;
       ptx::tc_fence_after();
-      float m = -INFINITY;
+      float m[2] = {-INFINITY, -INFINITY};
       for (int n = 0; n < N; n += 16) {
         uint32_t v[16];
         ptx::tmem_ld16(lane_base + buf * N + n, v);
         ptx::tmem_wait_ld(v);
-        if (n + 16 <= R) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) m = fmaxf(m, __uint_as_float(v[j]));
-        } else {
+        if (n + 16 > R) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (n + j < R) m = fmaxf(m, __uint_as_float(v[j]));
+            if (n + j >= R) v[j] = 0xff800000u;  // -inf: no query
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          m[j & 1] = max_nan(m[j & 1], __uint_as_float(v[j]), __uint_as_float(v[j + 8]));
       }
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars->acc_empty[buf]));
       if (p < w.full) {
         const bool there = id >= 0 && id < d.num_blocks;
-        scores[((int64_t)w.b * d.Hkv + w.h) * d.max_blocks + p] = there ? m : -INFINITY;
+        scores[((int64_t)w.b * d.Hkv + w.h) * d.max_blocks + p] = there ? max_nan(m[0], m[1]) : -INFINITY;
         if (!there) raise_status(status, SPEC_ERR_DEVICE_BOUNDS);
       }
     }

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
         const float qv = qs[dd * kLdQ + ty * RPT + r];
-        const float qp = fmaxf(qv, 0.f), qn = fminf(qv, 0.f);
+        const float qp = max_nan(qv, 0.f), qn = min_nan(qv, 0.f);
 #pragma unroll
         for (int k = 0; k < PPT; ++k) acc[r][k] = fmaf(qp, c[k], fmaf(qn, a[k], acc[r][k]));
       }
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
 #pragma unroll
-      for (int k = 0; k < PPT; ++k) best[k] = fmaxf(best[k], acc[r][k]);
+      for (int k = 0; k < PPT; ++k) best[k] = max_nan(best[k], acc[r][k]);
   }
 #pragma unroll
   for (int k = 0; k < PPT; ++k) red[ty * kTile + tx * PPT + k] = best[k];
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
   if (tid < kTile && page0 + tid < d.max_blocks) {
     float m = red[tid];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) m = fmaxf(m, red[k * kTile + tid]);
+    for (int k = 1; k < 8; ++k) m = max_nan(m, red[k * kTile + tid]);
     bool there = page0 + tid < full;
     if (there) {
       const int id = __ldcg(block_table + (int64_t)b * d.max_blocks + page0 + tid);

@@ -35,6 +35,24 @@ struct SelectArgs {
   uint32_t* status;
 };
 
+// Extrema that keep a NaN: a page whose sums hold one gets it as its score, and the
+// selection says so.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 cudaError_t page_bounds_launch(const BoundsArgs& a, cudaStream_t st, int* launches);
 cudaError_t page_score_launch(const ScoreArgs& a, cudaStream_t st, int* launches);
 bool page_score_tc_ok(const spec_dims& d);
