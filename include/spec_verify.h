@@ -341,8 +341,10 @@ spec_status spec_page_select(const float* scores, const int32_t* ctx_lens, int32
  *                 head, strictly ascending, below ctx / 16 (0 of them: the last
  *                 page and the new rows alone)
  * Other arguments and results as in spec_verify_attn, with the rounding of
- * spec_verify_attn_window.  Table entries and keys and values of other pages are
- * not read and may be anything.  A request whose list breaks the rules fails
+ * spec_verify_attn_window.  The outputs are those of a model that attends to these
+ * positions alone: behind them, what accept and reject preserve is that model's
+ * distribution, not the one with attention to every position.
+ * Table entries and keys and values of other pages are not read and may be anything.  A request whose list breaks the rules fails
  * (SPEC_ERR_INVALID_ARG: caches untouched, out = 0, lse = -inf).
  * dims->softmax_scale is not negative.
  */

@@ -34,7 +34,9 @@ static int attn_split_keys(const spec_dims& d) {
 
 // Whether every request reads a shared prefix itself (its pages come from L2 after
 // the first), rather than one pass over it for the batch with a merge after it.
-// The pass and the merge cost 10 to 25 us, the other grows with the requests.
+// A pass of its own with its merge costs some 20 to 30 us more than reading nothing,
+// the requests' reads grow with their number.  The figures are a GB300's (152 SMs);
+// elsewhere either way gives the same results.
 // Measured, us, requests / one pass (B, Hkv, group, M, prefix):
 //   tensor cores: the requests' reads cost 82 us for 10^6 keys (heads of 128), the pass
 //   24 us and 0.8 for 10^9 operations of whole units of 256 rows.  38 / 62 (64, 1, 4, 1,
@@ -43,8 +45,8 @@ static int attn_split_keys(const spec_dims& d) {
 //   4096), 60 / 51 (64, 8, 4, 1, 1024), 81 / 60 (4, 8, 4, 1, 24576), 121 / 144 (1, 8, 4, 1,
 //   131072)
 //   CUDA cores: the requests' reads cost 2.75 us for 10^6 elements of keys and 0.15 for
-//   10^6 products (more than 8 rows), the pass 21 or 29 us (heads of 64, 128) and 0.09
-//   for 10^6 products of whole tiles of 64 rows.  fp32, heads of 64: 21 / 29 (8, 8, 1,
+//   10^6 products, the pass 21 or 29 us (heads of 64, 128) and 0.09 for 10^6 products
+//   of whole tiles of 64 rows.  fp32, heads of 64: 21 / 29 (8, 8, 1,
 //   1, 512), 40 / 39 (8, 8, 1, 1, 2048), 41 / 50 (4, 8, 1, 1, 4096), 69 / 81 (2, 8, 1, 1,
 //   16384), 79 / 39 (64, 8, 1, 1, 512), 112 / 44 (26, 8, 1, 1, 2208); heads of 128: 38 / 52
 //   (16, 2, 4, 1, 2048), 41 / 61 (4, 8, 4, 1, 2048), 46 / 57 (8, 8, 4, 5, 512), 74 / 69 (16, 8,

@@ -36,8 +36,16 @@
 // scheduler.
 //
 // O is rescaled in TMEM by the softmax threads only when a row's maximum grows by
-// more than 2^8.  Scores, maxima, sums and O are fp32, the probabilities bf16 for
-// P V (attn_tc.cu says what that costs).
+// more than 2^8.
+//
+// Rounding.  Scores, maxima, sums and O are fp32.  The probabilities are rounded to
+// bf16 for P V, as in attn_tc.cu, and the sums take them unrounded: an output is off
+// by 0.0023 of its size (2-norm) against fp64, where probabilities of twice the bits
+// leave 0.0017, the output's own rounding.  Those take a second product with what
+// the rounding leaves, and as many columns again, so tiles of 64 keys.  us for the
+// call with two products / with one in tiles of 64 keys / as it is: 64 chains of 5,
+// 64/8 heads, behind 32768 positions 409 / 357 / 344; 16 of them behind 8192 67 / 62 /
+// 62; 64 of them with heads of 64 behind 8192 128 / 112 / 108.
 //
 // TMEM: O_A [0, 128), O_B [128, 256), S_A [256, 336), S_B [336, 416), P_A [416,
 // 456), P_B [464, 504).

@@ -13,7 +13,8 @@
 // of all (b, h) pairs is cut into 64-key tiles (4 blocks of 16), and the
 // tiles of the whole batch are split over one persistent CTA per SM.
 //
-// Two launches per call:
+// Two launches per call, a third with view_merge_kernel; behind a shared prefix its
+// pass and its merge besides (attn_prefix.cu):
 //   attn_prep_kernel  one CTA per request: checks it (capacity, block ids,
 //                     topology) and, for a tree, the ancestor-or-self mask
 //                     of every row.  The last CTA
@@ -31,6 +32,7 @@
 //                     over CTAs leaves one partial per CTA, and the CTA that
 //                     completes the pair's tile count merges them by
 //                     log-sum-exp.
+//   view_merge_kernel  over views, the merge where few pairs are split finely
 //
 // Per CTA, warp-specialised:
 //   warps 10 and 7 (8 when R > 64)  producers: Q of each pair by TMA;
@@ -945,7 +947,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(
           if (tile0 > 0 || (kView && gather && own < cu.nt)) {
             // ---- a later share of a split pair: a partial for the CTA that
             // ran the pair's first tile (unnormalised O of this half's 64
-            // columns, the running maximum, this half's row sum, the tiles)
+            // columns, the running maximum, this half's row sum, the tiles);
+            // with gather the first share too, for view_merge_kernel
             float* prow = part + ((pair + c) * R + (real ? row : 0)) * (int64_t)S;
 #pragma unroll 1
             for (int cc = 0; cc < 2; ++cc) {

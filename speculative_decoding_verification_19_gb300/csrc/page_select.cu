@@ -242,9 +242,10 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(
 // Keys stay in shared memory, so a row is read once, and all passes go over it
 // with many warps an SM (keys in registers, 32 a thread: half the warps, unrolled
 // code past the instruction cache, 26 to 42 us where this takes 25).
-// What is left is a chain of some fifteen barriers and about 40 instructions a key:
-// 128 requests x 8 heads of 8192 pages at most, 18 MB: 25 us, one request 4.7 us,
-// where four passes over memory with the leading digits in few bins took 61 and 11.
+// What is left is a chain of some fifteen barriers and about 40 instructions a key, and
+// with 8192 pages 42 KB a CTA, so five CTAs an SM: 128 requests x 8 heads, 18 MB, are
+// 1.35 waves of rows and take 25 us, one request 4.8 us, where four passes over memory
+// with the leading digits in few bins took 61 and 11.
 constexpr int kSelThreads = 256;
 
 __device__ __forceinline__ uint32_t order_key(float x) {
