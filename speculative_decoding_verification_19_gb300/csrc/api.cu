@@ -275,10 +275,14 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
   } else {
     return SPEC_ERR_INVALID_ARG;
   }
-  if (view.mode == kViewPrefix && prefix_in_requests(*dims, view.prefix_len, use_tc))
-    view.mode = kViewWhole;
   const WsLayout lay = workspace_layout(*dims);
   if (view.mode != kViewNone && ws_bytes < lay.total) return SPEC_ERR_INVALID_ARG;
+  // (a pass that the workspace has no room for, were the rule to ask for one where
+  // view_total expects none, is not run)
+  if (view.mode == kViewPrefix &&
+      (prefix_in_requests(*dims, view.prefix_len, use_tc) ||
+       view_places(*dims, lay, kViewPrefix, use_tc, lay.plain).end > lay.total))
+    view.mode = kViewWhole;
   AttnArgs a;
   a.q = q;
   a.k_new = k_new;
