@@ -340,13 +340,6 @@ size_t attn_win_smem_bytes(int rows, int D) {
          (sizeof(ulonglong2) + sizeof(int)) * (size_t)rows;
 }
 
-__device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, unsigned long long b,
-                                                       unsigned long long c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 template <typename T, int D, int RPW>
 __global__ void __launch_bounds__(kWinThreads, RPW <= 8 ? 3 : (D == 64 ? 2 : 1)) attn_win_split_kernel(
     const T* q, const T* k_cache, const T* v_cache, const int32_t* table, int64_t stride_b,
@@ -465,7 +458,7 @@ __global__ void __launch_bounds__(kWinThreads, RPW <= 8 ? 3 : (D == 64 ? 2 : 1))
       for (int j = 0; j < RPW; ++j) {
         const ulonglong2 qv =
             reinterpret_cast<const ulonglong2*>(qs + (warp + kWinWarps * j) * D)[d4];
-        sc2[j] = fma_pair(qv.y, kv.y, fma_pair(qv.x, kv.x, sc2[j]));
+        sc2[j] = fma2(qv.y, kv.y, fma2(qv.x, kv.x, sc2[j]));
       }
     }
     // tiles of cached keys inside every row's window (a depth is at most

@@ -60,12 +60,6 @@ __device__ __forceinline__ float lo_of(unsigned long long x) { return __uint_as_
 __device__ __forceinline__ float hi_of(unsigned long long x) {
   return __uint_as_float((uint32_t)(x >> 32));
 }
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
-                                                   unsigned long long c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 // kOwn: the same tiles over views of the requests (attn_win_split_kernel's work)
 // for more than 32 rows per KV head: 64 rows of a request, its view's keys in

@@ -120,6 +120,14 @@ struct PdlLaunch {  // use in place: cfg points at attr
   PdlLaunch& operator=(const PdlLaunch&) = delete;
 };
 
+// a b + c of two fp32 values side by side, each rounded once.
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
+                                                   unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // ---------------------------------------------------------------------------
 // bounded waits
 // ---------------------------------------------------------------------------
