@@ -73,9 +73,23 @@ static bool prefix_in_requests(const spec_dims& d, int64_t prefix_len, bool tc) 
 // The tensor-core attention takes the shape: bf16 heads of 128, up to 128 rows per KV
 // head, tiles of all pairs counted in 32 bits.
 static bool attn_tc_ok(const spec_dims& d) {
-  return d.kv_dtype == SPEC_BF16 && d.D == 128 && (d.Hq / d.Hkv) * d.M <= 128 &&
+  return d.kv_dtype == SPEC_BF16 && d.D == 128 && (int64_t)(d.Hq / d.Hkv) * d.M <= 128 &&
          (int64_t)d.B * d.Hkv * ceil_div64((int64_t)d.max_blocks * kBlock, 64) <
              ((int64_t)1 << 31);
+}
+
+// Positions, and a request's (KV head, page) pairs, of views stay 32-bit; KV heads are
+// a grid's second extent.
+static bool view_counts_ok(const spec_dims& d) {
+  return (int64_t)d.max_blocks * kBlock <= INT32_MAX / 2 && d.Hkv <= 65535 &&
+         (int64_t)d.max_blocks * d.Hkv <= INT32_MAX / 2;
+}
+// Dims whose calls on views are not refused (the others have no room for them, and
+// sizes of these do not overflow).
+static bool view_dims_ok(const spec_dims& d) {
+  return d.B <= 65535 && d.Hkv >= 1 && d.Hq >= d.Hkv && d.Hq % d.Hkv == 0 &&
+         (int64_t)(d.Hq / d.Hkv) * d.M <= kMaxNodes && (d.D == 64 || d.D == 128) &&
+         d.max_blocks >= 1 && view_counts_ok(d);
 }
 
 // Where a call on views of this mode keeps what it needs (tc: on tensor cores).  The
@@ -172,8 +186,7 @@ WsLayout workspace_layout(const spec_dims& d) {
   }
   off = rsf_layout(d, off, &L);
   L.plain = L.total = off;
-  if (group > 0 && L.rows <= kMaxNodes && d.max_blocks > 0)  // views of other dims are refused
-    L.total = view_total(d, L);
+  if (view_dims_ok(d)) L.total = view_total(d, L);
   return L;
 }
 
@@ -256,7 +269,7 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) ||
       !aligned16(v_cache) || !aligned16(out))
     return SPEC_ERR_INVALID_ARG;
-  const int R = (dims->Hq / dims->Hkv) * dims->M;
+  const int64_t R = (int64_t)(dims->Hq / dims->Hkv) * dims->M;
   // kernel choice: the tensor-core kernel whenever it supports the shape
   // (bf16, D = 128, up to 128 rows per KV head): even a few rows per KV head
   // run faster there than on CUDA cores; CUDA cores otherwise
@@ -276,6 +289,7 @@ static spec_status attn_common(const void* q, const void* k_new, const void* v_n
     return SPEC_ERR_INVALID_ARG;
   }
   const WsLayout lay = workspace_layout(*dims);
+  if (view.mode != kViewNone && !view_dims_ok(*dims)) return SPEC_ERR_UNSUPPORTED;
   if (view.mode != kViewNone && ws_bytes < lay.total) return SPEC_ERR_INVALID_ARG;
   // (a pass that the workspace has no room for, were the rule to ask for one where
   // view_total expects none, is not run)
@@ -361,12 +375,7 @@ spec_status spec_verify_attn_window(const void* q, const void* k_new, const void
 static spec_status check_view(const spec_dims* d) {
   if (d == nullptr) return SPEC_ERR_INVALID_ARG;
   if (!(d->softmax_scale >= 0.f) || !(d->softmax_scale < INFINITY)) return SPEC_ERR_INVALID_ARG;
-  // positions, and a request's (KV head, page) pairs, stay 32-bit; KV heads are a
-  // grid's second extent
-  if ((int64_t)d->max_blocks * kBlock > INT32_MAX / 2 || d->Hkv > 65535 ||
-      (int64_t)d->max_blocks * d->Hkv > INT32_MAX / 2)
-    return SPEC_ERR_UNSUPPORTED;
-  return SPEC_OK;
+  return view_counts_ok(*d) ? SPEC_OK : SPEC_ERR_UNSUPPORTED;
 }
 
 spec_status spec_verify_attn_prefix(const void* q, const void* k_new, const void* v_new,

@@ -66,3 +66,19 @@ def test_calls_on_views_need_all_of_it(lib, kw, plain):
     d.attn_impl = sv.ATTN_TENSOR_CORES
     d.D = 64  # not on tensor cores
     assert prefix_call(lib, d, 1 << 40) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,n", [
+    (dict(D=0), 90880), (dict(D=-1), 78592), (dict(Hq=3, Hkv=2), 858624), (dict(Hkv=0), 40960),
+    (dict(Hq=1 << 25, M=128), None), (dict(D=-1, Hq=40, Hkv=1, kv_dtype=F32), None),
+    (dict(B=2**31 - 1, Hq=2**31 - 1, Hkv=2**31 - 1, max_blocks=2**31 - 1), None)])
+def test_sizes_of_dims_that_calls_refuse(lib, kw, n):
+    """A size, and no more: nothing is divided by what they multiply to."""
+    got = sv.workspace_size(sv.make_dims(**(dict(B=2, M=3, Hq=4, Hkv=2, max_blocks=40) | kw)))
+    assert n is None or got == n
+
+
+def test_groups_past_32_bits_are_refused(lib):
+    d = sv.make_dims(B=2, M=128, Hq=1 << 25, Hkv=1, max_blocks=40)  # 2^32 rows per KV head
+    assert plain_call(lib, d, 2**64 - 1) == UNSUPPORTED
+    assert prefix_call(lib, d, 2**64 - 1) == UNSUPPORTED
