@@ -343,9 +343,10 @@ spec_status spec_page_select(const float* scores, const int32_t* ctx_lens, int32
  * Other arguments and results as in spec_verify_attn, with the rounding of
  * spec_verify_attn_window.  The outputs are those of a model that attends to these
  * positions alone: behind them, what accept and reject preserve is that model's
- * distribution, not the one with attention to every position.
- * Table entries and keys and values of other pages are not read and may be anything.  A request whose list breaks the rules fails
- * (SPEC_ERR_INVALID_ARG: caches untouched, out = 0, lse = -inf).
+ * distribution, not the one with attention to every position.  Table entries and
+ * keys and values of other pages are not read and may be anything.  A request whose
+ * list breaks the rules fails (SPEC_ERR_INVALID_ARG: caches untouched, out = 0,
+ * lse = -inf).
  * dims->softmax_scale is not negative.
  */
 spec_status spec_verify_attn_pages(const void* q, const void* k_new, const void* v_new,

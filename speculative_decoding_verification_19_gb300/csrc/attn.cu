@@ -655,7 +655,8 @@ int view_ranges_most(const spec_dims& d, int mode, int max_splits) {
   }
   const int64_t most = (int64_t)d.max_blocks * kBlock;
   const int64_t use = ceil_div64(most, view_range_keys(d, most));
-  return (int)min(ranges, use + use / 32 + 1);  // (whole keys a range: shorter tables may have more)
+  // (a shorter view may be cut into a few more, as ranges are whole keys)
+  return (int)min(ranges, use + use / 32 + 1);
 }
 
 template <typename T>
